@@ -414,6 +414,136 @@ kinv_status kinv_decode_advance(const int32_t* tokens, int32_t* history, int his
                                 int32_t* hist_len, int64_t* step, int32_t* pos,
                                 int32_t* kv_len, int B, kinv_stream stream);
 
+/* -------------------------------------------------- trees of drafted tokens
+ * A batch of trees of drafted tokens to be verified in one step (the pages
+ * have no counterpart: drafting changes only how many rows a step carries,
+ * and a step whose rows do not depend on one another gives a drafted token
+ * the bits it would have as a decode step of its own).
+ *
+ * Sequence b has ctx_len[b] keys in its cache (slots 0 .. ctx_len[b] - 1) and
+ * n_nodes[b] drafted nodes, rows row_offset[b] .. row_offset[b] + n_nodes[b]
+ * - 1 of the row tensors.  parent[row] is the index (within the sequence) of
+ * the node's parent, below the node's own index, or -1: the node follows the
+ * context itself.  With t ancestors a node has depth t: it is the token at
+ * position ctx_len[b] + t, and its keys and values sit in cache slot
+ * ctx_len[b] + (its index).
+ *
+ * All arrays: device int32; ctx_len, n_nodes, row_offset [B]; parent
+ * [total_rows].  max_nodes (<= KINV_TREE_MAX_NODES) bounds n_nodes[b], max_kv
+ * bounds ctx_len[b] + n_nodes[b] (the cache's slots per sequence), and
+ * row_offset[b] + n_nodes[b] <= total_rows.  The rows of different sequences
+ * must not overlap.  A sequence whose device-side numbers break a bound, or
+ * that holds a parent outside [-1, own index), is left out of every call below
+ * -- nothing of it is written -- and the status word records
+ * KINV_ERR_INVALID_ARG.  Rows that belong to no sequence are left as they
+ * were.  The struct itself is read on the host before a call returns. */
+#define KINV_TREE_MAX_NODES 64
+typedef struct {
+  const int32_t* ctx_len;
+  const int32_t* n_nodes;
+  const int32_t* row_offset;
+  const int32_t* parent;
+  int B;
+  int total_rows;
+  int max_nodes;
+  int max_kv;
+} kinv_tree;
+
+/* kinv_rope_append for the rows of drafted trees: the same per-head arithmetic
+ * (optional RMSNorm, then the rotation by the node's position ctx_len[b] +
+ * depth), the keys and values written to the node's slot ctx_len[b] + index.
+ * A drafted token's q, k and v therefore have the bits that kinv_rope_append
+ * gives the same row at the same position.
+ * qkv: device bf16 [total_rows][(Hq + 2 Hkv) D] (ld_qkv); q_out: bf16
+ * [total_rows][Hq][D]; caches and strides as in kinv_rope_append (element
+ * (b, slot, g, d) at b*seq_stride + slot*tok_stride + g*D + d); requirements
+ * and errors as there, and KINV_ERR_UNSUPPORTED for max_nodes >
+ * KINV_TREE_MAX_NODES or B > 65535. */
+kinv_status kinv_rope_append_tree(const void* qkv, int64_t ld_qkv, void* q_out, void* k_cache,
+                                  void* v_cache, int64_t seq_stride, int64_t tok_stride,
+                                  const kinv_tree* tree, const void* q_norm, const void* k_norm,
+                                  float eps, int Hq, int Hkv, int D, float rope_base,
+                                  kinv_stream stream);
+
+/* Attention of drafted nodes: node i of sequence b attends to the context
+ * (slots 0 .. ctx_len[b] - 1), to its ancestors and to itself (slots ctx_len[b]
+ * + ancestor index), which the cache must already hold.
+ * Each row is computed with exactly the arithmetic of kinv_attn_decode for a
+ * sequence of length ctx_len[b] + depth + 1 whose cache holds the context and
+ * then the node's path in order (splits at absolute positions, the key of the
+ * ancestor at depth t in the place of position ctx_len[b] + t), so a drafted
+ * token's bits are those of the decode step that would follow its path, and
+ * do not depend on the other nodes, the tree's shape or the batch.
+ * q, out: device bf16 [total_rows][Hq][D] (contiguous).  Caches and strides as
+ * for kinv_attn_decode.  workspace: device, 16-byte aligned, at least
+ * kinv_attn_tree_workspace(B, total_rows, max_nodes, Hq, Hkv, D, max_kv,
+ * split_len) bytes; two calls that may run at the same time need one each.
+ * Requirements as for kinv_attn_decode. */
+size_t kinv_attn_tree_workspace(int B, int total_rows, int max_nodes, int Hq, int Hkv, int D,
+                                int max_kv, int split_len);
+kinv_status kinv_attn_tree(const void* q, const void* k_cache, const void* v_cache,
+                           int64_t seq_stride, int64_t tok_stride, const kinv_tree* tree,
+                           void* out, int Hq, int Hkv, int D, int split_len, float scale,
+                           void* workspace, size_t workspace_bytes, kinv_stream stream);
+
+/* The drafted tokens that the model agrees with, and their place in the cache.
+ * tokens[row]: the node's token; next_tokens[row]: the model's own token after
+ * the node (e.g. sampled from the row's logits).  Node 0 of a sequence is a
+ * token that was already decided, so it is always taken; the path goes on to
+ * the lowest-indexed child of its last node whose token equals next_tokens of
+ * that node, and ends where there is none.  For each sequence with n_nodes[b]
+ * > 0, with the path's node j_t at depth t < n_accepted[b]:
+ *   path[b][t]       = j_t
+ *   out_tokens[b][t] = next_tokens of j_t (the tokens this step decides: the
+ *                      drafted ones it confirms, then one more)
+ *   cache slot ctx_len[b] + t = the bits of slot ctx_len[b] + j_t,
+ * in every one of n_layers layers of both caches, so that the slots 0 ..
+ * ctx_len[b] + n_accepted[b] - 1 then hold what decoding those tokens one by
+ * one would have put there; the slots behind them are left as they were.
+ * path and out_tokens beyond n_accepted[b] are -1; n_accepted[b] = 0 for a
+ * sequence without nodes.
+ * n_accepted: device int32 [B]; path, out_tokens: device int32
+ * [B][max_nodes].  None of them may overlap the tree's arrays, tokens or
+ * next_tokens.  Element (layer, b, slot, g, d) of a cache is at
+ * layer*layer_stride + b*seq_stride + slot*tok_stride + g*D + d.  n_layers = 0
+ * moves nothing (k_cache and v_cache may then be NULL).
+ * Requirements: D % 8 == 0, strides multiples of 8, 16-byte aligned caches,
+ * n_layers <= 65535. */
+kinv_status kinv_tree_accept(const kinv_tree* tree, const int32_t* tokens,
+                             const int32_t* next_tokens, void* k_cache, void* v_cache,
+                             int n_layers, int64_t layer_stride, int64_t seq_stride,
+                             int64_t tok_stride, int Hkv, int D, int32_t* n_accepted,
+                             int32_t* path, int32_t* out_tokens, kinv_stream stream);
+
+/* ------------------------------------------------------ log probabilities
+ * Per row r of logits x (V of them), with m = max x and S = sum e^(x - m):
+ *   logprob[r][j]    = x[ids[r][j]] - m - ln S         (j < n_ids)
+ *   entropy[r]       = ln S - (sum e^(x - m) (x - m)) / S       (nats)
+ *   top_ids[r][j], top_logprobs[r][j]: the j-th likeliest id and its log
+ *                      probability, by (x descending, id ascending), j < top_k.
+ * The row is cut into units of 512 ids; a warp takes a unit's maximum and sums
+ * in one fixed order and the units are folded in one fixed order, all in fp32,
+ * so a row's bits do not depend on the other rows.
+ * NaN logits count as -infinity (as in kinv_sample).  -infinity has probability
+ * 0 (logprob -infinity).  In a row that holds +infinity those ids share the
+ * whole probability equally.  In a row of -infinity only, every logprob is
+ * -infinity and the entropy 0.  An id below 0 is padding: its logprob is 0.
+ * An id >= V gives NaN and the status word records KINV_ERR_INVALID_ARG.
+ *
+ * logits: device fp32 or bf16 [rows][ld] (16-byte loads where the base and ld
+ * allow, any alignment works); ids: device int32 [rows][n_ids]; logprob fp32
+ * [rows][n_ids]; entropy (nullable) fp32 [rows]; top_ids int32, top_logprobs
+ * fp32 [rows][top_k].  ids and logprob may be NULL when n_ids = 0, the top
+ * arrays when top_k = 0.  workspace: device, 16-byte aligned, at least
+ * kinv_logprobs_workspace(rows, V) bytes (may be 0 and then NULL); two calls
+ * that may run at the same time need one each.
+ * Requirements: 1 <= V <= 1048576, ld >= V, 0 <= top_k <= 32, top_k <= V. */
+size_t kinv_logprobs_workspace(int rows, int V);
+kinv_status kinv_logprobs(const void* logits, kinv_dtype dtype, int64_t ld, int rows, int V,
+                          const int32_t* ids, int n_ids, float* logprob, float* entropy,
+                          int top_k, int32_t* top_ids, float* top_logprobs, void* workspace,
+                          size_t workspace_bytes, kinv_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

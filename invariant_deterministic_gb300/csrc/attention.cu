@@ -41,6 +41,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "attn_mma.cuh"
 #include "common.cuh"
 
 namespace kinv {
@@ -76,49 +77,6 @@ __device__ __forceinline__ bool seq_ok(const AttnParams& p, int b) {
 
 __device__ __forceinline__ void report_bad_length(const AttnParams& p) {
   if (threadIdx.x == 0 && p.status) atomicExch(p.status, DEV_ATTN_BAD_LENGTH);
-}
-
-// A 16-byte cp.async with an L2 eviction policy (createpolicy).
-__device__ __forceinline__ void cp_async16_hint(uint32_t dst, const void* src, uint64_t policy) {
-  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
-                                        uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
-                                          uint32_t& r3) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
-               : "r"(addr));
-}
-// D = A . B + D, one 16 x 8 x 16 warp MMA, bf16 inputs, fp32 accumulation.
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// A softmax weight as the pair hi + lo of bf16 values: hi = bf16(x) and
-// lo = bf16(x - hi) (x - hi is exact in fp32), so hi + lo carries x to about
-// 16 significant bits where bf16 alone keeps 8.
-__device__ __forceinline__ void split_bf16(float x, float& hi, float& lo) {
-  hi = __bfloat162float(__float2bfloat16_rn(x));
-  lo = __bfloat162float(__float2bfloat16_rn(__fsub_rn(x, hi)));
 }
 
 template <int D>
@@ -913,13 +871,6 @@ kinv_status launch_prefill_tc(const void* q, const void* k_cache, const void* v_
   if (attr != KINV_OK) return attr;
   return launch_kernel(attn_prefill_tc_kernel<D>, dim3(a.tiles_per_seq, a.Hkv, B), dim3(kTcThreads), smem, stream, 1,
                        mq, mk, mv, a);
-}
-
-// c = fp32(scale * log2 e), the scores' factor in the base-2 softmax; a
-// scale that is not a positive finite number means 1 / sqrt(D).
-float base2_factor(float scale, int D) {
-  const float s = (scale > 0.f && std::isfinite(scale)) ? scale : 1.0f / sqrtf(static_cast<float>(D));
-  return static_cast<float>(static_cast<double>(s) * 1.4426950408889634074);
 }
 
 kinv_status check_common(const void* q, const void* k, const void* v, int64_t seq_stride,

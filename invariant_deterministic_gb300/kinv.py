@@ -64,6 +64,16 @@ SIGNATURES = {
     "kinv_swiglu": (_i32, [_c_p, _i64, _c_p, _i64, _i32, _i32, _c_p]),
     "kinv_rope_append": (_i32, [_c_p, _i64, _c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p,
                                 _f32, _i32, _i32, _i32, _i32, _f32, _c_p]),
+    "kinv_rope_append_tree": (_i32, [_c_p, _i64, _c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _f32,
+                                     _i32, _i32, _i32, _f32, _c_p]),
+    "kinv_attn_tree_workspace": (_sz, [_i32] * 8),
+    "kinv_attn_tree": (_i32, [_c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _i32, _i32, _i32, _i32, _f32,
+                              _c_p, _sz, _c_p]),
+    "kinv_tree_accept": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i32, _i64, _i64, _i64, _i32, _i32, _c_p,
+                                _c_p, _c_p, _c_p]),
+    "kinv_logprobs_workspace": (_sz, [_i32, _i32]),
+    "kinv_logprobs": (_i32, [_c_p, _i32, _i64, _i32, _i32, _c_p, _i32, _c_p, _c_p, _i32, _c_p, _c_p, _c_p,
+                             _sz, _c_p]),
     "kinv_decode_advance": (_i32, [_c_p, _c_p, _i32, _c_p, _c_p, _c_p, _c_p, _i32, _c_p]),
 }
 
@@ -333,6 +343,180 @@ def attn_prefill(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len: int, 
                                    float(scale), _ptr(workspace), workspace.numel(),
                                    _stream(stream)), "kinv_attn_prefill")
     return out
+
+
+# --------------------------------------------------- trees of drafted tokens
+TREE_MAX_NODES = 64
+
+
+class TreeStruct(ctypes.Structure):
+    """kinv_tree: a batch of trees of drafted tokens."""
+    _fields_ = [("ctx_len", _c_p), ("n_nodes", _c_p), ("row_offset", _c_p), ("parent", _c_p),
+                ("B", _i32), ("total_rows", _i32), ("max_nodes", _i32), ("max_kv", _i32)]
+
+
+class Tree:
+    """A batch of trees of drafted tokens over device int32 tensors (kept while
+    the tree is used): ctx_len, n_nodes, row_offset [B], parent [total_rows]
+    (index of the parent within the sequence, or -1).  Node i of sequence b is
+    row row_offset[b] + i, sits in cache slot ctx_len[b] + i and has position
+    ctx_len[b] + its depth.  max_nodes bounds n_nodes, max_kv bounds ctx_len +
+    n_nodes (the cache's slots).  The tensors may be refilled between calls."""
+
+    def __init__(self, ctx_len, n_nodes, row_offset, parent, max_nodes: int, max_kv: int):
+        for t, name in ((ctx_len, "ctx_len"), (n_nodes, "n_nodes"), (row_offset, "row_offset"),
+                        (parent, "parent")):
+            _need(t, torch.int32, name)
+            if t.dim() != 1 or not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous vector")
+        b = ctx_len.shape[0]
+        if n_nodes.shape[0] != b or row_offset.shape[0] != b:
+            raise ValueError("Tree: ctx_len, n_nodes and row_offset must have one entry per sequence")
+        self.tensors = (ctx_len, n_nodes, row_offset, parent)
+        self.B, self.total_rows, self.max_nodes, self.max_kv = b, parent.shape[0], int(max_nodes), int(max_kv)
+        self.struct = TreeStruct(_ptr(ctx_len), _ptr(n_nodes), _ptr(row_offset), _ptr(parent), b,
+                                 self.total_rows, self.max_nodes, self.max_kv)
+        self.ptr = ctypes.byref(self.struct)
+
+
+def _need_tree_cache(k_cache, v_cache, tree: Tree, what: str):
+    """The caches [B][slots][Hkv][D] hold the tree's sequences and max_kv slots each."""
+    _need(k_cache, torch.bfloat16, "k_cache")
+    _need(v_cache, torch.bfloat16, "v_cache")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError(f"{what}: the caches must share shape and strides")
+    bsz, slots, _, d = k_cache.shape
+    if k_cache.stride(3) != 1 or k_cache.stride(2) != d:
+        raise ValueError(f"{what}: a slot's heads must be contiguous")
+    if bsz < tree.B or slots < tree.max_kv:
+        raise ValueError(f"{what}: the caches are smaller than the tree's sequences and max_kv")
+
+
+def rope_append_tree(qkv, q_out, k_cache, v_cache, tree: Tree, n_q, n_kv, head_dim, rope_base,
+                     q_norm=None, k_norm=None, eps=1e-6, stream=None):
+    """kinv_rope_append for the rows of drafted trees: qkv [rows][(Hq + 2 Hkv) D]
+    rotated by each node's position -> q_out [rows][Hq][D], keys and values into
+    the caches [B][slots][Hkv][D] at the node's slot."""
+    _need(qkv, torch.bfloat16, "qkv")
+    _need(q_out, torch.bfloat16, "q_out")
+    _need_tree_cache(k_cache, v_cache, tree, "rope_append_tree")
+    if (qkv.shape[0] < tree.total_rows or qkv.stride(1) != 1 or not q_out.is_contiguous()
+            or qkv.shape[1] != (n_q + 2 * n_kv) * head_dim
+            or q_out.numel() < tree.total_rows * n_q * head_dim or tuple(k_cache.shape[2:]) != (n_kv, head_dim)):
+        raise ValueError("rope_append_tree: shapes or layouts do not match")
+    _check(lib().kinv_rope_append_tree(_ptr(qkv), qkv.stride(0), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+                                       k_cache.stride(0), k_cache.stride(1), tree.ptr, _ptr(q_norm),
+                                       _ptr(k_norm), float(eps), n_q, n_kv, head_dim, float(rope_base),
+                                       _stream(stream)), "kinv_rope_append_tree")
+    return q_out
+
+
+def attn_tree_workspace(tree: Tree, n_q: int, n_kv: int, head_dim: int, split_len: int = SPLIT_LEN) -> int:
+    return int(lib().kinv_attn_tree_workspace(tree.B, tree.total_rows, tree.max_nodes, n_q, n_kv, head_dim,
+                                              tree.max_kv, split_len))
+
+
+def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_len=SPLIT_LEN,
+              scale: float = 0.0, stream=None):
+    """q [rows][Hq][D]; caches [B][slots][Hkv][D], which already hold the
+    nodes' keys and values in their slots.  Each row has the bits of attn_decode
+    behind the context and the node's path."""
+    _need(q, torch.bfloat16, "q")
+    _need_tree_cache(k_cache, v_cache, tree, "attn_tree")
+    rows, hq, d = q.shape
+    hkv = k_cache.shape[2]
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, torch.bfloat16, "out")
+    if (not q.is_contiguous() or not out.is_contiguous() or rows < tree.total_rows
+            or out.shape != q.shape or k_cache.shape[3] != d):
+        raise ValueError("attn_tree: shapes or layouts do not match")
+    if workspace is None:
+        workspace = torch.empty(max(attn_tree_workspace(tree, hq, hkv, d, split_len), 16), dtype=torch.uint8,
+                                device=q.device)
+    _check(lib().kinv_attn_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.stride(0), k_cache.stride(1),
+                                tree.ptr, _ptr(out), hq, hkv, d, split_len, float(scale), _ptr(workspace),
+                                workspace.numel(), _stream(stream)), "kinv_attn_tree")
+    return out
+
+
+def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=None, out_tokens=None,
+                stream=None):
+    """The path of drafted nodes that the model's own tokens agree with, moved
+    to its place in the cache.  tokens, next_tokens: int32 [rows] (a node's
+    token, the model's token after it); kv: [layers][2][B][slots][Hkv][D] bf16,
+    changed in place (None: only the path is found).  Returns (n_accepted [B],
+    path [B][max_nodes], out_tokens [B][max_nodes]) int32."""
+    _need(tokens, torch.int32, "tokens")
+    _need(next_tokens, torch.int32, "next_tokens")
+    dev = tokens.device
+    if (tokens.shape[0] < tree.total_rows or next_tokens.shape[0] < tree.total_rows
+            or not tokens.is_contiguous() or not next_tokens.is_contiguous()):
+        raise ValueError("tree_accept: tokens and next_tokens must be contiguous, one entry per row")
+    if n_accepted is None:
+        n_accepted = torch.empty(tree.B, dtype=torch.int32, device=dev)
+    if path is None:
+        path = torch.empty(tree.B, tree.max_nodes, dtype=torch.int32, device=dev)
+    if out_tokens is None:
+        out_tokens = torch.empty(tree.B, tree.max_nodes, dtype=torch.int32, device=dev)
+    for t, n, name in ((n_accepted, tree.B, "n_accepted"), (path, tree.B * tree.max_nodes, "path"),
+                       (out_tokens, tree.B * tree.max_nodes, "out_tokens")):
+        _need(t, torch.int32, name)
+        if t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"tree_accept: {name} must be contiguous and hold the tree's entries")
+    if kv is None:
+        kp = vp = None
+        layers = ls = ss = ts = hkv = d = 0
+    else:
+        _need(kv, torch.bfloat16, "kv")
+        layers, two, bsz, slots, hkv, d = kv.shape
+        ls, cs, ss, ts, hs, es = kv.stride()
+        if two != 2 or bsz < tree.B or slots < tree.max_kv or es != 1 or hs != d:
+            raise ValueError("tree_accept: kv must be [layers][2][B][slots][Hkv][D] with room for the tree")
+        kp, vp = _ptr(kv), _ptr(kv) + 2 * cs
+    _check(lib().kinv_tree_accept(tree.ptr, _ptr(tokens), _ptr(next_tokens), kp, vp, layers, ls, ss, ts, hkv, d,
+                                  _ptr(n_accepted), _ptr(path), _ptr(out_tokens), _stream(stream)),
+           "kinv_tree_accept")
+    return n_accepted, path, out_tokens
+
+
+# --------------------------------------------------------- log probabilities
+def logprobs_workspace(rows: int, vocab: int) -> int:
+    return int(lib().kinv_logprobs_workspace(rows, vocab))
+
+
+def logprobs(logits, ids=None, top_k: int = 0, workspace=None, stream=None):
+    """logits fp32 or bf16 [rows][V]; ids int32 [rows][n] (negative: padding).
+    Returns (logprobs fp32 [rows][n] or None, entropy fp32 [rows], top_ids int32
+    [rows][top_k] or None, top_logprobs fp32 [rows][top_k] or None)."""
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits: expected torch.float32 or torch.bfloat16, got {logits.dtype}")
+    _need(logits, logits.dtype, "logits")
+    rows, v = logits.shape
+    if logits.stride(1) != 1:
+        raise ValueError("logprobs: the ids of a row must be contiguous")
+    dev = logits.device
+    n_ids, lp = 0, None
+    if ids is not None:
+        _need(ids, torch.int32, "ids")
+        if ids.dim() != 2 or ids.shape[0] != rows or not ids.is_contiguous():
+            raise ValueError("logprobs: ids must be a contiguous [rows][n]")
+        n_ids = ids.shape[1]
+        lp = torch.empty(rows, n_ids, dtype=torch.float32, device=dev)
+    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    top_ids = top_lp = None
+    if top_k:
+        top_ids = torch.empty(rows, top_k, dtype=torch.int32, device=dev)
+        top_lp = torch.empty(rows, top_k, dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = logprobs_workspace(rows, v)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _check(lib().kinv_logprobs(_ptr(logits), F32 if logits.dtype == torch.float32 else BF16,
+                               logits.stride(0) if rows > 1 else max(logits.stride(0), v), rows, v, _ptr(ids),
+                               n_ids, _ptr(lp), _ptr(entropy), int(top_k), _ptr(top_ids), _ptr(top_lp),
+                               _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                               _stream(stream)), "kinv_logprobs")
+    return lp, entropy, top_ids, top_lp
 
 
 # ------------------------------------------------------------------ sampler
