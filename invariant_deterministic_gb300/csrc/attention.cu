@@ -32,8 +32,6 @@
 // bits of the mma.sync step, and both take the sums above in the same order,
 // so a decode step equals a one-row prefill bit for bit and a prompt's rows
 // have the same bits for every chunking.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <cmath>
@@ -42,6 +40,7 @@
 #include <type_traits>
 
 #include "attn_mma.cuh"
+#include "attn_tc.cuh"
 #include "common.cuh"
 
 namespace kinv {
@@ -377,25 +376,6 @@ struct PrefillTcArgs {
   float c2;            // fp32(scale * log2 e) > 0
   int* status;
 };
-
-// tcgen05 instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B,
-// A K-major, B K-major (b_mn = 0) or MN-major (b_mn = 1), N, M = 128.
-__host__ __device__ constexpr uint32_t tc_idesc(int n, int b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(b_mn) << 16) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-}
-// Shared-memory descriptors, 128-byte swizzle, version 1.  K-major: rows of
-// 128 bytes (64 bf16 of K), 8-row groups 1024 bytes apart.  MN-major: rows of
-// 128 bytes along MN (64 bf16) per K index, 8 K rows 1024 bytes apart (stride
-// field), the next 64 MN elements `mn_stride` bytes further (leading field).
-__device__ __forceinline__ uint64_t desc_k_sw128(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((mn_stride >> 4) & 0x3FFFu) << 16) |
-         (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -811,39 +791,6 @@ kinv_status launch(const AttnParams& p, dim3 split_grid, dim3 merge_grid, cudaSt
   const kinv_status st = launch_kernel(kernel, split_grid, dim3(kThreads), smem, stream, 1, p);
   if (st != KINV_OK) return st;
   return launch_kernel(attn_merge_kernel<D>, merge_grid, dim3(D), 0, stream, 1, p);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 tma_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
-// A bf16 tensor of rank `r` (dims innermost first, byte strides of dims 1..),
-// boxes of `box` elements, 128-byte swizzle, out-of-range elements zero.
-bool encode_map(CUtensorMap* map, const void* ptr, int r, const uint64_t* dims, const uint64_t* strides,
-                const uint32_t* box) {
-  auto fn = tma_encoder();
-  if (!fn) return false;
-  cuuint64_t d[5], st[4];
-  cuuint32_t bx[5], es[5];
-  for (int i = 0; i < r; ++i) {
-    d[i] = dims[i];
-    bx[i] = box[i];
-    es[i] = 1;
-    if (i + 1 < r) st[i] = strides[i];
-  }
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, r, const_cast<void*>(ptr), d, st, bx, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Prefill with the tcgen05 kernel: one block per (sequence, kv head, tile of

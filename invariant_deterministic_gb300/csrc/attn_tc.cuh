@@ -1,0 +1,66 @@
+// Pieces shared by the tcgen05 attention kernels (prefill and drafted trees):
+// instruction and shared-memory descriptors, and the tensor maps of Q, K and V.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+
+namespace kinv {
+
+// tcgen05 instruction descriptor, kind::f16: fp32 accumulate, bf16 A and B,
+// A K-major, B K-major (b_mn = 0) or MN-major (b_mn = 1), N, M = 128.
+__host__ __device__ constexpr uint32_t tc_idesc(int n, int b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+// Shared-memory descriptors, 128-byte swizzle, version 1.  K-major: rows of
+// 128 bytes (64 bf16 of K), 8-row groups 1024 bytes apart.  MN-major: rows of
+// 128 bytes along MN (64 bf16) per K index, 8 K rows 1024 bytes apart (stride
+// field), the next 64 MN elements `mn_stride` bytes further (leading field).
+__device__ __forceinline__ uint64_t desc_k_sw128(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((mn_stride >> 4) & 0x3FFFu) << 16) |
+         (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 tma_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+// A bf16 tensor of rank `r` (dims innermost first, byte strides of dims 1..),
+// boxes of `box` elements, 128-byte swizzle, out-of-range elements zero.
+inline bool encode_map(CUtensorMap* map, const void* ptr, int r, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+  auto fn = tma_encoder();
+  if (!fn) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < r; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < r) st[i] = strides[i];
+  }
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, r, const_cast<void*>(ptr), d, st, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace kinv

@@ -15,6 +15,7 @@
 #include <math.h>
 
 #include "attn_mma.cuh"
+#include "attn_tc.cuh"
 #include "common.cuh"
 #include "tree.cuh"
 
@@ -24,6 +25,9 @@ namespace {
 constexpr int kSplit = 256;    // keys per split, as in decode and prefill
 constexpr int kThreads = 256;  // eight warps, 32 positions each for the softmax
 constexpr int kMaxG = 8;
+// From this many (sequence, kv head, split) triples the cache may hold, the
+// splits within the context go to the tcgen05 kernel.
+constexpr int kMinSplitsTc = 64;
 
 struct TreeAttnParams {
   kinv_tree tree;
@@ -37,6 +41,7 @@ struct TreeAttnParams {
   int Hq, Hkv, G;
   int S;         // splits per row in the workspace
   float c2;      // fp32(scale * log2 e) > 0
+  int tail_only; // the splits that end within the context are another kernel's
   int* status;
 };
 
@@ -70,13 +75,13 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
   pdl_wait();
   const int g = blockIdx.x % p.Hkv;
   const int tile = blockIdx.x / p.Hkv;
-  const int s = blockIdx.y;
   const int b = blockIdx.z;
   int n, ctx, off;
   if (!tree_bounds(p.tree, b, n, ctx, off)) {
     report_bad_tree(p);
     return;
   }
+  const int s = (p.tail_only ? ctx / kSplit : 0) + static_cast<int>(blockIdx.y);
   const int G = p.G;
   const int npt = R / G;  // nodes of a tile
   const int n0 = tile * npt;
@@ -361,6 +366,403 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
     }
 }
 
+// ---------------------------------------------------------------------------
+// The splits that end within the context, on the tcgen05 tensor cores: 128
+// pairs of one (sequence, kv head) against 256 keys, the arithmetic of the
+// prefill kernel without a mask, each split's (m, l, o) stored as a partial.
+//
+// A unit is (sequence, kv head, up to two tiles of 128 pairs, split); the
+// tiles of a unit share its K and V in shared memory.  The units of all
+// sequences, splits fastest, are dealt to the blocks (one per SM) in equal
+// runs, counted on the device from the trees' own numbers.
+// Roles (18 warps): warps 0-15 take the softmax, four threads per pair: warp w
+// holds TMEM lanes 32 (w % 4) .. + 31 (lane = pair) and keys 64 (w / 4) ..
+// + 63 of each split, so a tile's softmax is four warps deep on every
+// scheduler; the four exchange raw maxima and 32-key group
+// sums through shared memory, in the decode kernel's order.  Warp 16 lane 0
+// issues the MMAs, warp 17 lane 0 the TMA loads.
+// Tensor memory: scores R in columns 0-255, overwritten chunk by chunk with P
+// (64-key chunk j: 32-key group h as packed bf16 pairs, hi at 64 j + 32 h, lo
+// 16 columns further), O in two buffers of D columns after it.  The MMAs run
+// in issue order: step i + 1's scores of keys 128 h .. follow step i's P.V of
+// chunks 2h and 2h + 1, which read the P that they overwrite; the softmax
+// threads store step i - 1's O while step i's P.V runs.
+constexpr int kTcSoftmax = 512;  // 16 warps
+constexpr int kTcThreads = kTcSoftmax + 64;
+constexpr int kTcPairs = 128;
+constexpr int kTcTiles = 2;      // tiles of a unit
+constexpr int kTcBars = 15;
+
+struct UnitCursor {
+  int b, g, tp, s;         // sequence, kv head, tile pair, split
+  int n, ctx, off;         // of the sequence
+  int splits, pairs;       // splits within the context, tile pairs
+};
+
+// Sequence c.b's numbers; returns its units.
+__device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, UnitCursor& c) {
+  c.splits = c.pairs = 0;
+  if (!tree_bounds(p.tree, c.b, c.n, c.ctx, c.off)) return 0;
+  c.splits = c.ctx / kSplit;
+  c.pairs = (c.n * p.G + kTcTiles * kTcPairs - 1) / (kTcTiles * kTcPairs);
+  return static_cast<int64_t>(p.Hkv) * c.pairs * c.splits;
+}
+__device__ __forceinline__ void cursor_next(const TreeAttnParams& p, UnitCursor& c) {
+  if (++c.s < c.splits) return;
+  c.s = 0;
+  if (++c.tp < c.pairs) return;
+  c.tp = 0;
+  if (++c.g < p.Hkv) return;
+  c.g = 0;
+  while (++c.b < p.tree.B && cursor_load(p, c) == 0) {
+  }
+}
+__device__ __forceinline__ int cursor_tiles(const TreeAttnParams& p, const UnitCursor& c) {
+  return min(kTcTiles, (c.n * p.G + kTcPairs - 1) / kTcPairs - c.tp * kTcTiles);
+}
+
+// This block's run of units, by one warp: cursor at its first and its length.
+__device__ __forceinline__ void cursor_start(const TreeAttnParams& p, UnitCursor& out, int& count) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  UnitCursor c;
+  for (c.b = lane; c.b < p.tree.B; c.b += 32) total += cursor_load(p, c);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (lane == 0) count = static_cast<int>(u1 - u0);
+  if (u1 == u0) return;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.tree.B; b0 += 32) {
+    c.b = b0 + lane;
+    const int64_t mine = c.b < p.tree.B ? cursor_load(p, c) : 0;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const bool here = before + incl - mine <= u0 && u0 < before + incl;
+    if (here) {
+      const int64_t u = u0 - (before + incl - mine);
+      c.s = static_cast<int>(u % c.splits);
+      c.tp = static_cast<int>(u / c.splits % c.pairs);
+      c.g = static_cast<int>(u / c.splits / c.pairs);
+      out = c;
+    }
+    if (__any_sync(0xffffffffu, here)) return;
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// 32 bytes to global memory in one store (a whole sector).
+__device__ __forceinline__ void st_global_v8(float* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    attn_tree_ctx_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const TreeAttnParams p) {
+  constexpr int DS = D / 64;                // 64-wide slices of the head dimension
+  constexpr int Q_SLICE = kTcPairs * 128;   // [128 pairs][64]
+  constexpr int Q_BYTES = DS * Q_SLICE;
+  constexpr int KV_SLICE = kSplit * 128;    // [256 keys][64]
+  constexpr int KV_BYTES = DS * KV_SLICE;
+  constexpr int DQ = D / 4;                 // output columns per softmax thread
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* q_s = base;                         // kTcTiles tiles
+  unsigned char* k_s = q_s + kTcTiles * Q_BYTES;
+  unsigned char* v_s = k_s + KV_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(v_s + KV_BYTES);
+  float* x_max = reinterpret_cast<float*>(bars + kTcBars + 1);  // [4][128] raw maxima
+  float* x_sum = x_max + 4 * kTcPairs;                          // [8][128] 32-key group sums
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ UnitCursor start;
+  __shared__ int count_s;
+  const uint32_t k_full = smem_addr(bars + 0), k_empty = smem_addr(bars + 1);
+  const uint32_t v_full = smem_addr(bars + 2), v_empty = smem_addr(bars + 3);
+  auto s_full = [&](int h) { return smem_addr(bars + 4 + h); };    // R of keys 128 h .. written
+  auto p_full = [&](int j) { return smem_addr(bars + 6 + j); };    // P chunk j written
+  auto o_full = [&](int i) { return smem_addr(bars + 10 + i); };   // O buffer i complete
+  auto o_empty = [&](int i) { return smem_addr(bars + 12 + i); };  // O buffer i read
+  const uint32_t done_bar = smem_addr(bars + 14);
+
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  pdl_wait();
+  if (warp == 0) cursor_start(p, start, count_s);
+  __syncthreads();
+  const int count = count_s;
+  if (count == 0) {
+    pdl_launch_dependents();
+    return;
+  }
+  UnitCursor c = start;
+  if (t == 0) {
+    for (int i = 0; i < kTcBars; ++i) {
+      // p_full: the 128 threads of its chunk; o_empty: every softmax thread
+      const int arrivals = (i >= 6 && i < 10) ? kTcPairs : (i == 12 || i == 13) ? kTcSoftmax : 1;
+      mbar_init(smem_addr(bars + i), arrivals);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) tmem_alloc(smem_addr(&tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();  // after the TMEM allocation
+  int* status = p.status;
+
+  if (warp == 17) {
+    // ---- TMA: K (with the Q tiles of a new group) of unit u + 1 as soon as
+    // unit u's score MMAs are done, its V as soon as unit u's P.V MMAs are done
+    if (lane == 0) {
+      const uint64_t q_pol = l2_policy_evict_last(), kv_pol = l2_policy_evict_first();
+      auto load_k = [&](bool group) {
+        const int tiles = group ? cursor_tiles(p, c) : 0;
+        mbar_arrive_expect_tx(k_full, KV_BYTES + tiles * Q_BYTES);
+        for (int i = 0; i < tiles; ++i)
+          for (int ds = 0; ds < DS; ++ds)
+            tma_load_3d(smem_addr(q_s + i * Q_BYTES + ds * Q_SLICE), &tmQ, 64 * ds, c.g * p.G,
+                        c.off + (c.tp * kTcTiles + i) * (kTcPairs / p.G), k_full, q_pol);
+        for (int ds = 0; ds < DS; ++ds)
+          tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full, kv_pol);
+      };
+      auto load_v = [&]() {
+        mbar_arrive_expect_tx(v_full, KV_BYTES);
+        for (int ds = 0; ds < DS; ++ds)
+          tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, c.g, c.s * kSplit, c.b, v_full, kv_pol);
+      };
+      load_k(true);
+      load_v();
+      int k_issued = 1, v_issued = 1;
+      for (int u = 0; u + 1 < count; ++u) {
+        cursor_next(p, c);
+        bool ok = !abort_flag && mbar_wait_bounded(k_empty, u & 1, status, DEV_TIMEOUT_ATTN);
+        if (ok) {
+          load_k(c.s == 0);
+          ++k_issued;
+          ok = !abort_flag && mbar_wait_bounded(v_empty, u & 1, status, DEV_TIMEOUT_ATTN);
+        }
+        if (!ok) {
+          abort_flag = 1;
+          break;
+        }
+        load_v();
+        ++v_issued;
+      }
+      // loads still in flight (only after an abort) land before the block exits
+      mbar_wait_bounded(k_full, (k_issued - 1) & 1, nullptr, 0);
+      mbar_wait_bounded(v_full, (v_issued - 1) & 1, nullptr, 0);
+    }
+    __syncwarp();
+  } else if (warp == 16) {
+    // ---- MMA issue: a step is (unit, tile); each iteration issues the last
+    // step's P.V and this step's scores, interleaved
+    if (lane == 0) {
+      constexpr uint32_t idesc_r = tc_idesc(128, 0);
+      constexpr uint32_t idesc_o = tc_idesc(D, 1);
+      const uint64_t qd = desc_k_sw128(smem_addr(q_s)), kd = desc_k_sw128(smem_addr(k_s));
+      const uint64_t vd = desc_mn_sw128(smem_addr(v_s), KV_SLICE);
+      bool ok = true, has_pv = false;
+      int i = 0;                       // steps whose scores were issued
+      int pv_unit = 0;                 // the last step's unit, and its place there
+      bool pv_first = false, pv_last = false;
+      for (int u = 0; u <= count && ok; ++u) {
+        const int tiles = u < count ? cursor_tiles(p, c) : 1;
+        for (int tile = 0; tile < tiles && ok; ++tile) {
+          const bool has_r = u < count;
+          const uint32_t ob = (i - 1) & 1, ph = (i - 1) & 1;  // of the last step
+          if (has_pv) {
+            if (pv_first) ok = mbar_wait_bounded(v_full, pv_unit & 1, status, DEV_TIMEOUT_ATTN);
+            ok = ok && !abort_flag &&
+                 mbar_wait_bounded(o_empty(ob), (((i - 1) >> 1) & 1) ^ 1, status, DEV_TIMEOUT_ATTN);
+          }
+          if (ok && has_r && tile == 0) ok = !abort_flag && mbar_wait_bounded(k_full, u & 1, status, DEV_TIMEOUT_ATTN);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t o_col = tmem + 256 + ob * D;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (has_pv) {
+              ok = !abort_flag && mbar_wait_bounded(p_full(j), ph, status, DEV_TIMEOUT_ATTN);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t vdesc = vd + static_cast<uint64_t>(((4 * j + kk) * 2048) >> 4);
+                const uint32_t p_hi = tmem + static_cast<uint32_t>(64 * j + 32 * (kk >> 1) + 8 * (kk & 1));
+                umma_bf16_tmem_a(o_col, p_hi, vdesc, idesc_o, (j | kk) != 0 ? 1u : 0u);
+                umma_bf16_tmem_a(o_col, p_hi + 16, vdesc, idesc_o, 1u);
+              }
+            }
+            if (has_r && (j & 1)) {
+              const int h = j >> 1;
+              const uint64_t qt = qd + static_cast<uint64_t>(tile * Q_BYTES >> 4);
+#pragma unroll
+              for (int ds = 0; ds < DS; ++ds)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16(tmem + static_cast<uint32_t>(128 * h),
+                            qt + static_cast<uint64_t>((ds * Q_SLICE + kk * 32) >> 4),
+                            kd + static_cast<uint64_t>((ds * KV_SLICE + h * 128 * 128 + kk * 32) >> 4), idesc_r,
+                            (ds | kk) != 0 ? 1u : 0u);
+              umma_commit(s_full(h));
+            }
+          }
+          if (!ok) break;
+          if (has_pv) {
+            if (pv_last) umma_commit(v_empty);
+            umma_commit(o_full(ob));
+          }
+          if (has_r) {
+            if (tile == tiles - 1) umma_commit(k_empty);
+            has_pv = true;
+            pv_unit = u;
+            pv_first = tile == 0;
+            pv_last = tile == tiles - 1;
+            ++i;
+          }
+        }
+        if (u < count) cursor_next(p, c);
+      }
+      if (!ok) abort_flag = 1;
+      umma_commit(done_bar);
+      mbar_wait_bounded(done_bar, 0, status, DEV_TIMEOUT_ATTN);
+    }
+    __syncwarp();
+  } else {
+    // ---- four threads per pair
+    const int quad = warp & 3, j = warp >> 2;  // lanes 32 quad .., keys 64 j .. and output columns D/4 j ..
+    const int pr = quad * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const float c2 = p.c2;
+    bool ok = true;
+    auto quad_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory"); };
+    // the quadrant's barrier, returning whether `v` holds for any of its threads
+    auto quad_sync_or = [&](bool v) {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+          "bar.red.or.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(r)
+          : "r"(static_cast<uint32_t>(v)), "r"(1 + quad)
+          : "memory");
+      return r != 0;
+    };
+    auto check = [&](bool waited) {
+      if (__any_sync(0xffffffffu, !waited || abort_flag)) {
+        abort_flag = 1;
+        ok = false;
+      }
+    };
+    // stores this thread's D/4 columns of step i's O as the partial at `at`
+    auto store_o = [&](int i, int64_t at, bool live) {
+      check(mbar_wait_bounded(o_full(i & 1), (i >> 1) & 1, status, DEV_TIMEOUT_ATTN));
+      tc_fence_after();
+      if (__any_sync(0xffffffffu, live)) {
+        uint32_t v[32];
+        tmem_ld32(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
+        if (live) {
+#pragma unroll
+          for (int d = 0; d < DQ; d += 8) st_global_v8(p.ws_o + at * D + j * DQ + d, v + d);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(o_empty(i & 1));
+    };
+    int i = 0;
+    int64_t at_prev = 0;
+    bool live_prev = false;
+    for (int u = 0; u < count && ok; ++u) {
+      const int tiles = cursor_tiles(p, c);
+      for (int tile = 0; tile < tiles; ++tile, ++i) {
+        const int pair = (c.tp * kTcTiles + tile) * kTcPairs + pr;
+        const int node = pair / p.G;
+        const bool live = node < c.n;
+        const int64_t at = (static_cast<int64_t>(c.off + node) * p.Hq + c.g * p.G + pair % p.G) * p.S + c.s;
+        const bool any = __any_sync(0xffffffffu, live);  // the same for the quadrant's four warps
+        check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
+        tc_fence_after();
+        uint32_t v[32];
+        if (any) {
+          float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld32(lane_base + 64 * j + 32 * h, v);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+              mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            }
+          }
+          x_max[j * kTcPairs + pr] = fmaxf(mx[0], mx[1]);
+        }
+        // one decision for the quadrant's 128 threads: leave if any has given up
+        if (quad_sync_or(!ok || abort_flag)) {
+          ok = false;
+          break;
+        }
+        float m = 0.f;
+        if (any) {
+          m = __fmul_rn(fmaxf(fmaxf(x_max[pr], x_max[kTcPairs + pr]), fmaxf(x_max[2 * kTcPairs + pr], x_max[3 * kTcPairs + pr])), c2);
+          const float2 c2x2 = make_float2(c2, c2), neg_m2 = make_float2(-m, -m);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld32(lane_base + 64 * j + 32 * h, v);
+            uint32_t hp[16], lp[16];  // bf16 pairs of the high and the low halves
+            // l in the decode kernel's order: key 8nb + 2tq + e into partial tq
+            // in (nb, e) order, then (0 + 1) + (2 + 3)
+            float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 arg = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg_m2);
+              const float2 x = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+              const __nv_bfloat162 h2 = __float22bfloat162_rn(x);
+              const __nv_bfloat162 l2 =
+                  __float22bfloat162_rn(__ffma2_rn(__bfloat1622float2(h2), make_float2(-1.f, -1.f), x));
+              hp[e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+              lp[e / 2] = *reinterpret_cast<const uint32_t*>(&l2);
+              sq[e / 2 % 4] = __fadd_rn(__fadd_rn(sq[e / 2 % 4], x.x), x.y);
+            }
+            tmem_st16(lane_base + 64 * j + 32 * h, hp);
+            tmem_st16(lane_base + 64 * j + 32 * h + 16, lp);
+            x_sum[(2 * j + h) * kTcPairs + pr] = __fadd_rn(__fadd_rn(sq[0], sq[1]), __fadd_rn(sq[2], sq[3]));
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(p_full(j));
+        if (i > 0) store_o(i - 1, at_prev, live_prev);
+        quad_sync();
+        if (j == 0 && live) {
+          float l = x_sum[pr];
+#pragma unroll
+          for (int q = 1; q < 8; ++q) l = __fadd_rn(l, x_sum[q * kTcPairs + pr]);
+          *reinterpret_cast<float2*>(p.ws_ml + at * 2) = make_float2(m, l);
+        }
+        at_prev = at;
+        live_prev = live;
+      }
+      cursor_next(p, c);
+    }
+    if (ok) store_o(i - 1, at_prev, live_prev);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 // One block per (query head, node, sequence); thread d folds column d over the
 // splits the node sees, with the decode merge's arithmetic.
 template <int D>
@@ -417,19 +819,55 @@ kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (attr != KINV_OK) return attr;
   const int tiles = (p.tree.max_nodes * p.G + 16 * MT - 1) / (16 * MT);
-  return launch_kernel(kernel, dim3(p.Hkv * tiles, p.S, p.tree.B), dim3(kThreads), smem, stream, 1, p);
+  const int splits = p.tail_only ? (p.S < 2 ? p.S : 2) : p.S;
+  return launch_kernel(kernel, dim3(p.Hkv * tiles, splits, p.tree.B), dim3(kThreads), smem, stream, 1, p);
 }
 
 template <int D>
-kinv_status launch(const TreeAttnParams& p, cudaStream_t stream) {
-  const kinv_status st = p.tree.max_nodes * p.G <= 16 ? launch_split<D, 1>(p, stream) : launch_split<D, 2>(p, stream);
+constexpr size_t ctx_smem_bytes() {
+  return 1024 + kTcTiles * static_cast<size_t>(D / 64) * kTcPairs * 128 + 2 * static_cast<size_t>(D / 64) * kSplit * 128 +
+         (kTcBars + 1) * 8 + 12 * kTcPairs * 4;
+}
+
+// The tensor maps of the context kernel; false where a stride or size is
+// outside what a map can describe.
+template <int D>
+bool encode_maps(const TreeAttnParams& p, CUtensorMap* mq, CUtensorMap* mk, CUtensorMap* mv) {
+  const uint64_t qd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.Hq), static_cast<uint64_t>(p.tree.total_rows)};
+  const uint64_t qs[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(p.Hq) * D * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(kTcPairs / p.G)};
+  const uint64_t kd[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.Hkv), static_cast<uint64_t>(p.tree.max_kv),
+                          static_cast<uint64_t>(p.tree.B)};
+  // one sequence: any sequence stride describes it (the coordinate is 0)
+  const int64_t sst = p.tree.B > 1 ? p.seq_stride : static_cast<int64_t>(p.tree.max_kv) * p.tok_stride;
+  const uint64_t ks[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(p.tok_stride) * 2, static_cast<uint64_t>(sst) * 2};
+  const uint32_t kb[4] = {64, 1, static_cast<uint32_t>(kSplit), 1};
+  return encode_map(mq, p.q, 3, qd, qs, qb) && encode_map(mk, p.k, 4, kd, ks, kb) && encode_map(mv, p.v, 4, kd, ks, kb);
+}
+
+template <int D>
+kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
+  const size_t smem = ctx_smem_bytes<D>();
+  const int sms = sm_count();
+  CUtensorMap mq, mk, mv;
+  p.tail_only = static_cast<int64_t>(p.tree.B) * p.Hkv * (p.tree.max_kv / kSplit) >= kMinSplitsTc &&
+                smem <= static_cast<size_t>(max_smem_optin()) && encode_maps<D>(p, &mq, &mk, &mv);
+  kinv_status st = p.tree.max_nodes * p.G <= 16 ? launch_split<D, 1>(p, stream) : launch_split<D, 2>(p, stream);
   if (st != KINV_OK) return st;
+  if (p.tail_only) {
+    void (*kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const TreeAttnParams) = attn_tree_ctx_kernel<D>;
+    st = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (st != KINV_OK) return st;
+    st = launch_kernel(kernel, dim3(sms), dim3(kTcThreads), smem, stream, 1, mq, mk, mv, p);
+    if (st != KINV_OK) return st;
+  }
   return launch_kernel(attn_tree_merge_kernel<D>, dim3(p.Hq, p.tree.max_nodes, p.tree.B), dim3(D), 0, stream, 1, p);
 }
 
 size_t tree_workspace_bytes(int64_t rows, int Hq, int D, int S) {
+  // 256 to align the partials, which are stored 32 bytes at a time
   const size_t o = static_cast<size_t>(rows) * Hq * S * D * 4;
-  return ((o + 255) / 256) * 256 + static_cast<size_t>(rows) * Hq * S * 2 * 4;
+  return 256 + ((o + 255) / 256) * 256 + static_cast<size_t>(rows) * Hq * S * 2 * 4;
 }
 
 }  // namespace
@@ -473,9 +911,10 @@ extern "C" kinv_status kinv_attn_tree(const void* q, const void* k_cache, const 
   p.seq_stride = seq_stride;
   p.tok_stride = tok_stride;
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.ws_o = static_cast<float*>(workspace);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
+  p.ws_o = reinterpret_cast<float*>(ws);
   const size_t o_bytes = static_cast<size_t>(tree->total_rows) * Hq * S * D * 4;
-  p.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + ((o_bytes + 255) / 256) * 256);
+  p.ws_ml = reinterpret_cast<float*>(ws + ((o_bytes + 255) / 256) * 256);
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = G;

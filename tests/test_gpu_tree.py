@@ -115,6 +115,21 @@ def test_long_context(kinv, n):
     c.check_bits(c.run(), f"{n} nodes")
 
 
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_many_splits_with_every_head_layout(kinv, hq, hkv, d):
+    """Contexts of several splits (enough of them for the tensor-core path, which
+    deals the splits of all sequences out in equal runs), ragged trees, sequences
+    without a whole split and without nodes in between."""
+    ctx = [2600, 100, 0, 5000, 256, 511, 7000, 1023, 1024, 30, 4096, 255, 9000]
+    n = [5, 64, 3, 0, 64, 1, 33, 40, 64, 8, 17, 2, 63]
+    parents = [shape_parents(["bushy", "chain", "forest"][i % 3], k, i) if k else [] for i, k in enumerate(n)]
+    c = Case(kinv, ctx, parents, hq, hkv, d, seed=50, gap=1, pad_tok=8)
+    out = torch.full_like(c.q, 7.0)
+    c.run(out=out)
+    assert kinv.last_device_status() == 0
+    c.check_bits(out, "many splits")
+
+
 def test_batch_and_slot_invariance(kinv):
     parents = [shape_parents("bushy", k, k) for k in (5, 64, 1, 30)]
     ctx = [1000, 300, 0, 513]
