@@ -521,7 +521,7 @@ kinv_status kinv_tree_accept(const kinv_tree* tree, const int32_t* tokens,
  *   entropy[r]       = ln S - (sum e^(x - m) (x - m)) / S       (nats)
  *   top_ids[r][j], top_logprobs[r][j]: the j-th likeliest id and its log
  *                      probability, by (x descending, id ascending), j < top_k.
- * The row is cut into units of 512 ids; a warp takes a unit's maximum and sums
+ * The row is cut into units of 1024 ids; a warp takes a unit's maximum and sums
  * in one fixed order and the units are folded in one fixed order, all in fp32,
  * so a row's bits do not depend on the other rows.
  * NaN logits count as -infinity (as in kinv_sample).  -infinity has probability
@@ -534,15 +534,11 @@ kinv_status kinv_tree_accept(const kinv_tree* tree, const int32_t* tokens,
  * allow, any alignment works); ids: device int32 [rows][n_ids]; logprob fp32
  * [rows][n_ids]; entropy (nullable) fp32 [rows]; top_ids int32, top_logprobs
  * fp32 [rows][top_k].  ids and logprob may be NULL when n_ids = 0, the top
- * arrays when top_k = 0.  workspace: device, 16-byte aligned, at least
- * kinv_logprobs_workspace(rows, V) bytes (may be 0 and then NULL); two calls
- * that may run at the same time need one each.
+ * arrays when top_k = 0.
  * Requirements: 1 <= V <= 1048576, ld >= V, 0 <= top_k <= 32, top_k <= V. */
-size_t kinv_logprobs_workspace(int rows, int V);
 kinv_status kinv_logprobs(const void* logits, kinv_dtype dtype, int64_t ld, int rows, int V,
                           const int32_t* ids, int n_ids, float* logprob, float* entropy,
-                          int top_k, int32_t* top_ids, float* top_logprobs, void* workspace,
-                          size_t workspace_bytes, kinv_stream stream);
+                          int top_k, int32_t* top_ids, float* top_logprobs, kinv_stream stream);
 
 #ifdef __cplusplus
 }

@@ -1,24 +1,29 @@
 // Log probabilities of given tokens, entropy and the likeliest alternatives of
 // rows of logits (kinv_logprobs), one pass over the row.
 //
-// The row is cut into units of 512 ids.  One warp takes a unit (16 ids a lane)
+// The row is cut into units of 1024 ids.  One warp takes a unit (32 ids a lane)
 // and leaves, with m_u = max x and a = (x - m_u) log2 e,
 //   S_u = sum 2^a,   T_u = sum 2^a a
-// a lane's ids in order, then a butterfly.  A row folds its units with M =
-// max m_u and w_u = 2^((m_u - M) log2 e):  S = sum w_u S_u,  T = sum w_u (T_u +
-// S_u (m_u - M) log2 e), lane l of a warp the units l, l + 32, ... in order,
-// then a butterfly; ln S, x - M - ln S and the entropy ln S - ln 2 T / S follow.
-// Which warp or block takes a unit changes nothing.  a is clamped at -200, so
-// NaN (dropped by the maximum) and -infinity weigh 2^-200 -> 0 and the product
-// 2^a a stays finite.
+// (a lane's ids in order on two chains, then a butterfly).  A row folds its
+// units with M = max m_u and w_u = 2^((m_u - M) log2 e):  S = sum w_u S_u,
+// T = sum w_u (T_u + S_u (m_u - M) log2 e), lane l of a warp the units l, l + 32,
+// ... in order, then a butterfly; ln S, x - M - ln S and the entropy ln S -
+// ln 2 T / S follow.  Which warp or block takes a unit changes nothing.  a is
+// clamped at -200, so NaN (dropped by the maximum) and -infinity weigh 2^-200
+// -> 0 and the product 2^a a stays finite.
 //
 // The k likeliest ids: every warp keeps its 32 best as 64-bit keys (the logit's
 // ordered bits, then the complement of the id: larger is better and no two are
-// equal), one per lane in descending order.  An id enters only if its key beats
-// the k-th; entrants wait in shared memory and are merged 32 at a time by a
-// bitonic network.  The lists of the warps and blocks of a row are merged the
-// same way, and the result does not depend on the order, since the keys are
-// distinct.
+// equal), one per lane in descending order.  An id enters only if its logit
+// reaches a floor that k ids are known to reach (from the block's first units,
+// then from the best k of any of its warps) and its key beats the warp's k-th;
+// entrants wait in shared memory and are merged 32 at a time by a bitonic
+// network.  The lists of the warps and blocks of a row are merged the same way,
+// and the result does not depend on the order, since the keys are distinct.
+//
+// A row is one block, or a cluster of up to eight when there are few rows; the
+// blocks put their units' sums and their list into the first block's shared
+// memory, so nothing goes through global memory.
 #include <math.h>
 
 #include "common.cuh"
@@ -29,7 +34,8 @@ namespace {
 constexpr int DEV_LOGPROBS_BAD_ID = dev_code(9, KINV_ERR_INVALID_ARG);
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnit = 512;
+constexpr int kUnit = 1024;
+constexpr int kPerLane = kUnit / 32;
 constexpr int kMaxTop = 32;
 constexpr int kPending = 64;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -48,8 +54,6 @@ struct LogprobParams {
   int top_k;
   int32_t* top_ids;
   float* top_logprobs;
-  float* ws_unit;  // [rows][units][3]: m, S, T
-  u64* ws_top;     // [rows][parts][32]
   int* status;
 };
 
@@ -75,7 +79,7 @@ __device__ __forceinline__ T sort_desc(T v) {
 #pragma unroll
     for (int j = k >> 1; j > 0; j >>= 1) {
       const T o = __shfl_xor_sync(0xffffffffu, v, j);
-      const bool keep_max = ((lane & j) == 0) == ((lane & k) == 0 || k == 32);
+      const bool keep_max = ((lane & j) == 0) == ((lane & k) == 0);
       v = keep_max ? (v > o ? v : o) : (v < o ? v : o);
     }
   }
@@ -94,39 +98,46 @@ __device__ __forceinline__ u64 merge_desc(u64 a, u64 b) {
   return v;
 }
 
-// A lane's 16 logits of a unit.  fp32: x[4 i + j] is id 128 i + 4 lane + j;
-// bf16: x[8 i + j] is id 256 i + 8 lane + j.  Ids past V read as -infinity.
+// A lane's 32 logits of a unit as raw 32-bit words, in 16-byte groups 32 lanes
+// apart: element e (counted over the lane's words) is id (e / W) 32 W + lane W
+// + e % W of the unit, W = 16 bytes of elements.  Ids past V read as -infinity.
 template <typename T>
 __device__ __forceinline__ int unit_id(int lane, int e) {
   constexpr int W = 16 / sizeof(T);
   return (e / W) * 32 * W + lane * W + e % W;
 }
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_unit(const T* row, int first, int V, float (&x)[16]) {
+__device__ __forceinline__ void load_unit(const T* row, int first, int V, uint32_t (&x)[kPerLane * sizeof(T) / 4]) {
   const int lane = threadIdx.x & 31;
   constexpr int W = 16 / sizeof(T);
   if (VEC && first + kUnit <= V) {
 #pragma unroll
-    for (int i = 0; i < 16 / W; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(row + first + (i * 32 + lane) * W);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (sizeof(T) == 4) {
-          x[4 * i + j] = __uint_as_float(w[j]);
-        } else {
-          x[(8 * i + 2 * j) & 15] = bf16_lo(w[j]);
-          x[(8 * i + 2 * j + 1) & 15] = bf16_hi(w[j]);
-        }
-      }
+    for (int i = 0; i < kPerLane / W; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + first + (i * 32 + lane) * W));
+      x[4 * i] = v.x;
+      x[4 * i + 1] = v.y;
+      x[4 * i + 2] = v.z;
+      x[4 * i + 3] = v.w;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int id = first + unit_id<T>(lane, e);
-      x[e] = id < V ? static_cast<float>(row[id]) : -INFINITY;
+    for (int w = 0; w < kPerLane * static_cast<int>(sizeof(T)) / 4; ++w) {
+      if (sizeof(T) == 4) {
+        const int id = first + unit_id<T>(lane, w);
+        x[w] = id < V ? reinterpret_cast<const uint32_t*>(row)[id] : 0xFF800000u;
+      } else {
+        const int id = first + unit_id<T>(lane, 2 * w);
+        const uint16_t* r16 = reinterpret_cast<const uint16_t*>(row);
+        x[w] = (id < V ? r16[id] : 0xFF80u) | (id + 1 < V ? r16[id + 1] : 0xFF80u) << 16;
+      }
     }
   }
+}
+// Elements 2i and 2i + 1 of a lane's words.
+template <typename T, int N>
+__device__ __forceinline__ float2 pair_of(const uint32_t (&x)[N], int i) {
+  return sizeof(T) == 4 ? make_float2(__uint_as_float(x[2 * i % N]), __uint_as_float(x[(2 * i + 1) % N]))
+                        : make_float2(bf16_lo(x[i % N]), bf16_hi(x[i % N]));
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -140,37 +151,223 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Results of a row from its units' sums and its 32 best keys (lane i the
-// i-th); one warp.
-template <typename T>
-__device__ void finish_row(const LogprobParams& p, int64_t r, const float* unit, u64 best) {
-  const int lane = threadIdx.x & 31;
-  float M = -INFINITY;
-  for (int u = lane; u < p.units; u += 32) M = fmaxf(M, unit[3 * u]);
-  M = warp_max(M);
-  float S = 0.f, Tt = 0.f;
-  for (int u = lane; u < p.units; u += 32) {
-    const float m = unit[3 * u], s = unit[3 * u + 1], t = unit[3 * u + 2];
-    const float d = m == M ? 0.f : __fmul_rn(__fsub_rn(m, M), kLog2e);
-    const float w = ex2_approx(d);
-    if (w > 0.f) {
-      S = __fadd_rn(S, __fmul_rn(w, s));
-      Tt = __fadd_rn(Tt, __fmul_rn(w, __fmaf_rn(s, d, t)));
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// The block's eight lists in shared memory, merged pairwise; warp 0 returns the
+// result.  Called by every thread after the lists were written (no barrier yet).
+__device__ __forceinline__ u64 merge_block(u64 (*lists)[32]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  u64 v = 0;
+#pragma unroll
+  for (int half = kWarps / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (warp < half) {
+      v = merge_desc(lists[warp][lane], lists[warp + half][lane]);
+      lists[warp][lane] = v;
     }
   }
-  S = warp_sum(S);
-  Tt = warp_sum(Tt);
-  const float ln_s = logf(S);
-  auto logprob = [&](float x) {
-    x = no_nan(x);
+  return v;
+}
+
+// One block, or a cluster of p.parts blocks, per row.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams p) {
+  constexpr int N = kPerLane * sizeof(T) / 4;
+  extern __shared__ float s_unit[];  // [units][3]: m, S, T (of the cluster's first block)
+  __shared__ u64 pending[kWarps][kPending];
+  __shared__ u64 lists[kWarps][32];
+  __shared__ uint32_t s_first[kWarps];
+  __shared__ uint32_t s_floor;
+  __shared__ float s_row[3];
+  if (threadIdx.x == 0) s_floor = 0;
+  if (p.parts > 1) cluster_arrive_relaxed();  // the first block runs: its shared memory may be written
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t r = blockIdx.x / p.parts;
+  const int part = blockIdx.x % p.parts;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* row = static_cast<const T*>(p.x) + r * p.ld;
+  const int u_end = min(p.units, (part + 1) * p.units_per_part);
+  const int top_k = p.top_k;
+  u64 best = 0;  // lane i: the i-th best key (0: none)
+  u64 bar = 0;   // the k-th best
+  uint32_t floor_hi = 0;
+  int waiting = 0;
+  auto merge_waiting = [&](int n) {  // the last n entrants
+    const u64 v = lane < n ? pending[warp][waiting - n + lane] : static_cast<u64>(0);
+    __syncwarp();
+    best = merge_desc(best, sort_desc(v));
+    waiting -= n;
+    bar = __shfl_sync(0xffffffffu, best, top_k - 1);
+    if (lane == 0) atomicMax(&s_floor, static_cast<uint32_t>(bar >> 32));
+  };
+  uint32_t x[N];
+  int u = part * p.units_per_part + warp;
+  if (u < u_end) load_unit<T, VEC>(row, u * kUnit, p.V, x);
+  const uint32_t unit_base = smem_addr(s_unit);
+  if (p.parts > 1) cluster_wait();
+  const uint32_t unit_dst = p.parts > 1 ? map_to_rank(unit_base, 0) : unit_base;
+  bool first = true;
+  // the block's warps take the same number of turns (a barrier in the first)
+  for (int turn = 0; first || u < u_end; ++turn, u += kWarps) {
+    uint32_t nx[N];
+    const bool here = u < u_end;
+    if (u + kWarps < u_end) load_unit<T, VEC>(row, (u + kWarps) * kUnit, p.V, nx);
+    float lm = -INFINITY;
+    if (here) {
+      if (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) lm = fmax3(lm, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      } else {
+        __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&x[0]);
+#pragma unroll
+        for (int i = 1; i < N; ++i) b = __hmax2(b, *reinterpret_cast<const __nv_bfloat162*>(&x[i]));
+        lm = fmaxf(__low2float(b), __high2float(b));
+      }
+      lm = no_nan(lm);
+    }
+    if (first && top_k > 0) {
+      // with q = ceil(k / 8): each warp's q-th largest lane maximum; the
+      // ceil(k / q)-th largest of those is reached by at least k ids
+      const int q = (top_k + kWarps - 1) / kWarps, need = (top_k + q - 1) / q;
+      const uint32_t mine = __shfl_sync(0xffffffffu, sort_desc(here ? ordered(lm) : 0u), q - 1);
+      if (lane == 0) s_first[warp] = mine;
+      __syncthreads();
+      const uint32_t v = s_first[lane & (kWarps - 1)];
+      int rank = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const uint32_t o = s_first[w];
+        rank += o > v || (o == v && w < (lane & (kWarps - 1)));
+      }
+      floor_hi = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == need - 1)) - 1);
+    }
+    first = false;
+    if (!here) break;
+    const float m = warp_max(lm);
+    float s = 0.f, t = 0.f;
+    if (m == INFINITY) {  // the ids at +infinity share the row
+#pragma unroll
+      for (int i = 0; i < kPerLane / 2; ++i) {
+        const float2 v = pair_of<T>(x, i);
+        s += (v.x == INFINITY ? 1.f : 0.f) + (v.y == INFINITY ? 1.f : 0.f);
+      }
+    } else if (m > -INFINITY) {
+      const float2 neg_m = make_float2(-m, -m), c2 = make_float2(kLog2e, kLog2e);
+      float2 s2 = make_float2(0.f, 0.f), t2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kPerLane / 2; ++i) {
+        float2 a = __fmul2_rn(__fadd2_rn(pair_of<T>(x, i), neg_m), c2);
+        a = make_float2(fmaxf(a.x, -200.f), fmaxf(a.y, -200.f));
+        const float2 w = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+        s2 = __fadd2_rn(s2, w);
+        t2 = __ffma2_rn(w, a, t2);
+      }
+      s = __fadd_rn(s2.x, s2.y);
+      t = __fadd_rn(t2.x, t2.y);
+    }
+    s = warp_sum(s);
+    t = warp_sum(t);
+    if (lane < 3) st_cluster_f32(unit_dst + (3 * u + lane) * 4, lane == 0 ? m : lane == 1 ? s : t);
+    if (top_k > 0) {
+      floor_hi = max(floor_hi, *static_cast<volatile uint32_t*>(&s_floor));
+      if (__any_sync(0xffffffffu, ordered(lm) >= floor_hi)) {
+        // which of the lane's ids reach the floor; then one id a lane at a time
+        const float floor = floor_hi ? unordered(floor_hi) : -INFINITY;
+        uint32_t mask = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane / 2; ++i) {
+          const float2 v = pair_of<T>(x, i);
+          mask |= (v.x < floor ? 0u : 1u << (2 * i)) | (v.y < floor ? 0u : 2u << (2 * i));
+        }
+        while (__any_sync(0xffffffffu, mask != 0)) {
+          u64 key = 0;
+          if (mask) {
+            const int id = u * kUnit + unit_id<T>(lane, __ffs(mask) - 1);
+            mask &= mask - 1;
+            if (id < p.V) key = top_key(static_cast<float>(row[id]), id);
+          }
+          const bool in = key > bar;
+          const unsigned who = __ballot_sync(0xffffffffu, in);
+          if (in) pending[warp][waiting + __popc(who & ((1u << lane) - 1))] = key;
+          waiting += __popc(who);
+          __syncwarp();
+          if (waiting >= 32) merge_waiting(32);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = nx[i];
+  }
+  // the row's list and sums to the first block
+  if (top_k > 0) {
+    if (waiting) merge_waiting(waiting);
+    lists[warp][lane] = best;
+    best = merge_block(lists);
+  }
+  if (p.parts > 1) {
+    if (top_k > 0) {
+      // the other blocks' lists go where the first block's `pending` was (its
+      // own warps are past it: the merge's barriers above, then the cluster's)
+      if (warp == 0) lists[0][lane] = best;
+      cluster_sync();
+      if (part != 0) {
+        if (warp == 0) st_cluster_u64(map_to_rank(smem_addr(&pending[0][0]), 0) + (part * 32 + lane) * 8, best);
+      }
+    }
+    cluster_sync();
+    if (part != 0) return;
+    if (top_k > 0) {
+      u64(*got)[32] = reinterpret_cast<u64(*)[32]>(&pending[0][0]);
+      const u64 v = warp == 0 ? lists[0][lane] : warp < p.parts ? got[warp][lane] : static_cast<u64>(0);
+      __syncthreads();
+      lists[warp][lane] = v;
+      best = merge_block(lists);
+    }
+  }
+  __syncthreads();
+  // the fold of the units, by the last warp
+  if (warp == kWarps - 1) {
+    float M = -INFINITY;
+    for (int i = lane; i < p.units; i += 32) M = fmaxf(M, s_unit[3 * i]);
+    M = warp_max(M);
+    float S = 0.f, Tt = 0.f;
+    for (int i = lane; i < p.units; i += 32) {
+      const float m = s_unit[3 * i], s = s_unit[3 * i + 1], t = s_unit[3 * i + 2];
+      const float d = m == M ? 0.f : __fmul_rn(__fsub_rn(m, M), kLog2e);
+      const float w = ex2_approx(d);
+      if (w > 0.f) {
+        S = __fadd_rn(S, __fmul_rn(w, s));
+        Tt = __fadd_rn(Tt, __fmul_rn(w, __fmaf_rn(s, d, t)));
+      }
+    }
+    S = warp_sum(S);
+    Tt = warp_sum(Tt);
+    if (lane == 0) {
+      s_row[0] = M;
+      s_row[1] = logf(S);
+      if (p.entropy) p.entropy[r] = M == -INFINITY ? 0.f : __fsub_rn(s_row[1], __fmul_rn(kLn2, __fdiv_rn(Tt, S)));
+    }
+  }
+  __syncthreads();
+  const float M = s_row[0], ln_s = s_row[1];
+  auto logprob = [&](float v) {
+    v = no_nan(v);
     if (M == -INFINITY) return -INFINITY;
-    const float d = x == M ? 0.f : __fsub_rn(x, M);  // +infinity against +infinity: the shared maximum
+    const float d = v == M ? 0.f : __fsub_rn(v, M);  // +infinity against +infinity: the shared maximum
     return __fsub_rn(d, ln_s);
   };
-  const T* row = static_cast<const T*>(p.x) + r * p.ld;
-  if (lane == 0 && p.entropy)
-    p.entropy[r] = M == -INFINITY ? 0.f : __fsub_rn(ln_s, __fmul_rn(kLn2, __fdiv_rn(Tt, S)));
-  for (int j = lane; j < p.n_ids; j += 32) {
+  if (warp == 0 && lane < top_k) {
+    p.top_ids[r * top_k + lane] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+    p.top_logprobs[r * top_k + lane] = logprob(unordered(static_cast<uint32_t>(best >> 32)));
+  }
+  for (int j = static_cast<int>(threadIdx.x) - 32; j < p.n_ids; j += kThreads - 32) {
+    if (j < 0) break;
     const int id = p.ids[r * p.n_ids + j];
     float v = 0.f;
     if (id >= p.V) {
@@ -181,161 +378,22 @@ __device__ void finish_row(const LogprobParams& p, int64_t r, const float* unit,
     }
     p.logprob[r * p.n_ids + j] = v;
   }
-  if (lane < p.top_k) {
-    p.top_ids[r * p.top_k + lane] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
-    p.top_logprobs[r * p.top_k + lane] = logprob(unordered(static_cast<uint32_t>(best >> 32)));
-  }
 }
 
-// The block's lists in shared memory, one per warp, into one (warp 0).
-__device__ __forceinline__ u64 merge_block(u64 (*lists)[32], u64 mine) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  lists[warp][lane] = mine;
-  __syncthreads();
-  if (warp == 0) {
-#pragma unroll 1
-    for (int w = 1; w < kWarps; ++w) mine = merge_desc(mine, lists[w][lane]);
-  }
-  return mine;
-}
-
-// A block per (part of a row, row).
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobParams p) {
-  extern __shared__ float s_unit[];  // [units][3] when the row is one part
-  __shared__ u64 pending[kWarps][kPending];
-  __shared__ u64 lists[kWarps][32];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t r = blockIdx.x / p.parts;
-  const int part = blockIdx.x % p.parts;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* row = static_cast<const T*>(p.x) + r * p.ld;
-  float* unit = p.parts == 1 ? s_unit : p.ws_unit + r * p.units * 3;
-  const int u_end = min(p.units, (part + 1) * p.units_per_part);
-  u64 best = 0;   // lane i: the i-th best key (0: none)
-  u64 bar = 0;    // the k-th best
-  uint32_t bar_hi = 0;
-  int waiting = 0;
-  bool first = true;
-  for (int u = part * p.units_per_part + warp; u < u_end; u += kWarps) {
-    float x[16];
-    load_unit<T, VEC>(row, u * kUnit, p.V, x);
-    float lm = x[0];
-#pragma unroll
-    for (int e = 1; e < 16; ++e) lm = fmaxf(lm, x[e]);
-    lm = no_nan(lm);
-    const float m = warp_max(lm);
-    float s = 0.f, t = 0.f;
-    if (m == INFINITY) {  // the ids at +infinity share the row
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s += x[e] == INFINITY ? 1.f : 0.f;
-    } else if (m > -INFINITY) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float a = fmaxf(__fmul_rn(__fsub_rn(x[e], m), kLog2e), -200.f);
-        const float w = ex2_approx(a);
-        s = __fadd_rn(s, w);
-        t = __fmaf_rn(w, a, t);
-      }
-    }
-    s = warp_sum(s);
-    t = warp_sum(t);
-    if (lane == 0) {
-      unit[3 * u] = m;
-      unit[3 * u + 1] = s;
-      unit[3 * u + 2] = t;
-    }
-    if (p.top_k > 0) {
-      uint32_t floor_hi = bar_hi;
-      if (first) {
-        // k lanes hold an id at or above the k-th of the lanes' maxima
-        floor_hi = __shfl_sync(0xffffffffu, sort_desc(ordered(lm)), p.top_k - 1);
-      }
-      if (__any_sync(0xffffffffu, ordered(lm) >= floor_hi)) {
-#pragma unroll 1
-        for (int e0 = 0; e0 < 16; e0 += 4) {
-#pragma unroll
-          for (int e1 = 0; e1 < 4; ++e1) {
-            float xe = x[e1];
-#pragma unroll
-            for (int q = 1; q < 4; ++q) xe = e0 == 4 * q ? x[4 * q + e1] : xe;
-            const int id = u * kUnit + unit_id<T>(lane, e0 + e1);
-            const u64 key = id < p.V ? top_key(xe, id) : 0;
-            const bool in = key > bar && static_cast<uint32_t>(key >> 32) >= floor_hi;
-            const unsigned who = __ballot_sync(0xffffffffu, in);
-            if (who) {
-              if (in) pending[warp][waiting + __popc(who & ((1u << lane) - 1))] = key;
-              waiting += __popc(who);
-              __syncwarp();
-              if (waiting >= 32) {
-                best = merge_desc(best, sort_desc(pending[warp][waiting - 32 + lane]));
-                waiting -= 32;
-                bar = __shfl_sync(0xffffffffu, best, p.top_k - 1);
-                __syncwarp();
-              }
-            }
-          }
-        }
-        if (first && waiting) {
-          const u64 v = lane < waiting ? pending[warp][lane] : 0;
-          best = merge_desc(best, sort_desc(v));
-          bar = __shfl_sync(0xffffffffu, best, p.top_k - 1);
-          waiting = 0;
-          __syncwarp();
-        }
-        bar_hi = static_cast<uint32_t>(bar >> 32);
-      }
-      first = false;
-    }
-  }
-  if (p.top_k > 0) {
-    if (waiting) best = merge_desc(best, sort_desc(lane < waiting ? pending[warp][lane] : static_cast<u64>(0)));
-    best = merge_block(lists, best);
-  } else {
-    __syncthreads();
-  }
-  if (warp != 0) return;
-  if (p.parts == 1)
-    finish_row<T>(p, r, s_unit, best);
-  else if (p.top_k > 0)
-    p.ws_top[(r * p.parts + part) * 32 + lane] = best;
-}
-
-// Rows of several parts: a block per row.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_finish_kernel(const LogprobParams p) {
-  __shared__ u64 lists[kWarps][32];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t r = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  u64 best = 0;
-  if (p.top_k > 0) {
-    for (int part = warp; part < p.parts; part += kWarps)
-      best = merge_desc(best, p.ws_top[(r * p.parts + part) * 32 + lane]);
-    best = merge_block(lists, best);
-  }
-  if (warp == 0) finish_row<T>(p, r, p.ws_unit + r * p.units * 3, best);
-}
-
+// Blocks per row: enough to give every SM two, while each keeps a unit per warp.
 int part_count(int rows, int units) {
-  const int most = (units + kWarps - 1) / kWarps;
-  const int want = (152 * 4 + rows - 1) / rows;
-  return want < most ? want : most;
+  int parts = 1;
+  while (parts < 8 && static_cast<int64_t>(rows) * parts < 304 && units > parts * kWarps) parts *= 2;
+  return parts;
 }
-
-size_t unit_bytes(int rows, int units) { return (static_cast<size_t>(rows) * units * 12 + 255) / 256 * 256; }
 
 template <typename T>
 kinv_status launch(const LogprobParams& p, int rows, bool vec, cudaStream_t stream) {
-  const size_t smem = p.parts == 1 ? static_cast<size_t>(p.units) * 12 : 0;
+  const size_t smem = static_cast<size_t>(p.units) * 12;
   auto* kernel = vec ? logprobs_kernel<T, true> : logprobs_kernel<T, false>;
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (attr != KINV_OK) return attr;
-  const kinv_status st = launch_kernel(kernel, dim3(static_cast<unsigned>(rows) * p.parts), dim3(kThreads), smem, stream, 1, p);
-  if (st != KINV_OK || p.parts == 1) return st;
-  return launch_kernel(logprobs_finish_kernel<T>, dim3(rows), dim3(kThreads), 0, stream, 1, p);
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(rows) * p.parts), dim3(kThreads), smem, stream, p.parts, p);
 }
 
 }  // namespace
@@ -343,17 +401,9 @@ kinv_status launch(const LogprobParams& p, int rows, bool vec, cudaStream_t stre
 
 using namespace kinv;
 
-extern "C" size_t kinv_logprobs_workspace(int rows, int V) {
-  if (rows <= 0 || V <= 0) return 0;
-  const int units = (V + kUnit - 1) / kUnit;
-  const int parts = part_count(rows, units);
-  return parts == 1 ? 0 : unit_bytes(rows, units) + static_cast<size_t>(rows) * parts * 32 * 8;
-}
-
 extern "C" kinv_status kinv_logprobs(const void* logits, kinv_dtype dtype, int64_t ld, int rows, int V,
                                      const int32_t* ids, int n_ids, float* logprob, float* entropy, int top_k,
-                                     int32_t* top_ids, float* top_logprobs, void* workspace,
-                                     size_t workspace_bytes, kinv_stream stream) {
+                                     int32_t* top_ids, float* top_logprobs, kinv_stream stream) {
   if (rows < 0 || V <= 0 || n_ids < 0 || top_k < 0 || ld < V || top_k > V) return KINV_ERR_INVALID_ARG;
   if (dtype != KINV_F32 && dtype != KINV_BF16) return KINV_ERR_INVALID_ARG;
   if (V > 1048576 || top_k > kMaxTop) return KINV_ERR_UNSUPPORTED;
@@ -369,15 +419,6 @@ extern "C" kinv_status kinv_logprobs(const void* logits, kinv_dtype dtype, int64
   p.units = (V + kUnit - 1) / kUnit;
   p.parts = part_count(rows, p.units);
   p.units_per_part = (p.units + p.parts - 1) / p.parts;
-  if (static_cast<int64_t>(rows) * p.parts > 0x7fffffff) return KINV_ERR_UNSUPPORTED;
-  const size_t need = kinv_logprobs_workspace(rows, V);
-  if (need > 0) {
-    if (!workspace) return KINV_ERR_INVALID_ARG;
-    if (!aligned16(workspace)) return KINV_ERR_ALIGNMENT;
-    if (workspace_bytes < need) return KINV_ERR_WORKSPACE;
-    p.ws_unit = static_cast<float*>(workspace);
-    p.ws_top = reinterpret_cast<u64*>(static_cast<char*>(workspace) + unit_bytes(rows, p.units));
-  }
   p.ids = ids;
   p.n_ids = n_ids;
   p.logprob = logprob;

@@ -71,9 +71,7 @@ SIGNATURES = {
                               _c_p, _sz, _c_p]),
     "kinv_tree_accept": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i32, _i64, _i64, _i64, _i32, _i32, _c_p,
                                 _c_p, _c_p, _c_p]),
-    "kinv_logprobs_workspace": (_sz, [_i32, _i32]),
-    "kinv_logprobs": (_i32, [_c_p, _i32, _i64, _i32, _i32, _c_p, _i32, _c_p, _c_p, _i32, _c_p, _c_p, _c_p,
-                             _sz, _c_p]),
+    "kinv_logprobs": (_i32, [_c_p, _i32, _i64, _i32, _i32, _c_p, _i32, _c_p, _c_p, _i32, _c_p, _c_p, _c_p]),
     "kinv_decode_advance": (_i32, [_c_p, _c_p, _i32, _c_p, _c_p, _c_p, _c_p, _i32, _c_p]),
 }
 
@@ -117,9 +115,18 @@ def _check(status: int, where: str) -> None:
         raise KinvError(status, where)
 
 
+# the current stream's handle without building a Stream object (0.1 against 3
+# microseconds a call), where this PyTorch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and _get_device is not None:
+        return _raw_stream(_get_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t):
@@ -481,11 +488,7 @@ def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=
 
 
 # --------------------------------------------------------- log probabilities
-def logprobs_workspace(rows: int, vocab: int) -> int:
-    return int(lib().kinv_logprobs_workspace(rows, vocab))
-
-
-def logprobs(logits, ids=None, top_k: int = 0, workspace=None, stream=None):
+def logprobs(logits, ids=None, top_k: int = 0, stream=None):
     """logits fp32 or bf16 [rows][V]; ids int32 [rows][n] (negative: padding).
     Returns (logprobs fp32 [rows][n] or None, entropy fp32 [rows], top_ids int32
     [rows][top_k] or None, top_logprobs fp32 [rows][top_k] or None)."""
@@ -508,13 +511,9 @@ def logprobs(logits, ids=None, top_k: int = 0, workspace=None, stream=None):
     if top_k:
         top_ids = torch.empty(rows, top_k, dtype=torch.int32, device=dev)
         top_lp = torch.empty(rows, top_k, dtype=torch.float32, device=dev)
-    if workspace is None:
-        need = logprobs_workspace(rows, v)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _check(lib().kinv_logprobs(_ptr(logits), F32 if logits.dtype == torch.float32 else BF16,
                                logits.stride(0) if rows > 1 else max(logits.stride(0), v), rows, v, _ptr(ids),
                                n_ids, _ptr(lp), _ptr(entropy), int(top_k), _ptr(top_ids), _ptr(top_lp),
-                               _ptr(workspace), workspace.numel() if workspace is not None else 0,
                                _stream(stream)), "kinv_logprobs")
     return lp, entropy, top_ids, top_lp
 

@@ -5,8 +5,8 @@ Tolerances.  A term 2^a of S has the error of ex2.approx (2 ulp: 2^-22) and of
 its argument a = fl(fl(x - m) log2e): three roundings of at most 2^-24 relative
 (difference, product, the constant), times ln 2 |a| <= ln V + ... as a relative
 error of the term; weighted by the terms themselves the sum of |a| ln 2 p is at
-most ln V <= 14, so 42 * 2^-24.  Every term passes at most 16 + 5 additions in
-its unit and 64 + 5 in the fold (90 * 2^-24), so S is off by at most (4 + 42 +
+most ln V <= 14, so 42 * 2^-24.  Every term passes at most 17 + 5 additions in
+its unit and 63 + 5 in the fold (90 * 2^-24), so S is off by at most (4 + 42 +
 90) 2^-24 = 8.2e-6 relative and ln S by that much absolutely, plus one rounding
 of ln S and two of the differences (2^-23 relative).  The entropy ln S - ln 2
 T / S carries T's and S's relative errors (8.2e-6 each, T's terms have one more
@@ -75,7 +75,7 @@ def test_many_rows_have_the_bits_of_one(kinv, dtype):
     x = logits(rows, v + 13, 5, dtype)[:, :v]            # an odd row length: no 16-byte loads
     ids = torch.randint(0, v, (rows, 2), generator=synth.gen(2)).to(torch.int32).cuda()
     whole = check(kinv, x, ids, 20, rows=[0, 7, 1299])
-    for r0, n in ((0, 1), (7, 1), (100, 3), (640, 70), (0, 607), (0, 609)):
+    for r0, n in ((0, 1), (7, 1), (100, 3), (640, 70), (0, 160), (0, 303), (0, 305)):
         part = kinv.logprobs(x[r0: r0 + n], ids[r0: r0 + n], top_k=20)
         for a, b in zip(part, whole):
             assert_same_bits(a, b[r0: r0 + n], f"rows {r0} .. {r0 + n}")
@@ -137,23 +137,22 @@ def test_an_id_beyond_the_vocabulary_is_reported(kinv):
     assert torch.isnan(lp[0, 1]) and torch.isnan(lp[1, 0]) and lp[1, 1] == 0 and torch.isfinite(lp[0, 0])
 
 
-def test_workspace_streams_and_capture(kinv):
+def test_two_streams_and_capture(kinv):
     x = logits(4, 151936, 2)
     ids = torch.randint(0, 151936, (4, 1), generator=synth.gen(3)).to(torch.int32).cuda()
     want = kinv.logprobs(x, ids, top_k=8)
-    need = kinv.logprobs_workspace(4, 151936)
-    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
-    for a, b in zip(kinv.logprobs(x, ids, top_k=8, workspace=ws[:need]), want):
-        assert_same_bits(a, b, "a workspace of NaN bits")
-    assert torch.all(ws[need:] == 0xFF)
-    with pytest.raises(kinv.KinvError) as e:
-        kinv.logprobs(x, ids, top_k=8, workspace=ws[: need - 1])
-    assert e.value.status == kinv.ERR_WORKSPACE
-    s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(6):
+        outs.append(kinv.logprobs(x, ids, top_k=8, stream=streams[i % 2]))
+    torch.cuda.synchronize()
+    for o in outs:
+        for a, b in zip(o, want):
+            assert_same_bits(a, b, "two streams")
+    s = streams[0]
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=s):
-        got = kinv.logprobs(x, ids, top_k=8, workspace=ws)
+        got = kinv.logprobs(x, ids, top_k=8)
     for seed in (2, 6):
         x.copy_(logits(4, 151936, seed))
         g.replay()
