@@ -38,7 +38,7 @@ struct TreeAttnParams {
   __nv_bfloat16* out;
   float* ws_o;   // [total_rows][Hq][S][D]
   float* ws_ml;  // [total_rows][Hq][S][2]
-  int Hq, Hkv, G;
+  int Hq, Hkv, G, gs;  // G = Hq / Hkv = 1 << gs
   int S;         // splits per row in the workspace
   float c2;      // fp32(scale * log2 e) > 0
   int tail_only; // the splits that end within the context are another kernel's
@@ -51,23 +51,24 @@ __device__ __forceinline__ void report_bad_tree(const TreeAttnParams& p) {
 
 // One block per (kv head, tile of 16 MT pairs, split, sequence).
 template <int D, int MT>
-__global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAttnParams p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const TreeAttnParams p) {
   constexpr int C8 = D / 8;   // 16-byte chunks per key row
   constexpr int KS = D / 16;  // 16-wide k steps of q . k
   constexpr int R = 16 * MT;  // pairs of the tile
-  // rows of 16-byte chunks, chunk c of row r at chunk c ^ (r & 7): K, then V
-  // (up to 256 context keys, or up to 255 and the drafted ones); the scores by
-  // position [R][256] fp32, then P_hi and P_lo [R][256] in their place; the
-  // path of each node of the tile; a row of zeros
+  // scores by position [R][256] fp32, then P_hi and P_lo [R][256] in their
+  // place (8-key chunk kc of row r at chunk kc ^ (r & 7)); a row of zeros; the
+  // path of each node of the tile; K, then V (rows of 16-byte chunks, chunk c of
+  // row r at chunk c ^ (r & 7)): up to 256 context keys, or up to 255 and the
+  // drafted ones
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  constexpr int KV_ROWS = kSplit + kTreeMaxNodes;
-  unsigned char* kv = smem_raw;
-  unsigned char* pt = kv + KV_ROWS * D * 2;
+  unsigned char* pt = smem_raw;
   unsigned char* pt_lo = pt + R * kSplit * 2;
   float* scores = reinterpret_cast<float*>(pt);
   unsigned char* zrow = pt_lo + R * kSplit * 2;
-  unsigned char* paths = zrow + D * 2;  // [R][64]
+  unsigned char* paths = zrow + D * 2;  // [R >> gs][64]
+  unsigned char* kv = paths + (R >> p.gs) * kTreeMaxNodes;
   __shared__ TreeInfo ti;
+  __shared__ int depth[kTreeMaxNodes];
   __shared__ float wmax[kThreads / 32][R];
   __shared__ float wsum[kThreads / 32][R];
 
@@ -82,8 +83,8 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
     return;
   }
   const int s = (p.tail_only ? ctx / kSplit : 0) + static_cast<int>(blockIdx.y);
-  const int G = p.G;
-  const int npt = R / G;  // nodes of a tile
+  const int gs = p.gs;  // G = 1 << gs
+  const int npt = R >> gs;  // nodes of a tile
   const int n0 = tile * npt;
   const int k0 = s * kSplit;
   if (n0 >= n || k0 >= ctx + n) return;
@@ -100,33 +101,26 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
   const int drafted = tail ? n0 + nodes : 0;  // ancestors have lower indices: later nodes are nobody's here
   const int rows = c + drafted;
   const int64_t seq_off = b * p.seq_stride + g * D;
-  const uint64_t kv_policy = l2_policy_evict_first();
+  // other tiles read the same keys: the default L2 policy keeps them
   auto load = [&](const __nv_bfloat16* src) {
     for (int idx = t; idx < rows * C8; idx += kThreads) {
       const int r = idx / C8, ch = idx % C8;
       const int slot = r < c ? k0 + r : ctx + r - c;
-      cp_async16_hint(kv_base + static_cast<uint32_t>(r * D * 2 + ((ch ^ (r & 7)) << 4)),
-                      src + seq_off + static_cast<int64_t>(slot) * p.tok_stride + ch * 8, kv_policy);
+      cp_async16(kv_base + static_cast<uint32_t>(r * D * 2 + ((ch ^ (r & 7)) << 4)),
+                 src + seq_off + static_cast<int64_t>(slot) * p.tok_stride + ch * 8);
     }
     cp_async_commit();
   };
   load(p.k);
 
   if (tail) {
-    if (warp == 0) tree_load(p.tree, b, ti);
+    if (warp == 0) {
+      tree_load(p.tree, b, ti);
+      __syncwarp();
+      depth[lane] = __popcll(ti.mask[lane]) - 1;
+      depth[lane + 32] = __popcll(ti.mask[lane + 32]) - 1;
+    }
     for (int i = t; i < D * 2 / 16; i += kThreads) *reinterpret_cast<uint4*>(zrow + 16 * i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (!ti.ok) {
-      report_bad_tree(p);
-      cp_async_wait<0>();
-      return;
-    }
-    // the path of a node: the set bits of its mask, ascending
-    for (int idx = t; idx < nodes * kTreeMaxNodes; idx += kThreads) {
-      const int i = idx / kTreeMaxNodes, j = idx % kTreeMaxNodes;
-      const unsigned long long m = ti.mask[n0 + i];
-      if (m >> j & 1) paths[i * kTreeMaxNodes + __popcll(m & ((1ull << j) - 1))] = static_cast<unsigned char>(j);
-    }
   }
 
   // q fragments (A operand), straight from global: MMA row r of tile mt is pair
@@ -136,7 +130,9 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
   for (int mt = 0; mt < MT; ++mt) {
     const int r_lo = mt * 16 + gq, r_hi = r_lo + 8;
     auto row = [&](int r) -> const __nv_bfloat16* {
-      return r / G < nodes ? p.q + (static_cast<int64_t>(off + n0 + r / G) * p.Hq + g * G + r % G) * D : nullptr;
+      return r >> gs < nodes
+                 ? p.q + (static_cast<int64_t>(off + n0 + (r >> gs)) * p.Hq + (g << gs) + (r & ((1 << gs) - 1))) * D
+                 : nullptr;
     };
     const __nv_bfloat16 *q_lo = row(r_lo), *q_hi = row(r_hi);
 #pragma unroll
@@ -150,6 +146,17 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
   }
   cp_async_wait<0>();
   __syncthreads();
+  if (tail) {
+    if (!ti.ok) {
+      report_bad_tree(p);
+      return;
+    }
+    // the path of a node: the set bits of its mask, ascending
+    for (int idx = t; idx < nodes * kTreeMaxNodes; idx += kThreads) {
+      const int i = idx / kTreeMaxNodes, j = idx % kTreeMaxNodes;
+      if (ti.mask[n0 + i] >> j & 1) paths[i * kTreeMaxNodes + depth[j]] = static_cast<unsigned char>(j);
+    }
+  }
 
   // scores of eight key rows (from `key0`) against the tile's pairs
   auto score_block = [&](int key0, float (&sc)[MT][4]) {
@@ -170,8 +177,9 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
       }
     }
   };
-  float sc[4][MT][4];  // warp w: positions 32w + 8nb + 2tq (+1), pairs gq and gq + 8 of each MMA tile
-  int cnt[MT][2];      // positions of this split that the pair sees
+  // warp w: positions 32w + 8nb + 2tq (+1), pairs gq and gq + 8 of each MMA tile
+  float sc[4][MT][4];
+  int cnt[MT][2];  // positions of this split that the pair sees
   int cnt_max = 0;
   if (!tail) {
 #pragma unroll
@@ -179,47 +187,49 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) cnt[mt][h] = (mt * 16 + h * 8 + gq) / G < nodes ? kSplit : 0;
+      for (int h = 0; h < 2; ++h) cnt[mt][h] = (mt * 16 + h * 8 + gq) >> gs < nodes ? kSplit : 0;
     cnt_max = kSplit;
   } else {
     // every key row's scores, put at the position the key has for the pair
+    unsigned long long mask[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = (mt * 16 + h * 8 + gq) >> gs;
+        mask[mt][h] = i < nodes ? ti.mask[n0 + i] : 0ull;
+        cnt[mt][h] = i < nodes ? max(0, min(kSplit, ctx + depth[n0 + i] + 1 - k0)) : 0;
+      }
     for (int blk = warp; blk * 8 < rows; blk += kThreads / 32) {
       float one[MT][4];
       score_block(blk * 8, one);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int e = 0; e < 2; ++e) {
+        const int key = blk * 8 + 2 * tq + e, j = key - c;
+        int at = key;
+        if (j >= 0) at = j < drafted ? c + depth[j] - shift : kSplit;
+        if (at < 0 || at >= kSplit || (j >= 0 && at < c)) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int pair = mt * 16 + gq + (i >> 1) * 8;
-          const int key = blk * 8 + 2 * tq + (i & 1);
-          if (pair / G >= nodes || key >= rows) continue;
-          int at = key;
-          if (key >= c) {
-            const int j = key - c;
-            if (!(ti.mask[n0 + pair / G] >> j & 1)) continue;
-            at = c + __popcll(ti.mask[j]) - 1 - shift;
-            if (at < c || at >= kSplit) continue;
-          }
-          scores[pair * kSplit + at] = one[mt][i];
-        }
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (j < 0 || (mask[mt][h] >> j & 1)) scores[(mt * 16 + h * 8 + gq) * kSplit + at] = one[mt][2 * h + e];
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int pair = mt * 16 + h * 8 + gq;
-        const int i = pair / G;
-        cnt[mt][h] = i < nodes ? max(0, min(kSplit, ctx + __popcll(ti.mask[n0 + i]) - k0)) : 0;
+        const float* row = scores + (mt * 16 + h * 8 + gq) * kSplit + warp * 32 + 2 * tq;
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = warp * 32 + nb * 8 + 2 * tq + e;
-            sc[nb][mt][2 * h + e] = at < cnt[mt][h] ? scores[pair * kSplit + at] : 0.f;
-          }
+        for (int nb = 0; nb < 4; ++nb) {
+          const float2 v = *reinterpret_cast<const float2*>(row + nb * 8);
+          sc[nb][mt][2 * h] = v.x;
+          sc[nb][mt][2 * h + 1] = v.y;
+        }
       }
-    for (int i = 0; i < nodes; ++i) cnt_max = max(cnt_max, min(kSplit, ctx + __popcll(ti.mask[n0 + i]) - k0));
+    for (int i = 0; i < nodes; ++i) cnt_max = max(cnt_max, min(kSplit, ctx + depth[n0 + i] + 1 - k0));
   }
   __syncthreads();  // every warp is done with K and with the scores' array
   load(p.v);
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
     ldsm_x4(pt_lo_base + o, al[0], al[1], al[2], al[3]);
   };
   const int shared_steps = c / 16;  // steps that hold context keys only
-#pragma unroll 2
+#pragma unroll 4
   for (int kk = 0; kk < shared_steps; ++kk) {
     uint32_t b0, b1, b2, b3;
     const int key = kk * 16 + (lane & 15);
@@ -311,15 +321,23 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
   }
   for (int kk = shared_steps; kk * 16 < cnt_max; ++kk) {
     const int at = kk * 16 + (lane & 15);  // the position whose V row this lane addresses
+    const int dep = at - c + shift;        // of a node's ancestor at this position
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+      const int i0 = (mt * 16) >> gs, i1 = min(nodes, ((mt + 1) * 16) >> gs);
+      if (i0 >= i1) continue;
       uint32_t ah[4], al[4];
       load_p(mt, kk, ah, al);
-      for (int i = mt * 16 / G; i < min(nodes, (mt + 1) * 16 / G); ++i) {
-        const int depth = at - c + shift;  // of the node's ancestor at this position
+      float was[2][4];  // the accumulators before this step
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) was[nb][e] = oc[mt][nb][e];
+#pragma unroll 2
+      for (int i = i0; i < i1; ++i) {
         uint32_t addr = zrow_base + (vchunk << 4);
-        if (at < c || depth < __popcll(ti.mask[n0 + i])) {
-          const int row = at < c ? at : c + paths[i * kTreeMaxNodes + depth];
+        if (at < c || dep <= depth[n0 + i]) {
+          const int row = at < c ? at : c + paths[i * kTreeMaxNodes + dep];
           addr = kv_base + static_cast<uint32_t>(row * D * 2 + ((vchunk ^ (row & 7)) << 4));
         }
         uint32_t b0, b1, b2, b3;
@@ -328,14 +346,14 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) tmp[nb][e] = oc[mt][nb][e];
+          for (int e = 0; e < 4; ++e) tmp[nb][e] = was[nb][e];
         mma_bf16_16816(tmp[0], ah, b0, b1);
         mma_bf16_16816(tmp[1], ah, b2, b3);
         mma_bf16_16816(tmp[0], al, b0, b1);
         mma_bf16_16816(tmp[1], al, b2, b3);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          if ((mt * 16 + h * 8 + gq) / G == i) {
+          if ((mt * 16 + h * 8 + gq) >> gs == i) {
 #pragma unroll
             for (int nb = 0; nb < 2; ++nb) {
               oc[mt][nb][2 * h] = tmp[nb][2 * h];
@@ -351,7 +369,8 @@ __global__ void __launch_bounds__(kThreads) attn_tree_split_kernel(const TreeAtt
     for (int h = 0; h < 2; ++h) {
       if (cnt[mt][h] <= 0) continue;
       const int pair = mt * 16 + h * 8 + gq;
-      const int64_t base = (static_cast<int64_t>(off + n0 + pair / G) * p.Hq + g * G + pair % G) * p.S + s;
+      const int64_t base =
+          (static_cast<int64_t>(off + n0 + (pair >> gs)) * p.Hq + (g << gs) + (pair & ((1 << gs) - 1))) * p.S + s;
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb)
         *reinterpret_cast<float2*>(p.ws_o + base * D + warp * 16 + nb * 8 + 2 * tq) =
@@ -763,59 +782,83 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// One block per (query head, node, sequence); thread d folds column d over the
-// splits the node sees, with the decode merge's arithmetic.
+// A warp per (node, query head): a lane folds D/32 columns over the splits the
+// node sees, with the decode merge's arithmetic.  The first partials are
+// requested before the tree is read: a node of any depth sees the splits up to
+// position ctx_len.
+constexpr int kMergeWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(D) attn_tree_merge_kernel(const TreeAttnParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) attn_tree_merge_kernel(const TreeAttnParams p) {
+  constexpr int W = D / 32;  // columns of a lane
+  constexpr int CH = 8;      // partials loaded ahead of the (sequential) fold
   __shared__ TreeInfo ti;
   pdl_launch_dependents();
   pdl_wait();
-  const int h = blockIdx.x, node = blockIdx.y, b = blockIdx.z;
-  if (threadIdx.x < 32) tree_load(p.tree, b, ti);
-  __syncthreads();
-  if (!ti.ok || node >= ti.n) return;
-  const int d = threadIdx.x;
-  const int64_t row = ti.off + node;
-  const int len = ti.ctx + __popcll(ti.mask[node]);
-  const int ns = (len + kSplit - 1) / kSplit;
-  const int64_t base = (row * p.Hq + h) * p.S;
-  float m_acc = -INFINITY, l_acc = 0.f, o_acc = 0.f;
-  constexpr int CH = 8;  // partials loaded ahead of the (sequential) fold
-  for (int s0 = 0; s0 < ns; s0 += CH) {
-    float mv[CH], lv[CH], ov[CH];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.x * kMergeWarps + warp, node = blockIdx.y, b = blockIdx.z;
+  int n, ctx, off;
+  if (!tree_bounds(p.tree, b, n, ctx, off) || node >= n) return;
+  const bool mine = h < p.Hq;
+  const int64_t row = off + node;
+  const int64_t base = (row * p.Hq + (mine ? h : 0)) * p.S;
+  float2 ml[CH];
+  float o[CH][W];
+  auto load = [&](int s0, int ns) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (s0 + i < ns) {
-        const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (base + s0 + i) * 2);
-        mv[i] = ml.x;
-        lv[i] = ml.y;
-        ov[i] = p.ws_o[(base + s0 + i) * D + d];
+      if (s0 + i >= ns) continue;
+      ml[i] = *reinterpret_cast<const float2*>(p.ws_ml + (base + s0 + i) * 2);
+      const float* src = p.ws_o + (base + s0 + i) * D + lane * W;
+      if (W == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        o[i][0] = v.x, o[i][1] = v.y, o[i][2 % W] = v.z, o[i][3 % W] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        o[i][0] = v.x, o[i][1] = v.y;
       }
     }
+  };
+  const int sure = ctx / kSplit + 1;  // splits that every node sees
+  load(0, sure);
+  if (warp == 0) tree_load(p.tree, b, ti);
+  __syncthreads();
+  if (!ti.ok || !mine) return;
+  const int ns = (ctx + __popcll(ti.mask[node]) + kSplit - 1) / kSplit;
+  float m_acc = -INFINITY, l_acc = 0.f, o_acc[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) o_acc[w] = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += CH) {
+    if (s0 > 0 || (sure < CH && ns > sure)) load(s0, ns);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (s0 + i < ns) {
-        const float m_new = fmaxf(m_acc, mv[i]);
+        const float m_new = fmaxf(m_acc, ml[i].x);
         const float a = ex2_approx(__fsub_rn(m_acc, m_new));
-        const float c = ex2_approx(__fsub_rn(mv[i], m_new));
-        l_acc = __fadd_rn(__fmul_rn(l_acc, a), __fmul_rn(lv[i], c));
-        o_acc = __fadd_rn(__fmul_rn(o_acc, a), __fmul_rn(ov[i], c));
+        const float c = ex2_approx(__fsub_rn(ml[i].x, m_new));
+        l_acc = __fadd_rn(__fmul_rn(l_acc, a), __fmul_rn(ml[i].y, c));
+#pragma unroll
+        for (int w = 0; w < W; ++w) o_acc[w] = __fadd_rn(__fmul_rn(o_acc[w], a), __fmul_rn(o[i][w], c));
         m_acc = m_new;
       }
     }
   }
-  p.out[(row * p.Hq + h) * D + d] = __float2bfloat16_rn(__fdiv_rn(o_acc, l_acc));
-}
-
-template <int D, int MT>
-constexpr size_t split_smem_bytes() {
-  return static_cast<size_t>(kSplit + kTreeMaxNodes) * D * 2 + 2 * 16 * MT * kSplit * 2 + D * 2 + 16 * MT * kTreeMaxNodes;
+  __nv_bfloat16* dst = p.out + (row * p.Hq + h) * D + lane * W;
+  uint32_t packed[2];
+#pragma unroll
+  for (int w = 0; w < W; w += 2) packed[w / 2] = pack_bf16(__fdiv_rn(o_acc[w], l_acc), __fdiv_rn(o_acc[w + 1], l_acc));
+  if (W == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = packed[0];
 }
 
 template <int D, int MT>
 kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
   void (*kernel)(const TreeAttnParams) = attn_tree_split_kernel<D, MT>;
-  const size_t smem = split_smem_bytes<D, MT>();
+  // 256 key rows, or up to 255 and the drafted ones; scores are taken eight rows at a time
+  const int kv_rows = kSplit + (p.tree.max_nodes + 7) / 8 * 8;
+  const size_t smem = 2 * 16 * MT * kSplit * 2 + D * 2 + (16 * MT / p.G) * kTreeMaxNodes + static_cast<size_t>(kv_rows) * D * 2;
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (attr != KINV_OK) return attr;
   const int tiles = (p.tree.max_nodes * p.G + 16 * MT - 1) / (16 * MT);
@@ -852,7 +895,11 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
   p.tail_only = static_cast<int64_t>(p.tree.B) * p.Hkv * (p.tree.max_kv / kSplit) >= kMinSplitsTc &&
                 smem <= static_cast<size_t>(max_smem_optin()) && encode_maps<D>(p, &mq, &mk, &mv);
-  kinv_status st = p.tree.max_nodes * p.G <= 16 ? launch_split<D, 1>(p, stream) : launch_split<D, 2>(p, stream);
+  // tiles of 16 pairs where they are the whole tree, or where tiles of 32 would
+  // leave SMs without a block
+  const int pairs = p.tree.max_nodes * p.G;
+  const bool small = pairs <= 16 || static_cast<int64_t>(p.tree.B) * p.Hkv * ((pairs + 31) / 32) * (p.tail_only ? 1 : p.S) < sms;
+  kinv_status st = small ? launch_split<D, 1>(p, stream) : launch_split<D, 2>(p, stream);
   if (st != KINV_OK) return st;
   if (p.tail_only) {
     void (*kernel)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const TreeAttnParams) = attn_tree_ctx_kernel<D>;
@@ -861,7 +908,8 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
     st = launch_kernel(kernel, dim3(sms), dim3(kTcThreads), smem, stream, 1, mq, mk, mv, p);
     if (st != KINV_OK) return st;
   }
-  return launch_kernel(attn_tree_merge_kernel<D>, dim3(p.Hq, p.tree.max_nodes, p.tree.B), dim3(D), 0, stream, 1, p);
+  return launch_kernel(attn_tree_merge_kernel<D>, dim3((p.Hq + kMergeWarps - 1) / kMergeWarps, p.tree.max_nodes, p.tree.B),
+                       dim3(32 * kMergeWarps), 0, stream, 1, p);
 }
 
 size_t tree_workspace_bytes(int64_t rows, int Hq, int D, int S) {
@@ -918,6 +966,7 @@ extern "C" kinv_status kinv_attn_tree(const void* q, const void* k_cache, const 
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = G;
+  p.gs = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
   p.S = static_cast<int>(S);
   p.c2 = base2_factor(scale, D);
   p.status = device_status_word();

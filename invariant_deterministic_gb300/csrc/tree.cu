@@ -12,11 +12,16 @@
 namespace kinv {
 namespace {
 
-// A block per (node, heads of its row, sequence): the node's position from its
-// depth, the rotation's angles in fp64, then one head per warp with the code
+// A block per (node, heads of its row, sequence), a warp per head in turn.  A
+// warp requests its first kRopeAhead heads before anything else is known of the
+// tree than the node's row; meanwhile one warp finds the node's depth and then
+// D/2 threads form the rotation's angles in fp64; the heads go through the code
 // of kinv_rope_append.
+constexpr int kRopeThreads = 256;
+constexpr int kRopeAhead = 6;
+
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kRopeThreads)
     rope_append_tree_kernel(const __nv_bfloat16* __restrict__ qkv, int64_t ld_qkv,
                             __nv_bfloat16* __restrict__ q_out, __nv_bfloat16* __restrict__ k_cache,
                             __nv_bfloat16* __restrict__ v_cache, int64_t seq_stride, int64_t tok_stride,
@@ -24,46 +29,86 @@ __global__ void __launch_bounds__(256)
                             const __nv_bfloat16* __restrict__ k_norm, float eps, int Hq, int Hkv,
                             int heads_per_block, int* status, const RopeFreqs freqs) {
   constexpr int HALF = D / 2;
-  constexpr int P = D / 64;
+  constexpr int P = D / 64;  // pairs per lane
+  constexpr int WARPS = kRopeThreads / 32;
   __shared__ TreeInfo ti;
   __shared__ float cs[HALF], sn[HALF];
   pdl_launch_dependents();
   pdl_wait();
   const int node = blockIdx.x, b = blockIdx.z;
-  if (threadIdx.x < 32) tree_load(tree, b, ti);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int n, ctx, off;
+  if (!tree_bounds(tree, b, n, ctx, off)) {
+    if (threadIdx.x == 0 && node == 0 && blockIdx.y == 0 && status) atomicExch(status, DEV_TREE_BAD);
+    return;
+  }
+  if (node >= n) return;
+  const int64_t r = off + node;
+  const __nv_bfloat16* row = qkv + r * ld_qkv;
+  const int64_t slot = b * seq_stride + static_cast<int64_t>(ctx + node) * tok_stride;
+  const int heads = Hq + 2 * Hkv;
+  const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per_block);
+  // a lane's P values of each half of a head (for a value head likewise: D bits copied)
+  uint32_t lo[kRopeAhead], hi[kRopeAhead];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kRopeAhead; ++i) {
+      const int h = h0 + i * WARPS;
+      if (h >= h_end) continue;
+      const __nv_bfloat16* src = row + h * D + lane * P;
+      if (P == 2) {
+        lo[i] = *reinterpret_cast<const uint32_t*>(src);
+        hi[i] = *reinterpret_cast<const uint32_t*>(src + HALF);
+      } else {
+        lo[i] = *reinterpret_cast<const uint16_t*>(src);
+        hi[i] = *reinterpret_cast<const uint16_t*>(src + HALF);
+      }
+    }
+  };
+  int h0 = blockIdx.y * heads_per_block + warp;
+  load(h0);
+  if (warp == 0) tree_load(tree, b, ti);
   __syncthreads();
   if (!ti.ok) {
     if (threadIdx.x == 0 && node == 0 && blockIdx.y == 0 && status) atomicExch(status, DEV_TREE_BAD);
     return;
   }
-  if (node >= ti.n) return;
-  const int p = ti.ctx + __popcll(ti.mask[node]) - 1;
-  const int64_t r = ti.off + node;
-  for (int i = threadIdx.x; i < HALF; i += blockDim.x) rope_angle(p, freqs.inv_freq[i], cs[i], sn[i]);
+  const int p = ctx + __popcll(ti.mask[node]) - 1;
+  if (threadIdx.x < HALF) rope_angle(p, freqs.inv_freq[threadIdx.x], cs[threadIdx.x], sn[threadIdx.x]);
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  const __nv_bfloat16* row = qkv + r * ld_qkv;
-  const int64_t slot = b * seq_stride + static_cast<int64_t>(ti.ctx + node) * tok_stride;
-  const int heads = Hq + 2 * Hkv;
-  const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per_block);
-  for (int h = blockIdx.y * heads_per_block + warp; h < h_end; h += nwarps) {
-    const __nv_bfloat16* src = row + h * D;
-    if (h >= Hq + Hkv) {  // value head: copy bits
-      const int g = h - Hq - Hkv;
-      for (int c = lane; c < D / 8; c += 32)
-        reinterpret_cast<uint4*>(v_cache + slot + g * D)[c] = reinterpret_cast<const uint4*>(src)[c];
-      continue;
-    }
-    float a[P], bb[P], c[P], sv[P];
+  float c[P], sv[P];
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      a[j] = __bfloat162float(src[lane * P + j]);
-      bb[j] = __bfloat162float(src[HALF + lane * P + j]);
-      c[j] = cs[lane * P + j];
-      sv[j] = sn[lane * P + j];
+  for (int j = 0; j < P; ++j) {
+    c[j] = cs[lane * P + j];
+    sv[j] = sn[lane * P + j];
+  }
+  for (; h0 < h_end; h0 += kRopeAhead * WARPS) {
+#pragma unroll
+    for (int i = 0; i < kRopeAhead; ++i) {
+      const int h = h0 + i * WARPS;
+      if (h >= h_end) continue;
+      if (h >= Hq + Hkv) {
+        __nv_bfloat16* dst = v_cache + slot + (h - Hq - Hkv) * D + lane * P;
+        if (P == 2) {
+          *reinterpret_cast<uint32_t*>(dst) = lo[i];
+          *reinterpret_cast<uint32_t*>(dst + HALF) = hi[i];
+        } else {
+          *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(lo[i]);
+          *reinterpret_cast<uint16_t*>(dst + HALF) = static_cast<uint16_t>(hi[i]);
+        }
+        continue;
+      }
+      float a[P], bb[P];
+      a[0] = bf16_lo(lo[i]);
+      bb[0] = bf16_lo(hi[i]);
+      if (P == 2) {
+        a[P - 1] = bf16_hi(lo[i]);
+        bb[P - 1] = bf16_hi(hi[i]);
+      }
+      __nv_bfloat16* dst = h < Hq ? q_out + (r * Hq + h) * D : k_cache + slot + (h - Hq) * D;
+      rope_norm_rotate<D>(a, bb, c, sv, h < Hq ? q_norm : k_norm, eps, lane, dst);
     }
-    __nv_bfloat16* dst = h < Hq ? q_out + (r * Hq + h) * D : k_cache + slot + (h - Hq) * D;
-    rope_norm_rotate<D>(a, bb, c, sv, h < Hq ? q_norm : k_norm, eps, lane, dst);
+    load(h0 + kRopeAhead * WARPS);
   }
 }
 
@@ -182,8 +227,18 @@ extern "C" kinv_status kinv_rope_append_tree(const void* qkv, int64_t ld_qkv, vo
   if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || ld_qkv % 8 ||
       seq_stride % 8 || tok_stride % 8)
     return KINV_ERR_ALIGNMENT;
-  RopeFreqs freqs;
-  for (int i = 0; i < D / 2; ++i) freqs.inv_freq[i] = std::pow(static_cast<double>(rope_base), -2.0 * i / D);
+  // the frequencies of the last base and head size this thread used
+  static thread_local struct {
+    float base;
+    int D;
+    RopeFreqs f;
+  } last = {0.f, 0, {}};
+  if (last.base != rope_base || last.D != D) {
+    for (int i = 0; i < D / 2; ++i) last.f.inv_freq[i] = std::pow(static_cast<double>(rope_base), -2.0 * i / D);
+    last.base = rope_base;
+    last.D = D;
+  }
+  const RopeFreqs& freqs = last.f;
   const int heads = Hq + 2 * Hkv;
   const int hpb = tree->total_rows >= 512 ? heads : 8;
   const dim3 grid(tree->max_nodes, (heads + hpb - 1) / hpb, tree->B);
@@ -195,7 +250,7 @@ extern "C" kinv_status kinv_rope_append_tree(const void* qkv, int64_t ld_qkv, vo
   auto* qn = static_cast<const __nv_bfloat16*>(q_norm);
   auto* kn = static_cast<const __nv_bfloat16*>(k_norm);
   auto* kernel = D == 128 ? rope_append_tree_kernel<128> : rope_append_tree_kernel<64>;
-  return launch_kernel(kernel, grid, dim3(256), 0, stream, 1, src, ld_qkv, qo, k, v, seq_stride, tok_stride,
+  return launch_kernel(kernel, grid, dim3(kRopeThreads), 0, stream, 1, src, ld_qkv, qo, k, v, seq_stride, tok_stride,
                        *tree, qn, kn, eps, Hq, Hkv, hpb, status, freqs);
 }
 
