@@ -36,8 +36,11 @@ struct TreeAttnParams {
   const __nv_bfloat16* v;
   int64_t seq_stride, tok_stride;
   __nv_bfloat16* out;
-  float* ws_o;   // [total_rows][Hq][S][D]
-  float* ws_ml;  // [total_rows][Hq][S][2]
+  // partials, GP = total_rows * G pairs (row, head of the group) of a kv head side
+  // by side, so that a warp's stores and loads of 32 pairs are contiguous
+  float* ws_o;   // [Hkv][S][D / 8][GP][8]
+  float* ws_ml;  // [Hkv][S][GP][2]
+  int64_t GP;
   int Hq, Hkv, G, gs;  // G = Hq / Hkv = 1 << gs
   int S;         // splits per row in the workspace
   float c2;      // fp32(scale * log2 e) > 0
@@ -369,18 +372,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
     for (int h = 0; h < 2; ++h) {
       if (cnt[mt][h] <= 0) continue;
       const int pair = mt * 16 + h * 8 + gq;
-      const int64_t base =
-          (static_cast<int64_t>(off + n0 + (pair >> gs)) * p.Hq + (g << gs) + (pair & ((1 << gs) - 1))) * p.S + s;
+      const int64_t gs_at = static_cast<int64_t>(g) * p.S + s;
+      const int64_t gp = (static_cast<int64_t>(off + n0) << gs) + pair;
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb)
-        *reinterpret_cast<float2*>(p.ws_o + base * D + warp * 16 + nb * 8 + 2 * tq) =
+        *reinterpret_cast<float2*>(p.ws_o + ((gs_at * (D / 8) + 2 * warp + nb) * p.GP + gp) * 8 + 2 * tq) =
             make_float2(oc[mt][nb][2 * h], oc[mt][nb][2 * h + 1]);
       if (warp == 0 && tq == 0) {
         float l = wsum[0][pair];
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w) l = __fadd_rn(l, wsum[w][pair]);
-        p.ws_ml[base * 2 + 0] = m[mt][h];
-        p.ws_ml[base * 2 + 1] = l;
+        *reinterpret_cast<float2*>(p.ws_ml + (gs_at * p.GP + gp) * 2) = make_float2(m[mt][h], l);
       }
     }
 }
@@ -423,7 +425,7 @@ __device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, UnitCurs
   c.splits = c.pairs = 0;
   if (!tree_bounds(p.tree, c.b, c.n, c.ctx, c.off)) return 0;
   c.splits = c.ctx / kSplit;
-  c.pairs = (c.n * p.G + kTcTiles * kTcPairs - 1) / (kTcTiles * kTcPairs);
+  c.pairs = ((c.n << p.gs) + kTcTiles * kTcPairs - 1) / (kTcTiles * kTcPairs);
   return static_cast<int64_t>(p.Hkv) * c.pairs * c.splits;
 }
 __device__ __forceinline__ void cursor_next(const TreeAttnParams& p, UnitCursor& c) {
@@ -437,7 +439,7 @@ __device__ __forceinline__ void cursor_next(const TreeAttnParams& p, UnitCursor&
   }
 }
 __device__ __forceinline__ int cursor_tiles(const TreeAttnParams& p, const UnitCursor& c) {
-  return min(kTcTiles, (c.n * p.G + kTcPairs - 1) / kTcPairs - c.tp * kTcTiles);
+  return min(kTcTiles, ((c.n << p.gs) + kTcPairs - 1) / kTcPairs - c.tp * kTcTiles);
 }
 
 // This block's run of units, by one warp: cursor at its first and its length.
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < tiles; ++i)
           for (int ds = 0; ds < DS; ++ds)
             tma_load_3d(smem_addr(q_s + i * Q_BYTES + ds * Q_SLICE), &tmQ, 64 * ds, c.g * p.G,
-                        c.off + (c.tp * kTcTiles + i) * (kTcPairs / p.G), k_full, q_pol);
+                        c.off + ((c.tp * kTcTiles + i) * kTcPairs >> p.gs), k_full, q_pol);
         for (int ds = 0; ds < DS; ++ds)
           tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full, kv_pol);
       };
@@ -691,7 +693,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_ld32(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
         if (live) {
 #pragma unroll
-          for (int d = 0; d < DQ; d += 8) st_global_v8(p.ws_o + at * D + j * DQ + d, v + d);
+          for (int d = 0; d < DQ; d += 8) st_global_v8(p.ws_o + (at + (j * DQ + d) / 8 * p.GP) * 8, v + d);
         }
       }
       tc_fence_before();
@@ -704,9 +706,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int tiles = cursor_tiles(p, c);
       for (int tile = 0; tile < tiles; ++tile, ++i) {
         const int pair = (c.tp * kTcTiles + tile) * kTcPairs + pr;
-        const int node = pair / p.G;
-        const bool live = node < c.n;
-        const int64_t at = (static_cast<int64_t>(c.off + node) * p.Hq + c.g * p.G + pair % p.G) * p.S + c.s;
+        const bool live = pair < c.n << p.gs;
+        const int64_t gs_at = static_cast<int64_t>(c.g) * p.S + c.s, gp = (static_cast<int64_t>(c.off) << p.gs) + pair;
+        const int64_t at = gs_at * (D / 8) * p.GP + gp;
         const bool any = __any_sync(0xffffffffu, live);  // the same for the quadrant's four warps
         check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
         tc_fence_after();
@@ -765,7 +767,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float l = x_sum[pr];
 #pragma unroll
           for (int q = 1; q < 8; ++q) l = __fadd_rn(l, x_sum[q * kTcPairs + pr]);
-          *reinterpret_cast<float2*>(p.ws_ml + at * 2) = make_float2(m, l);
+          *reinterpret_cast<float2*>(p.ws_ml + (gs_at * p.GP + gp) * 2) = make_float2(m, l);
         }
         at_prev = at;
         live_prev = live;
@@ -782,52 +784,48 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// A warp per (node, query head): a lane folds D/32 columns over the splits the
-// node sees, with the decode merge's arithmetic.  The first partials are
-// requested before the tree is read: a node of any depth sees the splits up to
-// position ctx_len.
-constexpr int kMergeWarps = 8;
+// Folds the splits that each node sees, with the decode merge's arithmetic.  A
+// block takes 16 pairs of a (sequence, kv head), warp k their columns 8k .. 8k +
+// 7: a lane half of them for one pair, so a warp's loads of a split are 512
+// contiguous bytes.  The first partials are requested before the tree is read: a
+// node of any depth sees the splits up to position ctx_len.
+constexpr int kMergePairs = 16;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) attn_tree_merge_kernel(const TreeAttnParams p) {
-  constexpr int W = D / 32;  // columns of a lane
-  constexpr int CH = 8;      // partials loaded ahead of the (sequential) fold
+__global__ void __launch_bounds__(4 * D) attn_tree_merge_kernel(const TreeAttnParams p) {
+  constexpr int CH = 8;  // partials loaded ahead of the (sequential) fold
   __shared__ TreeInfo ti;
   pdl_launch_dependents();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x * kMergeWarps + warp, node = blockIdx.y, b = blockIdx.z;
+  const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int pair = blockIdx.x * kMergePairs + (lane >> 1);
   int n, ctx, off;
-  if (!tree_bounds(p.tree, b, n, ctx, off) || node >= n) return;
-  const bool mine = h < p.Hq;
-  const int64_t row = off + node;
-  const int64_t base = (row * p.Hq + (mine ? h : 0)) * p.S;
+  if (!tree_bounds(p.tree, b, n, ctx, off) || static_cast<int>(blockIdx.x) * kMergePairs >= n << p.gs) return;
+  const bool live = pair < n << p.gs;
+  const int64_t gp = (static_cast<int64_t>(off) << p.gs) + (live ? pair : 0);
+  const float* ml_at = p.ws_ml + (static_cast<int64_t>(g) * p.S * p.GP + gp) * 2;
+  const float* o_at = p.ws_o + ((static_cast<int64_t>(g) * p.S * (D / 8) + k) * p.GP + gp) * 8 + (lane & 1) * 4;
+  const int64_t ml_step = p.GP * 2, o_step = p.GP * D;
   float2 ml[CH];
-  float o[CH][W];
+  float4 o[CH];
   auto load = [&](int s0, int ns) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (s0 + i >= ns) continue;
-      ml[i] = *reinterpret_cast<const float2*>(p.ws_ml + (base + s0 + i) * 2);
-      const float* src = p.ws_o + (base + s0 + i) * D + lane * W;
-      if (W == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        o[i][0] = v.x, o[i][1] = v.y, o[i][2 % W] = v.z, o[i][3 % W] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        o[i][0] = v.x, o[i][1] = v.y;
-      }
+      ml[i] = *reinterpret_cast<const float2*>(ml_at + (s0 + i) * ml_step);
+      o[i] = *reinterpret_cast<const float4*>(o_at + (s0 + i) * o_step);
     }
   };
   const int sure = ctx / kSplit + 1;  // splits that every node sees
   load(0, sure);
-  if (warp == 0) tree_load(p.tree, b, ti);
+  if (k == 0) tree_load(p.tree, b, ti);
   __syncthreads();
-  if (!ti.ok || !mine) return;
+  if (!ti.ok || !live) return;
+  const int node = pair >> p.gs;
   const int ns = (ctx + __popcll(ti.mask[node]) + kSplit - 1) / kSplit;
-  float m_acc = -INFINITY, l_acc = 0.f, o_acc[W];
-#pragma unroll
-  for (int w = 0; w < W; ++w) o_acc[w] = 0.f;
+  float m_acc = -INFINITY, l_acc = 0.f;
+  float4 o_acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < ns; s0 += CH) {
     if (s0 > 0 || (sure < CH && ns > sure)) load(s0, ns);
 #pragma unroll
@@ -837,20 +835,18 @@ __global__ void __launch_bounds__(32 * kMergeWarps) attn_tree_merge_kernel(const
         const float a = ex2_approx(__fsub_rn(m_acc, m_new));
         const float c = ex2_approx(__fsub_rn(ml[i].x, m_new));
         l_acc = __fadd_rn(__fmul_rn(l_acc, a), __fmul_rn(ml[i].y, c));
-#pragma unroll
-        for (int w = 0; w < W; ++w) o_acc[w] = __fadd_rn(__fmul_rn(o_acc[w], a), __fmul_rn(o[i][w], c));
+        o_acc.x = __fadd_rn(__fmul_rn(o_acc.x, a), __fmul_rn(o[i].x, c));
+        o_acc.y = __fadd_rn(__fmul_rn(o_acc.y, a), __fmul_rn(o[i].y, c));
+        o_acc.z = __fadd_rn(__fmul_rn(o_acc.z, a), __fmul_rn(o[i].z, c));
+        o_acc.w = __fadd_rn(__fmul_rn(o_acc.w, a), __fmul_rn(o[i].w, c));
         m_acc = m_new;
       }
     }
   }
-  __nv_bfloat16* dst = p.out + (row * p.Hq + h) * D + lane * W;
-  uint32_t packed[2];
-#pragma unroll
-  for (int w = 0; w < W; w += 2) packed[w / 2] = pack_bf16(__fdiv_rn(o_acc[w], l_acc), __fdiv_rn(o_acc[w + 1], l_acc));
-  if (W == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = packed[0];
+  const int64_t head = static_cast<int64_t>(off + node) * p.Hq + (g << p.gs) + (pair & ((1 << p.gs) - 1));
+  *reinterpret_cast<uint2*>(p.out + head * D + 8 * k + (lane & 1) * 4) =
+      make_uint2(pack_bf16(__fdiv_rn(o_acc.x, l_acc), __fdiv_rn(o_acc.y, l_acc)),
+                 pack_bf16(__fdiv_rn(o_acc.z, l_acc), __fdiv_rn(o_acc.w, l_acc)));
 }
 
 template <int D, int MT>
@@ -908,8 +904,8 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
     st = launch_kernel(kernel, dim3(sms), dim3(kTcThreads), smem, stream, 1, mq, mk, mv, p);
     if (st != KINV_OK) return st;
   }
-  return launch_kernel(attn_tree_merge_kernel<D>, dim3((p.Hq + kMergeWarps - 1) / kMergeWarps, p.tree.max_nodes, p.tree.B),
-                       dim3(32 * kMergeWarps), 0, stream, 1, p);
+  return launch_kernel(attn_tree_merge_kernel<D>, dim3((pairs + kMergePairs - 1) / kMergePairs, p.Hkv, p.tree.B),
+                       dim3(4 * D), 0, stream, 1, p);
 }
 
 size_t tree_workspace_bytes(int64_t rows, int Hq, int D, int S) {
@@ -966,6 +962,7 @@ extern "C" kinv_status kinv_attn_tree(const void* q, const void* k_cache, const 
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = G;
+  p.GP = static_cast<int64_t>(tree->total_rows) * G;
   p.gs = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
   p.S = static_cast<int>(S);
   p.c2 = base2_factor(scale, D);
