@@ -392,61 +392,65 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
 // pairs of one (sequence, kv head) against 256 keys, the arithmetic of the
 // prefill kernel without a mask, each split's (m, l, o) stored as a partial.
 //
-// A unit is (sequence, kv head, up to two tiles of 128 pairs, split); the
-// tiles of a unit share its K and V in shared memory.  The units of all
-// sequences, splits fastest, are dealt to the blocks (one per SM) in equal
-// runs, counted on the device from the trees' own numbers.
+// A step is (sequence, kv head, split, tile of 128 pairs).  The steps of all
+// sequences, tiles fastest (a split's further tiles find its K and V in L2),
+// then splits, are dealt to the blocks (one per SM) in equal runs, counted on
+// the device from the trees' own numbers.
 // Roles (18 warps): warps 0-15 take the softmax, four threads per pair: warp w
 // holds TMEM lanes 32 (w % 4) .. + 31 (lane = pair) and keys 64 (w / 4) ..
 // + 63 of each split, so a tile's softmax is four warps deep on every
-// scheduler; the four exchange raw maxima and 32-key group
-// sums through shared memory, in the decode kernel's order.  Warp 16 lane 0
-// issues the MMAs, warp 17 lane 0 the TMA loads.
+// scheduler; the four exchange raw maxima and 32-key group sums through shared
+// memory, in the decode kernel's order.  Warp 16 lane 0 issues the MMAs, warp 17
+// lane 0 the TMA loads.
 // Tensor memory: scores R in columns 0-255, overwritten chunk by chunk with P
 // (64-key chunk j: 32-key group h as packed bf16 pairs, hi at 64 j + 32 h, lo
 // 16 columns further), O in two buffers of D columns after it.  The MMAs run
 // in issue order: step i + 1's scores of keys 128 h .. follow step i's P.V of
 // chunks 2h and 2h + 1, which read the P that they overwrite; the softmax
 // threads store step i - 1's O while step i's P.V runs.
+// The partials leave through shared memory and bulk copies: stored straight from
+// registers they held up every other shared-memory access of the SM for about
+// 2,500 cycles a step (21 - 25 bytes a cycle).
 constexpr int kTcSoftmax = 512;  // 16 warps
 constexpr int kTcThreads = kTcSoftmax + 64;
 constexpr int kTcPairs = 128;
-constexpr int kTcTiles = 2;      // tiles of a unit
 constexpr int kTcBars = 15;
+constexpr int kStageSlots = 3;   // 1 KB chunks (32 pairs x 8 columns) a warp stages
 
-struct UnitCursor {
-  int b, g, tp, s;         // sequence, kv head, tile pair, split
-  int n, ctx, off;         // of the sequence
-  int splits, pairs;       // splits within the context, tile pairs
+struct StepCursor {
+  int b, g, s, tile;
+  int ctx, off;            // of the sequence
+  int pairs, splits, tiles;
 };
 
-// Sequence c.b's numbers; returns its units.
-__device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, UnitCursor& c) {
-  c.splits = c.pairs = 0;
-  if (!tree_bounds(p.tree, c.b, c.n, c.ctx, c.off)) return 0;
+// Sequence c.b's numbers; returns its steps.
+__device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, StepCursor& c) {
+  int n;
+  c.splits = c.tiles = 0;
+  if (!tree_bounds(p.tree, c.b, n, c.ctx, c.off)) return 0;
+  c.pairs = n << p.gs;
   c.splits = c.ctx / kSplit;
-  c.pairs = ((c.n << p.gs) + kTcTiles * kTcPairs - 1) / (kTcTiles * kTcPairs);
-  return static_cast<int64_t>(p.Hkv) * c.pairs * c.splits;
+  c.tiles = (c.pairs + kTcPairs - 1) / kTcPairs;
+  return static_cast<int64_t>(p.Hkv) * c.splits * c.tiles;
 }
-__device__ __forceinline__ void cursor_next(const TreeAttnParams& p, UnitCursor& c) {
-  if (++c.s < c.splits) return;
+// The next step; whether it begins another (sequence, kv head).
+__device__ __forceinline__ bool cursor_next(const TreeAttnParams& p, StepCursor& c) {
+  if (++c.tile < c.tiles) return false;
+  c.tile = 0;
+  if (++c.s < c.splits) return false;
   c.s = 0;
-  if (++c.tp < c.pairs) return;
-  c.tp = 0;
-  if (++c.g < p.Hkv) return;
+  if (++c.g < p.Hkv) return true;
   c.g = 0;
   while (++c.b < p.tree.B && cursor_load(p, c) == 0) {
   }
-}
-__device__ __forceinline__ int cursor_tiles(const TreeAttnParams& p, const UnitCursor& c) {
-  return min(kTcTiles, ((c.n << p.gs) + kTcPairs - 1) / kTcPairs - c.tp * kTcTiles);
+  return true;
 }
 
-// This block's run of units, by one warp: cursor at its first and its length.
-__device__ __forceinline__ void cursor_start(const TreeAttnParams& p, UnitCursor& out, int& count) {
+// This block's run of steps, by one warp: cursor at its first and its length.
+__device__ __forceinline__ void cursor_start(const TreeAttnParams& p, StepCursor& out, int& count) {
   const int lane = threadIdx.x & 31;
   int64_t total = 0;
-  UnitCursor c;
+  StepCursor c;
   for (c.b = lane; c.b < p.tree.B; c.b += 32) total += cursor_load(p, c);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -466,9 +470,9 @@ __device__ __forceinline__ void cursor_start(const TreeAttnParams& p, UnitCursor
     const bool here = before + incl - mine <= u0 && u0 < before + incl;
     if (here) {
       const int64_t u = u0 - (before + incl - mine);
-      c.s = static_cast<int>(u % c.splits);
-      c.tp = static_cast<int>(u / c.splits % c.pairs);
-      c.g = static_cast<int>(u / c.splits / c.pairs);
+      c.tile = static_cast<int>(u % c.tiles);
+      c.s = static_cast<int>(u / c.tiles % c.splits);
+      c.g = static_cast<int>(u / c.tiles / c.splits);
       out = c;
     }
     if (__any_sync(0xffffffffu, here)) return;
@@ -476,12 +480,18 @@ __device__ __forceinline__ void cursor_start(const TreeAttnParams& p, UnitCursor
   }
 }
 
-// 32 bytes to global memory in one store (a whole sector).
-__device__ __forceinline__ void st_global_v8(float* dst, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// An asynchronous copy of `bytes` (a multiple of 16) from shared to global
+// memory, in this thread's current bulk group.
+__device__ __forceinline__ void bulk_store(float* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's latest groups still read their source.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -496,15 +506,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  unsigned char* q_s = base;                         // kTcTiles tiles
-  unsigned char* k_s = q_s + kTcTiles * Q_BYTES;
+  unsigned char* q_s = base;
+  unsigned char* k_s = q_s + Q_BYTES;
   unsigned char* v_s = k_s + KV_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(v_s + KV_BYTES);
+  unsigned char* stage = v_s + KV_BYTES;    // [16 warps][kStageSlots][32 pairs][8] fp32
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 16 * kStageSlots * 1024);
   float* x_max = reinterpret_cast<float*>(bars + kTcBars + 1);  // [4][128] raw maxima
   float* x_sum = x_max + 4 * kTcPairs;                          // [8][128] 32-key group sums
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ UnitCursor start;
+  __shared__ StepCursor start;
   __shared__ int count_s;
   const uint32_t k_full = smem_addr(bars + 0), k_empty = smem_addr(bars + 1);
   const uint32_t v_full = smem_addr(bars + 2), v_empty = smem_addr(bars + 3);
@@ -523,7 +534,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_launch_dependents();
     return;
   }
-  UnitCursor c = start;
   if (t == 0) {
     for (int i = 0; i < kTcBars; ++i) {
       // p_full: the 128 threads of its chunk; o_empty: every softmax thread
@@ -542,35 +552,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int* status = p.status;
 
   if (warp == 17) {
-    // ---- TMA: K (with the Q tiles of a new group) of unit u + 1 as soon as
-    // unit u's score MMAs are done, its V as soon as unit u's P.V MMAs are done
+    // ---- TMA: K of step i + 1 (with its Q, where that is another) as soon as
+    // step i's score MMAs are done, its V as soon as step i's P.V MMAs are done
     if (lane == 0) {
-      const uint64_t q_pol = l2_policy_evict_last(), kv_pol = l2_policy_evict_first();
-      auto load_k = [&](bool group) {
-        const int tiles = group ? cursor_tiles(p, c) : 0;
-        mbar_arrive_expect_tx(k_full, KV_BYTES + tiles * Q_BYTES);
-        for (int i = 0; i < tiles; ++i)
+      StepCursor c = start;
+      const uint64_t q_pol = l2_policy_evict_last();
+      // a split that several tiles read stays in L2 until the last of them
+      const uint64_t first_pol = l2_policy_evict_first();
+      auto load_k = [&](bool new_q) {
+        mbar_arrive_expect_tx(k_full, KV_BYTES + (new_q ? Q_BYTES : 0));
+        if (new_q)
           for (int ds = 0; ds < DS; ++ds)
-            tma_load_3d(smem_addr(q_s + i * Q_BYTES + ds * Q_SLICE), &tmQ, 64 * ds, c.g * p.G,
-                        c.off + ((c.tp * kTcTiles + i) * kTcPairs >> p.gs), k_full, q_pol);
+            tma_load_3d(smem_addr(q_s + ds * Q_SLICE), &tmQ, 64 * ds, c.g << p.gs, c.off + (c.tile * kTcPairs >> p.gs),
+                        k_full, q_pol);
+        const uint64_t pol = c.tile + 1 < c.tiles ? q_pol : first_pol;
         for (int ds = 0; ds < DS; ++ds)
-          tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full, kv_pol);
+          tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full, pol);
       };
       auto load_v = [&]() {
         mbar_arrive_expect_tx(v_full, KV_BYTES);
+        const uint64_t pol = c.tile + 1 < c.tiles ? q_pol : first_pol;
         for (int ds = 0; ds < DS; ++ds)
-          tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, c.g, c.s * kSplit, c.b, v_full, kv_pol);
+          tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, c.g, c.s * kSplit, c.b, v_full, pol);
       };
       load_k(true);
       load_v();
       int k_issued = 1, v_issued = 1;
-      for (int u = 0; u + 1 < count; ++u) {
-        cursor_next(p, c);
-        bool ok = !abort_flag && mbar_wait_bounded(k_empty, u & 1, status, DEV_TIMEOUT_ATTN);
+      for (int i = 0; i + 1 < count; ++i) {
+        const bool new_q = cursor_next(p, c) || c.tiles > 1;
+        bool ok = !abort_flag && mbar_wait_bounded(k_empty, i & 1, status, DEV_TIMEOUT_ATTN);
         if (ok) {
-          load_k(c.s == 0);
+          load_k(new_q);
           ++k_issued;
-          ok = !abort_flag && mbar_wait_bounded(v_empty, u & 1, status, DEV_TIMEOUT_ATTN);
+          ok = !abort_flag && mbar_wait_bounded(v_empty, i & 1, status, DEV_TIMEOUT_ATTN);
         }
         if (!ok) {
           abort_flag = 1;
@@ -585,74 +599,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     __syncwarp();
   } else if (warp == 16) {
-    // ---- MMA issue: a step is (unit, tile); each iteration issues the last
-    // step's P.V and this step's scores, interleaved
+    // ---- MMA issue: iteration i issues step i - 1's P.V chunks and step i's
+    // scores, interleaved
     if (lane == 0) {
       constexpr uint32_t idesc_r = tc_idesc(128, 0);
       constexpr uint32_t idesc_o = tc_idesc(D, 1);
       const uint64_t qd = desc_k_sw128(smem_addr(q_s)), kd = desc_k_sw128(smem_addr(k_s));
       const uint64_t vd = desc_mn_sw128(smem_addr(v_s), KV_SLICE);
-      bool ok = true, has_pv = false;
-      int i = 0;                       // steps whose scores were issued
-      int pv_unit = 0;                 // the last step's unit, and its place there
-      bool pv_first = false, pv_last = false;
-      for (int u = 0; u <= count && ok; ++u) {
-        const int tiles = u < count ? cursor_tiles(p, c) : 1;
-        for (int tile = 0; tile < tiles && ok; ++tile) {
-          const bool has_r = u < count;
-          const uint32_t ob = (i - 1) & 1, ph = (i - 1) & 1;  // of the last step
+      bool ok = true;
+      for (int i = 0; i <= count && ok; ++i) {
+        const bool has_r = i < count, has_pv = i > 0;
+        const uint32_t ob = (i - 1) & 1;  // the last step's O buffer, and its barriers' phase
+        if (has_pv)
+          ok = !abort_flag && mbar_wait_bounded(v_full, ob, status, DEV_TIMEOUT_ATTN) &&
+               mbar_wait_bounded(o_empty(ob), (((i - 1) >> 1) & 1) ^ 1, status, DEV_TIMEOUT_ATTN);
+        if (ok && has_r) ok = !abort_flag && mbar_wait_bounded(k_full, i & 1, status, DEV_TIMEOUT_ATTN);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t o_col = tmem + 256 + ob * D;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
           if (has_pv) {
-            if (pv_first) ok = mbar_wait_bounded(v_full, pv_unit & 1, status, DEV_TIMEOUT_ATTN);
-            ok = ok && !abort_flag &&
-                 mbar_wait_bounded(o_empty(ob), (((i - 1) >> 1) & 1) ^ 1, status, DEV_TIMEOUT_ATTN);
-          }
-          if (ok && has_r && tile == 0) ok = !abort_flag && mbar_wait_bounded(k_full, u & 1, status, DEV_TIMEOUT_ATTN);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t o_col = tmem + 256 + ob * D;
+            ok = !abort_flag && mbar_wait_bounded(p_full(j), ob, status, DEV_TIMEOUT_ATTN);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (has_pv) {
-              ok = !abort_flag && mbar_wait_bounded(p_full(j), ph, status, DEV_TIMEOUT_ATTN);
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t vdesc = vd + static_cast<uint64_t>(((4 * j + kk) * 2048) >> 4);
-                const uint32_t p_hi = tmem + static_cast<uint32_t>(64 * j + 32 * (kk >> 1) + 8 * (kk & 1));
-                umma_bf16_tmem_a(o_col, p_hi, vdesc, idesc_o, (j | kk) != 0 ? 1u : 0u);
-                umma_bf16_tmem_a(o_col, p_hi + 16, vdesc, idesc_o, 1u);
-              }
-            }
-            if (has_r && (j & 1)) {
-              const int h = j >> 1;
-              const uint64_t qt = qd + static_cast<uint64_t>(tile * Q_BYTES >> 4);
-#pragma unroll
-              for (int ds = 0; ds < DS; ++ds)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16(tmem + static_cast<uint32_t>(128 * h),
-                            qt + static_cast<uint64_t>((ds * Q_SLICE + kk * 32) >> 4),
-                            kd + static_cast<uint64_t>((ds * KV_SLICE + h * 128 * 128 + kk * 32) >> 4), idesc_r,
-                            (ds | kk) != 0 ? 1u : 0u);
-              umma_commit(s_full(h));
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t vdesc = vd + static_cast<uint64_t>(((4 * j + kk) * 2048) >> 4);
+              const uint32_t p_hi = tmem + static_cast<uint32_t>(64 * j + 32 * (kk >> 1) + 8 * (kk & 1));
+              umma_bf16_tmem_a(o_col, p_hi, vdesc, idesc_o, (j | kk) != 0 ? 1u : 0u);
+              umma_bf16_tmem_a(o_col, p_hi + 16, vdesc, idesc_o, 1u);
             }
           }
-          if (!ok) break;
-          if (has_pv) {
-            if (pv_last) umma_commit(v_empty);
-            umma_commit(o_full(ob));
-          }
-          if (has_r) {
-            if (tile == tiles - 1) umma_commit(k_empty);
-            has_pv = true;
-            pv_unit = u;
-            pv_first = tile == 0;
-            pv_last = tile == tiles - 1;
-            ++i;
+          if (has_r && (j & 1)) {
+            const int h = j >> 1;
+#pragma unroll
+            for (int ds = 0; ds < DS; ++ds)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_bf16(tmem + static_cast<uint32_t>(128 * h), qd + static_cast<uint64_t>((ds * Q_SLICE + kk * 32) >> 4),
+                          kd + static_cast<uint64_t>((ds * KV_SLICE + h * 128 * 128 + kk * 32) >> 4), idesc_r,
+                          (ds | kk) != 0 ? 1u : 0u);
+            umma_commit(s_full(h));
           }
         }
-        if (u < count) cursor_next(p, c);
+        if (!ok) break;
+        if (has_pv) {
+          umma_commit(v_empty);
+          umma_commit(o_full(ob));
+        }
+        if (has_r) umma_commit(k_empty);
       }
       if (!ok) abort_flag = 1;
       umma_commit(done_bar);
@@ -664,6 +660,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int quad = warp & 3, j = warp >> 2;  // lanes 32 quad .., keys 64 j .. and output columns D/4 j ..
     const int pr = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t slots = smem_addr(stage) + warp * kStageSlots * 1024;
     const float c2 = p.c2;
     bool ok = true;
     auto quad_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory"); };
@@ -684,97 +681,117 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = false;
       }
     };
-    // stores this thread's D/4 columns of step i's O as the partial at `at`
-    auto store_o = [&](int i, int64_t at, bool live) {
+    // sends this warp's D/4 columns of step i's O, `live` pairs from the
+    // warp's first, to the partial at `at` (the warp's first pair)
+    auto store_o = [&](int i, int64_t at, int live) {
       check(mbar_wait_bounded(o_full(i & 1), (i >> 1) & 1, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
-      if (__any_sync(0xffffffffu, live)) {
+      if (live > 0) {
         uint32_t v[32];
         tmem_ld32(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
-        if (live) {
+        // as many chunks at a time as there are slots
 #pragma unroll
-          for (int d = 0; d < DQ; d += 8) st_global_v8(p.ws_o + (at + (j * DQ + d) / 8 * p.GP) * 8, v + d);
+        for (int k0 = 0; k0 < DQ / 8; k0 += kStageSlots) {
+          if (lane == 0) bulk_wait_read<0>();  // the slots' last copies have read them
+          __syncwarp();
+#pragma unroll
+          for (int k = k0; k < DQ / 8 && k < k0 + kStageSlots; ++k) {
+            const uint32_t slot = slots + (k - k0) * 1024 + lane * 32;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot), "r"(v[8 * k]), "r"(v[8 * k + 1]),
+                         "r"(v[8 * k + 2]), "r"(v[8 * k + 3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot + 16), "r"(v[8 * k + 4]),
+                         "r"(v[8 * k + 5]), "r"(v[8 * k + 6]), "r"(v[8 * k + 7])
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int k = k0; k < DQ / 8 && k < k0 + kStageSlots; ++k)
+              bulk_store(p.ws_o + (at + (j * (DQ / 8) + k) * p.GP) * 8, slots + (k - k0) * 1024, live * 32);
+            bulk_commit();
+          }
         }
       }
       tc_fence_before();
       mbar_arrive(o_empty(i & 1));
     };
-    int i = 0;
+    // the step's place: partial of the warp's first pair, its live pairs
+    StepCursor c = start;
     int64_t at_prev = 0;
-    bool live_prev = false;
-    for (int u = 0; u < count && ok; ++u) {
-      const int tiles = cursor_tiles(p, c);
-      for (int tile = 0; tile < tiles; ++tile, ++i) {
-        const int pair = (c.tp * kTcTiles + tile) * kTcPairs + pr;
-        const bool live = pair < c.n << p.gs;
-        const int64_t gs_at = static_cast<int64_t>(c.g) * p.S + c.s, gp = (static_cast<int64_t>(c.off) << p.gs) + pair;
-        const int64_t at = gs_at * (D / 8) * p.GP + gp;
-        const bool any = __any_sync(0xffffffffu, live);  // the same for the quadrant's four warps
-        check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
-        tc_fence_after();
-        uint32_t v[32];
-        if (any) {
-          float mx[2] = {-INFINITY, -INFINITY};
+    int live_prev = 0;
+    for (int i = 0; i < count; ++i) {
+      const int pair0 = c.tile * kTcPairs + quad * 32;
+      const int live = min(32, c.pairs - pair0);  // of the warp's 32 pairs (the same for the quadrant's four warps)
+      const int64_t gp = (static_cast<int64_t>(c.off) << p.gs) + pair0;
+      const int64_t gs_at = static_cast<int64_t>(c.g) * p.S + c.s;
+      const int64_t at = gs_at * (D / 8) * p.GP + gp;
+      check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
+      tc_fence_after();
+      uint32_t v[32];
+      if (live > 0) {
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld32(lane_base + 64 * j + 32 * h, v);
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld32(lane_base + 64 * j + 32 * h, v);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-              mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-            }
+          for (int e = 0; e < 32; e += 4) {
+            mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
           }
-          x_max[j * kTcPairs + pr] = fmaxf(mx[0], mx[1]);
         }
-        // one decision for the quadrant's 128 threads: leave if any has given up
-        if (quad_sync_or(!ok || abort_flag)) {
-          ok = false;
-          break;
-        }
-        float m = 0.f;
-        if (any) {
-          m = __fmul_rn(fmaxf(fmaxf(x_max[pr], x_max[kTcPairs + pr]), fmaxf(x_max[2 * kTcPairs + pr], x_max[3 * kTcPairs + pr])), c2);
-          const float2 c2x2 = make_float2(c2, c2), neg_m2 = make_float2(-m, -m);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld32(lane_base + 64 * j + 32 * h, v);
-            uint32_t hp[16], lp[16];  // bf16 pairs of the high and the low halves
-            // l in the decode kernel's order: key 8nb + 2tq + e into partial tq
-            // in (nb, e) order, then (0 + 1) + (2 + 3)
-            float sq[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 arg = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg_m2);
-              const float2 x = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
-              const __nv_bfloat162 h2 = __float22bfloat162_rn(x);
-              const __nv_bfloat162 l2 =
-                  __float22bfloat162_rn(__ffma2_rn(__bfloat1622float2(h2), make_float2(-1.f, -1.f), x));
-              hp[e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
-              lp[e / 2] = *reinterpret_cast<const uint32_t*>(&l2);
-              sq[e / 2 % 4] = __fadd_rn(__fadd_rn(sq[e / 2 % 4], x.x), x.y);
-            }
-            tmem_st16(lane_base + 64 * j + 32 * h, hp);
-            tmem_st16(lane_base + 64 * j + 32 * h + 16, lp);
-            x_sum[(2 * j + h) * kTcPairs + pr] = __fadd_rn(__fadd_rn(sq[0], sq[1]), __fadd_rn(sq[2], sq[3]));
-          }
-          tmem_st_wait();
-        }
-        tc_fence_before();
-        mbar_arrive(p_full(j));
-        if (i > 0) store_o(i - 1, at_prev, live_prev);
-        quad_sync();
-        if (j == 0 && live) {
-          float l = x_sum[pr];
-#pragma unroll
-          for (int q = 1; q < 8; ++q) l = __fadd_rn(l, x_sum[q * kTcPairs + pr]);
-          *reinterpret_cast<float2*>(p.ws_ml + (gs_at * p.GP + gp) * 2) = make_float2(m, l);
-        }
-        at_prev = at;
-        live_prev = live;
+        x_max[j * kTcPairs + pr] = fmaxf(mx[0], mx[1]);
       }
+      // one decision for the quadrant's 128 threads: leave if any has given up
+      if (quad_sync_or(!ok || abort_flag)) {
+        ok = false;
+        break;
+      }
+      float m = 0.f;
+      if (live > 0) {
+        m = __fmul_rn(fmaxf(fmaxf(x_max[pr], x_max[kTcPairs + pr]), fmaxf(x_max[2 * kTcPairs + pr], x_max[3 * kTcPairs + pr])), c2);
+        const float2 c2x2 = make_float2(c2, c2), neg_m2 = make_float2(-m, -m);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tmem_ld32(lane_base + 64 * j + 32 * h, v);
+          uint32_t hp[16], lp[16];  // bf16 pairs of the high and the low halves
+          // l in the decode kernel's order: key 8nb + 2tq + e into partial tq
+          // in (nb, e) order, then (0 + 1) + (2 + 3)
+          float sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 arg = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg_m2);
+            const float2 x = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+            const __nv_bfloat162 h2 = __float22bfloat162_rn(x);
+            const __nv_bfloat162 l2 =
+                __float22bfloat162_rn(__ffma2_rn(__bfloat1622float2(h2), make_float2(-1.f, -1.f), x));
+            hp[e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+            lp[e / 2] = *reinterpret_cast<const uint32_t*>(&l2);
+            sq[e / 2 % 4] = __fadd_rn(__fadd_rn(sq[e / 2 % 4], x.x), x.y);
+          }
+          tmem_st16(lane_base + 64 * j + 32 * h, hp);
+          tmem_st16(lane_base + 64 * j + 32 * h + 16, lp);
+          x_sum[(2 * j + h) * kTcPairs + pr] = __fadd_rn(__fadd_rn(sq[0], sq[1]), __fadd_rn(sq[2], sq[3]));
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      mbar_arrive(p_full(j));
+      quad_sync();
+      if (j == 0 && lane < live) {
+        float l = x_sum[pr];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) l = __fadd_rn(l, x_sum[q * kTcPairs + pr]);
+        *reinterpret_cast<float2*>(p.ws_ml + (gs_at * p.GP + gp + lane) * 2) = make_float2(m, l);
+      }
+      if (i > 0) store_o(i - 1, at_prev, live_prev);
+      at_prev = at;
+      live_prev = live;
       cursor_next(p, c);
     }
-    if (ok) store_o(i - 1, at_prev, live_prev);
+    if (ok) store_o(count - 1, at_prev, live_prev);
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -864,8 +881,8 @@ kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
 
 template <int D>
 constexpr size_t ctx_smem_bytes() {
-  return 1024 + kTcTiles * static_cast<size_t>(D / 64) * kTcPairs * 128 + 2 * static_cast<size_t>(D / 64) * kSplit * 128 +
-         (kTcBars + 1) * 8 + 12 * kTcPairs * 4;
+  return 1024 + static_cast<size_t>(D / 64) * kTcPairs * 128 + 2 * static_cast<size_t>(D / 64) * kSplit * 128 +
+         16 * kStageSlots * 1024 + (kTcBars + 1) * 8 + 12 * kTcPairs * 4;
 }
 
 // The tensor maps of the context kernel; false where a stride or size is
