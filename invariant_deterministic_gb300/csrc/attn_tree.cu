@@ -36,11 +36,13 @@ struct TreeAttnParams {
   const __nv_bfloat16* v;
   int64_t seq_stride, tok_stride;
   __nv_bfloat16* out;
-  // partials, GP = total_rows * G pairs (row, head of the group) of a kv head side
-  // by side, so that a warp's stores and loads of 32 pairs are contiguous
-  float* ws_o;   // [Hkv][S][D / 8][GP][8]
-  float* ws_ml;  // [Hkv][S][GP][2]
-  int64_t GP;
+  // Partials, 16 pairs of a (sequence, kv head) side by side: a group's splits
+  // follow each other, a split is [D / 8][16 pairs][8].  Group (b, g, i) has
+  // index (b * Hkv + g) * groups + i; its pairs are 16 i .. 16 i + 15.
+  float* ws_o;    // [B * Hkv * groups][S][D / 8][16][8]
+  float* ws_ml;   // [B * Hkv * groups][S][16][2]
+  int* ws_cov;    // [B * Hkv]: splits that the partial of split 0 stands for
+  int groups;
   int Hq, Hkv, G, gs;  // G = Hq / Hkv = 1 << gs
   int S;         // splits per row in the workspace
   float c2;      // fp32(scale * log2 e) > 0
@@ -50,6 +52,12 @@ struct TreeAttnParams {
 
 __device__ __forceinline__ void report_bad_tree(const TreeAttnParams& p) {
   if (threadIdx.x == 0 && p.status) atomicExch(p.status, DEV_TREE_BAD);
+}
+
+// Where the partial of a group's split begins, in pairs (rows of D values in
+// ws_o, of 2 in ws_ml); bg = b * Hkv + g.
+__device__ __forceinline__ int64_t partial_at(const TreeAttnParams& p, int bg, int group, int s) {
+  return ((static_cast<int64_t>(bg) * p.groups + group) * p.S + s) * 16;
 }
 
 // One block per (kv head, tile of 16 MT pairs, split, sequence).
@@ -372,19 +380,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
     for (int h = 0; h < 2; ++h) {
       if (cnt[mt][h] <= 0) continue;
       const int pair = mt * 16 + h * 8 + gq;
-      const int64_t gs_at = static_cast<int64_t>(g) * p.S + s;
-      const int64_t gp = (static_cast<int64_t>(off + n0) << gs) + pair;
+      const int64_t at = partial_at(p, b * p.Hkv + g, tile * MT + mt, s);
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb)
-        *reinterpret_cast<float2*>(p.ws_o + ((gs_at * (D / 8) + 2 * warp + nb) * p.GP + gp) * 8 + 2 * tq) =
+        *reinterpret_cast<float2*>(p.ws_o + at * D + ((2 * warp + nb) * 16 + h * 8 + gq) * 8 + 2 * tq) =
             make_float2(oc[mt][nb][2 * h], oc[mt][nb][2 * h + 1]);
       if (warp == 0 && tq == 0) {
         float l = wsum[0][pair];
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w) l = __fadd_rn(l, wsum[w][pair]);
-        *reinterpret_cast<float2*>(p.ws_ml + (gs_at * p.GP + gp) * 2) = make_float2(m[mt][h], l);
+        *reinterpret_cast<float2*>(p.ws_ml + (at + h * 8 + gq) * 2) = make_float2(m[mt][h], l);
       }
     }
+  if (s == 0 && tile == 0 && t == 0) p.ws_cov[b * p.Hkv + g] = 1;
 }
 
 // ---------------------------------------------------------------------------
@@ -402,12 +410,17 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
 // scheduler; the four exchange raw maxima and 32-key group sums through shared
 // memory, in the decode kernel's order.  Warp 16 lane 0 issues the MMAs, warp 17
 // lane 0 the TMA loads.
-// Tensor memory: scores R in columns 0-255, overwritten chunk by chunk with P
-// (64-key chunk j: 32-key group h as packed bf16 pairs, hi at 64 j + 32 h, lo
-// 16 columns further), O in two buffers of D columns after it.  The MMAs run
+// Tensor memory: scores R in columns 0-255, overwritten 16 keys at a time with
+// their P (packed bf16 pairs: hi in the first eight of the 16 columns, lo in the
+// others), O in two buffers of D columns after it.  The MMAs run
 // in issue order: step i + 1's scores of keys 128 h .. follow step i's P.V of
 // chunks 2h and 2h + 1, which read the P that they overwrite; the softmax
 // threads store step i - 1's O while step i's P.V runs.
+// A block whose run begins a (sequence, kv head) at split 0 folds the splits it
+// takes from there on with the merge kernel's arithmetic (32 columns of a pair
+// per thread) and leaves their state as the partial of split 0 (ws_cov: how many
+// splits that is); only the splits of a run's first, already begun sequence and
+// of trees with more than one tile leave a partial each.
 // The partials leave through shared memory and bulk copies: stored straight from
 // registers they held up every other shared-memory access of the SM for about
 // 2,500 cycles a step (21 - 25 bytes a cycle).
@@ -415,7 +428,7 @@ constexpr int kTcSoftmax = 512;  // 16 warps
 constexpr int kTcThreads = kTcSoftmax + 64;
 constexpr int kTcPairs = 128;
 constexpr int kTcBars = 15;
-constexpr int kStageSlots = 3;   // 1 KB chunks (32 pairs x 8 columns) a warp stages
+constexpr int kStage = 2048;     // bytes a warp stages at a time: two groups x two 8-column chunks
 
 struct StepCursor {
   int b, g, s, tile;
@@ -486,11 +499,8 @@ __device__ __forceinline__ void bulk_store(float* dst, uint32_t src, uint32_t by
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Waits until at most N of this thread's latest groups still read their source.
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
+// Waits until this thread's copies have read their source / are complete.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 template <int D>
@@ -509,13 +519,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   unsigned char* q_s = base;
   unsigned char* k_s = q_s + Q_BYTES;
   unsigned char* v_s = k_s + KV_BYTES;
-  unsigned char* stage = v_s + KV_BYTES;    // [16 warps][kStageSlots][32 pairs][8] fp32
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 16 * kStageSlots * 1024);
+  unsigned char* stage = v_s + KV_BYTES;    // [16 warps][2 groups][2 chunks][16 pairs][8] fp32
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 16 * kStage);
   float* x_max = reinterpret_cast<float*>(bars + kTcBars + 1);  // [4][128] raw maxima
   float* x_sum = x_max + 4 * kTcPairs;                          // [8][128] 32-key group sums
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ StepCursor start;
+  __shared__ StepCursor groups[16];  // of each softmax warp, advanced where its (sequence, kv head) changes
   __shared__ int count_s;
   const uint32_t k_full = smem_addr(bars + 0), k_empty = smem_addr(bars + 1);
   const uint32_t v_full = smem_addr(bars + 2), v_empty = smem_addr(bars + 3);
@@ -626,9 +637,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint64_t vdesc = vd + static_cast<uint64_t>(((4 * j + kk) * 2048) >> 4);
-              const uint32_t p_hi = tmem + static_cast<uint32_t>(64 * j + 32 * (kk >> 1) + 8 * (kk & 1));
+              const uint32_t p_hi = tmem + static_cast<uint32_t>(64 * j + 16 * kk);
               umma_bf16_tmem_a(o_col, p_hi, vdesc, idesc_o, (j | kk) != 0 ? 1u : 0u);
-              umma_bf16_tmem_a(o_col, p_hi + 16, vdesc, idesc_o, 1u);
+              umma_bf16_tmem_a(o_col, p_hi + 8, vdesc, idesc_o, 1u);
             }
           }
           if (has_r && (j & 1)) {
@@ -660,7 +671,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int quad = warp & 3, j = warp >> 2;  // lanes 32 quad .., keys 64 j .. and output columns D/4 j ..
     const int pr = quad * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t slots = smem_addr(stage) + warp * kStageSlots * 1024;
+    const uint32_t slot = smem_addr(stage) + warp * kStage;
     const float c2 = p.c2;
     bool ok = true;
     auto quad_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + quad) : "memory"); };
@@ -681,62 +692,105 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = false;
       }
     };
-    // sends this warp's D/4 columns of step i's O, `live` pairs from the
-    // warp's first, to the partial at `at` (the warp's first pair)
-    auto store_o = [&](int i, int64_t at, int live) {
+    // sends D/4 columns of 32 pairs, this thread's in v, to the partial at `at`
+    // (that of the first of the warp's two groups; `second`: the other has pairs)
+    auto send = [&](const uint32_t (&v)[DQ], int64_t at, bool second) {
+#pragma unroll
+      for (int k0 = 0; k0 < DQ / 8; k0 += 2) {
+        if (lane == 0) bulk_wait_read();  // the last copies have read the stage
+        __syncwarp();
+#pragma unroll
+        for (int k = k0; k < k0 + 2; ++k) {
+          const uint32_t dst = slot + (lane >> 4) * 1024 + (k - k0) * 512 + (lane & 15) * 32;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[8 * k]), "r"(v[8 * k + 1]),
+                       "r"(v[8 * k + 2]), "r"(v[8 * k + 3])
+                       : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 16), "r"(v[8 * k + 4]), "r"(v[8 * k + 5]),
+                       "r"(v[8 * k + 6]), "r"(v[8 * k + 7])
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          float* dst = p.ws_o + at * D + (j * (DQ / 8) + k0) * 128;
+          bulk_store(dst, slot, 1024);
+          if (second) bulk_store(dst + static_cast<int64_t>(p.S) * 16 * D, slot + 1024, 1024);
+          bulk_commit();
+        }
+      }
+    };
+    // the state of the splits folded so far (l of the first quarter's threads only)
+    float o_acc[DQ], m_acc = 0.f, l_acc = 0.f;
+    // what the last step left, of the same (sequence, kv head): its place, live
+    // pairs and statistics
+    int tile_prev = 0, s_prev = 0, live_prev = 0;
+    float m_prev = 0.f, l_prev = 0.f;
+    bool folding = false;  // this (sequence, kv head) is folded
+    int bg = 0;            // its b * Hkv + g
+    // takes step i's O: folds it, or sends it as a partial
+    auto take_o = [&](int i) {
       check(mbar_wait_bounded(o_full(i & 1), (i >> 1) & 1, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
-      if (live > 0) {
-        uint32_t v[32];
-        tmem_ld32(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
-        // as many chunks at a time as there are slots
+      if (live_prev > 0) {
+        uint32_t v[DQ];
+        if constexpr (DQ == 32)
+          tmem_ld32(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
+        else
+          tmem_ld16(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
+        if (!folding) {
+          send(v, partial_at(p, bg, (tile_prev * kTcPairs + quad * 32) >> 4, s_prev), live_prev > 16);
+        } else if (s_prev == 0) {
+          // the merge's first step: 0 * 0 + x * 1
+          m_acc = m_prev;
+          l_acc = __fadd_rn(0.f, l_prev);
 #pragma unroll
-        for (int k0 = 0; k0 < DQ / 8; k0 += kStageSlots) {
-          if (lane == 0) bulk_wait_read<0>();  // the slots' last copies have read them
-          __syncwarp();
+          for (int d = 0; d < DQ; ++d) o_acc[d] = __fadd_rn(0.f, __uint_as_float(v[d]));
+        } else {
+          const float m_new = fmaxf(m_acc, m_prev);
+          const float a = ex2_approx(__fsub_rn(m_acc, m_new));
+          const float c = ex2_approx(__fsub_rn(m_prev, m_new));
+          l_acc = __fadd_rn(__fmul_rn(l_acc, a), __fmul_rn(l_prev, c));
 #pragma unroll
-          for (int k = k0; k < DQ / 8 && k < k0 + kStageSlots; ++k) {
-            const uint32_t slot = slots + (k - k0) * 1024 + lane * 32;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot), "r"(v[8 * k]), "r"(v[8 * k + 1]),
-                         "r"(v[8 * k + 2]), "r"(v[8 * k + 3])
-                         : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot + 16), "r"(v[8 * k + 4]),
-                         "r"(v[8 * k + 5]), "r"(v[8 * k + 6]), "r"(v[8 * k + 7])
-                         : "memory");
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-#pragma unroll
-            for (int k = k0; k < DQ / 8 && k < k0 + kStageSlots; ++k)
-              bulk_store(p.ws_o + (at + (j * (DQ / 8) + k) * p.GP) * 8, slots + (k - k0) * 1024, live * 32);
-            bulk_commit();
-          }
+          for (int d = 0; d < DQ; ++d)
+            o_acc[d] = __fadd_rn(__fmul_rn(o_acc[d], a), __fmul_rn(__uint_as_float(v[d]), c));
+          m_acc = m_new;
         }
       }
       tc_fence_before();
       mbar_arrive(o_empty(i & 1));
     };
-    // the step's place: partial of the warp's first pair, its live pairs
-    StepCursor c = start;
-    int64_t at_prev = 0;
-    int live_prev = 0;
+    // the state of `splits` folded splits as the partial of split 0
+    auto leave_state = [&](int splits) {
+      if (live_prev > 0) {
+        const int64_t at = partial_at(p, bg, quad * 2, 0);
+        uint32_t v[DQ];
+#pragma unroll
+        for (int d = 0; d < DQ; ++d) v[d] = __float_as_uint(o_acc[d]);
+        send(v, at, live_prev > 16);
+        if (j == 0 && lane < live_prev)
+          *reinterpret_cast<float2*>(p.ws_ml + (at + (lane >> 4) * (static_cast<int64_t>(p.S) * 16) + (lane & 15)) * 2) =
+              make_float2(m_acc, l_acc);
+      }
+      if (warp == 0 && lane == 0) p.ws_cov[bg] = splits;
+    };
+    int s = start.s, tile = start.tile, pairs = start.pairs, splits = start.splits, tiles = start.tiles;
+    if (lane == 0) groups[warp] = start;
+    bg = start.b * p.Hkv + start.g;
+    folding = s == 0 && tiles == 1;
+    bool pending = false;  // the last step's O is not taken yet
     for (int i = 0; i < count; ++i) {
-      const int pair0 = c.tile * kTcPairs + quad * 32;
-      const int live = min(32, c.pairs - pair0);  // of the warp's 32 pairs (the same for the quadrant's four warps)
-      const int64_t gp = (static_cast<int64_t>(c.off) << p.gs) + pair0;
-      const int64_t gs_at = static_cast<int64_t>(c.g) * p.S + c.s;
-      const int64_t at = gs_at * (D / 8) * p.GP + gp;
+      const int pair0 = tile * kTcPairs + quad * 32;
+      const int live = min(32, pairs - pair0);  // of the warp's 32 pairs (the same for the quadrant's four warps)
       check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
-      uint32_t v[32];
       if (live > 0) {
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          tmem_ld32(lane_base + 64 * j + 32 * h, v);
+        for (int h = 0; h < 4; ++h) {
+          uint32_t v[16];
+          tmem_ld16(lane_base + 64 * j + 16 * h, v);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
+          for (int e = 0; e < 16; e += 4) {
             mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
             mx[1] = fmax3(mx[1], __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
           }
@@ -748,30 +802,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = false;
         break;
       }
-      float m = 0.f;
+      float m = 0.f, l = 0.f;
       if (live > 0) {
         m = __fmul_rn(fmaxf(fmaxf(x_max[pr], x_max[kTcPairs + pr]), fmaxf(x_max[2 * kTcPairs + pr], x_max[3 * kTcPairs + pr])), c2);
         const float2 c2x2 = make_float2(c2, c2), neg_m2 = make_float2(-m, -m);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          tmem_ld32(lane_base + 64 * j + 32 * h, v);
-          uint32_t hp[16], lp[16];  // bf16 pairs of the high and the low halves
           // l in the decode kernel's order: key 8nb + 2tq + e into partial tq
           // in (nb, e) order, then (0 + 1) + (2 + 3)
           float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 arg = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg_m2);
-            const float2 x = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
-            const __nv_bfloat162 h2 = __float22bfloat162_rn(x);
-            const __nv_bfloat162 l2 =
-                __float22bfloat162_rn(__ffma2_rn(__bfloat1622float2(h2), make_float2(-1.f, -1.f), x));
-            hp[e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
-            lp[e / 2] = *reinterpret_cast<const uint32_t*>(&l2);
-            sq[e / 2 % 4] = __fadd_rn(__fadd_rn(sq[e / 2 % 4], x.x), x.y);
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t col = lane_base + 64 * j + 32 * h + 16 * half;
+            uint32_t v[16], hp[8], lp[8];  // bf16 pairs of the high and the low halves
+            tmem_ld16(col, v);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 arg = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2x2, neg_m2);
+              const float2 x = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));
+              const __nv_bfloat162 h2 = __float22bfloat162_rn(x);
+              const __nv_bfloat162 l2 =
+                  __float22bfloat162_rn(__ffma2_rn(__bfloat1622float2(h2), make_float2(-1.f, -1.f), x));
+              hp[e / 2] = *reinterpret_cast<const uint32_t*>(&h2);
+              lp[e / 2] = *reinterpret_cast<const uint32_t*>(&l2);
+              sq[e / 2 % 4] = __fadd_rn(__fadd_rn(sq[e / 2 % 4], x.x), x.y);
+            }
+            tmem_st8(col, hp);
+            tmem_st8(col + 8, lp);
           }
-          tmem_st16(lane_base + 64 * j + 32 * h, hp);
-          tmem_st16(lane_base + 64 * j + 32 * h + 16, lp);
           x_sum[(2 * j + h) * kTcPairs + pr] = __fadd_rn(__fadd_rn(sq[0], sq[1]), __fadd_rn(sq[2], sq[3]));
         }
         tmem_st_wait();
@@ -780,17 +838,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_arrive(p_full(j));
       quad_sync();
       if (j == 0 && lane < live) {
-        float l = x_sum[pr];
+        l = x_sum[pr];
 #pragma unroll
         for (int q = 1; q < 8; ++q) l = __fadd_rn(l, x_sum[q * kTcPairs + pr]);
-        *reinterpret_cast<float2*>(p.ws_ml + (gs_at * p.GP + gp + lane) * 2) = make_float2(m, l);
+        if (!folding)
+          *reinterpret_cast<float2*>(p.ws_ml + (partial_at(p, bg, pair0 >> 4, s) + (lane >> 4) * (static_cast<int64_t>(p.S) * 16) + (lane & 15)) * 2) =
+              make_float2(m, l);
       }
-      if (i > 0) store_o(i - 1, at_prev, live_prev);
-      at_prev = at;
+      if (!folding && s == 0 && tile == 0 && warp == 0 && lane == 0) p.ws_cov[bg] = 1;
+      if (pending) take_o(i - 1);
+      pending = true;
+      tile_prev = tile;
+      s_prev = s;
       live_prev = live;
-      cursor_next(p, c);
+      m_prev = m;
+      l_prev = l;
+      bool end = false;  // of this (sequence, kv head)
+      if (++tile == tiles) {
+        tile = 0;
+        end = ++s == splits;
+      }
+      if (end || i + 1 == count) {
+        // its last O now, and its state
+        take_o(i);
+        pending = false;
+        if (folding && ok) leave_state(s);
+      }
+      if (end && i + 1 < count) {
+        if (lane == 0) {
+          StepCursor c = groups[warp];
+          c.tile = c.tiles - 1;
+          c.s = c.splits - 1;
+          cursor_next(p, c);
+          groups[warp] = c;
+        }
+        __syncwarp();
+        s = 0;
+        pairs = groups[warp].pairs;
+        splits = groups[warp].splits;
+        tiles = groups[warp].tiles;
+        bg = groups[warp].b * p.Hkv + groups[warp].g;
+        folding = tiles == 1;
+        __syncwarp();
+      }
     }
-    if (ok) store_o(count - 1, at_prev, live_prev);
     if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
@@ -802,52 +893,59 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Folds the splits that each node sees, with the decode merge's arithmetic.  A
-// block takes 16 pairs of a (sequence, kv head), warp k their columns 8k .. 8k +
-// 7: a lane half of them for one pair, so a warp's loads of a split are 512
+// block takes 16 pairs of a (sequence, kv head) and 32 columns, a warp eight of
+// them: a lane half of those for one pair, so a warp's loads of a split are 512
 // contiguous bytes.  The first partials are requested before the tree is read: a
 // node of any depth sees the splits up to position ctx_len.
 constexpr int kMergePairs = 16;
+constexpr int kMergeThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(4 * D) attn_tree_merge_kernel(const TreeAttnParams p) {
-  constexpr int CH = 8;  // partials loaded ahead of the (sequential) fold
+__global__ void __launch_bounds__(kMergeThreads, 8) attn_tree_merge_kernel(const TreeAttnParams p) {
+  constexpr int CH = 6;  // partials loaded ahead of the (sequential) fold
   __shared__ TreeInfo ti;
   pdl_launch_dependents();
   pdl_wait();
-  const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int QUARTERS = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int k = static_cast<int>(blockIdx.x) % QUARTERS * 4 + (threadIdx.x >> 5);
+  const int pair0 = static_cast<int>(blockIdx.x) / QUARTERS * kMergePairs;
   const int g = blockIdx.y, b = blockIdx.z;
-  const int pair = blockIdx.x * kMergePairs + (lane >> 1);
+  const int pair = pair0 + (lane >> 1);
   int n, ctx, off;
-  if (!tree_bounds(p.tree, b, n, ctx, off) || static_cast<int>(blockIdx.x) * kMergePairs >= n << p.gs) return;
+  if (!tree_bounds(p.tree, b, n, ctx, off) || pair0 >= n << p.gs) return;
   const bool live = pair < n << p.gs;
-  const int64_t gp = (static_cast<int64_t>(off) << p.gs) + (live ? pair : 0);
-  const float* ml_at = p.ws_ml + (static_cast<int64_t>(g) * p.S * p.GP + gp) * 2;
-  const float* o_at = p.ws_o + ((static_cast<int64_t>(g) * p.S * (D / 8) + k) * p.GP + gp) * 8 + (lane & 1) * 4;
-  const int64_t ml_step = p.GP * 2, o_step = p.GP * D;
+  const int64_t at = partial_at(p, b * p.Hkv + g, pair0 >> 4, 0) + (lane >> 1);
+  const float* ml_at = p.ws_ml + at * 2;
+  const float* o_at = p.ws_o + partial_at(p, b * p.Hkv + g, pair0 >> 4, 0) * D + (k * 16 + (lane >> 1)) * 8 + (lane & 1) * 4;
+  // partial q of the fold: 0 stands for the first cov splits, the others for one
+  // each (clamped: the count of a tree that is left out was never written)
+  const int cov = max(1, min(p.ws_cov[b * p.Hkv + g], ctx / kSplit));
   float2 ml[CH];
   float4 o[CH];
-  auto load = [&](int s0, int ns) {
+  auto load = [&](int q0, int nq) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (s0 + i >= ns) continue;
-      ml[i] = *reinterpret_cast<const float2*>(ml_at + (s0 + i) * ml_step);
-      o[i] = *reinterpret_cast<const float4*>(o_at + (s0 + i) * o_step);
+      if (q0 + i >= nq) continue;
+      const int s = q0 + i == 0 ? 0 : cov - 1 + q0 + i;
+      ml[i] = *reinterpret_cast<const float2*>(ml_at + static_cast<int64_t>(s) * 32);
+      o[i] = *reinterpret_cast<const float4*>(o_at + static_cast<int64_t>(s) * (16 * D));
     }
   };
-  const int sure = ctx / kSplit + 1;  // splits that every node sees
+  const int sure = ctx / kSplit + 2 - cov;  // partials that every node sees
   load(0, sure);
-  if (k == 0) tree_load(p.tree, b, ti);
+  if (threadIdx.x < 32) tree_load(p.tree, b, ti);
   __syncthreads();
   if (!ti.ok || !live) return;
   const int node = pair >> p.gs;
-  const int ns = (ctx + __popcll(ti.mask[node]) + kSplit - 1) / kSplit;
+  const int nq = (ctx + __popcll(ti.mask[node]) + kSplit - 1) / kSplit + 1 - cov;
   float m_acc = -INFINITY, l_acc = 0.f;
   float4 o_acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < ns; s0 += CH) {
-    if (s0 > 0 || (sure < CH && ns > sure)) load(s0, ns);
+  for (int q0 = 0; q0 < nq; q0 += CH) {
+    if (q0 > 0 || (sure < CH && nq > sure)) load(q0, nq);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      if (s0 + i < ns) {
+      if (q0 + i < nq) {
         const float m_new = fmaxf(m_acc, ml[i].x);
         const float a = ex2_approx(__fsub_rn(m_acc, m_new));
         const float c = ex2_approx(__fsub_rn(ml[i].x, m_new));
@@ -882,7 +980,7 @@ kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
 template <int D>
 constexpr size_t ctx_smem_bytes() {
   return 1024 + static_cast<size_t>(D / 64) * kTcPairs * 128 + 2 * static_cast<size_t>(D / 64) * kSplit * 128 +
-         16 * kStageSlots * 1024 + (kTcBars + 1) * 8 + 12 * kTcPairs * 4;
+         16 * kStage + (kTcBars + 1) * 8 + 12 * kTcPairs * 4;
 }
 
 // The tensor maps of the context kernel; false where a stride or size is
@@ -921,15 +1019,23 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
     st = launch_kernel(kernel, dim3(sms), dim3(kTcThreads), smem, stream, 1, mq, mk, mv, p);
     if (st != KINV_OK) return st;
   }
-  return launch_kernel(attn_tree_merge_kernel<D>, dim3((pairs + kMergePairs - 1) / kMergePairs, p.Hkv, p.tree.B),
-                       dim3(4 * D), 0, stream, 1, p);
+  return launch_kernel(attn_tree_merge_kernel<D>, dim3((pairs + kMergePairs - 1) / kMergePairs * (D / 32), p.Hkv, p.tree.B),
+                       dim3(kMergeThreads), 0, stream, 1, p);
 }
 
-size_t tree_workspace_bytes(int64_t rows, int Hq, int D, int S) {
-  // 256 to align the partials, which are stored 32 bytes at a time
-  const size_t o = static_cast<size_t>(rows) * Hq * S * D * 4;
-  return 256 + ((o + 255) / 256) * 256 + static_cast<size_t>(rows) * Hq * S * 2 * 4;
-}
+// The workspace: partials (on a 256-byte boundary), their statistics, ws_cov.
+struct TreeWorkspace {
+  int64_t groups, pairs;  // groups of a kv head; rows of D values in all
+  size_t o, ml, cov, bytes;
+  TreeWorkspace(int64_t B, int max_nodes, int Hq, int Hkv, int D, int64_t S) {
+    groups = (static_cast<int64_t>(max_nodes) * (Hq / Hkv) + 15) / 16;
+    pairs = B * Hkv * groups * S * 16;
+    o = 0;
+    ml = o + static_cast<size_t>(pairs) * D * 4;
+    cov = ml + static_cast<size_t>(pairs) * 8;
+    bytes = 256 + cov + static_cast<size_t>(B) * Hkv * 4;  // 256 to align the base
+  }
+};
 
 }  // namespace
 }  // namespace kinv
@@ -940,7 +1046,7 @@ extern "C" size_t kinv_attn_tree_workspace(int B, int total_rows, int max_nodes,
                                            int max_kv, int split_len) {
   if (B <= 0 || total_rows <= 0 || max_nodes <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_kv <= 0 || split_len <= 0)
     return 0;
-  return tree_workspace_bytes(total_rows, Hq, D, static_cast<int>((static_cast<int64_t>(max_kv) + split_len - 1) / split_len));
+  return TreeWorkspace(B, max_nodes, Hq, Hkv, D, (static_cast<int64_t>(max_kv) + split_len - 1) / split_len).bytes;
 }
 
 extern "C" kinv_status kinv_attn_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -963,7 +1069,8 @@ extern "C" kinv_status kinv_attn_tree(const void* q, const void* k_cache, const 
     return KINV_ERR_ALIGNMENT;
   const int64_t S = (static_cast<int64_t>(tree->max_kv) + kSplit - 1) / kSplit;
   if (S > 65535) return KINV_ERR_UNSUPPORTED;
-  if (workspace_bytes < tree_workspace_bytes(tree->total_rows, Hq, D, static_cast<int>(S))) return KINV_ERR_WORKSPACE;
+  const TreeWorkspace w(tree->B, tree->max_nodes, Hq, Hkv, D, S);
+  if (workspace_bytes < w.bytes) return KINV_ERR_WORKSPACE;
   TreeAttnParams p{};
   p.tree = *tree;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -973,13 +1080,13 @@ extern "C" kinv_status kinv_attn_tree(const void* q, const void* k_cache, const 
   p.tok_stride = tok_stride;
   p.out = static_cast<__nv_bfloat16*>(out);
   char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
-  p.ws_o = reinterpret_cast<float*>(ws);
-  const size_t o_bytes = static_cast<size_t>(tree->total_rows) * Hq * S * D * 4;
-  p.ws_ml = reinterpret_cast<float*>(ws + ((o_bytes + 255) / 256) * 256);
+  p.ws_o = reinterpret_cast<float*>(ws + w.o);
+  p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.ws_cov = reinterpret_cast<int*>(ws + w.cov);
+  p.groups = static_cast<int>(w.groups);
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = G;
-  p.GP = static_cast<int64_t>(tree->total_rows) * G;
   p.gs = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
   p.S = static_cast<int>(S);
   p.c2 = base2_factor(scale, D);

@@ -386,17 +386,25 @@ class Tree:
         self.ptr = ctypes.byref(self.struct)
 
 
-def _need_tree_cache(k_cache, v_cache, tree: Tree, what: str):
-    """The caches [B][slots][Hkv][D] hold the tree's sequences and max_kv slots each."""
-    _need(k_cache, torch.bfloat16, "k_cache")
-    _need(v_cache, torch.bfloat16, "v_cache")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+def _need_all(dtype, **tensors):
+    """_need for several tensors at once (one call while all is well)."""
+    for name, t in tensors.items():
+        if t.dtype != dtype or not t.is_cuda:
+            _need(t, dtype, name)
+
+
+def _tree_cache(k_cache, v_cache, tree: Tree, what: str):
+    """Shape and strides of the caches [B][slots][Hkv][D], which hold the
+    tree's sequences and max_kv slots each."""
+    shape, stride = k_cache.shape, k_cache.stride()
+    if v_cache.shape != shape or v_cache.stride() != stride:
         raise ValueError(f"{what}: the caches must share shape and strides")
-    bsz, slots, _, d = k_cache.shape
-    if k_cache.stride(3) != 1 or k_cache.stride(2) != d:
+    bsz, slots, _, d = shape
+    if stride[3] != 1 or stride[2] != d:
         raise ValueError(f"{what}: a slot's heads must be contiguous")
     if bsz < tree.B or slots < tree.max_kv:
         raise ValueError(f"{what}: the caches are smaller than the tree's sequences and max_kv")
+    return shape, stride
 
 
 def rope_append_tree(qkv, q_out, k_cache, v_cache, tree: Tree, n_q, n_kv, head_dim, rope_base,
@@ -404,17 +412,16 @@ def rope_append_tree(qkv, q_out, k_cache, v_cache, tree: Tree, n_q, n_kv, head_d
     """kinv_rope_append for the rows of drafted trees: qkv [rows][(Hq + 2 Hkv) D]
     rotated by each node's position -> q_out [rows][Hq][D], keys and values into
     the caches [B][slots][Hkv][D] at the node's slot."""
-    _need(qkv, torch.bfloat16, "qkv")
-    _need(q_out, torch.bfloat16, "q_out")
-    _need_tree_cache(k_cache, v_cache, tree, "rope_append_tree")
-    if (qkv.shape[0] < tree.total_rows or qkv.stride(1) != 1 or not q_out.is_contiguous()
-            or qkv.shape[1] != (n_q + 2 * n_kv) * head_dim
-            or q_out.numel() < tree.total_rows * n_q * head_dim or tuple(k_cache.shape[2:]) != (n_kv, head_dim)):
+    _need_all(torch.bfloat16, qkv=qkv, q_out=q_out, k_cache=k_cache, v_cache=v_cache)
+    shape, stride = _tree_cache(k_cache, v_cache, tree, "rope_append_tree")
+    (rows, width), (ld, step) = qkv.shape, qkv.stride()
+    if (rows < tree.total_rows or step != 1 or not q_out.is_contiguous() or width != (n_q + 2 * n_kv) * head_dim
+            or q_out.numel() < tree.total_rows * n_q * head_dim or shape[2] != n_kv or shape[3] != head_dim):
         raise ValueError("rope_append_tree: shapes or layouts do not match")
-    _check(lib().kinv_rope_append_tree(_ptr(qkv), qkv.stride(0), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
-                                       k_cache.stride(0), k_cache.stride(1), tree.ptr, _ptr(q_norm),
-                                       _ptr(k_norm), float(eps), n_q, n_kv, head_dim, float(rope_base),
-                                       _stream(stream)), "kinv_rope_append_tree")
+    _check(lib().kinv_rope_append_tree(qkv.data_ptr(), ld, q_out.data_ptr(), k_cache.data_ptr(),
+                                       v_cache.data_ptr(), stride[0], stride[1], tree.ptr, _ptr(q_norm),
+                                       _ptr(k_norm), eps, n_q, n_kv, head_dim, rope_base, _stream(stream)),
+           "kinv_rope_append_tree")
     return q_out
 
 
@@ -428,22 +435,22 @@ def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_l
     """q [rows][Hq][D]; caches [B][slots][Hkv][D], which already hold the
     nodes' keys and values in their slots.  Each row has the bits of attn_decode
     behind the context and the node's path."""
-    _need(q, torch.bfloat16, "q")
-    _need_tree_cache(k_cache, v_cache, tree, "attn_tree")
-    rows, hq, d = q.shape
-    hkv = k_cache.shape[2]
     if out is None:
         out = torch.empty_like(q)
-    _need(out, torch.bfloat16, "out")
+    _need_all(torch.bfloat16, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
+    shape, stride = _tree_cache(k_cache, v_cache, tree, "attn_tree")
+    rows, hq, d = q.shape
+    hkv = shape[2]
     if (not q.is_contiguous() or not out.is_contiguous() or rows < tree.total_rows
-            or out.shape != q.shape or k_cache.shape[3] != d):
+            or out.shape != q.shape or shape[3] != d):
         raise ValueError("attn_tree: shapes or layouts do not match")
     if workspace is None:
         workspace = torch.empty(max(attn_tree_workspace(tree, hq, hkv, d, split_len), 16), dtype=torch.uint8,
                                 device=q.device)
-    _check(lib().kinv_attn_tree(_ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.stride(0), k_cache.stride(1),
-                                tree.ptr, _ptr(out), hq, hkv, d, split_len, float(scale), _ptr(workspace),
-                                workspace.numel(), _stream(stream)), "kinv_attn_tree")
+    _check(lib().kinv_attn_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), stride[0], stride[1],
+                                tree.ptr, out.data_ptr(), hq, hkv, d, split_len, scale, workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(stream)),
+           "kinv_attn_tree")
     return out
 
 
@@ -454,36 +461,34 @@ def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=
     token, the model's token after it); kv: [layers][2][B][slots][Hkv][D] bf16,
     changed in place (None: only the path is found).  Returns (n_accepted [B],
     path [B][max_nodes], out_tokens [B][max_nodes]) int32."""
-    _need(tokens, torch.int32, "tokens")
-    _need(next_tokens, torch.int32, "next_tokens")
-    dev = tokens.device
-    if (tokens.shape[0] < tree.total_rows or next_tokens.shape[0] < tree.total_rows
-            or not tokens.is_contiguous() or not next_tokens.is_contiguous()):
-        raise ValueError("tree_accept: tokens and next_tokens must be contiguous, one entry per row")
+    dev, b, n = tokens.device, tree.B, tree.max_nodes
     if n_accepted is None:
-        n_accepted = torch.empty(tree.B, dtype=torch.int32, device=dev)
+        n_accepted = torch.empty(b, dtype=torch.int32, device=dev)
     if path is None:
-        path = torch.empty(tree.B, tree.max_nodes, dtype=torch.int32, device=dev)
+        path = torch.empty(b, n, dtype=torch.int32, device=dev)
     if out_tokens is None:
-        out_tokens = torch.empty(tree.B, tree.max_nodes, dtype=torch.int32, device=dev)
-    for t, n, name in ((n_accepted, tree.B, "n_accepted"), (path, tree.B * tree.max_nodes, "path"),
-                       (out_tokens, tree.B * tree.max_nodes, "out_tokens")):
-        _need(t, torch.int32, name)
-        if t.numel() < n or not t.is_contiguous():
-            raise ValueError(f"tree_accept: {name} must be contiguous and hold the tree's entries")
+        out_tokens = torch.empty(b, n, dtype=torch.int32, device=dev)
+    _need_all(torch.int32, tokens=tokens, next_tokens=next_tokens, n_accepted=n_accepted, path=path,
+              out_tokens=out_tokens)
+    for t, least in ((tokens, tree.total_rows), (next_tokens, tree.total_rows), (n_accepted, b), (path, b * n),
+                     (out_tokens, b * n)):
+        if t.numel() < least or not t.is_contiguous():
+            raise ValueError("tree_accept: tokens and next_tokens [rows], n_accepted [B], path and out_tokens "
+                             "[B][max_nodes] must be contiguous")
     if kv is None:
         kp = vp = None
         layers = ls = ss = ts = hkv = d = 0
     else:
-        _need(kv, torch.bfloat16, "kv")
+        _need_all(torch.bfloat16, kv=kv)
         layers, two, bsz, slots, hkv, d = kv.shape
         ls, cs, ss, ts, hs, es = kv.stride()
-        if two != 2 or bsz < tree.B or slots < tree.max_kv or es != 1 or hs != d:
+        if two != 2 or bsz < b or slots < tree.max_kv or es != 1 or hs != d:
             raise ValueError("tree_accept: kv must be [layers][2][B][slots][Hkv][D] with room for the tree")
-        kp, vp = _ptr(kv), _ptr(kv) + 2 * cs
-    _check(lib().kinv_tree_accept(tree.ptr, _ptr(tokens), _ptr(next_tokens), kp, vp, layers, ls, ss, ts, hkv, d,
-                                  _ptr(n_accepted), _ptr(path), _ptr(out_tokens), _stream(stream)),
-           "kinv_tree_accept")
+        kp = kv.data_ptr()
+        vp = kp + 2 * cs
+    _check(lib().kinv_tree_accept(tree.ptr, tokens.data_ptr(), next_tokens.data_ptr(), kp, vp, layers, ls, ss, ts,
+                                  hkv, d, n_accepted.data_ptr(), path.data_ptr(), out_tokens.data_ptr(),
+                                  _stream(stream)), "kinv_tree_accept")
     return n_accepted, path, out_tokens
 
 
@@ -492,29 +497,31 @@ def logprobs(logits, ids=None, top_k: int = 0, stream=None):
     """logits fp32 or bf16 [rows][V]; ids int32 [rows][n] (negative: padding).
     Returns (logprobs fp32 [rows][n] or None, entropy fp32 [rows], top_ids int32
     [rows][top_k] or None, top_logprobs fp32 [rows][top_k] or None)."""
-    if logits.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"logits: expected torch.float32 or torch.bfloat16, got {logits.dtype}")
-    _need(logits, logits.dtype, "logits")
-    rows, v = logits.shape
-    if logits.stride(1) != 1:
+    dt = logits.dtype
+    if dt is not torch.float32 and dt is not torch.bfloat16:
+        raise TypeError(f"logits: expected torch.float32 or torch.bfloat16, got {dt}")
+    _need(logits, dt, "logits")
+    (rows, v), (ld, step) = logits.shape, logits.stride()
+    if step != 1 and v > 1:
         raise ValueError("logprobs: the ids of a row must be contiguous")
     dev = logits.device
-    n_ids, lp = 0, None
+    n_ids, lp, lp_ptr, ids_ptr = 0, None, None, None
     if ids is not None:
         _need(ids, torch.int32, "ids")
         if ids.dim() != 2 or ids.shape[0] != rows or not ids.is_contiguous():
             raise ValueError("logprobs: ids must be a contiguous [rows][n]")
         n_ids = ids.shape[1]
         lp = torch.empty(rows, n_ids, dtype=torch.float32, device=dev)
+        lp_ptr, ids_ptr = lp.data_ptr(), ids.data_ptr()
     entropy = torch.empty(rows, dtype=torch.float32, device=dev)
-    top_ids = top_lp = None
+    top_ids = top_lp = top_ptr = top_lp_ptr = None
     if top_k:
         top_ids = torch.empty(rows, top_k, dtype=torch.int32, device=dev)
         top_lp = torch.empty(rows, top_k, dtype=torch.float32, device=dev)
-    _check(lib().kinv_logprobs(_ptr(logits), F32 if logits.dtype == torch.float32 else BF16,
-                               logits.stride(0) if rows > 1 else max(logits.stride(0), v), rows, v, _ptr(ids),
-                               n_ids, _ptr(lp), _ptr(entropy), int(top_k), _ptr(top_ids), _ptr(top_lp),
-                               _stream(stream)), "kinv_logprobs")
+        top_ptr, top_lp_ptr = top_ids.data_ptr(), top_lp.data_ptr()
+    _check(lib().kinv_logprobs(logits.data_ptr(), F32 if dt is torch.float32 else BF16,
+                               ld if rows > 1 else max(ld, v), rows, v, ids_ptr, n_ids, lp_ptr,
+                               entropy.data_ptr(), top_k, top_ptr, top_lp_ptr, _stream(stream)), "kinv_logprobs")
     return lp, entropy, top_ids, top_lp
 
 
