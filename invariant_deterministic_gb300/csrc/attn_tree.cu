@@ -25,6 +25,7 @@ namespace {
 constexpr int kSplit = 256;    // keys per split, as in decode and prefill
 constexpr int kThreads = 256;  // eight warps, 32 positions each for the softmax
 constexpr int kMaxG = 8;
+constexpr int kScoreLd = kSplit + 8;
 // From this many (sequence, kv head, split) triples the cache may hold, the
 // splits within the context go to the tcgen05 kernel.
 constexpr int kMinSplitsTc = 64;
@@ -41,7 +42,9 @@ struct TreeAttnParams {
   // index (b * Hkv + g) * groups + i; its pairs are 16 i .. 16 i + 15.
   float* ws_o;    // [B * Hkv * groups][S][D / 8][16][8]
   float* ws_ml;   // [B * Hkv * groups][S][16][2]
-  int* ws_cov;    // [B * Hkv]: splits that the partial of split 0 stands for
+  // [B * Hkv * groups], at the first group of each 128 pairs: how many splits
+  // their partials of split 0 stand for
+  int* ws_cov;
   int groups;
   int Hq, Hkv, G, gs;  // G = Hq / Hkv = 1 << gs
   int S;         // splits per row in the workspace
@@ -55,9 +58,9 @@ __device__ __forceinline__ void report_bad_tree(const TreeAttnParams& p) {
 }
 
 // Where the partial of a group's split begins, in pairs (rows of D values in
-// ws_o, of 2 in ws_ml); bg = b * Hkv + g.
-__device__ __forceinline__ int64_t partial_at(const TreeAttnParams& p, int bg, int group, int s) {
-  return ((static_cast<int64_t>(bg) * p.groups + group) * p.S + s) * 16;
+// ws_o, of 2 in ws_ml).
+__device__ __forceinline__ int64_t partial_at(const TreeAttnParams& p, int group, int s) {
+  return (static_cast<int64_t>(group) * p.S + s) * 16;
 }
 
 // One block per (kv head, tile of 16 MT pairs, split, sequence).
@@ -66,7 +69,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
   constexpr int C8 = D / 8;   // 16-byte chunks per key row
   constexpr int KS = D / 16;  // 16-wide k steps of q . k
   constexpr int R = 16 * MT;  // pairs of the tile
-  // scores by position [R][256] fp32, then P_hi and P_lo [R][256] in their
+  // scores by position [R][256] fp32 (rows kScoreLd apart: eight rows at one
+  // position would share a bank), then P_hi and P_lo [R][256] in their
   // place (8-key chunk kc of row r at chunk kc ^ (r & 7)); a row of zeros; the
   // path of each node of the tile; K, then V (rows of 16-byte chunks, chunk c of
   // row r at chunk c ^ (r & 7)): up to 256 context keys, or up to 255 and the
@@ -75,7 +79,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
   unsigned char* pt = smem_raw;
   unsigned char* pt_lo = pt + R * kSplit * 2;
   float* scores = reinterpret_cast<float*>(pt);
-  unsigned char* zrow = pt_lo + R * kSplit * 2;
+  unsigned char* zrow = pt + R * kScoreLd * 4;
   unsigned char* paths = zrow + D * 2;  // [R >> gs][64]
   unsigned char* kv = paths + (R >> p.gs) * kTreeMaxNodes;
   __shared__ TreeInfo ti;
@@ -122,8 +126,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
     }
     cp_async_commit();
   };
-  load(p.k);
-
+  // The tile's q rows first (into the scores' place, chunks swizzled as K's),
+  // then the tree, then the long loads: small loads behind K's would wait for it.
+  // Row r of the tile is pair r: node n0 + r / G, query head g G + r % G.
+  for (int idx = t; idx < (nodes << gs) * C8; idx += kThreads) {
+    const int r = idx / C8, ch = idx % C8;
+    cp_async16(pt_base + static_cast<uint32_t>(r * D * 2 + ((ch ^ (r & 7)) << 4)),
+               p.q + (static_cast<int64_t>(off + n0 + (r >> gs)) * p.Hq + (g << gs) + (r & ((1 << gs) - 1))) * D + ch * 8);
+  }
   if (tail) {
     if (warp == 0) {
       tree_load(p.tree, b, ti);
@@ -133,27 +143,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
     }
     for (int i = t; i < D * 2 / 16; i += kThreads) *reinterpret_cast<uint4*>(zrow + 16 * i) = make_uint4(0, 0, 0, 0);
   }
-
-  // q fragments (A operand), straight from global: MMA row r of tile mt is pair
-  // 16 mt + r, node n0 + pair / G, query head g G + pair % G
-  uint32_t qa[MT][KS][4];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int r_lo = mt * 16 + gq, r_hi = r_lo + 8;
-    auto row = [&](int r) -> const __nv_bfloat16* {
-      return r >> gs < nodes
-                 ? p.q + (static_cast<int64_t>(off + n0 + (r >> gs)) * p.Hq + (g << gs) + (r & ((1 << gs) - 1))) * D
-                 : nullptr;
-    };
-    const __nv_bfloat16 *q_lo = row(r_lo), *q_hi = row(r_hi);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int d0 = ks * 16 + 2 * tq;
-      qa[mt][ks][0] = q_lo ? *reinterpret_cast<const uint32_t*>(q_lo + d0) : 0u;
-      qa[mt][ks][1] = q_hi ? *reinterpret_cast<const uint32_t*>(q_hi + d0) : 0u;
-      qa[mt][ks][2] = q_lo ? *reinterpret_cast<const uint32_t*>(q_lo + d0 + 8) : 0u;
-      qa[mt][ks][3] = q_hi ? *reinterpret_cast<const uint32_t*>(q_hi + d0 + 8) : 0u;
-    }
+  load(p.k);
+  // V follows into the same buffer once K has been read: towards L2 meanwhile
+  for (int idx = t; idx < rows * D / 64; idx += kThreads) {
+    const int r = idx / (D / 64), slot = r < c ? k0 + r : ctx + r - c;
+    prefetch_l2(p.v + seq_off + static_cast<int64_t>(slot) * p.tok_stride + idx % (D / 64) * 64);
   }
   cp_async_wait<0>();
   __syncthreads();
@@ -168,6 +162,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
       if (ti.mask[n0 + i] >> j & 1) paths[i * kTreeMaxNodes + depth[j]] = static_cast<unsigned char>(j);
     }
   }
+  // q fragments (A operand): MMA row r of tile mt is pair 16 mt + r (rows of no
+  // pair hold anything, and so do their results, which nothing reads)
+  uint32_t qa[MT][KS][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int r = mt * 16 + (lane & 15), ch = 2 * ks + (lane >> 4);
+      ldsm_x4(pt_base + static_cast<uint32_t>(r * D * 2 + ((ch ^ (r & 7)) << 4)), qa[mt][ks][0], qa[mt][ks][1],
+              qa[mt][ks][2], qa[mt][ks][3]);
+    }
+  __syncthreads();  // the scores take q's place
 
   // scores of eight key rows (from `key0`) against the tile's pairs
   auto score_block = [&](int key0, float (&sc)[MT][4]) {
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            if (j < 0 || (mask[mt][h] >> j & 1)) scores[(mt * 16 + h * 8 + gq) * kSplit + at] = one[mt][2 * h + e];
+            if (j < 0 || (mask[mt][h] >> j & 1)) scores[(mt * 16 + h * 8 + gq) * kScoreLd + at] = one[mt][2 * h + e];
       }
     }
     __syncthreads();
@@ -232,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float* row = scores + (mt * 16 + h * 8 + gq) * kSplit + warp * 32 + 2 * tq;
+        const float* row = scores + (mt * 16 + h * 8 + gq) * kScoreLd + warp * 32 + 2 * tq;
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
           const float2 v = *reinterpret_cast<const float2*>(row + nb * 8);
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
     for (int h = 0; h < 2; ++h) {
       if (cnt[mt][h] <= 0) continue;
       const int pair = mt * 16 + h * 8 + gq;
-      const int64_t at = partial_at(p, b * p.Hkv + g, tile * MT + mt, s);
+      const int64_t at = partial_at(p, (b * p.Hkv + g) * p.groups + tile * MT + mt, s);
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb)
         *reinterpret_cast<float2*>(p.ws_o + at * D + ((2 * warp + nb) * 16 + h * 8 + gq) * 8 + 2 * tq) =
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
         *reinterpret_cast<float2*>(p.ws_ml + (at + h * 8 + gq) * 2) = make_float2(m[mt][h], l);
       }
     }
-  if (s == 0 && tile == 0 && t == 0) p.ws_cov[b * p.Hkv + g] = 1;
+  if (s == 0 && t == 0 && tile * R % 128 == 0) p.ws_cov[(b * p.Hkv + g) * p.groups + tile * MT] = 1;
 }
 
 // ---------------------------------------------------------------------------
@@ -400,10 +406,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
 // pairs of one (sequence, kv head) against 256 keys, the arithmetic of the
 // prefill kernel without a mask, each split's (m, l, o) stored as a partial.
 //
-// A step is (sequence, kv head, split, tile of 128 pairs).  The steps of all
-// sequences, tiles fastest (a split's further tiles find its K and V in L2),
-// then splits, are dealt to the blocks (one per SM) in equal runs, counted on
-// the device from the trees' own numbers.
+// A step is (sequence, kv head, tile of 128 pairs, split), a chain the steps of a
+// (sequence, kv head, tile).  The steps of all chains, one chain after the other,
+// are dealt to the blocks (one per SM) in equal runs, counted on the device from
+// the trees' own numbers.
 // Roles (18 warps): warps 0-15 take the softmax, four threads per pair: warp w
 // holds TMEM lanes 32 (w % 4) .. + 31 (lane = pair) and keys 64 (w / 4) ..
 // + 63 of each split, so a tile's softmax is four warps deep on every
@@ -416,11 +422,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
 // in issue order: step i + 1's scores of keys 128 h .. follow step i's P.V of
 // chunks 2h and 2h + 1, which read the P that they overwrite; the softmax
 // threads store step i - 1's O while step i's P.V runs.
-// A block whose run begins a (sequence, kv head) at split 0 folds the splits it
-// takes from there on with the merge kernel's arithmetic (32 columns of a pair
-// per thread) and leaves their state as the partial of split 0 (ws_cov: how many
-// splits that is); only the splits of a run's first, already begun sequence and
-// of trees with more than one tile leave a partial each.
+// A block folds the splits of every chain that it begins (at split 0) with the
+// merge kernel's arithmetic (32 columns of a pair per thread) and leaves their
+// state as the partial of split 0 (ws_cov: how many splits that is); only the
+// splits of a chain that another block began leave a partial each.
 // The partials leave through shared memory and bulk copies: stored straight from
 // registers they held up every other shared-memory access of the SM for about
 // 2,500 cycles a step (21 - 25 bytes a cycle).
@@ -431,27 +436,27 @@ constexpr int kTcBars = 15;
 constexpr int kStage = 2048;     // bytes a warp stages at a time: two groups x two 8-column chunks
 
 struct StepCursor {
-  int b, g, s, tile;
-  int ctx, off;            // of the sequence
+  int b, g, tile, s;
+  int off;                  // of the sequence
   int pairs, splits, tiles;
 };
 
 // Sequence c.b's numbers; returns its steps.
 __device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, StepCursor& c) {
-  int n;
+  int n, ctx;
   c.splits = c.tiles = 0;
-  if (!tree_bounds(p.tree, c.b, n, c.ctx, c.off)) return 0;
+  if (!tree_bounds(p.tree, c.b, n, ctx, c.off)) return 0;
   c.pairs = n << p.gs;
-  c.splits = c.ctx / kSplit;
+  c.splits = ctx / kSplit;
   c.tiles = (c.pairs + kTcPairs - 1) / kTcPairs;
   return static_cast<int64_t>(p.Hkv) * c.splits * c.tiles;
 }
-// The next step; whether it begins another (sequence, kv head).
+// The next step; whether it begins another chain.
 __device__ __forceinline__ bool cursor_next(const TreeAttnParams& p, StepCursor& c) {
-  if (++c.tile < c.tiles) return false;
-  c.tile = 0;
   if (++c.s < c.splits) return false;
   c.s = 0;
+  if (++c.tile < c.tiles) return true;
+  c.tile = 0;
   if (++c.g < p.Hkv) return true;
   c.g = 0;
   while (++c.b < p.tree.B && cursor_load(p, c) == 0) {
@@ -483,9 +488,9 @@ __device__ __forceinline__ void cursor_start(const TreeAttnParams& p, StepCursor
     const bool here = before + incl - mine <= u0 && u0 < before + incl;
     if (here) {
       const int64_t u = u0 - (before + incl - mine);
-      c.tile = static_cast<int>(u % c.tiles);
-      c.s = static_cast<int>(u / c.tiles % c.splits);
-      c.g = static_cast<int>(u / c.tiles / c.splits);
+      c.s = static_cast<int>(u % c.splits);
+      c.tile = static_cast<int>(u / c.splits % c.tiles);
+      c.g = static_cast<int>(u / c.splits / c.tiles);
       out = c;
     }
     if (__any_sync(0xffffffffu, here)) return;
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ StepCursor start;
-  __shared__ StepCursor groups[16];  // of each softmax warp, advanced where its (sequence, kv head) changes
+  __shared__ StepCursor chains[16];  // of each softmax warp, advanced where its chain ends
   __shared__ int count_s;
   const uint32_t k_full = smem_addr(bars + 0), k_empty = smem_addr(bars + 1);
   const uint32_t v_full = smem_addr(bars + 2), v_empty = smem_addr(bars + 3);
@@ -568,29 +573,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0) {
       StepCursor c = start;
       const uint64_t q_pol = l2_policy_evict_last();
-      // a split that several tiles read stays in L2 until the last of them
-      const uint64_t first_pol = l2_policy_evict_first();
+      const uint64_t kv_pol = l2_policy_evict_first();
       auto load_k = [&](bool new_q) {
         mbar_arrive_expect_tx(k_full, KV_BYTES + (new_q ? Q_BYTES : 0));
         if (new_q)
           for (int ds = 0; ds < DS; ++ds)
             tma_load_3d(smem_addr(q_s + ds * Q_SLICE), &tmQ, 64 * ds, c.g << p.gs, c.off + (c.tile * kTcPairs >> p.gs),
                         k_full, q_pol);
-        const uint64_t pol = c.tile + 1 < c.tiles ? q_pol : first_pol;
+        // keys that other tiles read too should stay in L2
         for (int ds = 0; ds < DS; ++ds)
-          tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full, pol);
+          tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full,
+                      c.tiles > 1 ? q_pol : kv_pol);
       };
       auto load_v = [&]() {
         mbar_arrive_expect_tx(v_full, KV_BYTES);
-        const uint64_t pol = c.tile + 1 < c.tiles ? q_pol : first_pol;
         for (int ds = 0; ds < DS; ++ds)
-          tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, c.g, c.s * kSplit, c.b, v_full, pol);
+          tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, c.g, c.s * kSplit, c.b, v_full,
+                      c.tiles > 1 ? q_pol : kv_pol);
       };
       load_k(true);
       load_v();
       int k_issued = 1, v_issued = 1;
       for (int i = 0; i + 1 < count; ++i) {
-        const bool new_q = cursor_next(p, c) || c.tiles > 1;
+        const bool new_q = cursor_next(p, c);
         bool ok = !abort_flag && mbar_wait_bounded(k_empty, i & 1, status, DEV_TIMEOUT_ATTN);
         if (ok) {
           load_k(new_q);
@@ -721,12 +726,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     // the state of the splits folded so far (l of the first quarter's threads only)
     float o_acc[DQ], m_acc = 0.f, l_acc = 0.f;
-    // what the last step left, of the same (sequence, kv head): its place, live
-    // pairs and statistics
-    int tile_prev = 0, s_prev = 0, live_prev = 0;
+    // what the last step left: its place, live pairs and statistics, whether it
+    // is folded, and (end_prev) whether the state is complete with it
+    int group_prev = 0, s_prev = 0, live_prev = 0;
     float m_prev = 0.f, l_prev = 0.f;
-    bool folding = false;  // this (sequence, kv head) is folded
-    int bg = 0;            // its b * Hkv + g
+    bool fold_prev = false, end_prev = false;
     // takes step i's O: folds it, or sends it as a partial
     auto take_o = [&](int i) {
       check(mbar_wait_bounded(o_full(i & 1), (i >> 1) & 1, status, DEV_TIMEOUT_ATTN));
@@ -737,8 +741,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tmem_ld32(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
         else
           tmem_ld16(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
-        if (!folding) {
-          send(v, partial_at(p, bg, (tile_prev * kTcPairs + quad * 32) >> 4, s_prev), live_prev > 16);
+        if (!fold_prev) {
+          send(v, partial_at(p, group_prev, s_prev), live_prev > 16);
         } else if (s_prev == 0) {
           // the merge's first step: 0 * 0 + x * 1
           m_acc = m_prev;
@@ -758,29 +762,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       tc_fence_before();
       mbar_arrive(o_empty(i & 1));
-    };
-    // the state of `splits` folded splits as the partial of split 0
-    auto leave_state = [&](int splits) {
-      if (live_prev > 0) {
-        const int64_t at = partial_at(p, bg, quad * 2, 0);
-        uint32_t v[DQ];
+      if (fold_prev && end_prev && ok) {  // the state as the partial of split 0
+        if (live_prev > 0) {
+          const int64_t at = partial_at(p, group_prev, 0);
+          uint32_t v[DQ];
 #pragma unroll
-        for (int d = 0; d < DQ; ++d) v[d] = __float_as_uint(o_acc[d]);
-        send(v, at, live_prev > 16);
-        if (j == 0 && lane < live_prev)
-          *reinterpret_cast<float2*>(p.ws_ml + (at + (lane >> 4) * (static_cast<int64_t>(p.S) * 16) + (lane & 15)) * 2) =
-              make_float2(m_acc, l_acc);
+          for (int d = 0; d < DQ; ++d) v[d] = __float_as_uint(o_acc[d]);
+          send(v, at, live_prev > 16);
+          if (j == 0 && lane < live_prev)
+            *reinterpret_cast<float2*>(p.ws_ml + (at + (lane >> 4) * (static_cast<int64_t>(p.S) * 16) + (lane & 15)) * 2) =
+                make_float2(m_acc, l_acc);
+        }
+        if (warp == 0 && lane == 0) p.ws_cov[group_prev] = s_prev + 1;
       }
-      if (warp == 0 && lane == 0) p.ws_cov[bg] = splits;
     };
-    int s = start.s, tile = start.tile, pairs = start.pairs, splits = start.splits, tiles = start.tiles;
-    if (lane == 0) groups[warp] = start;
-    bg = start.b * p.Hkv + start.g;
-    folding = s == 0 && tiles == 1;
-    bool pending = false;  // the last step's O is not taken yet
+    // the chain: its last step, this warp's live pairs (the same for the
+    // quadrant's four warps) and first group, whether this block folds it
+    int s = start.s, end, live, group;
+    bool folding = s == 0;
+    auto begin_chain = [&](const StepCursor& c) {
+      end = c.splits;
+      live = min(32, c.pairs - c.tile * kTcPairs - quad * 32);
+      group = (c.b * p.Hkv + c.g) * p.groups + c.tile * (kTcPairs / 16) + quad * 2;
+    };
+    begin_chain(start);
+    if (lane == 0) chains[warp] = start;
     for (int i = 0; i < count; ++i) {
-      const int pair0 = tile * kTcPairs + quad * 32;
-      const int live = min(32, pairs - pair0);  // of the warp's 32 pairs (the same for the quadrant's four warps)
       check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
       if (live > 0) {
@@ -842,46 +849,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int q = 1; q < 8; ++q) l = __fadd_rn(l, x_sum[q * kTcPairs + pr]);
         if (!folding)
-          *reinterpret_cast<float2*>(p.ws_ml + (partial_at(p, bg, pair0 >> 4, s) + (lane >> 4) * (static_cast<int64_t>(p.S) * 16) + (lane & 15)) * 2) =
+          *reinterpret_cast<float2*>(p.ws_ml + (partial_at(p, group, s) + (lane >> 4) * (static_cast<int64_t>(p.S) * 16) + (lane & 15)) * 2) =
               make_float2(m, l);
       }
-      if (!folding && s == 0 && tile == 0 && warp == 0 && lane == 0) p.ws_cov[bg] = 1;
-      if (pending) take_o(i - 1);
-      pending = true;
-      tile_prev = tile;
+      if (i > 0) take_o(i - 1);
+      group_prev = group;
       s_prev = s;
       live_prev = live;
       m_prev = m;
       l_prev = l;
-      bool end = false;  // of this (sequence, kv head)
-      if (++tile == tiles) {
-        tile = 0;
-        end = ++s == splits;
-      }
-      if (end || i + 1 == count) {
-        // its last O now, and its state
-        take_o(i);
-        pending = false;
-        if (folding && ok) leave_state(s);
-      }
-      if (end && i + 1 < count) {
+      fold_prev = folding;
+      ++s;
+      end_prev = s == end || i + 1 == count;
+      if (s == end && i + 1 < count) {
         if (lane == 0) {
-          StepCursor c = groups[warp];
-          c.tile = c.tiles - 1;
+          StepCursor c = chains[warp];
           c.s = c.splits - 1;
           cursor_next(p, c);
-          groups[warp] = c;
+          chains[warp] = c;
         }
         __syncwarp();
-        s = 0;
-        pairs = groups[warp].pairs;
-        splits = groups[warp].splits;
-        tiles = groups[warp].tiles;
-        bg = groups[warp].b * p.Hkv + groups[warp].g;
-        folding = tiles == 1;
+        begin_chain(chains[warp]);
         __syncwarp();
+        s = 0;
+        folding = true;
       }
     }
+    if (ok) take_o(count - 1);
     if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
@@ -915,12 +909,13 @@ __global__ void __launch_bounds__(kMergeThreads, 8) attn_tree_merge_kernel(const
   int n, ctx, off;
   if (!tree_bounds(p.tree, b, n, ctx, off) || pair0 >= n << p.gs) return;
   const bool live = pair < n << p.gs;
-  const int64_t at = partial_at(p, b * p.Hkv + g, pair0 >> 4, 0) + (lane >> 1);
+  const int group = (b * p.Hkv + g) * p.groups + (pair0 >> 4);
+  const int64_t at = partial_at(p, group, 0) + (lane >> 1);
   const float* ml_at = p.ws_ml + at * 2;
-  const float* o_at = p.ws_o + partial_at(p, b * p.Hkv + g, pair0 >> 4, 0) * D + (k * 16 + (lane >> 1)) * 8 + (lane & 1) * 4;
+  const float* o_at = p.ws_o + partial_at(p, group, 0) * D + (k * 16 + (lane >> 1)) * 8 + (lane & 1) * 4;
   // partial q of the fold: 0 stands for the first cov splits, the others for one
   // each (clamped: the count of a tree that is left out was never written)
-  const int cov = max(1, min(p.ws_cov[b * p.Hkv + g], ctx / kSplit));
+  const int cov = max(1, min(p.ws_cov[group - (pair0 >> 4) % 8], ctx / kSplit));
   float2 ml[CH];
   float4 o[CH];
   auto load = [&](int q0, int nq) {
@@ -969,7 +964,7 @@ kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
   void (*kernel)(const TreeAttnParams) = attn_tree_split_kernel<D, MT>;
   // 256 key rows, or up to 255 and the drafted ones; scores are taken eight rows at a time
   const int kv_rows = kSplit + (p.tree.max_nodes + 7) / 8 * 8;
-  const size_t smem = 2 * 16 * MT * kSplit * 2 + D * 2 + (16 * MT / p.G) * kTreeMaxNodes + static_cast<size_t>(kv_rows) * D * 2;
+  const size_t smem = 16 * MT * kScoreLd * 4 + D * 2 + (16 * MT / p.G) * kTreeMaxNodes + static_cast<size_t>(kv_rows) * D * 2;
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (attr != KINV_OK) return attr;
   const int tiles = (p.tree.max_nodes * p.G + 16 * MT - 1) / (16 * MT);
@@ -1033,7 +1028,7 @@ struct TreeWorkspace {
     o = 0;
     ml = o + static_cast<size_t>(pairs) * D * 4;
     cov = ml + static_cast<size_t>(pairs) * 8;
-    bytes = 256 + cov + static_cast<size_t>(B) * Hkv * 4;  // 256 to align the base
+    bytes = 256 + cov + static_cast<size_t>(B * Hkv * groups) * 4;  // 256 to align the base
   }
 };
 
@@ -1070,6 +1065,7 @@ extern "C" kinv_status kinv_attn_tree(const void* q, const void* k_cache, const 
   const int64_t S = (static_cast<int64_t>(tree->max_kv) + kSplit - 1) / kSplit;
   if (S > 65535) return KINV_ERR_UNSUPPORTED;
   const TreeWorkspace w(tree->B, tree->max_nodes, Hq, Hkv, D, S);
+  if (static_cast<int64_t>(tree->B) * Hkv * w.groups > 0x7fffffff) return KINV_ERR_UNSUPPORTED;
   if (workspace_bytes < w.bytes) return KINV_ERR_WORKSPACE;
   TreeAttnParams p{};
   p.tree = *tree;
