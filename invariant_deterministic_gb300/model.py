@@ -170,17 +170,24 @@ class Decoder:
             self.hist_len[b] = len(tail)
 
     # --------------------------------------------------------------- a layer
-    def layer(self, li: int, rows: int, seq, pos, attention) -> None:
+    def layer(self, li: int, rows: int, seq, pos, attention, tree=None) -> None:
         """One decoder layer on rows [0, rows): ``x`` holds the residual stream
         and ``ss`` its per-tile sums of squares; row r is sequence seq[r] at
-        position pos[r].  Leaves the updated stream and sums in place."""
+        position pos[r], or, with a kinv.Tree, a node of it.  Leaves the updated
+        stream and sums in place."""
         s, lw = self.s, self.w["layers"][li]
         x = self.x[:rows]
         norm_in = kinv.norm_in(self.ss[:rows], s.d_model, s.eps)
         kc, vc = self.kv[li, 0], self.kv[li, 1]
         qn = lw.get("q_norm") if s.qk_norm else None
         kn = lw.get("k_norm") if s.qk_norm else None
-        if FUSED_ROPE_MIN_ROWS <= rows <= FUSED_ROPE_MAX_ROWS:
+        if tree is not None:
+            with self._t("gemm_qkv"):
+                kinv.gemm_fused(x, self.w_qkv_f[li], norm_in, out=self.qkv[:rows])
+            with self._t("rope_append"):
+                kinv.rope_append_tree(self.qkv[:rows], self.q[:rows], kc, vc, tree, s.n_q, s.n_kv,
+                                      s.head_dim, s.rope_base, qn, kn, s.eps)
+        elif FUSED_ROPE_MIN_ROWS <= rows <= FUSED_ROPE_MAX_ROWS:
             # the QKV projection with RoPE and the KV append in its epilogue
             with self._t("gemm_qkv"):
                 kinv.gemm_qkv_rope(x, self.w_qkv_f[li], self.q[:rows], kc, vc, seq, pos, s.n_q, s.n_kv,
@@ -233,6 +240,57 @@ class Decoder:
             with self._t("decode_advance"):
                 kinv.decode_advance(self.tokens[:bsz], self.history[:bsz], self.hist_len[:bsz],
                                     self.step[:bsz], pos=self.pos[:bsz], kv_len=self.kv_len[:bsz])
+
+    # ---------------------------------------------------------- drafted trees
+    def tree_layers(self, tree, rows: int) -> None:
+        """All layers for the nodes of a kinv.Tree (rows [0, rows) of x hold
+        their tokens' embeddings); their keys and values go into the cache slots
+        behind each sequence's context, and x ends as the final residual stream.
+        Every row has the bits of the decode step that would follow its path."""
+        need = kinv.attn_tree_workspace(tree, self.s.n_q, self.s.n_kv, self.s.head_dim)
+        if need > self.ws.numel():
+            self.ws = torch.empty(need, dtype=torch.uint8, device=self.dev)
+
+        def attention(li, n, kc, vc):
+            with self._t("attn_tree"):
+                kinv.attn_tree(self.q[:n], kc, vc, tree, out=self.attn[:n], workspace=self.ws)
+        with self._t("row_sumsq"):
+            kinv.row_sumsq(self.x[:rows], self.ss[:rows])
+        for li in range(self.s.n_layers):
+            self.layer(li, rows, None, None, attention, tree=tree)
+
+    def lm_head(self, row0: int, out) -> torch.Tensor:
+        """Logits (final RMSNorm folded in) of rows row0 .. of the residual
+        stream, as many as ``out`` has rows."""
+        n = out.shape[0]
+        with self._t("gemm_lm_head"):
+            kinv.gemm_fused(self.x[row0: row0 + n], self.lm_head_f,
+                            kinv.norm_in(self.ss[row0: row0 + n], self.s.d_model, self.s.eps), out=out)
+        return out
+
+    # --------------------------------------------------------------- scoring
+    def score(self, seq: int, tokens: torch.Tensor, top_k: int = 0, chunk: int = 0):
+        """Prefills ``tokens`` (int32, device) as positions 0.. of sequence
+        ``seq`` and returns, for the rows of all but the last, (log probability
+        of the next token [n - 1], entropy [n - 1], top ids and log probabilities
+        [n - 1][top_k] or None).  A row's numbers do not depend on the chunking."""
+        n = int(tokens.shape[0])
+        if n < 2:
+            raise ValueError("score: at least two tokens are needed")
+        chunk = min(chunk or self.max_rows, self.max_rows)
+        got = []
+        for c0 in range(0, n - 1, chunk):
+            rows = min(chunk, n - 1 - c0)
+            kinv.embed(self.w["embed"], tokens[c0: c0 + rows], out=self.x[:rows])
+            self.prefill_chunk(seq, c0, rows)
+            for r0 in range(0, rows, self.B):  # as many rows at a time as the logits hold
+                m = min(self.B, rows - r0)
+                logits = self.lm_head(r0, self.logits[:m])
+                ids = tokens[c0 + r0 + 1: c0 + r0 + 1 + m].view(m, 1)
+                got.append(kinv.logprobs(logits, ids, top_k=top_k))
+        lp, ent, ids, top = zip(*got)
+        return (torch.cat(lp)[:, 0], torch.cat(ent), torch.cat(ids) if top_k else None,
+                torch.cat(top) if top_k else None)
 
     # --------------------------------------------------------------- prefill
     def prefill_chunk(self, seq: int, p0: int, rows: int) -> None:

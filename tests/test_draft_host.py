@@ -1,0 +1,77 @@
+"""The drafter's trees and the checks of drafted steps (no GPU)."""
+import pytest
+
+from invariant_deterministic_gb300 import draft
+
+
+def _paths(nodes, parents):
+    out = []
+    for i in range(len(nodes)):
+        p, j = [], i
+        while j >= 0:
+            p.insert(0, nodes[j])
+            j = parents[j]
+        out.append(p)
+    return out
+
+
+def test_ngram_tree_follows_earlier_occurrences():
+    #        0  1  2  3  4  5  6  7  8
+    tokens = [1, 2, 3, 9, 1, 2, 4, 1, 2]
+    nodes, parents = draft.ngram_tree(tokens, 64, n=2, depth=3)
+    paths = _paths(nodes, parents)
+    assert nodes[0] == 2 and parents[0] == -1
+    assert [2, 4, 1, 2] in paths and [2, 3, 9, 1] in paths     # after (1, 2): the latest first
+    assert all(0 <= p < i for i, p in enumerate(parents) if i)
+    assert len({tuple(p) for p in paths}) == len(paths)         # no two nodes say the same
+
+
+@pytest.mark.parametrize("most", [1, 2, 3, 5])
+def test_ngram_tree_keeps_its_size(most):
+    nodes, parents = draft.ngram_tree([5, 6] * 10, most)
+    assert 1 <= len(nodes) <= most and len(nodes) == len(parents)
+
+
+def test_ngram_tree_without_an_occurrence():
+    assert draft.ngram_tree([7], 8) == ([7], [-1])
+    assert draft.ngram_tree([1, 2, 3], 8) == ([3], [-1])
+
+
+class _Dec:
+    B, Lmax, hist_ld, max_rows = 2, 10, 4, 8
+
+
+def _dd(requests):
+    d = draft.DraftDecoder.__new__(draft.DraftDecoder)
+    d.dec, d.max_nodes, d.requests, d.prompt_len = _Dec, 4, requests, [2] * len(requests)
+    return d
+
+
+def test_step_inputs():
+    d = _dd([[1, 2, 3], [8, 9]])
+    token, parent, owner, step, n, hist, hist_len = d._inputs([([3, 4, 5, 6], [-1, 0, 0, 2]), ([], [])])
+    assert token == [3, 4, 5, 6] and parent == [-1, 0, 0, 2] and owner == [0] * 4 and n == [4, 0]
+    assert step == [1, 2, 2, 3]                                  # one token decided, then the path's
+    assert hist[0] == [1, 2, 3, 0] and hist_len[0] == 3
+    assert hist[1] == [1, 2, 3, 4] and hist[3] == [2, 3, 5, 6] and hist_len[3] == 4
+
+
+@pytest.mark.parametrize("tree", [([4], [-1]), ([3], [0]), ([3, 4], [-1]), ([3] * 5, [-1, 0, 1, 2, 3]),
+                                  ([3, 4], [-1, 1]), ([3, 4], [-1, -1])])
+def test_step_refuses_broken_trees(tree):
+    with pytest.raises(ValueError):
+        _dd([[1, 2, 3]])._inputs([tree])
+
+
+def test_step_refuses_a_tree_past_the_cache():
+    with pytest.raises(ValueError):
+        _dd([list(range(9))])._inputs([([8, 1, 2], [-1, 0, 1])])
+
+
+def test_decoder_limits():
+    class D:
+        B, max_rows = 4, 63
+    with pytest.raises(ValueError):
+        draft.DraftDecoder(D, 16)
+    with pytest.raises(ValueError):
+        draft.DraftDecoder(D, 65)
