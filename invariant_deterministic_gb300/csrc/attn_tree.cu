@@ -406,10 +406,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
 // pairs of one (sequence, kv head) against 256 keys, the arithmetic of the
 // prefill kernel without a mask, each split's (m, l, o) stored as a partial.
 //
-// A step is (sequence, kv head, tile of 128 pairs, split), a chain the steps of a
-// (sequence, kv head, tile).  The steps of all chains, one chain after the other,
-// are dealt to the blocks (one per SM) in equal runs, counted on the device from
-// the trees' own numbers.
+// A step is (sequence, kv head, split, tile of 128 pairs).  The steps are dealt to
+// the blocks (one per SM) in equal runs of T, counted on the device from the
+// trees' own numbers.  A block folds the splits that it takes from split 0 on, so
+// the order of the steps keeps such beginnings whole: first the first T splits of
+// every (sequence, kv head) that has more, a run each, then the shorter ones one
+// after the other, then all the rest, whose splits leave a partial each (also
+// those of trees of more than one tile, tiles fastest: a split's further tiles
+// find its K and V in L2).  A chain is a run of steps with the same rows.
 // Roles (18 warps): warps 0-15 take the softmax, four threads per pair: warp w
 // holds TMEM lanes 32 (w % 4) .. + 31 (lane = pair) and keys 64 (w / 4) ..
 // + 63 of each split, so a tile's softmax is four warps deep on every
@@ -422,10 +426,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
 // in issue order: step i + 1's scores of keys 128 h .. follow step i's P.V of
 // chunks 2h and 2h + 1, which read the P that they overwrite; the softmax
 // threads store step i - 1's O while step i's P.V runs.
-// A block folds the splits of every chain that it begins (at split 0) with the
-// merge kernel's arithmetic (32 columns of a pair per thread) and leaves their
-// state as the partial of split 0 (ws_cov: how many splits that is); only the
-// splits of a chain that another block began leave a partial each.
+// The fold takes the merge kernel's arithmetic (32 columns of a pair per thread);
+// the state of a block's splits is left as the partial of split 0 (ws_cov: how
+// many splits that is).
 // The partials leave through shared memory and bulk copies: stored straight from
 // registers they held up every other shared-memory access of the SM for about
 // 2,500 cycles a step (21 - 25 bytes a cycle).
@@ -436,31 +439,47 @@ constexpr int kTcBars = 15;
 constexpr int kStage = 2048;     // bytes a warp stages at a time: two groups x two 8-column chunks
 
 struct StepCursor {
-  int b, g, tile, s;
+  int part;                 // 0: beginnings of T splits, 1: whole short chains, 2: the rest
+  int b, g, s, tile;
   int off;                  // of the sequence
-  int pairs, splits, tiles;
+  int pairs, tiles;
+  int lo, splits;           // splits lo .. splits - 1 of a (sequence, kv head) belong to the part
+  int T;
 };
 
-// Sequence c.b's numbers; returns its steps.
-__device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, StepCursor& c) {
+// Sequence c.b's numbers; returns its steps in c.part, or in all of them.
+__device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, StepCursor& c, bool all = false) {
   int n, ctx;
-  c.splits = c.tiles = 0;
+  c.lo = c.splits = c.tiles = 0;
   if (!tree_bounds(p.tree, c.b, n, ctx, c.off)) return 0;
   c.pairs = n << p.gs;
-  c.splits = ctx / kSplit;
   c.tiles = (c.pairs + kTcPairs - 1) / kTcPairs;
-  return static_cast<int64_t>(p.Hkv) * c.splits * c.tiles;
+  const int splits = ctx / kSplit;
+  if (all)
+    c.splits = splits;
+  else if (c.tiles > 1)
+    c.splits = c.part == 2 ? splits : 0;
+  else if (splits <= c.T)
+    c.splits = c.part == 1 ? splits : 0;
+  else if (c.part != 1)
+    c.lo = c.part == 2 ? c.T : 0, c.splits = c.part == 2 ? splits : c.T;
+  return static_cast<int64_t>(p.Hkv) * (c.splits - c.lo) * c.tiles;
 }
 // The next step; whether it begins another chain.
 __device__ __forceinline__ bool cursor_next(const TreeAttnParams& p, StepCursor& c) {
-  if (++c.s < c.splits) return false;
-  c.s = 0;
   if (++c.tile < c.tiles) return true;
   c.tile = 0;
-  if (++c.g < p.Hkv) return true;
-  c.g = 0;
-  while (++c.b < p.tree.B && cursor_load(p, c) == 0) {
+  if (++c.s < c.splits) return c.tiles > 1;
+  if (++c.g >= p.Hkv) {
+    c.g = 0;
+    do {
+      if (++c.b >= p.tree.B) {
+        c.b = 0;
+        ++c.part;
+      }
+    } while (c.part < 3 && cursor_load(p, c) == 0);
   }
+  c.s = c.lo;
   return true;
 }
 
@@ -469,32 +488,38 @@ __device__ __forceinline__ void cursor_start(const TreeAttnParams& p, StepCursor
   const int lane = threadIdx.x & 31;
   int64_t total = 0;
   StepCursor c;
-  for (c.b = lane; c.b < p.tree.B; c.b += 32) total += cursor_load(p, c);
+  c.part = c.T = 0;
+  for (c.b = lane; c.b < p.tree.B; c.b += 32) total += cursor_load(p, c, true);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+  const int64_t T = (total + gridDim.x - 1) / gridDim.x;  // (far below 2^31 for any cache that memory holds)
+  const int64_t u0 = min(total, T * blockIdx.x), u1 = min(total, u0 + T);
   if (lane == 0) count = static_cast<int>(u1 - u0);
   if (u1 == u0) return;
+  c.T = static_cast<int>(T);
   int64_t before = 0;
-  for (int b0 = 0; b0 < p.tree.B; b0 += 32) {
-    c.b = b0 + lane;
-    const int64_t mine = c.b < p.tree.B ? cursor_load(p, c) : 0;
-    int64_t incl = mine;
+  for (c.part = 0; c.part < 3; ++c.part) {
+    for (int b0 = 0; b0 < p.tree.B; b0 += 32) {
+      c.b = b0 + lane;
+      const int64_t mine = c.b < p.tree.B ? cursor_load(p, c) : 0;
+      int64_t incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const bool here = before + incl - mine <= u0 && u0 < before + incl;
+      if (here) {
+        const int64_t u = u0 - (before + incl - mine);
+        const int splits = c.splits - c.lo;
+        c.tile = static_cast<int>(u % c.tiles);
+        c.s = c.lo + static_cast<int>(u / c.tiles % splits);
+        c.g = static_cast<int>(u / c.tiles / splits);
+        out = c;
+      }
+      if (__any_sync(0xffffffffu, here)) return;
+      before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const bool here = before + incl - mine <= u0 && u0 < before + incl;
-    if (here) {
-      const int64_t u = u0 - (before + incl - mine);
-      c.s = static_cast<int>(u % c.splits);
-      c.tile = static_cast<int>(u / c.splits % c.tiles);
-      c.g = static_cast<int>(u / c.splits / c.tiles);
-      out = c;
-    }
-    if (__any_sync(0xffffffffu, here)) return;
-    before += __shfl_sync(0xffffffffu, incl, 31);
   }
 }
 
@@ -546,10 +571,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 0) cursor_start(p, start, count_s);
   __syncthreads();
   const int count = count_s;
-  if (count == 0) {
-    pdl_launch_dependents();
-    return;
-  }
+  // (no early launch of the merge: its blocks beside these cost 25 us of 130 at
+  // 64 nodes behind 32,000 keys)
+  if (count == 0) return;
   if (t == 0) {
     for (int i = 0; i < kTcBars; ++i) {
       // p_full: the 128 threads of its chunk; o_empty: every softmax thread
@@ -564,7 +588,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  pdl_launch_dependents();  // after the TMEM allocation
   int* status = p.status;
 
   if (warp == 17) {
@@ -580,16 +603,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int ds = 0; ds < DS; ++ds)
             tma_load_3d(smem_addr(q_s + ds * Q_SLICE), &tmQ, 64 * ds, c.g << p.gs, c.off + (c.tile * kTcPairs >> p.gs),
                         k_full, q_pol);
-        // keys that other tiles read too should stay in L2
+        // keys that another tile is about to read should stay in L2
         for (int ds = 0; ds < DS; ++ds)
           tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full,
-                      c.tiles > 1 ? q_pol : kv_pol);
+                      c.tile + 1 < c.tiles ? q_pol : kv_pol);
       };
       auto load_v = [&]() {
         mbar_arrive_expect_tx(v_full, KV_BYTES);
         for (int ds = 0; ds < DS; ++ds)
           tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, c.g, c.s * kSplit, c.b, v_full,
-                      c.tiles > 1 ? q_pol : kv_pol);
+                      c.tile + 1 < c.tiles ? q_pol : kv_pol);
       };
       load_k(true);
       load_v();
@@ -778,15 +801,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     // the chain: its last step, this warp's live pairs (the same for the
     // quadrant's four warps) and first group, whether this block folds it
-    int s = start.s, end, live, group;
-    bool folding = s == 0;
+    int s, end, live, group;
+    bool folding;
     auto begin_chain = [&](const StepCursor& c) {
-      end = c.splits;
+      s = c.s;
+      end = c.tiles > 1 ? s + 1 : c.splits;
+      folding = s == 0;
       live = min(32, c.pairs - c.tile * kTcPairs - quad * 32);
       group = (c.b * p.Hkv + c.g) * p.groups + c.tile * (kTcPairs / 16) + quad * 2;
     };
     begin_chain(start);
     if (lane == 0) chains[warp] = start;
+    __syncwarp();
     for (int i = 0; i < count; ++i) {
       check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
@@ -864,15 +890,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (s == end && i + 1 < count) {
         if (lane == 0) {
           StepCursor c = chains[warp];
-          c.s = c.splits - 1;
+          c.s = s - 1;
           cursor_next(p, c);
           chains[warp] = c;
         }
         __syncwarp();
         begin_chain(chains[warp]);
         __syncwarp();
-        s = 0;
-        folding = true;
       }
     }
     if (ok) take_o(count - 1);
