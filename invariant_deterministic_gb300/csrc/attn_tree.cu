@@ -26,9 +26,14 @@ constexpr int kSplit = 256;    // keys per split, as in decode and prefill
 constexpr int kThreads = 256;  // eight warps, 32 positions each for the softmax
 constexpr int kMaxG = 8;
 constexpr int kScoreLd = kSplit + 8;
-// From this many (sequence, kv head, split) triples the cache may hold, the
-// splits within the context go to the tcgen05 kernel.
-constexpr int kMinSplitsTc = 64;
+// The splits within the context go to the tcgen05 kernel where (sequence, kv
+// head, split) triples that the cache may hold, times the tree's pairs beyond 16,
+// reach this.  Device time of a call with it / without, D = 128, 4 heads a kv head:
+//   16 pairs: 8,000 triples 227 / 212 us (never: one MMA tile, bound by the loads)
+//   32 pairs: 500 triples 40 / 37 us, 1,024 65 / 62, 8,000 227 / 316
+//   64 pairs: 136 triples 23 / 20 us, 280 26 / 30, 1,152 69 / 105
+//   256 pairs: 16 triples 22 / 20 us, 32 24 / 28, 280 37 / 123
+constexpr int64_t kMinWorkTc = 8192;
 
 struct TreeAttnParams {
   kinv_tree tree;
@@ -984,11 +989,16 @@ __global__ void __launch_bounds__(kMergeThreads, 8) attn_tree_merge_kernel(const
 }
 
 template <int D, int MT>
-kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
-  void (*kernel)(const TreeAttnParams) = attn_tree_split_kernel<D, MT>;
+size_t split_smem_bytes(const TreeAttnParams& p) {
   // 256 key rows, or up to 255 and the drafted ones; scores are taken eight rows at a time
   const int kv_rows = kSplit + (p.tree.max_nodes + 7) / 8 * 8;
-  const size_t smem = 16 * MT * kScoreLd * 4 + D * 2 + (16 * MT / p.G) * kTreeMaxNodes + static_cast<size_t>(kv_rows) * D * 2;
+  return 16 * MT * kScoreLd * 4 + D * 2 + (16 * MT / p.G) * kTreeMaxNodes + static_cast<size_t>(kv_rows) * D * 2;
+}
+
+template <int D, int MT>
+kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
+  void (*kernel)(const TreeAttnParams) = attn_tree_split_kernel<D, MT>;
+  const size_t smem = split_smem_bytes<D, MT>(p);
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (attr != KINV_OK) return attr;
   const int tiles = (p.tree.max_nodes * p.G + 16 * MT - 1) / (16 * MT);
@@ -1023,12 +1033,16 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
   const size_t smem = ctx_smem_bytes<D>();
   const int sms = sm_count();
   CUtensorMap mq, mk, mv;
-  p.tail_only = static_cast<int64_t>(p.tree.B) * p.Hkv * (p.tree.max_kv / kSplit) >= kMinSplitsTc &&
-                smem <= static_cast<size_t>(max_smem_optin()) && encode_maps<D>(p, &mq, &mk, &mv);
-  // tiles of 16 pairs where they are the whole tree, or where tiles of 32 would
-  // leave SMs without a block
   const int pairs = p.tree.max_nodes * p.G;
-  const bool small = pairs <= 16 || static_cast<int64_t>(p.tree.B) * p.Hkv * ((pairs + 31) / 32) * (p.tail_only ? 1 : p.S) < sms;
+  p.tail_only = pairs > 16 && static_cast<int64_t>(p.tree.B) * p.Hkv * (p.tree.max_kv / kSplit) * (pairs - 16) >= kMinWorkTc &&
+                smem <= static_cast<size_t>(max_smem_optin()) && encode_maps<D>(p, &mq, &mk, &mv);
+  // tiles of 16 pairs where they are the whole tree, where tiles of 32 would leave
+  // SMs without a block, and where two blocks with tiles of 32 (and 3 KB of
+  // statistics) do not fit an SM (8 trees of 64 nodes behind 300 keys: 48 us a
+  // call against 53; with 32 nodes, where they fit, 33 against 28)
+  const bool small = pairs <= 16 ||
+                     static_cast<int64_t>(p.tree.B) * p.Hkv * ((pairs + 31) / 32) * (p.tail_only ? 1 : p.S) < sms ||
+                     2 * (split_smem_bytes<D, 2>(p) + 3072 + smem_reserved_per_block()) > static_cast<size_t>(smem_per_sm());
   kinv_status st = small ? launch_split<D, 1>(p, stream) : launch_split<D, 2>(p, stream);
   if (st != KINV_OK) return st;
   if (p.tail_only) {
