@@ -69,7 +69,8 @@ const char* kinv_build_id(void);
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device: KINV_OK, or the last code recorded since the previous call --
  * KINV_ERR_TIMEOUT (a bounded wait gave up), KINV_ERR_INVALID_ARG (an
- * attention call met a device-side length outside its stated bounds) or
+ * attention call met a device-side length outside its stated bounds, a call on
+ * drafted trees a broken tree, kinv_logprobs an id beyond the vocabulary) or
  * KINV_ERR_UNSUPPORTED (a sampler row outside the supported settings).
  * Returns KINV_ERR_CUDA if the synchronisation itself fails. */
 int kinv_last_device_status(kinv_stream stream);

@@ -62,6 +62,11 @@ class DraftDecoder:
         i32 = dict(dtype=torch.int32, device=dec.dev)
         self.logits = torch.zeros(rows, dec.s.vocab, dtype=torch.float32, device=dec.dev)
         self.sampled = torch.zeros(rows, **i32)
+        # for the widest step: every slot with max_nodes nodes, the whole cache
+        seqs, most = torch.zeros(dec.B, **i32), torch.zeros(rows, **i32)
+        widest = kinv.Tree(seqs, seqs, seqs, most, max_nodes, dec.Lmax)
+        self.ws = torch.empty(max(16, kinv.attn_tree_workspace(widest, dec.s.n_q, dec.s.n_kv, dec.s.head_dim)),
+                              dtype=torch.uint8, device=dec.dev)
         self.requests = []
 
     def start(self, prompts, params, chunk: int = 0) -> None:
@@ -120,7 +125,7 @@ class DraftDecoder:
         tree = kinv.Tree(up(ctx), up(n), up(np.cumsum([0] + n[:-1]).tolist()), up(parent), self.max_nodes, dec.Lmax)
         tokens = up(token)
         kinv.embed(dec.w["embed"], tokens, out=dec.x[:rows])
-        dec.tree_layers(tree, rows)
+        dec.tree_layers(tree, rows, self.ws)
         logits = dec.lm_head(0, self.logits[:rows])
         size = synth.SAMPLING_DTYPE.itemsize
         params = dec.params.view(-1, size)[up(owner, torch.int64)].contiguous()

@@ -242,18 +242,15 @@ class Decoder:
                                     self.step[:bsz], pos=self.pos[:bsz], kv_len=self.kv_len[:bsz])
 
     # ---------------------------------------------------------- drafted trees
-    def tree_layers(self, tree, rows: int) -> None:
+    def tree_layers(self, tree, rows: int, workspace) -> None:
         """All layers for the nodes of a kinv.Tree (rows [0, rows) of x hold
         their tokens' embeddings); their keys and values go into the cache slots
         behind each sequence's context, and x ends as the final residual stream.
-        Every row has the bits of the decode step that would follow its path."""
-        need = kinv.attn_tree_workspace(tree, self.s.n_q, self.s.n_kv, self.s.head_dim)
-        if need > self.ws.numel():
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.dev)
-
+        Every row has the bits of the decode step that would follow its path.
+        workspace: kinv.attn_tree_workspace(tree, ...) bytes, the caller's."""
         def attention(li, n, kc, vc):
             with self._t("attn_tree"):
-                kinv.attn_tree(self.q[:n], kc, vc, tree, out=self.attn[:n], workspace=self.ws)
+                kinv.attn_tree(self.q[:n], kc, vc, tree, out=self.attn[:n], workspace=workspace)
         with self._t("row_sumsq"):
             kinv.row_sumsq(self.x[:rows], self.ss[:rows])
         for li in range(self.s.n_layers):

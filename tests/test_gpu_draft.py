@@ -61,18 +61,16 @@ def test_drafted_decoding_gives_the_tokens_and_the_cache_of_decoding(M, name):
     dec = M.Decoder(shape, w, max_batch=4, max_len=lmax, max_chunk=64)
     want = M.run_requests(dec, prompts, params, steps)
     plain = dec.kv.clone()
-    for draft in (M.draft.ngram_tree, _guesser(want, prompts, 99), _guesser(want, prompts, 2),
-                  lambda t, n: ([t[-1]], [-1])):
+    for draft, most in ((M.draft.ngram_tree, steps), (_guesser(want, prompts, 99), steps - 1),
+                        (_guesser(want, prompts, 2), steps - 1), (lambda t, n: ([t[-1]], [-1]), steps)):
         d2 = M.Decoder(shape, w, max_batch=4, max_len=lmax, max_chunk=64)
         got, taken = M.draft.run_requests_drafted(d2, prompts, params, steps, draft=draft, max_nodes=nodes)
         assert got == want
-        assert taken <= steps
+        assert taken <= most  # right guesses are taken
         # the cache of all but the last token (which neither run has put there)
         for b, p in enumerate(prompts):
             n = len(p) + steps - 1
             assert_same_bits(d2.kv[:, :, b, :n], plain[:, :, b, :n], f"cache of request {b}")
-        if draft is not M.draft.ngram_tree and isinstance(draft, type(_guesser)) and draft.__name__ == "draft":
-            assert taken < steps  # right guesses are taken
         assert M.kinv.last_device_status() == 0
 
 
