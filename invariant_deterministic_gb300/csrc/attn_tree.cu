@@ -414,11 +414,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
 // A step is (sequence, kv head, split, tile of 128 pairs).  The steps are dealt to
 // the blocks (one per SM) in equal runs of T, counted on the device from the
 // trees' own numbers.  A block folds the splits that it takes from split 0 on, so
-// the order of the steps keeps such beginnings whole: first the first T splits of
-// every (sequence, kv head) that has more, a run each, then the shorter ones one
-// after the other, then all the rest, whose splits leave a partial each (also
-// those of trees of more than one tile, tiles fastest: a split's further tiles
-// find its K and V in L2).  A chain is a run of steps with the same rows.
+// the order of the steps keeps such beginnings whole.  A chain is a (sequence, kv
+// head, tile).  First come the first T splits of every chain that has more and is
+// its tree's only tile, a run each; then the chains of at most T splits, one after
+// the other (a tree's further tiles read K and V again, which is no more than
+// their partials would be, written and read); then the rest, whose splits leave a
+// partial each, tiles fastest: a split's further tiles find its K and V in L2.
 // Roles (18 warps): warps 0-15 take the softmax, four threads per pair: warp w
 // holds TMEM lanes 32 (w % 4) .. + 31 (lane = pair) and keys 64 (w / 4) ..
 // + 63 of each split, so a tile's softmax is four warps deep on every
@@ -462,19 +463,26 @@ __device__ __forceinline__ int64_t cursor_load(const TreeAttnParams& p, StepCurs
   const int splits = ctx / kSplit;
   if (all)
     c.splits = splits;
-  else if (c.tiles > 1)
-    c.splits = c.part == 2 ? splits : 0;
   else if (splits <= c.T)
     c.splits = c.part == 1 ? splits : 0;
+  else if (c.tiles > 1)
+    c.splits = c.part == 2 ? splits : 0;
   else if (c.part != 1)
     c.lo = c.part == 2 ? c.T : 0, c.splits = c.part == 2 ? splits : c.T;
   return static_cast<int64_t>(p.Hkv) * (c.splits - c.lo) * c.tiles;
 }
-// The next step; whether it begins another chain.
+// The next step; whether its rows are others.
 __device__ __forceinline__ bool cursor_next(const TreeAttnParams& p, StepCursor& c) {
-  if (++c.tile < c.tiles) return true;
-  c.tile = 0;
-  if (++c.s < c.splits) return c.tiles > 1;
+  if (c.part == 2) {
+    if (++c.tile < c.tiles) return true;
+    c.tile = 0;
+    if (++c.s < c.splits) return c.tiles > 1;
+  } else {
+    if (++c.s < c.splits) return false;
+    c.s = c.lo;
+    if (++c.tile < c.tiles) return true;
+    c.tile = 0;
+  }
   if (++c.g >= p.Hkv) {
     c.g = 0;
     do {
@@ -517,8 +525,8 @@ __device__ __forceinline__ void cursor_start(const TreeAttnParams& p, StepCursor
       if (here) {
         const int64_t u = u0 - (before + incl - mine);
         const int splits = c.splits - c.lo;
-        c.tile = static_cast<int>(u % c.tiles);
-        c.s = c.lo + static_cast<int>(u / c.tiles % splits);
+        c.tile = static_cast<int>(c.part == 2 ? u % c.tiles : u / splits % c.tiles);
+        c.s = c.lo + static_cast<int>(c.part == 2 ? u / c.tiles % splits : u % splits);
         c.g = static_cast<int>(u / c.tiles / splits);
         out = c;
       }
@@ -810,7 +818,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool folding;
     auto begin_chain = [&](const StepCursor& c) {
       s = c.s;
-      end = c.tiles > 1 ? s + 1 : c.splits;
+      end = c.part == 2 && c.tiles > 1 ? s + 1 : c.splits;
       folding = s == 0;
       live = min(32, c.pairs - c.tile * kTcPairs - quad * 32);
       group = (c.b * p.Hkv + c.g) * p.groups + c.tile * (kTcPairs / 16) + quad * 2;

@@ -26,8 +26,8 @@
 // three ahead through shared memory instead of one ahead in registers were
 // slower (242 us at best).
 //
-// A row is one block, or a cluster of up to eight when there are few rows; the
-// blocks put their units' sums and their list into the first block's shared
+// A row is one block; a cluster of up to eight when there are few rows, or, where
+// there are many short ones, a warp.  A cluster's blocks put their units' sums and their list into the first block's shared
 // memory, so nothing goes through global memory.
 #include <math.h>
 
@@ -51,7 +51,8 @@ typedef unsigned long long u64;
 struct LogprobParams {
   const void* x;
   int64_t ld;
-  int V, units, parts, units_per_part;  // a row is `parts` blocks of `units_per_part` units
+  int rows, V, units;
+  int parts, units_per_part;  // a row is `parts` blocks of `units_per_part` units
   const int32_t* ids;
   int n_ids;
   float* logprob;
@@ -163,15 +164,17 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// The block's eight lists in shared memory, merged pairwise; warp 0 returns the
-// result.  Called by every thread after the lists were written (no barrier yet).
-__device__ __forceinline__ u64 merge_block(u64 (*lists)[32]) {
+// The lists of `n` warps of a row in shared memory, merged pairwise; the first of
+// them returns the result.  Called by every thread of the block after the lists
+// were written (no barrier yet); w: the warp's place among its row's.
+__device__ __forceinline__ u64 merge_lists(u64 (*lists)[32], int n, int w) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  u64 v = 0;
+  u64 v = lists[warp][lane];
 #pragma unroll
   for (int half = kWarps / 2; half > 0; half >>= 1) {
+    if (half >= n) continue;
     __syncthreads();
-    if (warp < half) {
+    if (w < half) {
       v = merge_desc(lists[warp][lane], lists[warp + half][lane]);
       lists[warp][lane] = v;
     }
@@ -179,25 +182,28 @@ __device__ __forceinline__ u64 merge_block(u64 (*lists)[32]) {
   return v;
 }
 
-// One block, or a cluster of p.parts blocks, per row.
-template <typename T, bool VEC>
+// WPR warps of a block (8 or 1), or a cluster of p.parts blocks, per row.
+template <typename T, bool VEC, int WPR>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_kernel(const LogprobParams p) {
   constexpr int N = kPerLane * sizeof(T) / 4;
-  extern __shared__ float s_unit[];  // [units][3]: m, S, T (of the cluster's first block)
+  extern __shared__ float s_units[];  // per row of the block [units][3]: m, S, T (a cluster's: in its first block)
   __shared__ u64 pending[kWarps][kPending];
   __shared__ u64 lists[kWarps][32];
   __shared__ uint32_t s_first[kWarps];
-  __shared__ uint32_t s_floor;
-  __shared__ float s_row[3];
-  if (threadIdx.x == 0) s_floor = 0;
+  __shared__ uint32_t s_floor[kWarps];
+  __shared__ float s_row[kWarps][2];
+  if (threadIdx.x < kWarps) s_floor[threadIdx.x] = 0;
   if (p.parts > 1) cluster_arrive_relaxed();  // the first block runs: its shared memory may be written
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t r = blockIdx.x / p.parts;
-  const int part = blockIdx.x % p.parts;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* row = static_cast<const T*>(p.x) + r * p.ld;
-  const int u_end = min(p.units, (part + 1) * p.units_per_part);
+  constexpr int wpr = WPR;
+  const int w = warp & (wpr - 1), mine = warp - w;  // the row's first warp names it in the block
+  const int part = blockIdx.x % p.parts;
+  auto row_of = [&]() { return static_cast<int64_t>(blockIdx.x / p.parts) * (kWarps / wpr) + warp / wpr; };
+  const bool live = row_of() < p.rows;
+  const T* row = static_cast<const T*>(p.x) + (live ? row_of() : 0) * p.ld;
+  const int u_end = live ? min(p.units, (part + 1) * p.units_per_part) : 0;
   const int top_k = p.top_k;
   u64 best = 0;  // lane i: the i-th best key (0: none)
   u64 bar = 0;   // the k-th best
@@ -209,20 +215,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_ker
     best = merge_desc(best, sort_desc(v));
     waiting -= n;
     bar = __shfl_sync(0xffffffffu, best, top_k - 1);
-    if (lane == 0) atomicMax(&s_floor, static_cast<uint32_t>(bar >> 32));
+    if (lane == 0) atomicMax(&s_floor[mine], static_cast<uint32_t>(bar >> 32));
   };
   uint32_t x[N];
-  int u = part * p.units_per_part + warp;
+  int u = part * p.units_per_part + w;
   if (u < u_end) load_unit<T, VEC>(row, u * kUnit, p.V, x);
-  const uint32_t unit_base = smem_addr(s_unit);
+  const uint32_t unit_base = smem_addr(s_units) + warp / wpr * p.units * 12;
   if (p.parts > 1) cluster_wait();
   const uint32_t unit_dst = p.parts > 1 ? map_to_rank(unit_base, 0) : unit_base;
   bool first = true;
   // the block's warps take the same number of turns (a barrier in the first)
-  for (int turn = 0; first || u < u_end; ++turn, u += kWarps) {
+  for (; first || u < u_end; u += wpr) {
     uint32_t nx[N];
     const bool here = u < u_end;
-    if (u + kWarps < u_end) load_unit<T, VEC>(row, (u + kWarps) * kUnit, p.V, nx);
+    if (u + wpr < u_end) load_unit<T, VEC>(row, (u + wpr) * kUnit, p.V, nx);
     float lm = -INFINITY;
     if (here) {
       if (sizeof(T) == 4) {
@@ -237,18 +243,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_ker
       lm = no_nan(lm);
     }
     if (first && top_k > 0) {
-      // with q = ceil(k / 8): each warp's q-th largest lane maximum; the
-      // ceil(k / q)-th largest of those is reached by at least k ids
-      const int q = (top_k + kWarps - 1) / kWarps, need = (top_k + q - 1) / q;
-      const uint32_t mine = __shfl_sync(0xffffffffu, sort_desc(here ? ordered(lm) : 0u), q - 1);
-      if (lane == 0) s_first[warp] = mine;
+      // with n of the row's warps holding a unit and q = ceil(k / n): each warp's
+      // q-th largest lane maximum; the ceil(k / q)-th largest of those is reached
+      // by at least k ids
+      const int n = max(1, min(wpr, u_end - part * p.units_per_part));
+      const int q = (top_k + n - 1) / n, need = (top_k + q - 1) / q;
+      const uint32_t kth = __shfl_sync(0xffffffffu, sort_desc(here ? ordered(lm) : 0u), q - 1);
+      if (lane == 0) s_first[warp] = kth;
       __syncthreads();
-      const uint32_t v = s_first[lane & (kWarps - 1)];
+      const int me = lane & (wpr - 1);
+      const uint32_t v = s_first[mine + me];
       int rank = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const uint32_t o = s_first[w];
-        rank += o > v || (o == v && w < (lane & (kWarps - 1)));
+      for (int o = 0; o < wpr; ++o) {
+        const uint32_t other = s_first[mine + o];
+        rank += other > v || (other == v && o < me);
       }
       floor_hi = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, rank == need - 1)) - 1);
     }
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_ker
     t = warp_sum(t);
     if (lane < 3) st_cluster_f32(unit_dst + (3 * u + lane) * 4, lane == 0 ? m : lane == 1 ? s : t);
     if (top_k > 0) {
-      floor_hi = max(floor_hi, *static_cast<volatile uint32_t*>(&s_floor));
+      floor_hi = max(floor_hi, *static_cast<volatile uint32_t*>(&s_floor[mine]));
       if (__any_sync(0xffffffffu, ordered(lm) >= floor_hi)) {
         // which of the lane's ids reach the floor; then one id a lane at a time
         const float floor = floor_hi ? unordered(floor_hi) : -INFINITY;
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_ker
   if (top_k > 0) {
     if (waiting) merge_waiting(waiting);
     lists[warp][lane] = best;
-    best = merge_block(lists);
+    best = merge_lists(lists, wpr, w);
   }
   if (p.parts > 1) {
     if (top_k > 0) {
@@ -332,12 +341,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_ker
       const u64 v = warp == 0 ? lists[0][lane] : warp < p.parts ? got[warp][lane] : static_cast<u64>(0);
       __syncthreads();
       lists[warp][lane] = v;
-      best = merge_block(lists);
+      best = merge_lists(lists, kWarps, warp);
     }
   }
   __syncthreads();
-  // the fold of the units, by the last warp
-  if (warp == kWarps - 1) {
+  const int64_t r = row_of();
+  const float* s_unit = s_units + warp / wpr * p.units * 3;
+  // the fold of the units, by the row's last warp
+  if (w == wpr - 1 && live) {
     float M = -INFINITY;
     for (int i = lane; i < p.units; i += 32) M = fmaxf(M, s_unit[3 * i]);
     M = warp_max(M);
@@ -354,25 +365,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_ker
     S = warp_sum(S);
     Tt = warp_sum(Tt);
     if (lane == 0) {
-      s_row[0] = M;
-      s_row[1] = logf(S);
-      if (p.entropy) p.entropy[r] = M == -INFINITY ? 0.f : __fsub_rn(s_row[1], __fmul_rn(kLn2, __fdiv_rn(Tt, S)));
+      const float ln_s = logf(S);
+      s_row[mine][0] = M;
+      s_row[mine][1] = ln_s;
+      if (p.entropy) p.entropy[r] = M == -INFINITY ? 0.f : __fsub_rn(ln_s, __fmul_rn(kLn2, __fdiv_rn(Tt, S)));
     }
   }
   __syncthreads();
-  const float M = s_row[0], ln_s = s_row[1];
+  if (!live) return;
+  const float M = s_row[mine][0], ln_s = s_row[mine][1];
   auto logprob = [&](float v) {
     v = no_nan(v);
     if (M == -INFINITY) return -INFINITY;
     const float d = v == M ? 0.f : __fsub_rn(v, M);  // +infinity against +infinity: the shared maximum
     return __fsub_rn(d, ln_s);
   };
-  if (warp == 0 && lane < top_k) {
+  if (w == 0 && lane < top_k) {
     p.top_ids[r * top_k + lane] = static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
     p.top_logprobs[r * top_k + lane] = logprob(unordered(static_cast<uint32_t>(best >> 32)));
   }
-  for (int j = static_cast<int>(threadIdx.x) - 32; j < p.n_ids; j += kThreads - 32) {
-    if (j < 0) break;
+  for (int j = w * 32 + lane; j < p.n_ids; j += wpr * 32) {
     const int id = p.ids[r * p.n_ids + j];
     float v = 0.f;
     if (id >= p.V) {
@@ -394,13 +406,23 @@ int part_count(int rows, int units) {
   return parts;
 }
 
-template <typename T>
-kinv_status launch(const LogprobParams& p, int rows, bool vec, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(p.units) * 12;
-  auto* kernel = vec ? logprobs_kernel<T, true> : logprobs_kernel<T, false>;
+template <typename T, int WPR>
+kinv_status launch(const LogprobParams& p, bool vec, cudaStream_t stream) {
+  constexpr int ROWS = kWarps / WPR;  // of a block
+  const size_t smem = static_cast<size_t>(p.units) * 12 * ROWS;
+  auto* kernel = vec ? logprobs_kernel<T, true, WPR> : logprobs_kernel<T, false, WPR>;
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (attr != KINV_OK) return attr;
-  return launch_kernel(kernel, dim3(static_cast<unsigned>(rows) * p.parts), dim3(kThreads), smem, stream, p.parts, p);
+  const int64_t blocks = (static_cast<int64_t>(p.rows) + ROWS - 1) / ROWS * p.parts;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, stream, p.parts, p);
+}
+
+// A warp per row where a block's eight would not have a unit each and the rows
+// alone fill the SMs with sixteen warps (4,096 rows of 5,000 fp32 with 20
+// alternatives: 34 us, 76 with eight warps a row; 8,192 rows of 500: 25 and 135).
+template <typename T>
+kinv_status launch(const LogprobParams& p, bool vec, cudaStream_t stream) {
+  return p.units <= kWarps && p.rows >= 152 * 16 ? launch<T, 1>(p, vec, stream) : launch<T, kWarps>(p, vec, stream);
 }
 
 }  // namespace
@@ -422,6 +444,7 @@ extern "C" kinv_status kinv_logprobs(const void* logits, kinv_dtype dtype, int64
   LogprobParams p{};
   p.x = logits;
   p.ld = ld;
+  p.rows = rows;
   p.V = V;
   p.units = (V + kUnit - 1) / kUnit;
   p.parts = part_count(rows, p.units);
@@ -435,5 +458,5 @@ extern "C" kinv_status kinv_logprobs(const void* logits, kinv_dtype dtype, int64
   p.top_logprobs = top_logprobs;
   p.status = device_status_word();
   const bool vec = aligned16(logits) && static_cast<size_t>(ld) * elem % 16 == 0;
-  return dtype == KINV_F32 ? launch<float>(p, rows, vec, stream) : launch<__nv_bfloat16>(p, rows, vec, stream);
+  return dtype == KINV_F32 ? launch<float>(p, vec, stream) : launch<__nv_bfloat16>(p, vec, stream);
 }

@@ -91,6 +91,19 @@ def test_many_rows_have_the_bits_of_one(kinv, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("v", [1, 40, 1023, 1025, 8192])
+def test_many_short_rows(kinv, dtype, v):
+    """Rows that take one warp of a block each, the last block part empty."""
+    rows, k = 2437, min(v, 32)
+    x = logits(rows, v, v, dtype)
+    ids = torch.randint(0, v, (rows, 2), generator=synth.gen(6)).to(torch.int32).cuda()
+    whole = check(kinv, x, ids, k, rows=[0, 9, rows - 1])
+    for r0, n in ((0, 1), (rows - 1, 1), (1000, 300)):
+        for a, b in zip(kinv.logprobs(x[r0: r0 + n], ids[r0: r0 + n], top_k=k), whole):
+            assert_same_bits(a, b[r0: r0 + n], f"rows {r0} .. {r0 + n}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("v", [600, 20000])
 def test_rows_where_it_can_go_wrong(kinv, dtype, v):
     inf, low = float("inf"), torch.finfo(dtype).min
