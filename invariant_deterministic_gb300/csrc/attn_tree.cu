@@ -68,9 +68,12 @@ __device__ __forceinline__ int64_t partial_at(const TreeAttnParams& p, int group
   return (static_cast<int64_t>(group) * p.S + s) * 16;
 }
 
-// One block per (kv head, tile of 16 MT pairs, split, sequence).
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const TreeAttnParams p) {
+// A split of a tile of 16 MT pairs of (sequence b, kv head g), by one block.  The
+// partial goes to the workspace or, LOCAL, to o_out [16 MT][D] and ml_out [16 MT][2]
+// in shared memory (then the tree is loaded whatever the split).
+template <int D, int MT, bool LOCAL>
+__device__ __forceinline__ void split_block(const TreeAttnParams& p, int g, int tile, int b, int part, TreeInfo& ti,
+                                            unsigned char* smem_raw, float* o_out, float* ml_out) {
   constexpr int C8 = D / 8;   // 16-byte chunks per key row
   constexpr int KS = D / 16;  // 16-wide k steps of q . k
   constexpr int R = 16 * MT;  // pairs of the tile
@@ -80,29 +83,22 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
   // path of each node of the tile; K, then V (rows of 16-byte chunks, chunk c of
   // row r at chunk c ^ (r & 7)): up to 256 context keys, or up to 255 and the
   // drafted ones
-  extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* pt = smem_raw;
   unsigned char* pt_lo = pt + R * kSplit * 2;
   float* scores = reinterpret_cast<float*>(pt);
   unsigned char* zrow = pt + R * kScoreLd * 4;
   unsigned char* paths = zrow + D * 2;  // [R >> gs][64]
   unsigned char* kv = paths + (R >> p.gs) * kTreeMaxNodes;
-  __shared__ TreeInfo ti;
   __shared__ int depth[kTreeMaxNodes];
   __shared__ float wmax[kThreads / 32][R];
   __shared__ float wsum[kThreads / 32][R];
 
-  pdl_launch_dependents();
-  pdl_wait();
-  const int g = blockIdx.x % p.Hkv;
-  const int tile = blockIdx.x / p.Hkv;
-  const int b = blockIdx.z;
   int n, ctx, off;
   if (!tree_bounds(p.tree, b, n, ctx, off)) {
     report_bad_tree(p);
     return;
   }
-  const int s = (p.tail_only ? ctx / kSplit : 0) + static_cast<int>(blockIdx.y);
+  const int s = (p.tail_only ? ctx / kSplit : 0) + part;
   const int gs = p.gs;  // G = 1 << gs
   const int npt = R >> gs;  // nodes of a tile
   const int n0 = tile * npt;
@@ -139,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
     cp_async16(pt_base + static_cast<uint32_t>(r * D * 2 + ((ch ^ (r & 7)) << 4)),
                p.q + (static_cast<int64_t>(off + n0 + (r >> gs)) * p.Hq + (g << gs) + (r & ((1 << gs) - 1))) * D + ch * 8);
   }
-  if (tail) {
+  if (tail || LOCAL) {
     if (warp == 0) {
       tree_load(p.tree, b, ti);
       __syncwarp();
@@ -156,11 +152,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
   }
   cp_async_wait<0>();
   __syncthreads();
+  if ((tail || LOCAL) && !ti.ok) {
+    report_bad_tree(p);
+    return;
+  }
   if (tail) {
-    if (!ti.ok) {
-      report_bad_tree(p);
-      return;
-    }
     // the path of a node: the set bits of its mask, ascending
     for (int idx = t; idx < nodes * kTreeMaxNodes; idx += kThreads) {
       const int i = idx / kTreeMaxNodes, j = idx % kTreeMaxNodes;
@@ -394,16 +390,88 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
       const int64_t at = partial_at(p, (b * p.Hkv + g) * p.groups + tile * MT + mt, s);
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb)
-        *reinterpret_cast<float2*>(p.ws_o + at * D + ((2 * warp + nb) * 16 + h * 8 + gq) * 8 + 2 * tq) =
+        *reinterpret_cast<float2*>(LOCAL ? o_out + pair * D + warp * 16 + nb * 8 + 2 * tq
+                                         : p.ws_o + at * D + ((2 * warp + nb) * 16 + h * 8 + gq) * 8 + 2 * tq) =
             make_float2(oc[mt][nb][2 * h], oc[mt][nb][2 * h + 1]);
       if (warp == 0 && tq == 0) {
         float l = wsum[0][pair];
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w) l = __fadd_rn(l, wsum[w][pair]);
-        *reinterpret_cast<float2*>(p.ws_ml + (at + h * 8 + gq) * 2) = make_float2(m[mt][h], l);
+        *reinterpret_cast<float2*>(LOCAL ? ml_out + pair * 2 : p.ws_ml + (at + h * 8 + gq) * 2) = make_float2(m[mt][h], l);
       }
     }
-  if (s == 0 && t == 0 && tile * R % 128 == 0) p.ws_cov[(b * p.Hkv + g) * p.groups + tile * MT] = 1;
+  if (!LOCAL && s == 0 && t == 0 && tile * R % 128 == 0) p.ws_cov[(b * p.Hkv + g) * p.groups + tile * MT] = 1;
+}
+
+// One block per (kv head, tile of 16 MT pairs, split, sequence).
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const TreeAttnParams p) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ TreeInfo ti;
+  pdl_launch_dependents();
+  pdl_wait();
+  split_block<D, MT, false>(p, blockIdx.x % p.Hkv, blockIdx.x / p.Hkv, blockIdx.z, blockIdx.y, ti, smem_raw, nullptr, nullptr);
+}
+
+// The whole call in one launch where a sequence has at most eight splits: a
+// cluster of a block per split (block rank s) of a (kv head, tile of 16 pairs,
+// sequence); the partials stay in shared memory, and the blocks of the context's
+// splits share the tile's pairs and fold them over the cluster in split order,
+// with the merge's arithmetic.  Taken while the blocks fit the SMs at two each: a
+// block keeps its SM until its cluster is done (4 nodes behind 200 keys, 16 blocks:
+// 8.8 us against 10.4 in two launches; 7 small-layer trees behind up to 1,021 keys,
+// 140 blocks: 9.6 against 11.4; 64 trees of 4 nodes behind 300 keys, 1,024 blocks:
+// 45 against 32).
+constexpr int kMaxFused = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) attn_tree_fused_kernel(const TreeAttnParams p) {
+  constexpr int W = D / 16;  // columns of a thread in the fold
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  float* o_s = reinterpret_cast<float*>(smem_raw);  // [16][D]
+  float* ml_s = o_s + 16 * D;                       // [16][2]
+  __shared__ TreeInfo ti;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int s = blockIdx.x, g = blockIdx.y % p.Hkv, tile = blockIdx.y / p.Hkv, b = blockIdx.z;
+  split_block<D, 1, true>(p, g, tile, b, s, ti, reinterpret_cast<unsigned char*>(ml_s + 32), o_s, ml_s);
+  cluster_sync();
+  int n, ctx, off;
+  const bool ok = tree_bounds(p.tree, b, n, ctx, off);
+  const int owners = ctx / kSplit + 1;  // these blocks loaded the tree
+  const int pair = threadIdx.x >> 4, col = (threadIdx.x & 15) * W;
+  const int node = ((tile * 16) >> p.gs) + (pair >> p.gs);
+  if (ok && s < owners && pair % owners == s && node < n && ti.ok) {
+    const int ns = (ctx + __popcll(ti.mask[node]) + kSplit - 1) / kSplit;
+    const uint32_t ml_at = smem_addr(ml_s + pair * 2), o_at = smem_addr(o_s + pair * D + col);
+    float m_acc = -INFINITY, l_acc = 0.f, o_acc[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) o_acc[w] = 0.f;
+#pragma unroll 4
+    for (int q = 0; q < ns; ++q) {
+      const uint32_t ml = map_to_rank(ml_at, q), at = map_to_rank(o_at, q);
+      const float m = ld_dsmem_f32(ml), l = ld_dsmem_f32(ml + 4);
+      float v[W];
+#pragma unroll
+      for (int w = 0; w < W; w += 4) {
+        const float4 x = ld_dsmem_v4(at + w * 4);
+        v[w] = x.x, v[w + 1] = x.y, v[w + 2] = x.z, v[w + 3] = x.w;
+      }
+      const float m_new = fmaxf(m_acc, m);
+      const float a = ex2_approx(__fsub_rn(m_acc, m_new));
+      const float c = ex2_approx(__fsub_rn(m, m_new));
+      l_acc = __fadd_rn(__fmul_rn(l_acc, a), __fmul_rn(l, c));
+#pragma unroll
+      for (int w = 0; w < W; ++w) o_acc[w] = __fadd_rn(__fmul_rn(o_acc[w], a), __fmul_rn(v[w], c));
+      m_acc = m_new;
+    }
+    const int64_t head = static_cast<int64_t>(off + node) * p.Hq + (g << p.gs) + (pair & ((1 << p.gs) - 1));
+#pragma unroll
+    for (int w = 0; w < W; w += 2)
+      *reinterpret_cast<uint32_t*>(p.out + head * D + col + w) =
+          pack_bf16(__fdiv_rn(o_acc[w], l_acc), __fdiv_rn(o_acc[w + 1], l_acc));
+  }
+  cluster_sync();  // no block leaves while its partial is read
 }
 
 // ---------------------------------------------------------------------------
@@ -1015,6 +1083,15 @@ kinv_status launch_split(const TreeAttnParams& p, cudaStream_t stream) {
 }
 
 template <int D>
+kinv_status launch_fused(const TreeAttnParams& p, cudaStream_t stream) {
+  const size_t smem = 16 * D * 4 + 32 * 4 + split_smem_bytes<D, 1>(p);
+  const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(attn_tree_fused_kernel<D>), smem);
+  if (attr != KINV_OK) return attr;
+  const int tiles = (p.tree.max_nodes * p.G + 15) / 16;
+  return launch_kernel(attn_tree_fused_kernel<D>, dim3(p.S, p.Hkv * tiles, p.tree.B), dim3(kThreads), smem, stream, p.S, p);
+}
+
+template <int D>
 constexpr size_t ctx_smem_bytes() {
   return 1024 + static_cast<size_t>(D / 64) * kTcPairs * 128 + 2 * static_cast<size_t>(D / 64) * kSplit * 128 +
          16 * kStage + (kTcBars + 1) * 8 + 12 * kTcPairs * 4;
@@ -1051,6 +1128,9 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
   const bool small = pairs <= 16 ||
                      static_cast<int64_t>(p.tree.B) * p.Hkv * ((pairs + 31) / 32) * (p.tail_only ? 1 : p.S) < sms ||
                      2 * (split_smem_bytes<D, 2>(p) + 3072 + smem_reserved_per_block()) > static_cast<size_t>(smem_per_sm());
+  if (small && !p.tail_only && p.S <= kMaxFused &&
+      static_cast<int64_t>(p.tree.B) * p.Hkv * ((pairs + 15) / 16) * p.S <= 2 * sms)
+    return launch_fused<D>(p, stream);
   kinv_status st = small ? launch_split<D, 1>(p, stream) : launch_split<D, 2>(p, stream);
   if (st != KINV_OK) return st;
   if (p.tail_only) {

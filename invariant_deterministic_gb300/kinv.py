@@ -386,13 +386,6 @@ class Tree:
         self.ptr = ctypes.byref(self.struct)
 
 
-def _need_all(dtype, **tensors):
-    """_need for several tensors at once (one call while all is well)."""
-    for name, t in tensors.items():
-        if t.dtype != dtype or not t.is_cuda:
-            _need(t, dtype, name)
-
-
 def _tree_cache(k_cache, v_cache, tree: Tree, what: str):
     """Shape and strides of the caches [B][slots][Hkv][D], which hold the
     tree's sequences and max_kv slots each."""
@@ -412,7 +405,11 @@ def rope_append_tree(qkv, q_out, k_cache, v_cache, tree: Tree, n_q, n_kv, head_d
     """kinv_rope_append for the rows of drafted trees: qkv [rows][(Hq + 2 Hkv) D]
     rotated by each node's position -> q_out [rows][Hq][D], keys and values into
     the caches [B][slots][Hkv][D] at the node's slot."""
-    _need_all(torch.bfloat16, qkv=qkv, q_out=q_out, k_cache=k_cache, v_cache=v_cache)
+    bf = torch.bfloat16
+    if not (qkv.dtype is q_out.dtype is k_cache.dtype is v_cache.dtype is bf and qkv.is_cuda and q_out.is_cuda
+            and k_cache.is_cuda and v_cache.is_cuda):
+        for t, name in ((qkv, "qkv"), (q_out, "q_out"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, bf, name)
     shape, stride = _tree_cache(k_cache, v_cache, tree, "rope_append_tree")
     (rows, width), (ld, step) = qkv.shape, qkv.stride()
     if (rows < tree.total_rows or step != 1 or not q_out.is_contiguous() or width != (n_q + 2 * n_kv) * head_dim
@@ -437,7 +434,11 @@ def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_l
     behind the context and the node's path."""
     if out is None:
         out = torch.empty_like(q)
-    _need_all(torch.bfloat16, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
+    bf = torch.bfloat16
+    if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is bf and q.is_cuda and out.is_cuda
+            and k_cache.is_cuda and v_cache.is_cuda):
+        for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (out, "out")):
+            _need(t, bf, name)
     shape, stride = _tree_cache(k_cache, v_cache, tree, "attn_tree")
     rows, hq, d = q.shape
     hkv = shape[2]
@@ -461,25 +462,30 @@ def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=
     token, the model's token after it); kv: [layers][2][B][slots][Hkv][D] bf16,
     changed in place (None: only the path is found).  Returns (n_accepted [B],
     path [B][max_nodes], out_tokens [B][max_nodes]) int32."""
-    dev, b, n = tokens.device, tree.B, tree.max_nodes
+    b, n, i32 = tree.B, tree.max_nodes, torch.int32
+    given = [(tokens, "tokens", tree.total_rows), (next_tokens, "next_tokens", tree.total_rows)]
     if n_accepted is None:
-        n_accepted = torch.empty(b, dtype=torch.int32, device=dev)
+        n_accepted = torch.empty(b, dtype=i32, device=tokens.device)
+    else:
+        given.append((n_accepted, "n_accepted", b))
     if path is None:
-        path = torch.empty(b, n, dtype=torch.int32, device=dev)
+        path = torch.empty(b, n, dtype=i32, device=tokens.device)
+    else:
+        given.append((path, "path", b * n))
     if out_tokens is None:
-        out_tokens = torch.empty(b, n, dtype=torch.int32, device=dev)
-    _need_all(torch.int32, tokens=tokens, next_tokens=next_tokens, n_accepted=n_accepted, path=path,
-              out_tokens=out_tokens)
-    for t, least in ((tokens, tree.total_rows), (next_tokens, tree.total_rows), (n_accepted, b), (path, b * n),
-                     (out_tokens, b * n)):
+        out_tokens = torch.empty(b, n, dtype=i32, device=tokens.device)
+    else:
+        given.append((out_tokens, "out_tokens", b * n))
+    for t, name, least in given:
+        if t.dtype is not i32 or not t.is_cuda:
+            _need(t, i32, name)
         if t.numel() < least or not t.is_contiguous():
-            raise ValueError("tree_accept: tokens and next_tokens [rows], n_accepted [B], path and out_tokens "
-                             "[B][max_nodes] must be contiguous")
+            raise ValueError(f"tree_accept: {name} must be contiguous with at least {least} entries")
     if kv is None:
         kp = vp = None
         layers = ls = ss = ts = hkv = d = 0
     else:
-        _need_all(torch.bfloat16, kv=kv)
+        _need(kv, torch.bfloat16, "kv")
         layers, two, bsz, slots, hkv, d = kv.shape
         ls, cs, ss, ts, hs, es = kv.stride()
         if two != 2 or bsz < b or slots < tree.max_kv or es != 1 or hs != d:
