@@ -87,6 +87,8 @@ class DraftDecoder:
         """Host arrays of a step: per node its token, parent, request, position
         in the request's output, and the sampler's history (its path included)."""
         dec, ld = self.dec, self.dec.hist_ld
+        if len(trees) != len(self.requests):
+            raise ValueError("a step has one tree per request (an empty one leaves its request as it is)")
         token, parent, owner, step, n, hist, hist_len = [], [], [], [], [], [], []
         for b, (nodes, parents) in enumerate(trees):
             seq = self.requests[b]
@@ -103,6 +105,8 @@ class DraftDecoder:
             for i, (t, p) in enumerate(zip(nodes, parents)):
                 if i and not 0 <= p < i:
                     raise ValueError("a node's parent comes before it")
+                if not 0 <= t < dec.s.vocab:
+                    raise ValueError("a drafted token lies outside the vocabulary")
                 paths.append(paths[p] + [t] if i else [])
                 tail = (seq[-ld:] + paths[i])[-ld:]
                 token.append(t), parent.append(p), owner.append(b)

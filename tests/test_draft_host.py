@@ -40,6 +40,9 @@ def test_ngram_tree_without_an_occurrence():
 class _Dec:
     B, Lmax, hist_ld, max_rows = 2, 10, 4, 8
 
+    class s:
+        vocab = 100
+
 
 def _dd(requests):
     d = draft.DraftDecoder.__new__(draft.DraftDecoder)
@@ -57,10 +60,17 @@ def test_step_inputs():
 
 
 @pytest.mark.parametrize("tree", [([4], [-1]), ([3], [0]), ([3, 4], [-1]), ([3] * 5, [-1, 0, 1, 2, 3]),
-                                  ([3, 4], [-1, 1]), ([3, 4], [-1, -1])])
+                                  ([3, 4], [-1, 1]), ([3, 4], [-1, -1]), ([3, -1], [-1, 0]), ([3, 100], [-1, 0])])
 def test_step_refuses_broken_trees(tree):
     with pytest.raises(ValueError):
         _dd([[1, 2, 3]])._inputs([tree])
+
+
+def test_step_needs_a_tree_per_request():
+    d = _dd([[1, 2, 3], [8, 9]])
+    for trees in ([], [([3], [-1])], [([3], [-1]), ([9], [-1]), ([], [])]):
+        with pytest.raises(ValueError):
+            d.step(trees)
 
 
 def test_step_refuses_a_tree_past_the_cache():

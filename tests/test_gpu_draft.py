@@ -124,5 +124,18 @@ def test_score_of_a_prompt(M):
         assert abs(lp[i].item() - full[int(tokens[i + 1])]) <= 8.2e-6 + 2.0 ** -22 * abs(lp[i].item())
         assert abs(ent[i].item() - h) <= 2.1e-4
         assert ids[i].tolist() == olp.top(d2.logits[0].cpu().numpy(), 4).tolist()
+    for seq, n, chunk in ((0, 1, 0), (3, 9, 0), (-1, 9, 0), (0, 9, -1)):
+        with pytest.raises(ValueError):
+            dec.score(seq, tokens[:n], chunk=chunk)
+    # the whole cache, and one more token than it can score
+    long = synth.uniform_int(202, 0, shape.vocab - 1, 4).cuda()
+    assert dec.score(2, long[:201])[0].shape == (200,)
     with pytest.raises(ValueError):
-        dec.score(0, tokens[:1])
+        dec.score(2, long)
+    # more rows than the logits hold at a time
+    M.SCORE_ROWS, rows = 20, M.SCORE_ROWS
+    try:
+        for a, b in zip(dec.score(1, tokens, top_k=4), (lp, ent, ids, top)):
+            assert_same_bits(a, b, "twenty rows at a time")
+    finally:
+        M.SCORE_ROWS = rows
