@@ -437,7 +437,9 @@ kinv_status kinv_decode_advance(const int32_t* tokens, int32_t* history, int his
  * that holds a parent outside [-1, own index), is left out of every call below
  * -- nothing of it is written -- and the status word records
  * KINV_ERR_INVALID_ARG.  Rows that belong to no sequence are left as they
- * were.  The struct itself is read on the host before a call returns. */
+ * were.  The struct itself is read on the host before a call returns; with B,
+ * total_rows or max_nodes 0 no sequence has a node, and the arrays are not
+ * read. */
 #define KINV_TREE_MAX_NODES 64
 typedef struct {
   const int32_t* ctx_len;

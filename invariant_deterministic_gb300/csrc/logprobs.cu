@@ -27,8 +27,9 @@
 // slower (242 us at best).
 //
 // A row is one block; a cluster of up to eight when there are few rows, or, where
-// there are many short ones, a warp.  A cluster's blocks put their units' sums and their list into the first block's shared
-// memory, so nothing goes through global memory.
+// there are many short ones, a warp.  A cluster's blocks put their units' sums and
+// their list into the first block's shared memory, so nothing goes through global
+// memory.
 #include <math.h>
 
 #include "common.cuh"

@@ -350,3 +350,68 @@ def test_accept_against_the_oracle(kinv, layers, hkv, d):
 
 def kv_slot(kv, b, slot):
     return kv[:, :, b, slot].clone()
+
+
+@pytest.mark.parametrize("n", [4, 64])
+def test_caches_past_32_bits(kinv, n):
+    """Slots 2.2 million elements apart: the last of a sequence's 1,000 lies past
+    2^31 elements and 2^32 bytes, for a few nodes and for the tensor-core path."""
+    hq, hkv, d, slots, tok = 32, 8, 128, 1000, 2_200_000
+    base = torch.empty(2, slots, tok, dtype=torch.bfloat16, device="cuda")
+    kv = base.as_strided((1, 2, 2, slots, hkv, d), (8, 4096, slots * tok, tok, d, 1))
+    ctx = [990 - n, 800]
+    parents = [shape_parents("bushy", n, 1), shape_parents("chain", n)]
+    c = Case(kinv, ctx, parents, hq, hkv, d, slots=slots, seed=120, poison=False)
+    kv[0, 0], kv[0, 1] = c.k, c.v
+    qkv = synth.normal_bf16((c.rows, (hq + 2 * hkv) * d), 1.0, 7, "cuda")
+    tok_, nxt = (synth.uniform_int(c.rows, 0, 2, s).to(torch.int32).cuda() for s in (8, 9))
+    got = []
+    for k, v in ((c.k, c.v), (kv[0, 0], kv[0, 1])):
+        q = torch.zeros(c.rows, hq, d, dtype=torch.bfloat16, device="cuda")
+        kinv.rope_append_tree(qkv, q, k, v, c.tree, hq, hkv, d, 1e6)
+        got.append((q, kinv.attn_tree(q, k, v, c.tree)))
+    for a, b in zip(*got):
+        assert_same_bits(a, b, "wide strides")
+    near = torch.stack([c.k, c.v])[None].contiguous()
+    for a, b in zip(kinv.tree_accept(c.tree, tok_, nxt, near), kinv.tree_accept(c.tree, tok_, nxt, kv)):
+        assert torch.equal(a, b)
+    assert_same_bits(kv, near, "the moved slots")
+    assert kinv.last_device_status() == 0
+
+
+def test_captured_accept_follows_its_tensors(kinv):
+    parents, n = shape_parents("bushy", 40, 5), 40
+    t = [torch.tensor(x, **I32) for x in ([7], [n], [0], parents)]
+    tree = kinv.Tree(*t, 64, 80)
+    tok, nxt = torch.zeros(n, **I32), torch.zeros(n, **I32)
+    kv = synth.normal_bf16((2, 2, 1, 80, 2, 64), 1.0, 4, "cuda")
+    start = kv.clone()
+    outs = [torch.empty(1, **I32), torch.empty(1, 64, **I32), torch.empty(1, 64, **I32)]
+    call = lambda: kinv.tree_accept(tree, tok, nxt, kv, *outs)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for seed, ctx in ((1, 7), (2, 0), (3, 40)):
+        t[0].fill_(ctx)
+        tok.copy_(synth.uniform_int(n, 0, 2, seed)), nxt.copy_(synth.uniform_int(n, 0, 2, seed + 9))
+        kv.copy_(start)
+        g.replay()
+        want = otree.accept(parents, tok.tolist(), nxt.tolist())
+        assert outs[0].tolist() == [len(want)] and outs[1][0, : len(want)].tolist() == want
+        for i, j in enumerate(want):
+            assert_same_bits(kv[:, :, 0, ctx + i], start[:, :, 0, ctx + j], f"slot {i}")
+
+
+@pytest.mark.parametrize("hq,hkv,d,n,B,slots", [(32, 8, 128, 9, 14, 1100), (32, 8, 128, 5, 66, 1100), (8, 1, 64, 3, 180, 1800),
+                                                (2, 2, 64, 33, 33, 2100)])
+def test_small_trees_of_many_sequences(kinv, hq, hkv, d, n, B, slots):
+    """Trees of 17 to 36 (node, head) pairs in batches that take the tensor-core
+    path: groups of 16 pairs that are not full, ragged down to one node."""
+    ctx = [(37 * b * b + 5) % (slots - n) for b in range(B)]
+    parents = [shape_parents(["bushy", "chain", "forest"][b % 3], 1 + (b * 7) % n if b else n, b) for b in range(B)]
+    c = Case(kinv, ctx, parents, hq, hkv, d, slots=slots, seed=130)
+    out = c.run()
+    assert kinv.last_device_status() == 0
+    c.check_bits(out, "small trees")
