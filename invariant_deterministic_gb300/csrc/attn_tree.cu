@@ -494,12 +494,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_fused_kernel(const Tree
 // scheduler; the four exchange raw maxima and 32-key group sums through shared
 // memory, in the decode kernel's order.  Warp 16 lane 0 issues the MMAs, warp 17
 // lane 0 the TMA loads.
-// Tensor memory: scores R in columns 0-255, overwritten 16 keys at a time with
-// their P (packed bf16 pairs: hi in the first eight of the 16 columns, lo in the
-// others), O in two buffers of D columns after it.  The MMAs run
-// in issue order: step i + 1's scores of keys 128 h .. follow step i's P.V of
-// chunks 2h and 2h + 1, which read the P that they overwrite; the softmax
-// threads store step i - 1's O while step i's P.V runs.
+// Tensor memory: three buffers of 128 columns for the scores R of half a split (128
+// keys), overwritten 16 keys at a time with their P (packed bf16 pairs: hi in the
+// first eight of the 16 columns, lo in the others), then O in D columns.  Half h of
+// step i takes buffer (2 i + h) % 3, so the third one receives the first half of
+// step i + 1's scores while the softmax of step i runs; the second half follows
+// step i's P.V of the first half, which frees its buffer, and then the softmax of
+// step i + 1 runs beside step i's P.V of the second half.  The softmax threads read
+// step i - 1's O just before they hand over step i's P, and fold or send it behind
+// that.  K and V arrive in halves as well, each as soon as the MMAs have read the
+// last step's.  (A call with the scores of a step behind the last step's P.V
+// and whole K and V tiles / this way: 16 trees of 32 nodes behind up to 32,700 keys
+// 304 / 286 us, 64 trees of 1 to 16 behind 2,000 to 4,100 158 / 143, one of 64
+// behind 32,000 105 / 100.)
 // The fold takes the merge kernel's arithmetic (32 columns of a pair per thread);
 // the state of a block's splits is left as the partial of split 0 (ws_cov: how
 // many splits that is).
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_fused_kernel(const Tree
 constexpr int kTcSoftmax = 512;  // 16 warps
 constexpr int kTcThreads = kTcSoftmax + 64;
 constexpr int kTcPairs = 128;
-constexpr int kTcBars = 15;
+constexpr int kTcBars = 19;
 constexpr int kStage = 2048;     // bytes a warp stages at a time: two groups x two 8-column chunks
 
 struct StepCursor {
@@ -604,6 +611,18 @@ __device__ __forceinline__ void cursor_start(const TreeAttnParams& p, StepCursor
   }
 }
 
+// Whether the barrier's phase of this parity is complete; never waits.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // An asynchronous copy of `bytes` (a multiple of 16) from shared to global
 // memory, in this thread's current bulk group.
 __device__ __forceinline__ void bulk_store(float* dst, uint32_t src, uint32_t bytes) {
@@ -623,6 +642,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int Q_BYTES = DS * Q_SLICE;
   constexpr int KV_SLICE = kSplit * 128;    // [256 keys][64]
   constexpr int KV_BYTES = DS * KV_SLICE;
+  constexpr int HALF = KV_SLICE / 2;        // 128 keys of a slice
+  constexpr uint32_t O_COL = 384;
   constexpr int DQ = D / 4;                 // output columns per softmax thread
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
@@ -639,13 +660,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ StepCursor start;
   __shared__ StepCursor chains[16];  // of each softmax warp, advanced where its chain ends
   __shared__ int count_s;
-  const uint32_t k_full = smem_addr(bars + 0), k_empty = smem_addr(bars + 1);
-  const uint32_t v_full = smem_addr(bars + 2), v_empty = smem_addr(bars + 3);
-  auto s_full = [&](int h) { return smem_addr(bars + 4 + h); };    // R of keys 128 h .. written
-  auto p_full = [&](int j) { return smem_addr(bars + 6 + j); };    // P chunk j written
-  auto o_full = [&](int i) { return smem_addr(bars + 10 + i); };   // O buffer i complete
-  auto o_empty = [&](int i) { return smem_addr(bars + 12 + i); };  // O buffer i read
-  const uint32_t done_bar = smem_addr(bars + 14);
+  auto k_full = [&](int h) { return smem_addr(bars + 0 + h); };    // of keys 128 h ..
+  auto k_empty = [&](int h) { return smem_addr(bars + 2 + h); };
+  auto v_full = [&](int h) { return smem_addr(bars + 4 + h); };
+  auto v_empty = [&](int h) { return smem_addr(bars + 6 + h); };
+  // R of keys 128 h .. written; two of each, as step i + 1's may be before every
+  // thread has seen step i's
+  auto s_full = [&](int i, int h) { return smem_addr(bars + 8 + 2 * (i & 1) + h); };
+  auto p_full = [&](int j) { return smem_addr(bars + 12 + j); };   // P chunk j written
+  const uint32_t o_full = smem_addr(bars + 16), o_empty = smem_addr(bars + 17), done_bar = smem_addr(bars + 18);
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   pdl_wait();
@@ -658,7 +681,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (t == 0) {
     for (int i = 0; i < kTcBars; ++i) {
       // p_full: the 128 threads of its chunk; o_empty: every softmax thread
-      const int arrivals = (i >= 6 && i < 10) ? kTcPairs : (i == 12 || i == 13) ? kTcSoftmax : 1;
+      const int arrivals = (i >= 12 && i < 16) ? kTcPairs : i == 17 ? kTcSoftmax : 1;
       mbar_init(smem_addr(bars + i), arrivals);
     }
     abort_flag = 0;
@@ -672,103 +695,141 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   int* status = p.status;
 
   if (warp == 17) {
-    // ---- TMA: K of step i + 1 (with its Q, where that is another) as soon as
-    // step i's score MMAs are done, its V as soon as step i's P.V MMAs are done
+    // ---- TMA: the halves of K (and its Q, where that is another) and V, in the
+    // order in which the MMAs give their places up
     if (lane == 0) {
       StepCursor c = start;
       const uint64_t q_pol = l2_policy_evict_last();
       const uint64_t kv_pol = l2_policy_evict_first();
-      auto load_k = [&](bool new_q) {
-        mbar_arrive_expect_tx(k_full, KV_BYTES + (new_q ? Q_BYTES : 0));
-        if (new_q)
-          for (int ds = 0; ds < DS; ++ds)
-            tma_load_3d(smem_addr(q_s + ds * Q_SLICE), &tmQ, 64 * ds, c.g << p.gs, c.off + (c.tile * kTcPairs >> p.gs),
-                        k_full, q_pol);
-        // keys that another tile is about to read should stay in L2
+      int vb, vg, vs;  // the step whose V is next
+      uint64_t v_pol;
+      // keys that another tile is about to read should stay in L2
+      auto pol = [&]() { return c.tile + 1 < c.tiles ? q_pol : kv_pol; };
+      auto v_is_next = [&]() { vb = c.b, vg = c.g, vs = c.s, v_pol = pol(); };
+      auto load_q = [&]() {
         for (int ds = 0; ds < DS; ++ds)
-          tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, c.g, c.s * kSplit, c.b, k_full,
-                      c.tile + 1 < c.tiles ? q_pol : kv_pol);
+          tma_load_3d(smem_addr(q_s + ds * Q_SLICE), &tmQ, 64 * ds, c.g << p.gs, c.off + (c.tile * kTcPairs >> p.gs),
+                      k_full(0), q_pol);
       };
-      auto load_v = [&]() {
-        mbar_arrive_expect_tx(v_full, KV_BYTES);
+      auto load_k = [&](int h, bool new_q) {
+        mbar_arrive_expect_tx(k_full(h), DS * HALF + (new_q ? Q_BYTES : 0));
         for (int ds = 0; ds < DS; ++ds)
-          tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, c.g, c.s * kSplit, c.b, v_full,
-                      c.tile + 1 < c.tiles ? q_pol : kv_pol);
+          tma_load_4d(smem_addr(k_s + ds * KV_SLICE + h * HALF), &tmK, 64 * ds, c.g, c.s * kSplit + 128 * h, c.b,
+                      k_full(h), pol());
       };
-      load_k(true);
-      load_v();
-      int k_issued = 1, v_issued = 1;
-      for (int i = 0; i + 1 < count; ++i) {
-        const bool new_q = cursor_next(p, c);
-        bool ok = !abort_flag && mbar_wait_bounded(k_empty, i & 1, status, DEV_TIMEOUT_ATTN);
-        if (ok) {
-          load_k(new_q);
-          ++k_issued;
-          ok = !abort_flag && mbar_wait_bounded(v_empty, i & 1, status, DEV_TIMEOUT_ATTN);
+      auto load_v = [&](int h) {
+        mbar_arrive_expect_tx(v_full(h), DS * HALF);
+        for (int ds = 0; ds < DS; ++ds)
+          tma_load_4d(smem_addr(v_s + ds * KV_SLICE + h * HALF), &tmV, 64 * ds, vg, vs * kSplit + 128 * h, vb,
+                      v_full(h), v_pol);
+      };
+      load_k(0, true);
+      load_q();
+      load_k(1, false);
+      v_is_next();
+      load_v(0);
+      load_v(1);
+      int k_issued[2] = {1, 1}, v_issued[2] = {1, 1};
+      bool ok = true;
+      for (int n = 1; n <= count && ok; ++n) {  // K of step n, V of step n - 1
+        const bool new_q = n < count && cursor_next(p, c);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (ok && n < count) {
+            ok = !abort_flag && mbar_wait_bounded(k_empty(h), (n - 1) & 1, status, DEV_TIMEOUT_ATTN);
+            if (ok) {
+              if (h == 1 && new_q) load_q();  // the last scores that read Q are done
+              load_k(h, h == 0 && new_q);
+              ++k_issued[h];
+            }
+          }
+          if (ok && n >= 2) {
+            ok = !abort_flag && mbar_wait_bounded(v_empty(h), n & 1, status, DEV_TIMEOUT_ATTN);
+            if (ok) {
+              load_v(h);
+              ++v_issued[h];
+            }
+          }
         }
-        if (!ok) {
-          abort_flag = 1;
-          break;
-        }
-        load_v();
-        ++v_issued;
+        v_is_next();
       }
+      if (!ok) abort_flag = 1;
       // loads still in flight (only after an abort) land before the block exits
-      mbar_wait_bounded(k_full, (k_issued - 1) & 1, nullptr, 0);
-      mbar_wait_bounded(v_full, (v_issued - 1) & 1, nullptr, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mbar_wait_bounded(k_full(h), (k_issued[h] - 1) & 1, nullptr, 0);
+        mbar_wait_bounded(v_full(h), (v_issued[h] - 1) & 1, nullptr, 0);
+      }
     }
     __syncwarp();
   } else if (warp == 16) {
-    // ---- MMA issue: iteration i issues step i - 1's P.V chunks and step i's
-    // scores, interleaved
+    // ---- MMA issue
     if (lane == 0) {
       constexpr uint32_t idesc_r = tc_idesc(128, 0);
       constexpr uint32_t idesc_o = tc_idesc(D, 1);
       const uint64_t qd = desc_k_sw128(smem_addr(q_s)), kd = desc_k_sw128(smem_addr(k_s));
       const uint64_t vd = desc_mn_sw128(smem_addr(v_s), KV_SLICE);
       bool ok = true;
-      for (int i = 0; i <= count && ok; ++i) {
-        const bool has_r = i < count, has_pv = i > 0;
-        const uint32_t ob = (i - 1) & 1;  // the last step's O buffer, and its barriers' phase
-        if (has_pv)
-          ok = !abort_flag && mbar_wait_bounded(v_full, ob, status, DEV_TIMEOUT_ATTN) &&
-               mbar_wait_bounded(o_empty(ob), (((i - 1) >> 1) & 1) ^ 1, status, DEV_TIMEOUT_ATTN);
-        if (ok && has_r) ok = !abort_flag && mbar_wait_bounded(k_full, i & 1, status, DEV_TIMEOUT_ATTN);
-        if (!ok) break;
+      auto wait = [&](uint32_t bar, int phase) {
+        ok = ok && !abort_flag && mbar_wait_bounded(bar, phase & 1, status, DEV_TIMEOUT_ATTN);
+        return ok;
+      };
+      // step i's scores of keys 128 h .., whose K is there
+      auto scores = [&](int i, int h) {
         tc_fence_after();
-        const uint32_t o_col = tmem + 256 + ob * D;
+        const uint32_t col = tmem + static_cast<uint32_t>((2 * i + h) % 3 * 128);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (has_pv) {
-            ok = !abort_flag && mbar_wait_bounded(p_full(j), ob, status, DEV_TIMEOUT_ATTN);
-            if (!ok) break;
-            tc_fence_after();
+        for (int ds = 0; ds < DS; ++ds)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t vdesc = vd + static_cast<uint64_t>(((4 * j + kk) * 2048) >> 4);
-              const uint32_t p_hi = tmem + static_cast<uint32_t>(64 * j + 16 * kk);
-              umma_bf16_tmem_a(o_col, p_hi, vdesc, idesc_o, (j | kk) != 0 ? 1u : 0u);
-              umma_bf16_tmem_a(o_col, p_hi + 8, vdesc, idesc_o, 1u);
-            }
-          }
-          if (has_r && (j & 1)) {
-            const int h = j >> 1;
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(col, qd + static_cast<uint64_t>((ds * Q_SLICE + kk * 32) >> 4),
+                      kd + static_cast<uint64_t>((ds * KV_SLICE + h * HALF + kk * 32) >> 4), idesc_r,
+                      (ds | kk) != 0 ? 1u : 0u);
+        umma_commit(s_full(i, h));
+        umma_commit(k_empty(h));
+      };
+      // step i's P.V of chunks 2h and 2h + 1
+      auto weighted = [&](int i, int h) {
+        if (!wait(v_full(h), i)) return;
+        const uint32_t p_col = tmem + static_cast<uint32_t>((2 * i + h) % 3 * 128);
 #pragma unroll
-            for (int ds = 0; ds < DS; ++ds)
+        for (int jj = 0; jj < 2; ++jj) {
+          if (!wait(p_full(2 * h + jj), i)) return;
+          tc_fence_after();
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_bf16(tmem + static_cast<uint32_t>(128 * h), qd + static_cast<uint64_t>((ds * Q_SLICE + kk * 32) >> 4),
-                          kd + static_cast<uint64_t>((ds * KV_SLICE + h * 128 * 128 + kk * 32) >> 4), idesc_r,
-                          (ds | kk) != 0 ? 1u : 0u);
-            umma_commit(s_full(h));
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t vdesc = vd + static_cast<uint64_t>(((8 * h + 4 * jj + kk) * 2048) >> 4);
+            const uint32_t p_hi = p_col + static_cast<uint32_t>(64 * jj + 16 * kk);
+            umma_bf16_tmem_a(tmem + O_COL, p_hi, vdesc, idesc_o, (h | jj | kk) != 0 ? 1u : 0u);
+            umma_bf16_tmem_a(tmem + O_COL, p_hi + 8, vdesc, idesc_o, 1u);
           }
         }
+        umma_commit(v_empty(h));
+        if (h == 1) umma_commit(o_full);
+      };
+      if (wait(k_full(0), 0)) scores(0, 0);
+      if (wait(k_full(1), 0)) scores(0, 1);
+      for (int i = 0; i < count && ok; ++i) {
+        const bool more = i + 1 < count;
+        int next = 0;  // halves of step i + 1's scores issued
+        auto try_scores = [&]() {
+          if (more && next < 2 && mbar_test(k_full(next), (i + 1) & 1)) scores(i + 1, next++);
+        };
+        // the first half's where its K comes before step i's P
+        if (more) {
+          const unsigned long long t0 = globaltimer_ns();
+          while (next == 0 && !mbar_test(p_full(0), i & 1)) {
+            try_scores();
+            if (abort_flag || globaltimer_ns() - t0 > kWaitLimitNs) break;
+          }
+        }
+        if (i > 0 && !wait(o_empty, i - 1)) break;
+        weighted(i, 0);
         if (!ok) break;
-        if (has_pv) {
-          umma_commit(v_empty);
-          umma_commit(o_full(ob));
-        }
-        if (has_r) umma_commit(k_empty);
+        if (next == 0) try_scores();
+        if (next == 1) try_scores();
+        weighted(i, 1);
+        for (; more && next < 2 && wait(k_full(next), i + 1);) scores(i + 1, next++);
       }
       if (!ok) abort_flag = 1;
       umma_commit(done_bar);
@@ -835,16 +896,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int group_prev = 0, s_prev = 0, live_prev = 0;
     float m_prev = 0.f, l_prev = 0.f;
     bool fold_prev = false, end_prev = false;
-    // takes step i's O: folds it, or sends it as a partial
-    auto take_o = [&](int i) {
-      check(mbar_wait_bounded(o_full(i & 1), (i >> 1) & 1, status, DEV_TIMEOUT_ATTN));
+    // step i's O out of tensor memory
+    auto read_o = [&](int i, uint32_t (&v)[DQ]) {
+      check(mbar_wait_bounded(o_full, i & 1, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
+      if constexpr (DQ == 32)
+        tmem_ld32(lane_base + O_COL + static_cast<uint32_t>(j * DQ), v);
+      else
+        tmem_ld16(lane_base + O_COL + static_cast<uint32_t>(j * DQ), v);
+      tc_fence_before();
+      mbar_arrive(o_empty);
+    };
+    // folds it, or sends it as a partial
+    auto take_o = [&](uint32_t (&v)[DQ]) {
       if (live_prev > 0) {
-        uint32_t v[DQ];
-        if constexpr (DQ == 32)
-          tmem_ld32(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
-        else
-          tmem_ld16(lane_base + 256 + static_cast<uint32_t>((i & 1) * D + j * DQ), v);
         if (!fold_prev) {
           send(v, partial_at(p, group_prev, s_prev), live_prev > 16);
         } else if (s_prev == 0) {
@@ -864,12 +929,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           m_acc = m_new;
         }
       }
-      tc_fence_before();
-      mbar_arrive(o_empty(i & 1));
       if (fold_prev && end_prev && ok) {  // the state as the partial of split 0
         if (live_prev > 0) {
           const int64_t at = partial_at(p, group_prev, 0);
-          uint32_t v[DQ];
 #pragma unroll
           for (int d = 0; d < DQ; ++d) v[d] = __float_as_uint(o_acc[d]);
           send(v, at, live_prev > 16);
@@ -895,14 +957,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0) chains[warp] = start;
     __syncwarp();
     for (int i = 0; i < count; ++i) {
-      check(mbar_wait_bounded(s_full(j >> 1), i & 1, status, DEV_TIMEOUT_ATTN));
+      check(mbar_wait_bounded(s_full(i, j >> 1), (i >> 1) & 1, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
+      const uint32_t r_col = lane_base + static_cast<uint32_t>((2 * i + (j >> 1)) % 3 * 128 + (j & 1) * 64);
       if (live > 0) {
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint32_t v[16];
-          tmem_ld16(lane_base + 64 * j + 16 * h, v);
+          tmem_ld16(r_col + 16 * h, v);
 #pragma unroll
           for (int e = 0; e < 16; e += 4) {
             mx[0] = fmax3(mx[0], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
@@ -927,7 +990,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           float sq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const uint32_t col = lane_base + 64 * j + 32 * h + 16 * half;
+            const uint32_t col = r_col + 32 * h + 16 * half;
             uint32_t v[16], hp[8], lp[8];  // bf16 pairs of the high and the low halves
             tmem_ld16(col, v);
 #pragma unroll
@@ -948,8 +1011,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tmem_st_wait();
       }
-      tc_fence_before();
-      mbar_arrive(p_full(j));
+      if (i > 0) {
+        uint32_t o[DQ];
+        read_o(i - 1, o);
+        mbar_arrive(p_full(j));
+        take_o(o);
+      } else {
+        tc_fence_before();
+        mbar_arrive(p_full(j));
+      }
       quad_sync();
       if (j == 0 && lane < live) {
         l = x_sum[pr];
@@ -959,7 +1029,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *reinterpret_cast<float2*>(p.ws_ml + (partial_at(p, group, s) + (lane >> 4) * (static_cast<int64_t>(p.S) * 16) + (lane & 15)) * 2) =
               make_float2(m, l);
       }
-      if (i > 0) take_o(i - 1);
       group_prev = group;
       s_prev = s;
       live_prev = live;
@@ -980,7 +1049,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
       }
     }
-    if (ok) take_o(count - 1);
+    if (ok) {
+      uint32_t o[DQ];
+      read_o(count - 1, o);
+      if (ok) take_o(o);
+    }
     if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
@@ -1109,7 +1182,7 @@ bool encode_maps(const TreeAttnParams& p, CUtensorMap* mq, CUtensorMap* mk, CUte
   // one sequence: any sequence stride describes it (the coordinate is 0)
   const int64_t sst = p.tree.B > 1 ? p.seq_stride : static_cast<int64_t>(p.tree.max_kv) * p.tok_stride;
   const uint64_t ks[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(p.tok_stride) * 2, static_cast<uint64_t>(sst) * 2};
-  const uint32_t kb[4] = {64, 1, static_cast<uint32_t>(kSplit), 1};
+  const uint32_t kb[4] = {64, 1, static_cast<uint32_t>(kSplit / 2), 1};
   return encode_map(mq, p.q, 3, qd, qs, qb) && encode_map(mk, p.k, 4, kd, ks, kb) && encode_map(mv, p.v, 4, kd, ks, kb);
 }
 
