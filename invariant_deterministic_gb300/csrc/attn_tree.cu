@@ -1079,13 +1079,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // block takes 16 pairs of a (sequence, kv head) and 32 columns, a warp eight of
 // them: a lane half of those for one pair, so a warp's loads of a split are 512
 // contiguous bytes.  The first partials are requested before the tree is read: a
-// node of any depth sees the splits up to position ctx_len.
+// node of any depth sees the splits up to position ctx_len.  A fold runs CH partials
+// behind its loads: six while blocks fill the SMs eight deep, sixteen where four per
+// SM are all there are (a call for 64 nodes behind 32,000 keys, 512 blocks: 98 us
+// with six, 91 with sixteen; 64 trees of 1 to 16 nodes, 8,192 blocks: 140 and 150).
 constexpr int kMergePairs = 16;
 constexpr int kMergeThreads = 128;
 
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 8) attn_tree_merge_kernel(const TreeAttnParams p) {
-  constexpr int CH = 6;  // partials loaded ahead of the (sequential) fold
+template <int D, int CH>
+__global__ void __launch_bounds__(kMergeThreads, CH > 6 ? 4 : 8) attn_tree_merge_kernel(const TreeAttnParams p) {
   __shared__ TreeInfo ti;
   pdl_launch_dependents();
   pdl_wait();
@@ -1224,8 +1226,10 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
     st = launch_kernel(kernel, dim3(sms), dim3(kTcThreads), smem, stream, 1, mq, mk, mv, p);
     if (st != KINV_OK) return st;
   }
-  return launch_kernel(attn_tree_merge_kernel<D>, dim3((pairs + kMergePairs - 1) / kMergePairs * (D / 32), p.Hkv, p.tree.B),
-                       dim3(kMergeThreads), 0, stream, 1, p);
+  const dim3 grid((pairs + kMergePairs - 1) / kMergePairs * (D / 32), p.Hkv, p.tree.B);
+  const bool deep = static_cast<int64_t>(grid.x) * grid.y * grid.z <= 4 * sms;
+  return launch_kernel(deep ? attn_tree_merge_kernel<D, 16> : attn_tree_merge_kernel<D, 6>, grid, dim3(kMergeThreads), 0,
+                       stream, 1, p);
 }
 
 // The workspace: partials (on a 256-byte boundary), their statistics, ws_cov.
