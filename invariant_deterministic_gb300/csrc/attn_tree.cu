@@ -408,8 +408,8 @@ template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const TreeAttnParams p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ TreeInfo ti;
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // behind the wait: the context kernel starts on what this kernel could
   split_block<D, MT, false>(p, blockIdx.x % p.Hkv, blockIdx.x / p.Hkv, blockIdx.z, blockIdx.y, ti, smem_raw, nullptr, nullptr);
 }
 
@@ -683,13 +683,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t o_full = smem_addr(bars + 16), o_empty = smem_addr(bars + 17), done_bar = smem_addr(bars + 18);
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  pdl_wait();
+  // No wait here: the kernel before this one is the tail's, which touches nothing that
+  // this one does, and it lets this one start only behind its own wait.  The wait
+  // stands at the end, as what follows needs both.  (No early launch of the merge: its
+  // blocks beside these cost 25 us of 130 at 64 nodes behind 32,000 keys.)
   if (warp == 0) cursor_start(p, start, count_s);
   __syncthreads();
   const int count = count_s;
-  // (no early launch of the merge: its blocks beside these cost 25 us of 130 at
-  // 64 nodes behind 32,000 keys)
-  if (count == 0) return;
+  if (count == 0) {
+    pdl_wait();
+    return;
+  }
   if (t == 0) {
     for (int i = 0; i < kTcBars; ++i) {
       // p_full: the 128 threads of its chunk; o_empty: every softmax thread
@@ -1073,6 +1077,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  pdl_wait();
 }
 
 // Folds the splits that each node sees, with the decode merge's arithmetic.  A
