@@ -26,14 +26,18 @@ constexpr int kSplit = 256;    // keys per split, as in decode and prefill
 constexpr int kThreads = 256;  // eight warps, 32 positions each for the softmax
 constexpr int kMaxG = 8;
 constexpr int kScoreLd = kSplit + 8;
-// The splits within the context go to the tcgen05 kernel where (sequence, kv
-// head, split) triples that the cache may hold, times the tree's pairs beyond 16,
-// reach this.  Device time of a call with it / without, D = 128, 4 heads a kv head:
-//   16 pairs: 8,000 triples 227 / 212 us (never: one MMA tile, bound by the loads)
-//   32 pairs: 500 triples 40 / 37 us, 1,024 65 / 62, 8,000 227 / 316
-//   64 pairs: 136 triples 23 / 20 us, 280 26 / 30, 1,152 69 / 105
-//   256 pairs: 16 triples 22 / 20 us, 32 24 / 28, 280 37 / 123
-constexpr int64_t kMinWorkTc = 8192;
+// The splits within the context go to the tcgen05 kernel from this many (sequence, kv
+// head, split) triples that the cache may hold times the tree's pairs; trees of at
+// most 16 pairs, one MMA tile that the loads bound, with D = 128 and from 512 triples.
+// Device time of a call with it / without:
+//   D = 128, 16 pairs: 256 triples 16.9 / 14.6 us, 512 23.7 / 24.3, 8,192 184 / 218
+//     32 pairs: 128 triples 15.2 / 13.9 us, 256 17.0 / 19.2, 8,192 193 / 307
+//     128 pairs: 16 triples 14.1 / 12.8 us, 64 14.8 / 16.6, 2,048 89 / 300
+//     256 pairs: 32 triples 15.9 / 25.1 us, 2,048 197 / 813
+//   D = 64, 16 pairs: 512 triples 26.1 / 20.2 us, 4,096 99.6 / 89.8
+//     33 pairs: 256 triples 21.8 / 29.3 us, 4,096 126 / 220
+constexpr int64_t kMinWorkTc = 5120;
+constexpr int64_t kMinTriplesTc = 512;
 
 struct TreeAttnParams {
   kinv_tree tree;
@@ -1210,7 +1214,8 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
   const int sms = sm_count();
   CUtensorMap mq, mk, mv;
   const int pairs = p.tree.max_nodes * p.G;
-  p.tail_only = pairs > 16 && static_cast<int64_t>(p.tree.B) * p.Hkv * (p.tree.max_kv / kSplit) * (pairs - 16) >= kMinWorkTc &&
+  const int64_t triples = static_cast<int64_t>(p.tree.B) * p.Hkv * (p.tree.max_kv / kSplit);
+  p.tail_only = (pairs > 16 ? triples * pairs >= kMinWorkTc : D == 128 && triples >= kMinTriplesTc) &&
                 smem <= static_cast<size_t>(max_smem_optin()) && encode_maps<D>(p, &mq, &mk, &mv);
   // tiles of 16 pairs where they are the whole tree, where tiles of 32 would leave
   // SMs without a block, and where two blocks with tiles of 32 (and 3 KB of

@@ -404,10 +404,10 @@ def test_captured_accept_follows_its_tensors(kinv):
             assert_same_bits(kv[:, :, 0, ctx + i], start[:, :, 0, ctx + j], f"slot {i}")
 
 
-@pytest.mark.parametrize("hq,hkv,d,n,B,slots", [(32, 8, 128, 9, 14, 1100), (32, 8, 128, 5, 66, 1100), (8, 1, 64, 3, 180, 1800),
+@pytest.mark.parametrize("hq,hkv,d,n,B,slots", [(32, 8, 128, 4, 18, 1100), (8, 1, 128, 1, 130, 1100), (32, 8, 128, 9, 14, 1100), (32, 8, 128, 5, 66, 1100), (8, 1, 64, 3, 180, 1800),
                                                 (2, 2, 64, 33, 33, 2100)])
 def test_small_trees_of_many_sequences(kinv, hq, hkv, d, n, B, slots):
-    """Trees of 17 to 36 (node, head) pairs in batches that take the tensor-core
+    """Trees of 8 to 36 (node, head) pairs in batches that take the tensor-core
     path: groups of 16 pairs that are not full, ragged down to one node."""
     ctx = [(37 * b * b + 5) % (slots - n) for b in range(B)]
     parents = [shape_parents(["bushy", "chain", "forest"][b % 3], 1 + (b * 7) % n if b else n, b) for b in range(B)]
