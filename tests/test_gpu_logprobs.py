@@ -142,6 +142,20 @@ def test_rows_where_it_can_go_wrong(kinv, dtype, v):
         assert_same_bits(a[-16:], b, "in a large batch")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_large_maxima(kinv, dtype):
+    """Maxima around 1e30 of either sign over ids far below them and masks."""
+    inf, low = float("inf"), torch.finfo(dtype).min
+    tops = (9.9e29, 1.01e30, -9.9e29, -1.01e30, 3e38, -3e38, 1e29, -1e29)
+    x = torch.empty(len(tops), 3000, dtype=dtype, device="cuda")
+    for r, m in enumerate(tops):
+        below = [t for t in (-2e30, -2.1e30, low, -inf, float("nan"), m - abs(m) / 16) if not t >= m]
+        x[r] = torch.tensor([below[i % len(below)] for i in range(3000)], dtype=torch.float64).to(dtype).cuda()
+        x[r, [10, 2500]] = m                              # two ids share the row
+    ids = torch.tensor([[10, 2500, 0, 1500]] * len(tops), dtype=torch.int32).cuda()
+    check(kinv, x, ids, 2)
+
+
 def test_an_id_beyond_the_vocabulary_is_reported(kinv):
     x = logits(2, 700, 1)
     ids = torch.tensor([[0, 700], [2147483647, -2147483648]], **dict(dtype=torch.int32, device="cuda"))
