@@ -138,6 +138,24 @@ __device__ __forceinline__ void load_unit(const T* row, int first, int V, uint32
       x[4 * i + 2] = v.z;
       x[4 * i + 3] = v.w;
     }
+  } else if (!VEC && sizeof(T) == 2 && first > 0 && first + kUnit + W <= V) {
+    // a row off the 16-byte grid: the two chunks that hold a lane's ids, both within
+    // the row, moved into place (512 rows of 50,001: 19.8 us, 25.5 id by id; 15.4 for
+    // 50,000)
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + first);
+    const uint32_t off = at & 15;  // the same for the warp
+    const uint4* p = reinterpret_cast<const uint4*>(at - off);
+#pragma unroll
+    for (int i = 0; i < kPerLane / W; ++i) {
+      const uint4 a = __ldg(p + i * 32 + lane), b = __ldg(p + i * 32 + lane + 1);
+      uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 6; ++j) w[j] = off & 8 ? w[j + 2] : w[j];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) w[j] = off & 4 ? w[j + 1] : w[j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[4 * i + j] = __funnelshift_r(w[j], w[j + 1], off & 2 ? 16 : 0);
+    }
   } else {
 #pragma unroll
     for (int w = 0; w < kPerLane * static_cast<int>(sizeof(T)) / 4; ++w) {

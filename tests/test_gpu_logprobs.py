@@ -156,6 +156,22 @@ def test_large_maxima(kinv, dtype):
     check(kinv, x, ids, 2)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("v", [700, 1030, 2060, 5000, 50001])
+def test_any_alignment_gives_the_same_bits(kinv, dtype, v):
+    """Rows at every offset from the 16-byte grid, with even and odd distances."""
+    plain = logits(6, v, 21, dtype)
+    ids = torch.randint(0, v, (6, 3), generator=synth.gen(5)).to(torch.int32).cuda()
+    want = kinv.logprobs(plain, ids, top_k=20)
+    for at in range(9):
+        for pad in (0, 1, 2, 4):
+            wide = torch.full((6, at + v + pad), float("nan"), dtype=dtype, device="cuda")
+            wide[:, at: at + v] = plain
+            for a, b in zip(kinv.logprobs(wide[:, at: at + v], ids, top_k=20), want):
+                assert_same_bits(a, b, f"offset {at}, distance {at + v + pad}")
+    assert kinv.last_device_status() == 0
+
+
 def test_an_id_beyond_the_vocabulary_is_reported(kinv):
     x = logits(2, 700, 1)
     ids = torch.tensor([[0, 700], [2147483647, -2147483648]], **dict(dtype=torch.int32, device="cuda"))
