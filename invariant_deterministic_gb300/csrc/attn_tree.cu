@@ -1223,7 +1223,7 @@ kinv_status launch(TreeAttnParams p, cudaStream_t stream) {
   // call against 53; with 32 nodes, where they fit, 33 against 28)
   const bool small = pairs <= 16 ||
                      static_cast<int64_t>(p.tree.B) * p.Hkv * ((pairs + 31) / 32) * (p.tail_only ? 1 : p.S) < sms ||
-                     2 * (split_smem_bytes<D, 2>(p) + 3072 + smem_reserved_per_block()) > static_cast<size_t>(smem_per_sm());
+                     2 * (split_smem_bytes<D, 2>(p) + 3 * 1024 + smem_reserved_per_block()) > static_cast<size_t>(smem_per_sm());
   if (small && !p.tail_only && p.S <= kMaxFused &&
       static_cast<int64_t>(p.tree.B) * p.Hkv * ((pairs + 15) / 16) * p.S <= 2 * sms)
     return launch_fused<D>(p, stream);
