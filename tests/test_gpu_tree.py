@@ -415,3 +415,52 @@ def test_small_trees_of_many_sequences(kinv, hq, hkv, d, n, B, slots):
     out = c.run()
     assert kinv.last_device_status() == 0
     c.check_bits(out, "small trees")
+
+
+@pytest.mark.parametrize("B,n,ctx", [(1, 64, 8000), (4, 16, 4000), (8, 4, 6000), (1, 64, 700)])
+def test_steps_behind_each_other(kinv, B, n, ctx):
+    """Rotation and attention of changing rows with nothing waiting in between: the
+    kernels of a step start early, but not before the rows are there.  On two streams
+    at once, then in one graph."""
+    def setup(seed):
+        c = Case(kinv, [ctx - 37 * b for b in range(B)], [shape_parents("bushy", n, b) for b in range(B)], 32, 8, 128,
+                 seed=seed, poison=False)
+        qkv = [synth.normal_bf16((c.rows, 48 * 128), 1.0, seed + 9 + i, "cuda") for i in range(3)]
+        ws = torch.empty(kinv.attn_tree_workspace(c.tree, 32, 8, 128), dtype=torch.uint8, device="cuda")
+        q = torch.empty(c.rows, 32, 128, dtype=torch.bfloat16, device="cuda")
+
+        def step(i, out):
+            kinv.rope_append_tree(qkv[i % 3], q, c.k, c.v, c.tree, 32, 8, 128, 1e6)
+            return kinv.attn_tree(q, c.k, c.v, c.tree, out=out, workspace=ws)
+
+        want = []
+        for i in range(3):
+            want.append(step(i, torch.empty_like(q)))
+            torch.cuda.synchronize()
+        return step, want
+
+    sides = [setup(200), setup(300)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for i in range(60):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                outs[k].append(sides[k][0](i, torch.empty_like(sides[k][1][0])))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for i, o in enumerate(outs[k]):
+            assert_same_bits(o, sides[k][1][i % 3], f"side {k} step {i}")
+    step, want = sides[0]
+    outs = [torch.empty_like(want[0]) for _ in range(7)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i, o in enumerate(outs):
+            step(i, o)
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        for i, o in enumerate(outs):
+            assert_same_bits(o, want[i % 3], f"captured step {i}")
+    assert kinv.last_device_status() == 0
