@@ -6,6 +6,10 @@ device memory and the current stream); each wrapper checks dtypes and
 contiguity, passes raw pointers, sizes and the current stream, and raises
 ``KinvError`` if the library returns a non-zero status.  There is no fallback:
 if the library has not been built, loading it raises.
+
+``stream=`` names the stream a call is enqueued on (default: the current one).
+The call waits for nothing on other streams: its inputs have to be ready there,
+and whoever reads its results elsewhere waits for it.
 """
 from __future__ import annotations
 
@@ -13,6 +17,7 @@ import ctypes
 import math
 import os
 from dataclasses import dataclass
+from functools import partial
 
 import numpy as np
 import torch
@@ -127,6 +132,42 @@ def _stream(stream=None) -> int:
     if _raw_stream is not None and _get_device is not None:
         return _raw_stream(_get_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _side(stream):
+    """``stream`` where it is another than the current one, else None."""
+    return None if stream is None or stream.cuda_stream == _stream() else stream
+
+
+def _scratch(side, make, *args, **kw):
+    """make(...), of the memory of the stream that the call runs on: a block of
+    the current stream's may be handed out again, or still be in use there,
+    while a kernel on another stream writes it."""
+    if side is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(side):
+        return make(*args, **kw)
+
+
+def _output(side, make, *args, **kw):
+    """The same for a tensor that goes to the caller, who reads it on the current
+    stream and may drop it there."""
+    t = _scratch(side, make, *args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _empty(side):
+    """torch.empty for what a call returns."""
+    return torch.empty if side is None else partial(_output, side, torch.empty)
+
+
+def _hold(side, *tensors) -> None:
+    """The memory of these is not reused before the call on ``side`` is done with
+    it, even if the caller drops them."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(side)
 
 
 def _ptr(t):
@@ -415,6 +456,9 @@ def rope_append_tree(qkv, q_out, k_cache, v_cache, tree: Tree, n_q, n_kv, head_d
     if (rows < tree.total_rows or step != 1 or not q_out.is_contiguous() or width != (n_q + 2 * n_kv) * head_dim
             or q_out.numel() < tree.total_rows * n_q * head_dim or shape[2] != n_kv or shape[3] != head_dim):
         raise ValueError("rope_append_tree: shapes or layouts do not match")
+    side = _side(stream)
+    if side is not None:
+        _hold(side, qkv, q_out, k_cache, v_cache, q_norm, k_norm, *tree.tensors)
     _check(lib().kinv_rope_append_tree(qkv.data_ptr(), ld, q_out.data_ptr(), k_cache.data_ptr(),
                                        v_cache.data_ptr(), stride[0], stride[1], tree.ptr, _ptr(q_norm),
                                        _ptr(k_norm), eps, n_q, n_kv, head_dim, rope_base, _stream(stream)),
@@ -432,8 +476,9 @@ def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_l
     """q [rows][Hq][D]; caches [B][slots][Hkv][D], which already hold the
     nodes' keys and values in their slots.  Each row has the bits of attn_decode
     behind the context and the node's path."""
+    side = _side(stream)
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if side is None else _output(side, torch.empty_like, q)
     bf = torch.bfloat16
     if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is bf and q.is_cuda and out.is_cuda
             and k_cache.is_cuda and v_cache.is_cuda):
@@ -446,8 +491,10 @@ def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_l
             or out.shape != q.shape or shape[3] != d):
         raise ValueError("attn_tree: shapes or layouts do not match")
     if workspace is None:
-        workspace = torch.empty(max(attn_tree_workspace(tree, hq, hkv, d, split_len), 16), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(side, torch.empty, max(attn_tree_workspace(tree, hq, hkv, d, split_len), 16),
+                             dtype=torch.uint8, device=q.device)
+    if side is not None:
+        _hold(side, q, k_cache, v_cache, out, workspace, *tree.tensors)
     _check(lib().kinv_attn_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), stride[0], stride[1],
                                 tree.ptr, out.data_ptr(), hq, hkv, d, split_len, scale, workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), _stream(stream)),
@@ -463,17 +510,19 @@ def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=
     changed in place (None: only the path is found).  Returns (n_accepted [B],
     path [B][max_nodes], out_tokens [B][max_nodes]) int32."""
     b, n, i32 = tree.B, tree.max_nodes, torch.int32
+    side = _side(stream)
+    empty = _empty(side)
     given = [(tokens, "tokens", tree.total_rows), (next_tokens, "next_tokens", tree.total_rows)]
     if n_accepted is None:
-        n_accepted = torch.empty(b, dtype=i32, device=tokens.device)
+        n_accepted = empty(b, dtype=i32, device=tokens.device)
     else:
         given.append((n_accepted, "n_accepted", b))
     if path is None:
-        path = torch.empty(b, n, dtype=i32, device=tokens.device)
+        path = empty(b, n, dtype=i32, device=tokens.device)
     else:
         given.append((path, "path", b * n))
     if out_tokens is None:
-        out_tokens = torch.empty(b, n, dtype=i32, device=tokens.device)
+        out_tokens = empty(b, n, dtype=i32, device=tokens.device)
     else:
         given.append((out_tokens, "out_tokens", b * n))
     for t, name, least in given:
@@ -492,6 +541,8 @@ def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=
             raise ValueError("tree_accept: kv must be [layers][2][B][slots][Hkv][D] with room for the tree")
         kp = kv.data_ptr()
         vp = kp + 2 * cs
+    if side is not None:
+        _hold(side, tokens, next_tokens, kv, n_accepted, path, out_tokens, *tree.tensors)
     _check(lib().kinv_tree_accept(tree.ptr, tokens.data_ptr(), next_tokens.data_ptr(), kp, vp, layers, ls, ss, ts,
                                   hkv, d, n_accepted.data_ptr(), path.data_ptr(), out_tokens.data_ptr(),
                                   _stream(stream)), "kinv_tree_accept")
@@ -510,21 +561,24 @@ def logprobs(logits, ids=None, top_k: int = 0, stream=None):
     (rows, v), (ld, step) = logits.shape, logits.stride()
     if step != 1 and v > 1:
         raise ValueError("logprobs: the ids of a row must be contiguous")
-    dev = logits.device
+    dev, side = logits.device, _side(stream)
+    empty = _empty(side)
     n_ids, lp, lp_ptr, ids_ptr = 0, None, None, None
     if ids is not None:
         _need(ids, torch.int32, "ids")
         if ids.dim() != 2 or ids.shape[0] != rows or not ids.is_contiguous():
             raise ValueError("logprobs: ids must be a contiguous [rows][n]")
         n_ids = ids.shape[1]
-        lp = torch.empty(rows, n_ids, dtype=torch.float32, device=dev)
+        lp = empty(rows, n_ids, dtype=torch.float32, device=dev)
         lp_ptr, ids_ptr = lp.data_ptr(), ids.data_ptr()
-    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
+    entropy = empty(rows, dtype=torch.float32, device=dev)
     top_ids = top_lp = top_ptr = top_lp_ptr = None
     if top_k:
-        top_ids = torch.empty(rows, top_k, dtype=torch.int32, device=dev)
-        top_lp = torch.empty(rows, top_k, dtype=torch.float32, device=dev)
+        top_ids = empty(rows, top_k, dtype=torch.int32, device=dev)
+        top_lp = empty(rows, top_k, dtype=torch.float32, device=dev)
         top_ptr, top_lp_ptr = top_ids.data_ptr(), top_lp.data_ptr()
+    if side is not None:
+        _hold(side, logits, ids)
     _check(lib().kinv_logprobs(logits.data_ptr(), F32 if dt is torch.float32 else BF16,
                                ld if rows > 1 else max(ld, v), rows, v, ids_ptr, n_ids, lp_ptr,
                                entropy.data_ptr(), top_k, top_ptr, top_lp_ptr, _stream(stream)), "kinv_logprobs")
