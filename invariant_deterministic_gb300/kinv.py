@@ -9,7 +9,9 @@ if the library has not been built, loading it raises.
 
 ``stream=`` names the stream a call is enqueued on (default: the current one).
 The call waits for nothing on other streams: its inputs have to be ready there,
-and whoever reads its results elsewhere waits for it.
+and whoever reads its results elsewhere waits for it.  What a call allocates is
+that stream's memory.  The calls on drafted trees and logprobs hold their inputs'
+memory for it too; for the others the caller keeps the inputs until they are done.
 """
 from __future__ import annotations
 
@@ -162,6 +164,10 @@ def _empty(side):
     return torch.empty if side is None else partial(_output, side, torch.empty)
 
 
+def _empty_like(side):
+    return torch.empty_like if side is None else partial(_output, side, torch.empty_like)
+
+
 def _hold(side, *tensors) -> None:
     """The memory of these is not reused before the call on ``side`` is done with
     it, even if the caller drops them."""
@@ -202,7 +208,7 @@ def gemm(a: torch.Tensor, w: torch.Tensor, out: torch.Tensor | None = None,
     if w.shape[1] != k or a.stride(1) != 1 or w.stride(1) != 1:
         raise ValueError("gemm: shapes or layouts do not match")
     if out is None:
-        out = torch.empty(m, n, dtype=out_dtype, device=a.device)
+        out = _empty(_side(stream))(m, n, dtype=out_dtype, device=a.device)
     if out.stride(1) != 1 or tuple(out.shape) != (m, n):
         raise ValueError("gemm: bad output")
     dt = F32 if out.dtype == torch.float32 else BF16
@@ -276,7 +282,7 @@ def gemm_swiglu(a: torch.Tensor, w_gu_il: torch.Tensor, out: torch.Tensor | None
     m, k = a.shape
     f = w_gu_il.shape[0] // 2
     if out is None:
-        out = torch.empty(m, f, dtype=torch.bfloat16, device=a.device)
+        out = _empty(_side(stream))(m, f, dtype=torch.bfloat16, device=a.device)
     _check(lib().kinv_gemm_swiglu(_ptr(a), a.stride(0), _ptr(w_gu_il), w_gu_il.stride(0), _ptr(out),
                                   out.stride(0), m, f, k, _fusion_ptr(fusion), _stream(stream)),
            "kinv_gemm_swiglu")
@@ -308,7 +314,7 @@ def rmsnorm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, residual=None, 
     _need(x, torch.bfloat16, "x")
     rows, dim = x.shape
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty_like(_side(stream))(x)
     _check(lib().kinv_rmsnorm(_ptr(x), x.stride(0), _ptr(residual), _ptr(w), _ptr(out),
                               out.stride(0), rows, dim, float(eps), _stream(stream)),
            "kinv_rmsnorm")
@@ -330,10 +336,10 @@ def attn_decode(q, k_cache, v_cache, kv_len, out=None, workspace=None, split_len
     bsz, hq, d = q.shape
     lmax, hkv = k_cache.shape[1], k_cache.shape[2]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(_side(stream))(q)
     need = attn_decode_workspace(bsz, hq, d, lmax, split_len)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(_side(stream), torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     _check(lib().kinv_attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.stride(0),
                                   k_cache.stride(1), _ptr(kv_len), _ptr(out), bsz, hq, hkv, d, lmax,
                                   split_len, float(scale), _ptr(workspace), workspace.numel(),
@@ -381,10 +387,10 @@ def attn_prefill(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len: int, 
     hkv = k_cache.shape[2]
     bsz = q_start.shape[0]
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(_side(stream))(q)
     need = attn_prefill_workspace(rows, hq, d, max_kv, split_len)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(_side(stream), torch.empty, max(need, 16), dtype=torch.uint8, device=q.device)
     _check(lib().kinv_attn_prefill(_ptr(q), _ptr(k_cache), _ptr(v_cache), k_cache.stride(0),
                                    k_cache.stride(1), _ptr(q_start), _ptr(q_len), _ptr(q_offset),
                                    _ptr(out), bsz, rows, max_q_len, max_kv, hq, hkv, d, split_len,
@@ -478,7 +484,7 @@ def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_l
     behind the context and the node's path."""
     side = _side(stream)
     if out is None:
-        out = torch.empty_like(q) if side is None else _output(side, torch.empty_like, q)
+        out = _empty_like(side)(q)
     bf = torch.bfloat16
     if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is bf and q.is_cuda and out.is_cuda
             and k_cache.is_cuda and v_cache.is_cuda):
@@ -620,7 +626,7 @@ def sample(logits, params_dev, history, hist_len, step, out=None, stream=None):
     _need(logits, torch.float32, "logits")
     bsz, v = logits.shape
     if out is None:
-        out = torch.empty(bsz, dtype=torch.int32, device=logits.device)
+        out = _empty(_side(stream))(bsz, dtype=torch.int32, device=logits.device)
     _check(lib().kinv_sample(_ptr(logits), logits.stride(0), bsz, v, _ptr(params_dev),
                              _ptr(history), history.shape[1] if history is not None else 0,
                              _ptr(hist_len), _ptr(step), _ptr(out), None, 0, _stream(stream)),
@@ -633,7 +639,7 @@ def embed(table, ids, out=None, stream=None):
     vocab, dim = table.shape
     rows = ids.shape[0]
     if out is None:
-        out = torch.empty(rows, dim, dtype=table.dtype, device=table.device)
+        out = _empty(_side(stream))(rows, dim, dtype=table.dtype, device=table.device)
     _check(lib().kinv_embed(_ptr(table), vocab, dim, _ptr(ids), _ptr(out), rows, _stream(stream)),
            "kinv_embed")
     return out
@@ -641,7 +647,7 @@ def embed(table, ids, out=None, stream=None):
 
 def add(x, y, out=None, stream=None):
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty_like(_side(stream))(x)
     _check(lib().kinv_add(_ptr(x), _ptr(y), _ptr(out), x.numel(), _stream(stream)), "kinv_add")
     return out
 
@@ -652,7 +658,7 @@ def scale_columns(w, g, out=None, stream=None):
     _need(g, torch.bfloat16, "g")
     n, k = w.shape
     if out is None:
-        out = torch.empty_like(w)
+        out = _empty_like(_side(stream))(w)
     _check(lib().kinv_scale_columns(_ptr(w), w.stride(0), _ptr(g), _ptr(out), out.stride(0), n, k,
                                     _stream(stream)), "kinv_scale_columns")
     return out
@@ -662,7 +668,7 @@ def swiglu(gu, out=None, stream=None):
     rows, two_f = gu.shape
     f = two_f // 2
     if out is None:
-        out = torch.empty(rows, f, dtype=gu.dtype, device=gu.device)
+        out = _empty(_side(stream))(rows, f, dtype=gu.dtype, device=gu.device)
     _check(lib().kinv_swiglu(_ptr(gu), gu.stride(0), _ptr(out), out.stride(0), rows, f,
                              _stream(stream)), "kinv_swiglu")
     return out

@@ -125,3 +125,25 @@ def test_a_captured_call_on_a_stream_beside(kinv):
         assert_same_bits(out[0], want[0], "replayed")
     del scratch
     assert kinv.last_device_status() == 0
+
+
+def test_decode_and_prefill_scratch_outlives_the_call(kinv):
+    """The same for the attention calls whose scratch is allocated by default."""
+    hq, hkv, d, lmax = 32, 8, 128, 4096
+    k, v = (synth.normal_bf16((4, lmax, hkv, d), 1.0, s, "cuda") for s in (410, 411))
+    q = synth.normal_bf16((4, hq, d), 1.0, 412, "cuda")
+    n = torch.tensor([4096, 3000, 1, 700], dtype=torch.int32, device="cuda")
+    start, lens, off = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (2000, 4, 0))
+    side = torch.cuda.Stream()
+    for call in (lambda s: kinv.attn_decode(q, k, v, n, stream=s),
+                 lambda s: kinv.attn_prefill(q, k, v, start, lens, off, 4, 2004, stream=s)):
+        want = call(None)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(BUSY)
+        out = call(side)
+        new = [torch.full((1 << b,), 0xFF, dtype=torch.uint8, device="cuda") for b in range(9, 27) for _ in range(2)]
+        torch.cuda.synchronize()
+        assert_same_bits(out, want)
+        del new
+    assert kinv.last_device_status() == 0

@@ -146,3 +146,32 @@ def test_on_the_current_stream_nothing_is_held(world, name, stream):
     call(stream)
     assert world.calls[0][1][-1] == MAIN.cuda_stream
     assert all(t.made_on is MAIN and not t.held for t in world.made) and not any(t.held for t in inputs)
+
+
+def other_calls():
+    a, w, row, q = Tensor((4, 256), BF), Tensor((256, 256), BF), Tensor((256,), BF), Tensor((3, 4, 64), BF)
+    k, v, n = Tensor((3, 512, 2, 64), BF), Tensor((3, 512, 2, 64), BF), Tensor((3,), I32)
+    x, h = Tensor((3, 100), F32), Tensor((3, 64), I32)
+    return {
+        "gemm": lambda s: kinv.gemm(a, w, stream=s),
+        "gemm_swiglu": lambda s: kinv.gemm_swiglu(a, w, stream=s),
+        "rmsnorm": lambda s: kinv.rmsnorm(a, row, stream=s),
+        "attn_decode": lambda s: kinv.attn_decode(q, k, v, n, stream=s),
+        "attn_prefill": lambda s: kinv.attn_prefill(q, k, v, n, n, n, 3, 512, stream=s),
+        "sample": lambda s: kinv.sample(x, row, h, n, n, stream=s),
+        "embed": lambda s: kinv.embed(w, n, stream=s),
+        "add": lambda s: kinv.add(a, a, stream=s),
+        "scale_columns": lambda s: kinv.scale_columns(w, row, stream=s),
+        "swiglu": lambda s: kinv.swiglu(a, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", list(other_calls()))
+def test_other_calls_allocate_on_their_stream(world, name):
+    out = other_calls()[name](SIDE)
+    assert world.calls[0][1][-1] == SIDE.cuda_stream
+    assert world.made and all(t.made_on is SIDE for t in world.made)
+    assert out.made_on is SIDE and MAIN in out.held
+    world.made.clear()
+    out = other_calls()[name](None)
+    assert world.calls[1][1][-1] == MAIN.cuda_stream and all(t.made_on is MAIN and not t.held for t in world.made)
