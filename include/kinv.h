@@ -518,6 +518,20 @@ kinv_status kinv_tree_accept(const kinv_tree* tree, const int32_t* tokens,
                              int64_t tok_stride, int Hkv, int D, int32_t* n_accepted,
                              int32_t* path, int32_t* out_tokens, kinv_stream stream);
 
+/* The same with results also for a sequence that is left out for its broken
+ * tree, in the outputs that `mark` names: n_accepted[b] = 0, path[b] and
+ * out_tokens[b] all -1 (for outputs whose memory held something else before).
+ * mark: KINV_TREE_MARK_* or'ed; other bits are KINV_ERR_INVALID_ARG.  0 is
+ * kinv_tree_accept. */
+#define KINV_TREE_MARK_COUNT 1
+#define KINV_TREE_MARK_PATH 2
+#define KINV_TREE_MARK_TOKENS 4
+kinv_status kinv_tree_accept_marked(const kinv_tree* tree, const int32_t* tokens,
+                                    const int32_t* next_tokens, void* k_cache, void* v_cache,
+                                    int n_layers, int64_t layer_stride, int64_t seq_stride,
+                                    int64_t tok_stride, int Hkv, int D, int32_t* n_accepted,
+                                    int32_t* path, int32_t* out_tokens, int mark, kinv_stream stream);
+
 /* ------------------------------------------------------ log probabilities
  * Per row r of logits x (V of them), with m = max x and S = sum e^(x - m):
  *   logprob[r][j]    = x[ids[r][j]] - m - ln S         (j < n_ids)

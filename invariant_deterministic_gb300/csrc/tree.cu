@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kAcceptThreads)
                        const int32_t* __restrict__ next_tokens, __nv_bfloat16* k_cache,
                        __nv_bfloat16* v_cache, int n_layers, int64_t layer_stride, int64_t seq_stride,
                        int64_t tok_stride, int chunks, int32_t* __restrict__ n_accepted,
-                       int32_t* __restrict__ path_out, int32_t* __restrict__ out_tokens, int* status) {
+                       int32_t* __restrict__ path_out, int32_t* __restrict__ out_tokens, int mark, int* status) {
   __shared__ int path[kTreeMaxNodes];
   __shared__ int s_len, s_ctx;
   pdl_launch_dependents();
@@ -177,8 +177,13 @@ __global__ void __launch_bounds__(kAcceptThreads)
             out_tokens[static_cast<int64_t>(b) * tree.max_nodes + t] = t < len ? (j < 32 ? from_lo : from_hi) : -1;
           }
         }
-      } else if (lane == 0 && status) {
-        atomicExch(status, DEV_TREE_BAD);
+      } else {  // left out: marked where the caller asks for it
+        if (lane == 0 && status) atomicExch(status, DEV_TREE_BAD);
+        if (lane == 0 && (mark & KINV_TREE_MARK_COUNT)) n_accepted[b] = 0;
+        for (int t = lane; t < tree.max_nodes; t += 32) {
+          if (mark & KINV_TREE_MARK_PATH) path_out[static_cast<int64_t>(b) * tree.max_nodes + t] = -1;
+          if (mark & KINV_TREE_MARK_TOKENS) out_tokens[static_cast<int64_t>(b) * tree.max_nodes + t] = -1;
+        }
       }
     }
     if (lane == 0) {
@@ -259,9 +264,20 @@ extern "C" kinv_status kinv_tree_accept(const kinv_tree* tree, const int32_t* to
                                         int n_layers, int64_t layer_stride, int64_t seq_stride,
                                         int64_t tok_stride, int Hkv, int D, int32_t* n_accepted,
                                         int32_t* path, int32_t* out_tokens, kinv_stream stream) {
+  return kinv_tree_accept_marked(tree, tokens, next_tokens, k_cache, v_cache, n_layers, layer_stride, seq_stride,
+                                 tok_stride, Hkv, D, n_accepted, path, out_tokens, 0, stream);
+}
+
+extern "C" kinv_status kinv_tree_accept_marked(const kinv_tree* tree, const int32_t* tokens,
+                                               const int32_t* next_tokens, void* k_cache, void* v_cache,
+                                               int n_layers, int64_t layer_stride, int64_t seq_stride,
+                                               int64_t tok_stride, int Hkv, int D, int32_t* n_accepted,
+                                               int32_t* path, int32_t* out_tokens, int mark,
+                                               kinv_stream stream) {
   const kinv_status st = tree_check(tree);
   if (st != KINV_OK) return st;
-  if (n_layers < 0) return KINV_ERR_INVALID_ARG;
+  if (n_layers < 0 || (mark & ~(KINV_TREE_MARK_COUNT | KINV_TREE_MARK_PATH | KINV_TREE_MARK_TOKENS)))
+    return KINV_ERR_INVALID_ARG;
   if (n_layers > 65535) return KINV_ERR_UNSUPPORTED;
   if (tree->B == 0) return KINV_OK;
   if (!n_accepted) return KINV_ERR_INVALID_ARG;
@@ -288,6 +304,6 @@ extern "C" kinv_status kinv_tree_accept(const kinv_tree* tree, const int32_t* to
   const dim3 grid(n_layers > 0 ? 2 * n_layers : 1, tree->B);
   return launch_kernel(tree_accept_kernel, grid, dim3(kAcceptThreads), 0, stream, 1, *tree, tokens, next_tokens,
                        static_cast<__nv_bfloat16*>(k_cache), static_cast<__nv_bfloat16*>(v_cache), n_layers,
-                       layer_stride, seq_stride, tok_stride, chunks, n_accepted, path, out_tokens,
+                       layer_stride, seq_stride, tok_stride, chunks, n_accepted, path, out_tokens, mark,
                        device_status_word());
 }

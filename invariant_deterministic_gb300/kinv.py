@@ -78,6 +78,8 @@ SIGNATURES = {
                               _c_p, _sz, _c_p]),
     "kinv_tree_accept": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i32, _i64, _i64, _i64, _i32, _i32, _c_p,
                                 _c_p, _c_p, _c_p]),
+    "kinv_tree_accept_marked": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i32, _i64, _i64, _i64, _i32, _i32, _c_p,
+                                       _c_p, _c_p, _i32, _c_p]),
     "kinv_logprobs": (_i32, [_c_p, _i32, _i64, _i32, _i32, _c_p, _i32, _c_p, _c_p, _i32, _c_p, _c_p, _c_p]),
     "kinv_decode_advance": (_i32, [_c_p, _c_p, _i32, _c_p, _c_p, _c_p, _c_p, _i32, _c_p]),
 }
@@ -401,6 +403,7 @@ def attn_prefill(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len: int, 
 
 # --------------------------------------------------- trees of drafted tokens
 TREE_MAX_NODES = 64
+MARK_COUNT, MARK_PATH, MARK_TOKENS = 1, 2, 4
 
 
 class TreeStruct(ctypes.Structure):
@@ -481,7 +484,9 @@ def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_l
               scale: float = 0.0, stream=None):
     """q [rows][Hq][D]; caches [B][slots][Hkv][D], which already hold the
     nodes' keys and values in their slots.  Each row has the bits of attn_decode
-    behind the context and the node's path."""
+    behind the context and the node's path.  Rows of no sequence, and those of a
+    sequence left out for its broken tree, are not written: they hold what ``out``
+    held, anything where it is not given."""
     side = _side(stream)
     if out is None:
         out = _empty_like(side)(q)
@@ -514,20 +519,26 @@ def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=
     to its place in the cache.  tokens, next_tokens: int32 [rows] (a node's
     token, the model's token after it); kv: [layers][2][B][slots][Hkv][D] bf16,
     changed in place (None: only the path is found).  Returns (n_accepted [B],
-    path [B][max_nodes], out_tokens [B][max_nodes]) int32."""
+    path [B][max_nodes], out_tokens [B][max_nodes]) int32.  For a sequence left out
+    for its broken tree those that are allocated here say 0 nodes and -1; those
+    that are given keep what they held."""
     b, n, i32 = tree.B, tree.max_nodes, torch.int32
     side = _side(stream)
     empty = _empty(side)
+    mark = 0    # results that are allocated here are defined for a sequence left out, too
     given = [(tokens, "tokens", tree.total_rows), (next_tokens, "next_tokens", tree.total_rows)]
     if n_accepted is None:
+        mark |= MARK_COUNT
         n_accepted = empty(b, dtype=i32, device=tokens.device)
     else:
         given.append((n_accepted, "n_accepted", b))
     if path is None:
+        mark |= MARK_PATH
         path = empty(b, n, dtype=i32, device=tokens.device)
     else:
         given.append((path, "path", b * n))
     if out_tokens is None:
+        mark |= MARK_TOKENS
         out_tokens = empty(b, n, dtype=i32, device=tokens.device)
     else:
         given.append((out_tokens, "out_tokens", b * n))
@@ -549,9 +560,9 @@ def tree_accept(tree: Tree, tokens, next_tokens, kv=None, n_accepted=None, path=
         vp = kp + 2 * cs
     if side is not None:
         _hold(side, tokens, next_tokens, kv, n_accepted, path, out_tokens, *tree.tensors)
-    _check(lib().kinv_tree_accept(tree.ptr, tokens.data_ptr(), next_tokens.data_ptr(), kp, vp, layers, ls, ss, ts,
-                                  hkv, d, n_accepted.data_ptr(), path.data_ptr(), out_tokens.data_ptr(),
-                                  _stream(stream)), "kinv_tree_accept")
+    _check(lib().kinv_tree_accept_marked(tree.ptr, tokens.data_ptr(), next_tokens.data_ptr(), kp, vp, layers, ls, ss,
+                                         ts, hkv, d, n_accepted.data_ptr(), path.data_ptr(), out_tokens.data_ptr(),
+                                         mark, _stream(stream)), "kinv_tree_accept")
     return n_accepted, path, out_tokens
 
 

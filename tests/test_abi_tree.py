@@ -144,3 +144,12 @@ def test_python_wrappers_refuse_wrong_tensors(lib):
         lib.logprobs(torch.zeros(2, 8, dtype=torch.float16))
     with pytest.raises(ValueError):
         lib.logprobs(torch.zeros(2, 8))
+
+
+def test_accept_marked_refuses_other_marks(lib):
+    call = lambda mark, **tree: lib.lib().kinv_tree_accept_marked(
+        _tree(lib, **tree), FAKE, FAKE, FAKE, FAKE, 1, 64 * 1024, 64 * 512, 64, 1, 64, FAKE, FAKE, FAKE, mark, None)
+    for mark in (8, -1, 1 << 30):
+        assert call(mark) == lib.ERR_INVALID_ARG
+    for change, status in BAD_TREES:
+        assert call(7, **change) == getattr(lib, "ERR_" + status)

@@ -49,13 +49,6 @@ class Tensor:
     def record_stream(self, s):
         self.held.append(s)
 
-    def unbind(self, dim=0):
-        assert dim == 0
-        parts = [Tensor(self.shape[1:], self.dtype, self.made_on) for _ in range(self.shape[0])]
-        for p in parts:
-            p.held = self.held
-        return tuple(parts)
-
 
 @pytest.fixture
 def world(monkeypatch):
@@ -78,12 +71,7 @@ def world(monkeypatch):
 
     class Torch:
         empty = staticmethod(make)
-        zeros = staticmethod(make)
         cuda = types.SimpleNamespace(stream=On, current_stream=lambda device=None: now[0])
-
-        @staticmethod
-        def full(shape, value, dtype=None, device=None):
-            return make(shape, dtype=dtype, device=device)
 
         @staticmethod
         def empty_like(t):
@@ -175,3 +163,16 @@ def test_other_calls_allocate_on_their_stream(world, name):
     world.made.clear()
     out = other_calls()[name](None)
     assert world.calls[1][1][-1] == MAIN.cuda_stream and all(t.made_on is MAIN and not t.held for t in world.made)
+
+
+@pytest.mark.parametrize("given", [(), ("path",), ("out_tokens",), ("n_accepted",), ("n_accepted", "path", "out_tokens")])
+def test_allocated_results_are_defined_for_a_sequence_left_out(world, given):
+    """The kernel marks the outputs that were allocated, and leaves those that were given."""
+    tok = Tensor((10,), I32)
+    mine = {name: Tensor((16,), I32) for name in given}
+    out = dict(zip(("n_accepted", "path", "out_tokens"), kinv.tree_accept(tree(), tok, tok, **mine)))
+    (name, args), = world.calls
+    assert name == "kinv_tree_accept_marked"
+    assert args[-2] == sum(bit for bit, x in ((1, "n_accepted"), (2, "path"), (4, "out_tokens")) if x not in given)
+    for x in given:
+        assert out[x] is mine[x]
