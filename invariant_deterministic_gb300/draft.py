@@ -145,8 +145,8 @@ def run_requests_drafted(dec: Decoder, prompts, params, steps: int, draft=ngram_
                          chunk: int = 0):
     """model.run_requests with drafted trees: the same output ids, in fewer
     steps where the guesses are good.  draft(tokens so far, most nodes) ->
-    (node tokens, parents), node 0 the last token.  Returns (each request's
-    output ids, model steps taken)."""
+    (node tokens, parents), node 0 the last token; ([], []) is no guess.  Returns
+    (each request's output ids, model steps taken)."""
     for p in prompts:
         if len(p) + steps > dec.Lmax:
             raise ValueError("prompt empty or too long for the decoder's cache")
@@ -154,13 +154,15 @@ def run_requests_drafted(dec: Decoder, prompts, params, steps: int, draft=ngram_
     dd.start(prompts, params, chunk=chunk)
     taken = 0
     while True:
-        trees = []
-        for b, seq in enumerate(dd.requests):
-            left = steps - (len(seq) - dd.prompt_len[b])
-            # a node more than the tokens still wanted could not be kept
-            trees.append(draft(seq, min(max_nodes, dec.Lmax - len(seq) + 1)) if left > 0 else ([], []))
-        if all(not t[0] for t in trees):
+        left = [steps - (len(seq) - n) for seq, n in zip(dd.requests, dd.prompt_len)]
+        if all(x <= 0 for x in left):
             break
+        trees = []
+        for seq, more in zip(dd.requests, left):
+            # no more nodes than the cache has slots for behind the request; without
+            # a guess the step decides one token
+            tree = draft(seq, min(max_nodes, dec.Lmax - len(seq) + 1)) if more > 0 else ([], [])
+            trees.append(([seq[-1]], [-1]) if more > 0 and not tree[0] else tree)
         dd.step(trees)
         taken += 1
     return [seq[n: n + steps] for seq, n in zip(dd.requests, dd.prompt_len)], taken

@@ -85,3 +85,40 @@ def test_decoder_limits():
         draft.DraftDecoder(D, 16)
     with pytest.raises(ValueError):
         draft.DraftDecoder(D, 65)
+
+
+class _Steps:
+    """Stands in for DraftDecoder: a step decides the next tokens of a fixed answer,
+    as many as the tree's chain from node 0 gets right, and one more."""
+
+    def __init__(self, dec, max_nodes):
+        self.most, self.trees = max_nodes, []
+
+    def start(self, prompts, params, chunk=0):
+        self.requests = [list(p) for p in prompts]
+        self.prompt_len = [len(p) for p in prompts]
+
+    def step(self, trees):
+        for seq, (nodes, parents) in zip(self.requests, trees):
+            if nodes:
+                assert nodes[0] == seq[-1] and parents[0] == -1 and len(nodes) <= self.most
+                last, right = seq[-1], 0
+                while right + 1 < len(nodes) and nodes[right + 1] == last + right + 1:
+                    right += 1
+                seq.extend(range(last + 1, last + right + 2))
+        self.trees.append(trees)
+
+
+def _drafted(monkeypatch, prompts, steps, guess):
+    monkeypatch.setattr(draft, "DraftDecoder", _Steps)
+    return draft.run_requests_drafted(_Dec, prompts, None, steps, draft=guess, max_nodes=4)
+
+
+def test_a_drafter_with_no_guess_leaves_the_answer_whole(monkeypatch):
+    prompts, want = [[1, 2], [7]], [[3, 4, 5, 6], [8, 9, 10, 11]]
+    assert _drafted(monkeypatch, prompts, 4, lambda t, n: ([], [])) == (want, 4)
+    # no guess for one request, in some of its steps, or in all but the first
+    assert _drafted(monkeypatch, prompts, 4, lambda t, n: ([], []) if t[0] == 7 else ([t[-1]], [-1])) == (want, 4)
+    once = lambda t, n: ([t[-1], t[-1] + 1], [-1, 0]) if len(t) < 3 else ([], [])
+    assert _drafted(monkeypatch, prompts, 4, once)[0] == want
+    assert _drafted(monkeypatch, prompts, 0, lambda t, n: ([], [])) == ([[], []], 0)
