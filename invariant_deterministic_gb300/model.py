@@ -274,6 +274,9 @@ class Decoder:
         ``seq`` and returns, for the rows of all but the last, (log probability
         of the next token [n - 1], entropy [n - 1], top ids and log probabilities
         [n - 1][top_k] or None).  A row's numbers do not depend on the chunking."""
+        kinv._need(tokens, torch.int32, "tokens")
+        if tokens.dim() != 1 or not tokens.is_contiguous():
+            raise ValueError("score: tokens must be a contiguous vector")
         n = int(tokens.shape[0])
         if n < 2 or n - 1 > self.Lmax or not 0 <= seq < self.B or chunk < 0:
             raise ValueError("score: two tokens at least, all but the last within the cache of one of its sequences")
