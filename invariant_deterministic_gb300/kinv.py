@@ -501,6 +501,8 @@ def attn_tree(q, k_cache, v_cache, tree: Tree, out=None, workspace=None, split_l
     if (not q.is_contiguous() or not out.is_contiguous() or rows < tree.total_rows
             or out.shape != q.shape or shape[3] != d):
         raise ValueError("attn_tree: shapes or layouts do not match")
+    if workspace is not None and not workspace.is_cuda:
+        raise ValueError("workspace: expected a CUDA tensor")
     if workspace is None:
         workspace = _scratch(side, torch.empty, max(attn_tree_workspace(tree, hq, hkv, d, split_len), 16),
                              dtype=torch.uint8, device=q.device)
