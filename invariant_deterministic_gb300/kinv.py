@@ -465,6 +465,10 @@ def rope_append_tree(qkv, q_out, k_cache, v_cache, tree: Tree, n_q, n_kv, head_d
     if (rows < tree.total_rows or step != 1 or not q_out.is_contiguous() or width != (n_q + 2 * n_kv) * head_dim
             or q_out.numel() < tree.total_rows * n_q * head_dim or shape[2] != n_kv or shape[3] != head_dim):
         raise ValueError("rope_append_tree: shapes or layouts do not match")
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None and not (t.dtype is bf and t.is_cuda and t.is_contiguous() and t.numel() >= head_dim):
+            _need(t, bf, name)
+            raise ValueError(f"rope_append_tree: {name} must hold a contiguous gain for each of a head's values")
     side = _side(stream)
     if side is not None:
         _hold(side, qkv, q_out, k_cache, v_cache, q_norm, k_norm, *tree.tensors)
