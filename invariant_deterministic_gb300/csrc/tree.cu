@@ -19,6 +19,7 @@ namespace {
 // of kinv_rope_append.
 constexpr int kRopeThreads = 256;
 constexpr int kRopeAhead = 6;
+constexpr int kRopeWholeRows = 128;  // from this many rows on a block takes a row whole (measured at the launch)
 
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads)
@@ -245,7 +246,12 @@ extern "C" kinv_status kinv_rope_append_tree(const void* qkv, int64_t ld_qkv, vo
   }
   const RopeFreqs& freqs = last.f;
   const int heads = Hq + 2 * Hkv;
-  const int hpb = tree->total_rows >= 512 ? heads : 8;
+  // A head per warp while the rows leave SMs free, whole rows behind that, where the
+  // angles, formed once per block, and the blocks themselves count (48 heads of 128,
+  // rows: us with 8 heads a block / with all: 8: 3.7 / 5.0, 64: 4.7 / 5.5, 128: 5.6 /
+  // 5.6, 256: 8.3 / 5.9, 512: 13.4 / 8.4, 2,048: 43 / 17.7; 16 and 24 heads a block lie
+  // between the two from 256 rows).
+  const int hpb = tree->total_rows >= kRopeWholeRows ? heads : 8;
   const dim3 grid(tree->max_nodes, (heads + hpb - 1) / hpb, tree->B);
   int* status = device_status_word();
   auto* k = static_cast<__nv_bfloat16*>(k_cache);
