@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4) logprobs_ker
 // 22 us as one block, 9 as eight).
 int part_count(int rows, int units) {
   int parts = 1;
-  while (parts < 8 && static_cast<int64_t>(rows) * parts < 152 && units > parts * kWarps) parts *= 2;
+  while (parts < 8 && static_cast<int64_t>(rows) * parts < sm_count() && units > parts * kWarps) parts *= 2;
   return parts;
 }
 
@@ -468,7 +468,7 @@ kinv_status launch(const LogprobParams& p, bool vec, cudaStream_t stream) {
 // alternatives: 34 us, 76 with eight warps a row; 8,192 rows of 500: 25 and 135).
 template <typename T>
 kinv_status launch(const LogprobParams& p, bool vec, cudaStream_t stream) {
-  return p.units <= kWarps && p.rows >= 152 * 16 ? launch<T, 1>(p, vec, stream) : launch<T, kWarps>(p, vec, stream);
+  return p.units <= kWarps && p.rows >= sm_count() * 16 ? launch<T, 1>(p, vec, stream) : launch<T, kWarps>(p, vec, stream);
 }
 
 }  // namespace
