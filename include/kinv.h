@@ -435,8 +435,8 @@ kinv_status kinv_decode_advance(const int32_t* tokens, int32_t* history, int his
  * row_offset[b] + n_nodes[b] <= total_rows.  The rows of different sequences
  * must not overlap.  A sequence whose device-side numbers break a bound, or
  * that holds a parent outside [-1, own index), is left out of every call below
- * -- nothing of it is written -- and the status word records
- * KINV_ERR_INVALID_ARG.  Rows that belong to no sequence are left as they
+ * -- nothing of it is written, but for what kinv_tree_accept_marked is asked to
+ * mark -- and the status word records KINV_ERR_INVALID_ARG.  Rows that belong to no sequence are left as they
  * were.  The struct itself is read on the host before a call returns; with B,
  * total_rows or max_nodes 0 no sequence has a node, and the arrays are not
  * read. */
@@ -481,6 +481,13 @@ kinv_status kinv_rope_append_tree(const void* qkv, int64_t ld_qkv, void* q_out, 
  * for kinv_attn_decode.  workspace: device, 16-byte aligned, at least
  * kinv_attn_tree_workspace(B, total_rows, max_nodes, Hq, Hkv, D, max_kv,
  * split_len) bytes; two calls that may run at the same time need one each.
+ * It has room for an fp32 partial of every (node, head) that max_nodes allows in
+ * every split that max_kv allows, about B max_nodes Hq (D + 2) 4 ceil(max_kv /
+ * split_len) bytes: with Hq 32 and D 128, 17 MB for 4 trees of 16 nodes in 4,096
+ * slots, 8.7 GB for 64 of 64 in 32,768.  max_nodes and max_kv also decide which
+ * kernels a call launches (never a bit of the result), so both pay for being
+ * close: one tree of 8 nodes behind 500 keys takes 10.8 us with max_kv 576 and
+ * 12.7 with 32,768.
  * Requirements as for kinv_attn_decode. */
 size_t kinv_attn_tree_workspace(int B, int total_rows, int max_nodes, int Hq, int Hkv, int D,
                                 int max_kv, int split_len);

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tree_split_kernel(const Tree
   split_block<D, MT, false>(p, blockIdx.x % p.Hkv, blockIdx.x / p.Hkv, blockIdx.z, blockIdx.y, ti, smem_raw, nullptr, nullptr);
 }
 
-// The whole call in one launch where a sequence has at most eight splits: a
+// The whole call in one launch where max_kv allows a sequence at most eight splits: a
 // cluster of a block per split (block rank s) of a (kv head, tile of 16 pairs,
 // sequence); the partials stay in shared memory, and the blocks of the context's
 // splits share the tile's pairs and fold them over the cluster in split order,
@@ -688,8 +688,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   // No wait here: the kernel before this one is the tail's, which touches nothing that
-  // this one does, and it lets this one start only behind its own wait.  The wait
-  // stands at the end, as what follows needs both.  (No early launch of the merge: its
+  // this one does, and every one of its blocks lets this one start only behind its own
+  // wait.  So all before the tail is complete when a block of this kernel runs: the
+  // writers of q, the caches and the tree, and the merge of an earlier call, which read
+  // the partials that this one overwrites.  The wait stands at the end, as what follows
+  // needs both.  (No early launch of the merge: its
   // blocks beside these cost 25 us of 130 at 64 nodes behind 32,000 keys.)
   if (warp == 0) cursor_start(p, start, count_s);
   __syncthreads();
