@@ -53,7 +53,7 @@ typedef enum {
   KINV_ERR_TIMEOUT = -6      /* a bounded device-side wait gave up */
 } kinv_status;
 
-typedef enum { KINV_BF16 = 0, KINV_F32 = 1 } kinv_dtype;
+typedef enum { KINV_BF16 = 0, KINV_F32 = 1, KINV_E4M3 = 2, KINV_I8 = 3 } kinv_dtype;
 
 /* Human-readable name of a status code (static string). */
 const char* kinv_status_string(int status);
@@ -69,8 +69,9 @@ const char* kinv_build_id(void);
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device: KINV_OK, or the last code recorded since the previous call --
  * KINV_ERR_TIMEOUT (a bounded wait gave up), KINV_ERR_INVALID_ARG (an
- * attention call met a device-side length outside its stated bounds, a call on
- * drafted trees a broken tree, kinv_logprobs an id beyond the vocabulary) or
+ * attention or 8-bit cache call met a device-side length or place outside its
+ * stated bounds, a call on drafted trees a broken tree, kinv_logprobs an id
+ * beyond the vocabulary) or
  * KINV_ERR_UNSUPPORTED (a sampler row outside the supported settings).
  * Returns KINV_ERR_CUDA if the synchronisation itself fails. */
 int kinv_last_device_status(kinv_stream stream);
@@ -295,6 +296,128 @@ kinv_status kinv_attn_prefill(const void* q, const void* k_cache, const void* v_
                               int Hq, int Hkv, int D, int split_len, float scale,
                               void* workspace, size_t workspace_bytes,
                               kinv_stream stream);
+
+/* ------------------------------------------- sliding window with sinks
+ * Attention whose rows see the last `window` keys, their own among them, and
+ * the first `sinks` keys of the sequence: the row at position p sees key j <= p
+ * if j > p - window or j < sinks (the pages have no counterpart).  window = 0
+ * means every key j <= p; where nothing is hidden a row has the bits of
+ * kinv_attn_decode.  The splits stay at
+ * their absolute offsets, splits without a visible key are left out, and hidden
+ * keys in the others have weight 0 and are not read (decode) or do not count
+ * (prefill), so the invariances hold as above: a row's bits depend on its own
+ * sequence alone, and a decode step equals a one-row prefill.
+ * What a hidden slot holds does not matter to decode, nor to prefill where it is
+ * hidden from every row of the call.  Where a value that is an infinity or NaN
+ * is visible to one row of a prompt chunk, other rows of the chunk near it may
+ * get NaN as well, as in kinv_attn_prefill.
+ * Arguments, requirements and errors as above; window < 0 or sinks < 0:
+ * KINV_ERR_INVALID_ARG.  The decode call's workspace grows with the window and
+ * the sinks instead of Lmax. */
+size_t kinv_attn_decode_window_workspace(int B, int Hq, int D, int Lmax, int split_len, int window, int sinks);
+kinv_status kinv_attn_decode_window(const void* q, const void* k_cache, const void* v_cache,
+                                    int64_t seq_stride, int64_t tok_stride,
+                                    const int32_t* kv_len, void* out,
+                                    int B, int Hq, int Hkv, int D, int Lmax, int split_len,
+                                    int window, int sinks, float scale, void* workspace,
+                                    size_t workspace_bytes, kinv_stream stream);
+kinv_status kinv_attn_prefill_window(const void* q, const void* k_cache, const void* v_cache,
+                                     int64_t seq_stride, int64_t tok_stride,
+                                     const int32_t* q_start, const int32_t* q_len,
+                                     const int32_t* q_offset, void* out,
+                                     int B, int total_rows, int max_q_len, int max_kv,
+                                     int Hq, int Hkv, int D, int split_len, int window, int sinks,
+                                     float scale, void* workspace, size_t workspace_bytes,
+                                     kinv_stream stream);
+
+/* ------------------------------------------------ 8-bit key/value cache
+ * Keys and values as 8-bit codes with a scale for every (token, kv head), keys
+ * and values apart (the pages have no counterpart).  A value is code * 2^E.
+ * With amax the largest magnitude among a vector's D bf16 values,
+ *   KINV_E4M3  E = the smallest e with amax <= 448 * 2^e, -100 <= E <= 119
+ *   KINV_I8    E = the smallest e with amax <= 127 * 2^e, -100 <= E <= 121
+ *   code = x * 2^-E rounded to the nearest code (ties to even, saturating)
+ * and E = -128 marks a vector that held an infinity or NaN; all of it reads back
+ * as NaN (its codes are 0).  code * 2^E is a bf16 number, so nothing is lost
+ * after the one rounding to a code: at most half a step, 2^-4 of the value
+ * (e4m3, 2^-10 * 2^E where that is more) or 2^E / 2 (int8).  A code depends on
+ * its own token alone, never on its neighbours in the cache, so the cache is the
+ * same for every chunking of a prompt.
+ *
+ * Element (b, slot, g, d) of k and v is the byte at b*seq_stride +
+ * slot*tok_stride + g*D + d; the exponents of (b, slot, g) are at
+ * b*exp_seq_stride + g*exp_head_stride + slot.  B sequences of `slots` slots.
+ * k, v 16-byte aligned, seq_stride and tok_stride multiples of 16, tok_stride >=
+ * Hkv*D, exp_head_stride >= slots; D in {64, 128}.  The struct is read on the
+ * host before a call returns.  Codes 0x7F and 0xFF of e4m3 and exponents outside
+ * [-126, 121] but for -128 are never written and must not be given. */
+typedef struct {
+  void* k;
+  void* v;
+  int8_t* k_exp;
+  int8_t* v_exp;
+  int64_t seq_stride;
+  int64_t tok_stride;
+  int64_t exp_seq_stride;
+  int64_t exp_head_stride;
+  int B;
+  int slots;
+  kinv_dtype dtype; /* KINV_E4M3 or KINV_I8 */
+} kinv_cache8;
+
+/* kinv_rope_append with the key and value heads in 8 bits: the codes of the
+ * rotated keys, rounded to bf16, and of the values.  The angles are carried a
+ * little further than there, so a query or key may differ by a bf16 step where
+ * it lies next to a rounding border.  Arguments, requirements and errors as
+ * there; no two rows of a call may name the same place.  A row whose sequence or position lies
+ * outside the cache is left out -- its row of q_out too -- and the status word
+ * records KINV_ERR_INVALID_ARG. */
+kinv_status kinv_rope_append8(const void* qkv, int64_t ld_qkv, void* q_out, const kinv_cache8* cache,
+                              const int32_t* seq, const int32_t* pos, const void* q_norm,
+                              const void* k_norm, float eps, int rows, int Hq, int Hkv, int D,
+                              float rope_base, kinv_stream stream);
+
+/* Keys and values between bf16 and the 8-bit cache: token i < len[b] of sequence
+ * b, at b*seq_stride + i*tok_stride + g*D + d of the bf16 k and v (elements),
+ * goes into (write) or comes from (read) slot start[b] + i.  start, len: device
+ * int32 [B], B at most the cache's; max_len bounds len[b].  A sequence whose
+ * numbers break a bound (0 <= len[b] <= max_len, 0 <= start[b], start[b] + len[b]
+ * <= slots) is left out and the status word records KINV_ERR_INVALID_ARG.
+ * Everything else in either cache stays as it was.  Strides multiples of 8,
+ * 16-byte aligned bases, Hkv <= 1024.  The sequences' slots and tokens must not
+ * overlap where they are written: a stride of 0 between sequences is refused
+ * there (as in kinv_rope_append8) when B > 1. */
+kinv_status kinv_cache8_write(const void* k, const void* v, int64_t seq_stride, int64_t tok_stride,
+                              const kinv_cache8* cache, const int32_t* start, const int32_t* len,
+                              int B, int max_len, int Hkv, int D, kinv_stream stream);
+kinv_status kinv_cache8_read(const kinv_cache8* cache, const int32_t* start, const int32_t* len,
+                             void* k, void* v, int64_t seq_stride, int64_t tok_stride, int B,
+                             int max_len, int Hkv, int D, kinv_stream stream);
+
+/* kinv_attn_decode and kinv_attn_prefill over the 8-bit cache, with a sliding
+ * window and sinks as above (window = 0: every key).  A row gets the bits that
+ * kinv_attn_decode_window and kinv_attn_prefill_window give on the cache read
+ * back, wherever no score, product or sum on the way leaves the normal range of
+ * fp32 (with e4m3 that asks for |q| below 2^37, and a weight below 2^-100 times
+ * the largest scale among its 256 keys may lose bits), so all their invariances
+ * hold; hidden slots and those behind a
+ * sequence's last key may hold anything.
+ * kv_len[b] in [0, slots], else zeros and KINV_ERR_INVALID_ARG in the status
+ * word; B at most the cache's, max_kv at most its slots; other arguments,
+ * requirements and errors as there.  workspace: device, 16-byte aligned, as many
+ * bytes as the query says; calls that may run at the same time need one each.
+ * The decode call's holds the split partials; the prefill call's holds the keys
+ * and values that its rows see, read back: B max_kv Hkv D 4 bytes. */
+size_t kinv_attn_decode8_workspace(int B, int Hq, int D, int slots, int window, int sinks, int split_len);
+kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache, const int32_t* kv_len, void* out,
+                              int B, int Hq, int Hkv, int D, int split_len, int window, int sinks,
+                              float scale, void* workspace, size_t workspace_bytes, kinv_stream stream);
+size_t kinv_attn_prefill8_workspace(int B, int total_rows, int Hq, int Hkv, int D, int max_kv, int split_len);
+kinv_status kinv_attn_prefill8(const void* q, const kinv_cache8* cache, const int32_t* q_start,
+                               const int32_t* q_len, const int32_t* q_offset, void* out, int B,
+                               int total_rows, int max_q_len, int max_kv, int Hq, int Hkv, int D,
+                               int split_len, int window, int sinks, float scale, void* workspace,
+                               size_t workspace_bytes, kinv_stream stream);
 
 /* --------------------------------------------------------------- sampler
  * Seeded sampler with the settings a Kinetic receipt records (Kinetic

@@ -42,6 +42,7 @@
 #include "attn_mma.cuh"
 #include "attn_tc.cuh"
 #include "common.cuh"
+#include "window.cuh"
 
 namespace kinv {
 namespace {
@@ -65,6 +66,7 @@ struct AttnParams {
   float c2;                 // fp32(scale * log2 e) > 0
   int max_len;              // Lmax: the bound 0 <= kv_len[b] <= Lmax (the host cannot read kv_len)
   int* status;              // device status word (a sequence outside the bound)
+  Window win;               // the sliding-window form: S counts the listed splits
 };
 
 // A sequence whose kv_len breaks the bound gets zeros and the call records
@@ -78,7 +80,9 @@ __device__ __forceinline__ void report_bad_length(const AttnParams& p) {
   if (threadIdx.x == 0 && p.status) atomicExch(p.status, DEV_ATTN_BAD_LENGTH);
 }
 
-template <int D>
+// WIN: a block takes a split that holds a key its row sees, loads the visible
+// keys alone and gives the others weight 0 and zero V.
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p) {
   constexpr int C8 = D / 8;               // 16-byte chunks per key row
   constexpr int SUB = 64;                 // keys per load stage
@@ -102,16 +106,25 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p
   // kv heads are the fastest grid index: the blocks reading the 256-byte
   // slices of the same token rows run side by side
   const int g = blockIdx.x;
-  const int s = blockIdx.y;
+  const int s = blockIdx.y;                            // place among the row's partials
   const int b = blockIdx.z;
   if (!seq_ok(p, b)) {
     report_bad_length(p);
     return;
   }
   const int len = p.kv_len[b];
-  const int k0 = s * kSplit;
+  int k0 = s * kSplit, lo = 0, sink = 0;
+  if (WIN) {
+    const int first = window_lo(p.win, len);
+    const SplitList list = visible_splits(p.win, first, len);
+    if (s >= list.count) return;
+    k0 = list.split(s) * kSplit;
+    lo = first - k0;
+    sink = p.win.sinks - k0;
+  }
   const int nmax = min(kSplit, len - k0);              // keys of this split
   if (nmax <= 0) return;
+  auto in_window = [&](int key) { return !WIN || key >= lo || key < sink; };
   const int G = p.G;                                   // (row, head) pairs: MMA rows 0..G-1
   const int t = threadIdx.x;
   const int lane = t & 31, warp = t >> 5;
@@ -128,6 +141,7 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p
     for (int idx = t; idx < rows * C8; idx += kThreads) {
       const int r = idx / C8, c = idx % C8;
       const int key = j * SUB + r;
+      if (!in_window(key)) continue;
       cp_async16_hint(kv_base + static_cast<uint32_t>(key * D * 2 + ((c ^ (key & 7)) << 4)),
                       src + seq_off + static_cast<int64_t>(key) * p.tok_stride + c * 8, kv_policy);
     }
@@ -179,6 +193,13 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p
     const int key = nmax + idx / C8, c = idx % C8;
     *reinterpret_cast<uint4*>(kv + key * D + ((c ^ (key & 7)) << 3)) = make_uint4(0, 0, 0, 0);
   }
+  if (WIN) {
+    const int h0 = max(sink, 0), h1 = min(lo, nmax);   // hidden keys before the window
+    for (int idx = t; idx < (h1 - h0) * C8; idx += kThreads) {
+      const int key = h0 + idx / C8, c = idx % C8;
+      *reinterpret_cast<uint4*>(kv + key * D + ((c ^ (key & 7)) << 3)) = make_uint4(0, 0, 0, 0);
+    }
+  }
   cp_async_commit();
 
   // --- softmax statistics.  A lane holds row gq (pair gq < G; the
@@ -193,7 +214,8 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p
   for (int nb = 0; nb < 4; ++nb) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
-      if (warp * 32 + nb * 8 + 2 * tq + e < cnt) mx = fmaxf(mx, sc[nb][e]);
+      if (warp * 32 + nb * 8 + 2 * tq + e < cnt && in_window(warp * 32 + nb * 8 + 2 * tq + e))
+        mx = fmaxf(mx, sc[nb][e]);
   }
 #pragma unroll
   for (int o = 1; o <= 2; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -210,7 +232,8 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p
     float x[2], h[2], l[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      x[e] = warp * 32 + nb * 8 + 2 * tq + e < cnt ? ex2_approx(__fmaf_rn(sc[nb][e], p.c2, -m)) : 0.f;
+      const int key = warp * 32 + nb * 8 + 2 * tq + e;
+      x[e] = key < cnt && in_window(key) ? ex2_approx(__fmaf_rn(sc[nb][e], p.c2, -m)) : 0.f;
       split_bf16(x[e], h[e], l[e]);
       sum = __fadd_rn(sum, x[e]);
     }
@@ -375,9 +398,13 @@ struct PrefillTcArgs {
   int max_len, max_q_len, total_rows;
   float c2;            // fp32(scale * log2 e) > 0
   int* status;
+  Window win;
 };
 
-template <int D>
+// WIN: a tile walks the splits that hold a key one of its rows sees (`it` counts
+// them, split_of(it) names them); a pair's hidden keys get weight 0, and V rows
+// hidden from the whole tile are zeroed like those past its last key.
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const PrefillTcArgs a) {
@@ -425,7 +452,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int row0 = off + first;           // q / out row of the tile's first row
   const int len0 = st0 + first + 1;       // keys the first row sees (row r: len0 + r)
   const int len_last = len0 + nrows - 1;
-  const int ns = (len_last + kSplit - 1) / kSplit;
+  const int tile_lo = WIN ? window_lo(a.win, len0) : 0;  // the first row's first window key
+  const SplitList list = visible_splits(a.win, tile_lo, len_last);
+  const int ns = WIN ? list.count : (len_last + kSplit - 1) / kSplit;
+  auto split_of = [&](int it) { return WIN ? list.split(it) : it; };
 
   if (t == 0) {
     for (int i = 0; i < kTcBars; ++i) {
@@ -456,13 +486,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto load_k = [&](int s) {
       mbar_arrive_expect_tx(k_full, KV_BYTES);
       for (int ds = 0; ds < DS; ++ds)
-        tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, g, s * kSplit, b, k_full, pol);
+        tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, g, split_of(s) * kSplit, b, k_full, pol);
       k_issued = s + 1;
     };
     auto load_v = [&](int s) {
       mbar_arrive_expect_tx(v_full, KV_BYTES);
       for (int ds = 0; ds < DS; ++ds)
-        tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, g, s * kSplit, b, v_full, pol);
+        tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, g, split_of(s) * kSplit, b, v_full, pol);
       v_issued = s + 1;
     };
     if (lane == 0) {
@@ -488,10 +518,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       stop = __shfl_sync(0xffffffffu, *abort_flag, 0) != 0;
       if (stop) break;
-      const int nmax = min(kSplit, len_last - s * kSplit);
+      const int nmax = min(kSplit, len_last - split_of(s) * kSplit);
       for (int idx = lane; idx < (kSplit - nmax) * DS * 8; idx += 32) {
         const int key = nmax + idx / (DS * 8), rest = idx % (DS * 8);
         *reinterpret_cast<uint4*>(v_s + (rest / 8) * KV_SLICE + key * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      if (WIN) {
+        const int h0 = max(a.win.sinks - split_of(s) * kSplit, 0), h1 = min(tile_lo - split_of(s) * kSplit, nmax);
+        for (int idx = lane; idx < (h1 - h0) * DS * 8; idx += 32) {
+          const int key = h0 + idx / (DS * 8), rest = idx % (DS * 8);
+          *reinterpret_cast<uint4*>(v_s + (rest / 8) * KV_SLICE + key * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -630,7 +667,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int jj = 0; jj < 32; jj += 2) {
             float2 o = make_float2(o_acc[32 * c + jj], o_acc[32 * c + jj + 1]);
             const float2 t = __fmul2_rn(make_float2(__uint_as_float(v[jj]), __uint_as_float(v[jj + 1])), fc2);
-            o = __fadd2_rn(unit ? o : __fmul2_rn(o, fa2), t);
+            if (WIN) {
+              // single adds: a packed add behind packed products is compiled to a
+              // fused one, which rounds once where the merge kernel rounds twice
+              const float2 u = unit ? o : __fmul2_rn(o, fa2);
+              o = make_float2(__fadd_rn(u.x, t.x), __fadd_rn(u.y, t.y));
+            } else {
+              o = __fadd2_rn(unit ? o : __fmul2_rn(o, fa2), t);
+            }
             o_acc[32 * c + jj] = o.x;
             o_acc[32 * c + jj + 1] = o.y;
           }
@@ -644,9 +688,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool in_prev = false;
     for (int s = 0; s < ns; ++s) {
       const uint32_t ph = s & 1;
-      const int cnt = min(kSplit, len - s * kSplit);
+      const int k0 = split_of(s) * kSplit;
+      const int cnt = min(kSplit, len - k0);
+      // the pair's first window key and the sinks' end within the split
+      const int lo = WIN ? window_lo(a.win, len) - k0 : 0, sink = WIN ? a.win.sinks - k0 : 0;
       // every pair of the tile sees the whole split: no key is masked
-      const bool whole = len0 - s * kSplit >= kSplit;
+      const bool whole = len0 - k0 >= kSplit &&
+                         (!WIN || window_lo(a.win, len_last) <= k0 || a.win.sinks >= k0 + kSplit);
+      auto sees = [&](int key) { return key < cnt && (!WIN || key >= lo || key < sink); };
       check(mbar_wait_bounded(s_full(half), ph, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
       // the raw maximum (exact in any order): this thread's 128 keys, four
@@ -668,7 +717,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int jj = 0; jj < 32; jj += 4) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (32 * c + jj + e < cnt) mx[e] = fmaxf(mx[e], __uint_as_float(v[jj + e]));
+              if (sees(32 * c + jj + e)) mx[e] = fmaxf(mx[e], __uint_as_float(v[jj + e]));
           }
         }
       }
@@ -703,7 +752,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               float x[2] = {ex2_approx(arg.x), ex2_approx(arg.y)};
               if (decltype(masked)::value) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) x[e] = 32 * c + jj + e < cnt ? x[e] : 0.f;
+                for (int e = 0; e < 2; ++e) x[e] = sees(32 * c + jj + e) ? x[e] : 0.f;
               }
               const __nv_bfloat162 h2 = __float22bfloat162_rn(make_float2(x[0], x[1]));
               const __nv_bfloat162 l2 = __float22bfloat162_rn(
@@ -746,7 +795,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (s > 0) fold(s - 1, m_prev, l_prev, in_prev);
       m_prev = m;
       l_prev = l;
-      in_prev = cnt > 0;
+      in_prev = cnt > 0 && (!WIN || lo < kSplit || sink > 0);
     }
     if (ok && ns > 0) fold(ns - 1, m_prev, l_prev, in_prev);
     if (ok && r < nrows) {
@@ -782,20 +831,23 @@ size_t split_smem_bytes() {
 }
 
 // Decode: attn_split_kernel, then the merge.
-template <int D>
+template <int D, bool WIN>
 kinv_status launch(const AttnParams& p, dim3 split_grid, dim3 merge_grid, cudaStream_t stream) {
-  void (*kernel)(const AttnParams) = attn_split_kernel<D>;
+  void (*kernel)(const AttnParams) = attn_split_kernel<D, WIN>;
   const size_t smem = split_smem_bytes<D>();
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (attr != KINV_OK) return attr;
   const kinv_status st = launch_kernel(kernel, split_grid, dim3(kThreads), smem, stream, 1, p);
   if (st != KINV_OK) return st;
+  if (WIN)
+    return launch_kernel(window_merge_kernel<D>, merge_grid, dim3(D), 0, stream, 1,
+                         MergeParams{p.ws_o, p.ws_ml, p.kv_len, p.out, p.Hq, p.S, p.max_len, p.win, p.status});
   return launch_kernel(attn_merge_kernel<D>, merge_grid, dim3(D), 0, stream, 1, p);
 }
 
 // Prefill with the tcgen05 kernel: one block per (sequence, kv head, tile of
 // 128 (row, head) pairs).
-template <int D>
+template <int D, bool WIN>
 kinv_status launch_prefill_tc(const void* q, const void* k_cache, const void* v_cache, int64_t seq_stride,
                               int64_t tok_stride, PrefillTcArgs a, int B, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
@@ -814,9 +866,9 @@ kinv_status launch_prefill_tc(const void* q, const void* k_cache, const void* v_
     return KINV_ERR_UNSUPPORTED;
   const size_t smem = prefill_tc_smem_bytes<D>();
   if (smem > static_cast<size_t>(max_smem_optin())) return KINV_ERR_UNSUPPORTED;
-  const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(attn_prefill_tc_kernel<D>), smem);
+  const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(attn_prefill_tc_kernel<D, WIN>), smem);
   if (attr != KINV_OK) return attr;
-  return launch_kernel(attn_prefill_tc_kernel<D>, dim3(a.tiles_per_seq, a.Hkv, B), dim3(kTcThreads), smem, stream, 1,
+  return launch_kernel(attn_prefill_tc_kernel<D, WIN>, dim3(a.tiles_per_seq, a.Hkv, B), dim3(kTcThreads), smem, stream, 1,
                        mq, mk, mv, a);
 }
 
@@ -859,7 +911,7 @@ namespace {
 kinv_status decode_check(const void* q, const void* k_cache, const void* v_cache, int64_t seq_stride,
                          int64_t tok_stride, const int32_t* kv_len, const void* out, int B, int Hq,
                          int Hkv, int D, int Lmax, int split_len, const void* workspace,
-                         size_t ws_bytes) {
+                         size_t ws_bytes, const Window& win = Window{0, 0}) {
   if (B < 0 || Lmax < 0) return KINV_ERR_INVALID_ARG;
   if (B == 0) return KINV_OK;
   if (!kv_len) return KINV_ERR_INVALID_ARG;
@@ -867,7 +919,7 @@ kinv_status decode_check(const void* q, const void* k_cache, const void* v_cache
                                       split_len, workspace);
   if (st != KINV_OK) return st;
   if (B > 65535) return KINV_ERR_UNSUPPORTED;
-  const int S = Lmax > 0 ? (Lmax + kSplit - 1) / kSplit : 1;
+  const int S = Lmax > 0 ? static_cast<int>(max_visible_splits(win.window, win.sinks, Lmax)) : 1;
   if (ws_bytes < workspace_bytes(B, Hq, D, S)) return KINV_ERR_WORKSPACE;
   return KINV_OK;
 }
@@ -875,8 +927,9 @@ kinv_status decode_check(const void* q, const void* k_cache, const void* v_cache
 // Enqueues a checked decode call with its partials in `workspace`.
 kinv_status decode_launch(const void* q, const void* k_cache, const void* v_cache, int64_t seq_stride,
                           int64_t tok_stride, const int32_t* kv_len, void* out, int B, int Hq, int Hkv,
-                          int D, int Lmax, float scale, void* workspace, cudaStream_t stream) {
-  const int S = Lmax > 0 ? (Lmax + kSplit - 1) / kSplit : 1;
+                          int D, int Lmax, float scale, void* workspace, cudaStream_t stream,
+                          const Window& win = Window{0, 0}) {
+  const int S = Lmax > 0 ? static_cast<int>(max_visible_splits(win.window, win.sinks, Lmax)) : 1;
   AttnParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k_cache);
@@ -895,9 +948,13 @@ kinv_status decode_launch(const void* q, const void* k_cache, const void* v_cach
   p.c2 = base2_factor(scale, D);
   p.max_len = Lmax;
   p.status = device_status_word();
+  p.win = win;
   const dim3 split_grid(Hkv, S, B), merge_grid(Hq, B, 1);
-  return D == 128 ? launch<128>(p, split_grid, merge_grid, stream)
-                  : launch<64>(p, split_grid, merge_grid, stream);
+  if (win.window > 0)
+    return D == 128 ? launch<128, true>(p, split_grid, merge_grid, stream)
+                    : launch<64, true>(p, split_grid, merge_grid, stream);
+  return D == 128 ? launch<128, false>(p, split_grid, merge_grid, stream)
+                  : launch<64, false>(p, split_grid, merge_grid, stream);
 }
 }  // namespace
 }  // namespace kinv
@@ -914,6 +971,26 @@ extern "C" kinv_status kinv_attn_decode(const void* q, const void* k_cache, cons
                        workspace, stream);
 }
 
+extern "C" size_t kinv_attn_decode_window_workspace(int B, int Hq, int D, int Lmax, int split_len, int window,
+                                                    int sinks) {
+  if (B <= 0 || Hq <= 0 || D <= 0 || Lmax <= 0 || split_len != kSplit || window < 0 || sinks < 0) return 0;
+  return workspace_bytes(B, Hq, D, static_cast<int>(max_visible_splits(window, sinks, Lmax)));
+}
+
+extern "C" kinv_status kinv_attn_decode_window(const void* q, const void* k_cache, const void* v_cache,
+                                               int64_t seq_stride, int64_t tok_stride, const int32_t* kv_len,
+                                               void* out, int B, int Hq, int Hkv, int D, int Lmax, int split_len,
+                                               int window, int sinks, float scale, void* workspace, size_t ws_bytes,
+                                               kinv_stream stream) {
+  if (window < 0 || sinks < 0) return KINV_ERR_INVALID_ARG;
+  const Window win{window, sinks};
+  const kinv_status st = decode_check(q, k_cache, v_cache, seq_stride, tok_stride, kv_len, out, B, Hq, Hkv,
+                                      D, Lmax, split_len, workspace, ws_bytes, win);
+  if (st != KINV_OK || B == 0) return st;
+  return decode_launch(q, k_cache, v_cache, seq_stride, tok_stride, kv_len, out, B, Hq, Hkv, D, Lmax, scale,
+                       workspace, stream, win);
+}
+
 extern "C" size_t kinv_attn_prefill_workspace(int total_rows, int Hq, int D, int max_kv,
                                               int split_len) {
   // the splits are folded on chip: no workspace
@@ -925,14 +1002,12 @@ extern "C" size_t kinv_attn_prefill_workspace(int total_rows, int Hq, int D, int
   return 0;
 }
 
-extern "C" kinv_status kinv_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
-                                         int64_t seq_stride, int64_t tok_stride,
-                                         const int32_t* q_start, const int32_t* q_len,
-                                         const int32_t* q_offset, void* out, int B,
-                                         int total_rows, int max_q_len, int max_kv, int Hq,
-                                         int Hkv, int D, int split_len, float scale,
-                                         void* workspace, size_t ws_bytes, kinv_stream stream) {
-  (void)ws_bytes;
+namespace kinv {
+namespace {
+kinv_status prefill(const void* q, const void* k_cache, const void* v_cache, int64_t seq_stride, int64_t tok_stride,
+                    const int32_t* q_start, const int32_t* q_len, const int32_t* q_offset, void* out, int B,
+                    int total_rows, int max_q_len, int max_kv, int Hq, int Hkv, int D, int split_len, float scale,
+                    void* workspace, kinv_stream stream, const Window& win, bool listed) {
   if (B < 0 || total_rows < 0 || max_q_len < 0 || max_kv < 0) return KINV_ERR_INVALID_ARG;
   if (B == 0 || total_rows == 0 || max_q_len == 0) return KINV_OK;
   if (!q_start || !q_len || !q_offset || max_kv <= 0) return KINV_ERR_INVALID_ARG;
@@ -958,8 +1033,38 @@ extern "C" kinv_status kinv_attn_prefill(const void* q, const void* k_cache, con
   a.status = device_status_word();
   if (a.tiles_per_seq > 65535 || B > 65535) return KINV_ERR_UNSUPPORTED;
   if (B > 1 && seq_stride <= 0) return KINV_ERR_INVALID_ARG;
-  return D == 128 ? launch_prefill_tc<128>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream)
-                  : launch_prefill_tc<64>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream);
+  a.win = win;
+  if (listed)
+    return D == 128 ? launch_prefill_tc<128, true>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream)
+                    : launch_prefill_tc<64, true>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream);
+  return D == 128 ? launch_prefill_tc<128, false>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream)
+                  : launch_prefill_tc<64, false>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream);
+}
+}  // namespace
+}  // namespace kinv
+
+extern "C" kinv_status kinv_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
+                                         int64_t seq_stride, int64_t tok_stride,
+                                         const int32_t* q_start, const int32_t* q_len,
+                                         const int32_t* q_offset, void* out, int B,
+                                         int total_rows, int max_q_len, int max_kv, int Hq,
+                                         int Hkv, int D, int split_len, float scale,
+                                         void* workspace, size_t ws_bytes, kinv_stream stream) {
+  (void)ws_bytes;
+  return prefill(q, k_cache, v_cache, seq_stride, tok_stride, q_start, q_len, q_offset, out, B, total_rows, max_q_len,
+                 max_kv, Hq, Hkv, D, split_len, scale, workspace, stream, Window{0, 0}, false);
+}
+
+extern "C" kinv_status kinv_attn_prefill_window(const void* q, const void* k_cache, const void* v_cache,
+                                                int64_t seq_stride, int64_t tok_stride, const int32_t* q_start,
+                                                const int32_t* q_len, const int32_t* q_offset, void* out, int B,
+                                                int total_rows, int max_q_len, int max_kv, int Hq, int Hkv, int D,
+                                                int split_len, int window, int sinks, float scale, void* workspace,
+                                                size_t ws_bytes, kinv_stream stream) {
+  (void)ws_bytes;
+  if (window < 0 || sinks < 0) return KINV_ERR_INVALID_ARG;
+  return prefill(q, k_cache, v_cache, seq_stride, tok_stride, q_start, q_len, q_offset, out, B, total_rows, max_q_len,
+                 max_kv, Hq, Hkv, D, split_len, scale, workspace, stream, Window{window, sinks}, true);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,77 @@
+// Reading the 8-bit cache back into bf16: for kinv_cache8_read, and for the keys
+// and values that a prompt chunk's rows see.
+#pragma once
+
+#include "cache8.cuh"
+#include "window.cuh"
+
+namespace kinv {
+
+constexpr int kReadTokens = 32;
+constexpr int kReadThreads = 256;
+
+struct ReadParams {
+  Cache8View cache;
+  __nv_bfloat16* k;   // token i of sequence b, head g at b*seq_stride + i*tok_stride + g*D
+  __nv_bfloat16* v;
+  int64_t seq_stride, tok_stride;
+  const int32_t* start;  // token i is slot start[b] + i, i < len[b] ...
+  const int32_t* len;
+  const int32_t* q_start;  // ... or, with these, slot i < q_start[b] + q_len[b] where a row of the chunk sees it
+  const int32_t* q_len;
+  int max_len, max_q_len, Hkv;
+  Window win;
+  int* status;
+};
+
+// Keys (z = 0) or values (z = 1) of kReadTokens tokens of one sequence, D / 16
+// lanes per (token, head): 16 codes in, 32 bytes out a lane.
+template <int D, bool I8>
+__global__ void __launch_bounds__(kReadThreads) cache8_read_kernel(const ReadParams p) {
+  constexpr int L = D / 16;
+  constexpr int PER = kReadThreads / L;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.y;
+  int start = 0, len, lo = 0;
+  if (p.q_start) {
+    // the attention kernel behind this one reports sequences outside the bounds
+    const int s0 = p.q_start[b], n = p.q_len[b];
+    if (n <= 0 || n > p.max_q_len || s0 < 0 || s0 > p.max_len - n) return;
+    len = s0 + n;
+    lo = window_lo(p.win, s0 + 1);
+  } else {
+    start = p.start[b];
+    len = p.len[b];
+    if (start < 0 || len < 0 || len > p.max_len || start > p.cache.slots - len) {
+      if (threadIdx.x == 0 && blockIdx.x == 0 && p.status) atomicExch(p.status, DEV_CACHE8_BAD_RANGE);
+      return;
+    }
+  }
+  const int i0 = blockIdx.x * kReadTokens;
+  const int n = min(kReadTokens, len - i0);
+  if (n <= 0 || (i0 >= p.win.sinks && i0 + n <= lo)) return;
+  const bool values = blockIdx.z != 0;
+  const unsigned char* src = (values ? p.cache.v : p.cache.k) + b * p.cache.seq_stride;
+  const int8_t* exps = (values ? p.cache.ve : p.cache.ke) + b * p.cache.eseq_stride + start + i0;
+  __nv_bfloat16* dst = (values ? p.v : p.k) + b * p.seq_stride;
+  const int sub = threadIdx.x % L;
+  for (int vec = threadIdx.x / L; vec < n * p.Hkv; vec += PER) {
+    const int i = vec / p.Hkv, g = vec % p.Hkv;
+    const uint4 c = *reinterpret_cast<const uint4*>(src + (start + i0 + i) * p.cache.tok_stride + g * D + sub * 16);
+    const float f = exponent_factor(exps[g * p.cache.ehead_stride + i]);
+    const uint2 x0 = decode4<I8>(c.x, f), x1 = decode4<I8>(c.y, f), x2 = decode4<I8>(c.z, f), x3 = decode4<I8>(c.w, f);
+    uint4* to = reinterpret_cast<uint4*>(dst + (i0 + i) * p.tok_stride + g * D + sub * 16);
+    to[0] = make_uint4(x0.x, x0.y, x1.x, x1.y);
+    to[1] = make_uint4(x2.x, x2.y, x3.x, x3.y);
+  }
+}
+
+inline kinv_status launch_cache8_read(const ReadParams& p, bool i8, int B, int D, cudaStream_t stream) {
+  const dim3 grid((p.max_len + kReadTokens - 1) / kReadTokens, B, 2);
+  auto run = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kReadThreads), 0, stream, 1, p); };
+  if (D == 128) return i8 ? run(cache8_read_kernel<128, true>) : run(cache8_read_kernel<128, false>);
+  return i8 ? run(cache8_read_kernel<64, true>) : run(cache8_read_kernel<64, false>);
+}
+
+}  // namespace kinv

@@ -10,8 +10,9 @@ if the library has not been built, loading it raises.
 ``stream=`` names the stream a call is enqueued on (default: the current one).
 The call waits for nothing on other streams: its inputs have to be ready there,
 and whoever reads its results elsewhere waits for it.  What a call allocates is
-that stream's memory.  The calls on drafted trees and logprobs hold their inputs'
-memory for it too; for the others the caller keeps the inputs until they are done.
+that stream's memory.  The calls on drafted trees, logprobs, the 8-bit cache and
+windowed attention hold their inputs' memory for it too; for the others the caller
+keeps the inputs until they are done.
 """
 from __future__ import annotations
 
@@ -29,7 +30,7 @@ LIB_PATH = os.path.join(_HERE, "libkinv.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = (
     0, -1, -2, -3, -4, -5, -6)
-BF16, F32 = 0, 1
+BF16, F32, E4M3, I8 = 0, 1, 2, 3
 SPLIT_LEN = 256
 
 _lib = None
@@ -62,6 +63,21 @@ SIGNATURES = {
     "kinv_attn_prefill_workspace": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "kinv_attn_prefill": (_i32, [_c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _i32, _i32,
                                  _i32, _i32, _i32, _i32, _i32, _i32, _f32, _c_p, _sz, _c_p]),
+    "kinv_attn_decode_window_workspace": (_sz, [_i32] * 7),
+    "kinv_attn_decode_window": (_i32, [_c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32,
+                                       _i32, _i32, _i32, _f32, _c_p, _sz, _c_p]),
+    "kinv_attn_prefill_window": (_i32, [_c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _i32, _i32, _i32,
+                                        _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _c_p, _sz, _c_p]),
+    "kinv_rope_append8": (_i32, [_c_p, _i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _f32, _i32, _i32, _i32, _i32,
+                                 _f32, _c_p]),
+    "kinv_cache8_write": (_i32, [_c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _c_p]),
+    "kinv_cache8_read": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _i64, _i64, _i32, _i32, _i32, _i32, _c_p]),
+    "kinv_attn_decode8_workspace": (_sz, [_i32] * 7),
+    "kinv_attn_decode8": (_i32, [_c_p, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _c_p,
+                                 _sz, _c_p]),
+    "kinv_attn_prefill8_workspace": (_sz, [_i32] * 7),
+    "kinv_attn_prefill8": (_i32, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                  _i32, _i32, _i32, _f32, _c_p, _sz, _c_p]),
     "kinv_sample_workspace": (_sz, [_i32, _i32]),
     "kinv_sample": (_i32, [_c_p, _i64, _i32, _i32, _c_p, _c_p, _i32, _c_p, _c_p, _c_p, _c_p, _sz,
                            _c_p]),
@@ -325,14 +341,67 @@ def rmsnorm(x: torch.Tensor, w: torch.Tensor, eps: float = 1e-6, residual=None, 
 
 # ---------------------------------------------------------------- attention
 def attn_decode_workspace(batch: int, n_q: int, head_dim: int, max_len: int,
-                          split_len: int = SPLIT_LEN) -> int:
+                          split_len: int = SPLIT_LEN, window: int = 0, sinks: int = 0) -> int:
+    if window:
+        return int(lib().kinv_attn_decode_window_workspace(batch, n_q, head_dim, max_len, split_len, window, sinks))
     return int(lib().kinv_attn_decode_workspace(batch, n_q, head_dim, max_len, split_len))
 
 
+def _window_inputs(q, k_cache, v_cache, out, batch: int, what: str):
+    """Checks of the windowed calls: (slots, Hkv, sequence and slot strides)."""
+    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (out, "out")):
+        _need(t, torch.bfloat16, name)
+    shape, stride = k_cache.shape, k_cache.stride()
+    if v_cache.shape != shape or v_cache.stride() != stride or len(shape) != 4:
+        raise ValueError(f"{what}: the caches must be [B][slots][Hkv][D] and share shape and strides")
+    if stride[3] != 1 or (stride[2] != shape[3] and shape[2] > 1) or shape[0] < batch:
+        raise ValueError(f"{what}: a slot's heads must be contiguous, and the caches hold every sequence")
+    if not q.is_contiguous() or not out.is_contiguous() or out.shape != q.shape or q.shape[2] != shape[3]:
+        raise ValueError(f"{what}: q and out must be contiguous [rows][Hq][D] of one shape")
+    return shape[1], shape[2], stride[0], stride[1]
+
+
+def _workspace(side, workspace, need: int, device):
+    if workspace is None:
+        return _scratch(side, torch.empty, max(need, 16), dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous CUDA tensor")
+    return workspace
+
+
+def _vectors(what: str, n: int, **tensors) -> None:
+    for name, t in tensors.items():
+        _need(t, torch.int32, name)
+        if t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be a contiguous vector of at least {n} entries")
+
+
+def _attn_decode_window(q, k_cache, v_cache, kv_len, out, workspace, split_len, window, sinks, scale, stream):
+    side = _side(stream)
+    if out is None:
+        out = _empty_like(side)(q)
+    bsz, hq, d = q.shape
+    lmax, hkv, s0, s1 = _window_inputs(q, k_cache, v_cache, out, bsz, "attn_decode")
+    _vectors("attn_decode", bsz, kv_len=kv_len)
+    workspace = _workspace(side, workspace, attn_decode_workspace(bsz, hq, d, lmax, split_len, window, sinks), q.device)
+    if side is not None:
+        _hold(side, q, k_cache, v_cache, kv_len, out, workspace)
+    _check(lib().kinv_attn_decode_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), s0, s1,
+                                         kv_len.data_ptr(), out.data_ptr(), bsz, hq, hkv, d, lmax, split_len, window,
+                                         sinks, scale, workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)),
+           "kinv_attn_decode_window")
+    return out
+
+
 def attn_decode(q, k_cache, v_cache, kv_len, out=None, workspace=None, split_len=SPLIT_LEN,
-                scale: float = 0.0, stream=None):
+                scale: float = 0.0, stream=None, window: int = 0, sinks: int = 0):
     """q [B][Hq][D]; caches [B][Lmax][Hkv][D] (or any layout with the same
-    last two dims and strides along B and L); kv_len int32 [B]."""
+    last two dims and strides along B and L); kv_len int32 [B].  With a window a
+    row sees its last ``window`` keys and the first ``sinks`` of its sequence."""
+    if window or sinks < 0:
+        return _attn_decode_window(q, k_cache, v_cache, kv_len, out, workspace, split_len, window, sinks, scale,
+                                   stream)
     _need(q, torch.bfloat16, "q")
     _need(kv_len, torch.int32, "kv_len")
     bsz, hq, d = q.shape
@@ -381,9 +450,35 @@ def attn_prefill_workspace(total_rows: int, n_q: int, head_dim: int, max_kv: int
     return int(lib().kinv_attn_prefill_workspace(total_rows, n_q, head_dim, max_kv, split_len))
 
 
+def _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len, max_kv, out, split_len, window,
+                         sinks, scale, stream):
+    side = _side(stream)
+    if out is None:
+        out = _empty_like(side)(q)
+    rows, hq, d = q.shape
+    bsz = q_start.shape[0]
+    slots, hkv, s0, s1 = _window_inputs(q, k_cache, v_cache, out, bsz, "attn_prefill")
+    if max_kv > slots:
+        raise ValueError("attn_prefill: the caches are smaller than max_kv")
+    _vectors("attn_prefill", bsz, q_start=q_start, q_len=q_len, q_offset=q_offset)
+    if side is not None:
+        _hold(side, q, k_cache, v_cache, q_start, q_len, q_offset, out)
+    _check(lib().kinv_attn_prefill_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), s0, s1,
+                                          q_start.data_ptr(), q_len.data_ptr(), q_offset.data_ptr(), out.data_ptr(),
+                                          bsz, rows, max_q_len, max_kv, hq, hkv, d, split_len, window, sinks, scale,
+                                          None, 0, _stream(stream)), "kinv_attn_prefill_window")
+    return out
+
+
 def attn_prefill(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len: int, max_kv: int,
-                 out=None, workspace=None, split_len=SPLIT_LEN, scale: float = 0.0, stream=None):
-    """q [rows][Hq][D]; per-sequence int32 q_start, q_len, q_offset [B]."""
+                 out=None, workspace=None, split_len=SPLIT_LEN, scale: float = 0.0, stream=None,
+                 window: int = 0, sinks: int = 0):
+    """q [rows][Hq][D]; per-sequence int32 q_start, q_len, q_offset [B].  With a
+    window a row sees its last ``window`` keys and the first ``sinks`` of its
+    sequence; rows of no sequence are not written."""
+    if window or sinks < 0:
+        return _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len, max_kv, out, split_len,
+                                    window, sinks, scale, stream)
     _need(q, torch.bfloat16, "q")
     rows, hq, d = q.shape
     hkv = k_cache.shape[2]
@@ -398,6 +493,196 @@ def attn_prefill(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len: int, 
                                    _ptr(out), bsz, rows, max_q_len, max_kv, hq, hkv, d, split_len,
                                    float(scale), _ptr(workspace), workspace.numel(),
                                    _stream(stream)), "kinv_attn_prefill")
+    return out
+
+
+# -------------------------------------------------------- 8-bit key/value cache
+CACHE8_DTYPES = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+class Cache8Struct(ctypes.Structure):
+    """kinv_cache8: an 8-bit key/value cache."""
+    _fields_ = [("k", _c_p), ("v", _c_p), ("k_exp", _c_p), ("v_exp", _c_p), ("seq_stride", _i64),
+                ("tok_stride", _i64), ("exp_seq_stride", _i64), ("exp_head_stride", _i64), ("B", _i32),
+                ("slots", _i32), ("dtype", _i32)]
+
+
+class Cache8:
+    """Keys and values as 8-bit codes with a power-of-two scale for every (token,
+    kv head): codes k, v [B][slots][Hkv][D] (torch.float8_e4m3fn or torch.int8), and
+    exponents k_exp, v_exp [B][Hkv][slots] (int8); a value is code * 2^exponent, an
+    exponent of -128 marks a vector of NaN.  Holds its tensors."""
+
+    def __init__(self, k, v, k_exp, v_exp):
+        if k.dtype not in CACHE8_DTYPES.values():
+            raise TypeError(f"k: expected torch.float8_e4m3fn or torch.int8, got {k.dtype}")
+        for t, dt, name in ((k, k.dtype, "k"), (v, k.dtype, "v"), (k_exp, torch.int8, "k_exp"),
+                            (v_exp, torch.int8, "v_exp")):
+            _need(t, dt, name)
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("Cache8: the codes must be [B][slots][Hkv][D] and share shape and strides")
+        bsz, slots, hkv, d = k.shape
+        s0, s1, s2, s3 = k.stride()
+        if s3 != 1 or (s2 != d and hkv > 1):
+            raise ValueError("Cache8: a slot's heads must be contiguous")
+        if tuple(k_exp.shape) != (bsz, hkv, slots) or v_exp.shape != k_exp.shape or v_exp.stride() != k_exp.stride() \
+                or (k_exp.stride(2) != 1 and slots > 1):
+            raise ValueError("Cache8: the exponents must be [B][Hkv][slots], a head's slots contiguous")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.B, self.slots, self.n_kv, self.head_dim, self.device = bsz, slots, hkv, d, k.device
+        self.struct = Cache8Struct(_ptr(k), _ptr(v), _ptr(k_exp), _ptr(v_exp), s0, s1, k_exp.stride(0),
+                                   k_exp.stride(1), bsz, slots, I8 if k.dtype == torch.int8 else E4M3)
+        self.ptr = ctypes.byref(self.struct)
+        self.tensors = (k, v, k_exp, v_exp)
+
+    @classmethod
+    def empty(cls, batch: int, slots: int, n_kv: int, head_dim: int, dtype: str = "e4m3", device="cuda"):
+        """A cache whose every value is 0; dtype "e4m3" or "int8"."""
+        if dtype not in CACHE8_DTYPES:
+            raise ValueError(f"dtype: expected one of {sorted(CACHE8_DTYPES)}, got {dtype!r}")
+        k, v = (torch.zeros(batch, slots, n_kv, head_dim, dtype=torch.uint8, device=device).view(CACHE8_DTYPES[dtype])
+                for _ in range(2))
+        ke, ve = (torch.zeros(batch, n_kv, slots, dtype=torch.int8, device=device) for _ in range(2))
+        return cls(k, v, ke, ve)
+
+    def sequences(self, first: int, last: int) -> "Cache8":
+        """Sequences first .. last - 1 of the same memory."""
+        return Cache8(*(t[first:last] for t in self.tensors))
+
+
+def rope_append8(qkv, q_out, cache: Cache8, seq, pos, n_q, n_kv, head_dim, rope_base, q_norm=None, k_norm=None,
+                 eps=1e-6, stream=None):
+    """rope_append with the keys and values of the rows quantised into ``cache`` at
+    [seq][pos]; q_out [rows][Hq][D] has rope_append's bits.  A row outside the cache
+    is left out (its q_out too) and recorded in the device status."""
+    bf = torch.bfloat16
+    for t, name in ((qkv, "qkv"), (q_out, "q_out")):
+        _need(t, bf, name)
+    (rows, width), (ld, step) = qkv.shape, qkv.stride()
+    if (step != 1 and width > 1) or width != (n_q + 2 * n_kv) * head_dim or not q_out.is_contiguous() \
+            or q_out.numel() < rows * n_q * head_dim or cache.n_kv != n_kv or cache.head_dim != head_dim:
+        raise ValueError("rope_append8: shapes or layouts do not match")
+    _vectors("rope_append8", rows, seq=seq, pos=pos)
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _need(t, bf, name)
+            if not t.is_contiguous() or t.numel() < head_dim:
+                raise ValueError(f"rope_append8: {name} must hold a contiguous gain for each of a head's values")
+    side = _side(stream)
+    if side is not None:
+        _hold(side, qkv, q_out, seq, pos, q_norm, k_norm, *cache.tensors)
+    _check(lib().kinv_rope_append8(qkv.data_ptr(), max(ld, width) if rows <= 1 else ld, q_out.data_ptr(), cache.ptr,
+                                   seq.data_ptr(), pos.data_ptr(), _ptr(q_norm), _ptr(k_norm), eps, rows, n_q, n_kv,
+                                   head_dim, rope_base, _stream(stream)), "kinv_rope_append8")
+    return q_out
+
+
+def _tokens(k, v, cache: Cache8, what: str):
+    """Shape and strides of bf16 k, v [B][n][Hkv][D] that go into or come out of ``cache``."""
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, torch.bfloat16, name)
+    shape, stride = k.shape, k.stride()
+    if len(shape) != 4 or v.shape != shape or v.stride() != stride:
+        raise ValueError(f"{what}: k and v must be [B][n][Hkv][D] and share shape and strides")
+    if tuple(shape[2:]) != (cache.n_kv, cache.head_dim) or shape[0] > cache.B or stride[3] != 1 \
+            or (stride[2] != shape[3] and shape[2] > 1):
+        raise ValueError(f"{what}: k and v must match the cache's heads and sequences, a token's heads contiguous")
+    return shape[0], shape[1], stride[0], stride[1] if shape[1] > 1 else shape[2] * shape[3]
+
+
+def cache8_write(cache: Cache8, k, v, start, length, stream=None) -> None:
+    """bf16 k, v [B][n][Hkv][D] into ``cache``: token i < length[b] of sequence b goes
+    to slot start[b] + i (int32 [B], device).  A sequence that does not fit is left
+    out and recorded in the device status."""
+    bsz, n, s0, s1 = _tokens(k, v, cache, "cache8_write")
+    _vectors("cache8_write", bsz, start=start, length=length)
+    side = _side(stream)
+    if side is not None:
+        _hold(side, k, v, start, length, *cache.tensors)
+    _check(lib().kinv_cache8_write(k.data_ptr(), v.data_ptr(), s0, s1, cache.ptr, start.data_ptr(), length.data_ptr(),
+                                   bsz, n, cache.n_kv, cache.head_dim, _stream(stream)), "kinv_cache8_write")
+
+
+def cache8_read(cache: Cache8, start, length, n: int = 0, k=None, v=None, stream=None):
+    """The reverse: (k, v) bf16 [B][n][Hkv][D] whose token i < length[b] is slot
+    start[b] + i (n bounds length).  Tokens from length[b] on, and those of a
+    sequence left out, keep what the given k and v held; where they are allocated
+    here they hold anything."""
+    side = _side(stream)
+    if (k is None) != (v is None):
+        raise ValueError("cache8_read: k and v are given together")
+    if k is None:
+        shape = (start.shape[0], n, cache.n_kv, cache.head_dim)
+        k, v = (_empty(side)(*shape, dtype=torch.bfloat16, device=cache.device) for _ in range(2))
+    bsz, n, s0, s1 = _tokens(k, v, cache, "cache8_read")
+    _vectors("cache8_read", bsz, start=start, length=length)
+    if side is not None:
+        _hold(side, k, v, start, length, *cache.tensors)
+    _check(lib().kinv_cache8_read(cache.ptr, start.data_ptr(), length.data_ptr(), k.data_ptr(), v.data_ptr(), s0, s1,
+                                  bsz, n, cache.n_kv, cache.head_dim, _stream(stream)), "kinv_cache8_read")
+    return k, v
+
+
+def _rows8(q, out, cache: Cache8, what: str):
+    for t, name in ((q, "q"), (out, "out")):
+        _need(t, torch.bfloat16, name)
+    if q.dim() != 3 or not q.is_contiguous() or not out.is_contiguous() or out.shape != q.shape \
+            or q.shape[2] != cache.head_dim:
+        raise ValueError(f"{what}: q and out must be contiguous [rows][Hq][D] of one shape, D the cache's")
+
+
+def attn_decode8_workspace(batch: int, n_q: int, head_dim: int, slots: int, window: int = 0, sinks: int = 0,
+                           split_len: int = SPLIT_LEN) -> int:
+    return int(lib().kinv_attn_decode8_workspace(batch, n_q, head_dim, slots, window, sinks, split_len))
+
+
+def attn_decode8(q, cache: Cache8, kv_len, out=None, workspace=None, window: int = 0, sinks: int = 0,
+                 split_len=SPLIT_LEN, scale: float = 0.0, stream=None):
+    """attn_decode over an 8-bit cache: q [B][Hq][D], kv_len int32 [B].  With a window
+    a row sees its last ``window`` keys and the first ``sinks`` of its sequence.  A row
+    has the bits of attn_decode on the cache read back."""
+    side = _side(stream)
+    if out is None:
+        out = _empty_like(side)(q)
+    _rows8(q, out, cache, "attn_decode8")
+    bsz, hq, d = q.shape
+    _vectors("attn_decode8", bsz, kv_len=kv_len)
+    workspace = _workspace(side, workspace, attn_decode8_workspace(bsz, hq, d, cache.slots, window, sinks, split_len)
+                           if workspace is None else 0, q.device)
+    if side is not None:
+        _hold(side, q, out, kv_len, workspace, *cache.tensors)
+    _check(lib().kinv_attn_decode8(q.data_ptr(), cache.ptr, kv_len.data_ptr(), out.data_ptr(), bsz, hq, cache.n_kv, d,
+                                   split_len, window, sinks, scale, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)),
+           "kinv_attn_decode8")
+    return out
+
+
+def attn_prefill8_workspace(batch: int, total_rows: int, n_q: int, n_kv: int, head_dim: int, max_kv: int,
+                            split_len: int = SPLIT_LEN) -> int:
+    return int(lib().kinv_attn_prefill8_workspace(batch, total_rows, n_q, n_kv, head_dim, max_kv, split_len))
+
+
+def attn_prefill8(q, cache: Cache8, q_start, q_len, q_offset, max_q_len: int, max_kv: int, out=None, workspace=None,
+                  window: int = 0, sinks: int = 0, split_len=SPLIT_LEN, scale: float = 0.0, stream=None):
+    """attn_prefill over an 8-bit cache, which already holds the rows' keys and
+    values: q [rows][Hq][D]; per-sequence int32 q_start, q_len, q_offset [B].  Rows of
+    no sequence are not written."""
+    side = _side(stream)
+    if out is None:
+        out = _empty_like(side)(q)
+    _rows8(q, out, cache, "attn_prefill8")
+    rows, hq, d = q.shape
+    bsz = q_start.shape[0]
+    _vectors("attn_prefill8", bsz, q_start=q_start, q_len=q_len, q_offset=q_offset)
+    workspace = _workspace(side, workspace, attn_prefill8_workspace(bsz, rows, hq, cache.n_kv, d, max_kv, split_len)
+                           if workspace is None else 0, q.device)
+    if side is not None:
+        _hold(side, q, out, q_start, q_len, q_offset, workspace, *cache.tensors)
+    _check(lib().kinv_attn_prefill8(q.data_ptr(), cache.ptr, q_start.data_ptr(), q_len.data_ptr(), q_offset.data_ptr(),
+                                    out.data_ptr(), bsz, rows, max_q_len, max_kv, hq, cache.n_kv, d, split_len, window,
+                                    sinks, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                    _stream(stream)), "kinv_attn_prefill8")
     return out
 
 

@@ -1,0 +1,375 @@
+"""Attention with a sliding window and sinks, and over the 8-bit cache: against
+the fp64 oracle, against each other's bits, and in the places where it can go
+wrong (lengths around the splits, hidden slots of NaN, other batches, chunkings,
+streams and graphs).
+
+What is asked of the bits: attention over an 8-bit cache = attention over the
+cache read back; a decode step = a one-row prefill; a row = the same row in any
+batch or chunk; a window that hides nothing = no window."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import assert_close, assert_same_bits, ensure_lib, f64, gpu, synth
+from oracle import window as owin
+
+pytestmark = gpu
+
+HEADS = [(32, 8, 128), (4, 2, 64), (8, 1, 128), (2, 2, 64), (4, 2, 128), (8, 1, 64)]
+I32 = dict(dtype=torch.int32, device="cuda")
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def kinv():
+    return ensure_lib()
+
+
+def i32(v):
+    return torch.tensor(v, **I32)
+
+
+def keys(shape, seed):
+    """Keys or values of uneven loudness."""
+    x = synth.normal_bf16(shape, 1.0, seed, "cuda")
+    return x * torch.exp2(torch.randint(-3, 3, shape[:-1] + (1,), generator=synth.gen(seed + 7, "cuda"), device="cuda").to(torch.bfloat16))
+
+
+def cache8(kinv, k, v, fmt):
+    bsz, slots, hkv, d = k.shape
+    c = kinv.Cache8.empty(bsz, slots, hkv, d, fmt)
+    kinv.cache8_write(c, k, v, i32([0] * bsz), i32([slots] * bsz))
+    return c, kinv.cache8_read(c, i32([0] * bsz), i32([slots] * bsz), slots)
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 33, 255, 256, 257, 400, 511, 512, 513, 700, 768, 1000, 1023, 1024, 1025, 1100]
+WINDOWS = [(1, 0), (1, 1), (16, 0), (64, 3), (255, 0), (256, 4), (257, 0), (300, 256), (300, 257), (512, 513), (700, 1), (5000, 9)]
+
+
+# ------------------------------------------------------------ sliding window
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (64, 3), (256, 300), (300, 0)])
+def test_window_decode_against_the_oracle(kinv, hq, hkv, d, window, sinks):
+    lens = [0, 1, 63, 64, 65, 256, 300, 556, 557, 700]
+    k, v = keys((len(lens), 700, hkv, d), 60), keys((len(lens), 700, hkv, d), 61)
+    q = synth.normal_bf16((len(lens), hq, d), 1.0, 62, "cuda")
+    out = kinv.attn_decode(q, k, v, i32(lens), window=window, sinks=sinks)
+    for b, n in enumerate(lens):
+        ref = owin.row(f64(q[b]), f64(k[b]), f64(v[b]), n - 1, window, sinks)
+        assert_close(f64(out[b]), ref, f"length {n}") if n else None
+    assert (out[0] == 0).all() and kinv.last_device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS[:4])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_window_decode_equals_prefill_and_full_attention_where_nothing_hides(kinv, hq, hkv, d, window, sinks):
+    k, v = keys((1, 1100, hkv, d), 70).expand(len(LENS), -1, -1, -1), keys((1, 1100, hkv, d), 71).expand(len(LENS), -1, -1, -1)
+    q = synth.normal_bf16((len(LENS), hq, d), 1.0, 72, "cuda")
+    out = kinv.attn_decode(q, k, v, i32(LENS), window=window, sinks=sinks)
+    full = kinv.attn_decode(q, k, v, i32(LENS))
+    for b, n in enumerate(LENS):
+        if n <= window + sinks or n <= window:
+            assert_same_bits(out[b], full[b], f"length {n}")
+        if n:
+            one = kinv.attn_prefill(q[b: b + 1], k[:1], v[:1], i32([n - 1]), i32([1]), i32([0]), 1, n, window=window, sinks=sinks)
+            assert_same_bits(one[0], out[b], f"prefill row {n - 1}")
+    assert kinv.last_device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS[:4])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (40, 0), (64, 3), (256, 4), (300, 280), (600, 1)])
+def test_window_prefill_rows_are_decode_steps_in_any_chunking(kinv, hq, hkv, d, window, sinks):
+    n = 900
+    k, v = keys((1, n, hkv, d), 80), keys((1, n, hkv, d), 81)
+    q = synth.normal_bf16((n, hq, d), 1.0, 82, "cuda")
+
+    def run(p0, rows):
+        return kinv.attn_prefill(q[p0: p0 + rows], k, v, i32([p0]), i32([rows]), i32([0]), rows, p0 + rows, window=window, sinks=sinks)
+
+    whole = run(0, n)
+    for chunk in (7, 129, 512):
+        parts = torch.cat([run(p, min(chunk, n - p)) for p in range(0, n, chunk)])
+        assert_same_bits(parts, whole, f"chunks of {chunk}")
+    rows = [0, 1, 39, 40, 255, 256, 300, 556, 580, 899]
+    dec = kinv.attn_decode(q[rows], k.expand(len(rows), -1, -1, -1), v.expand(len(rows), -1, -1, -1), i32([r + 1 for r in rows]),
+                           window=window, sinks=sinks)
+    assert_same_bits(whole[rows], dec, "decode steps")
+    for r in (300, 899):
+        assert_close(f64(whole[r]), owin.row(f64(q[r]), f64(k[0]), f64(v[0]), r, window, sinks), f"row {r}")
+    assert kinv.last_device_status() == 0
+
+
+def test_window_prefill_of_ragged_sequences(kinv):
+    hq, hkv, d, window, sinks = 32, 8, 128, 100, 2
+    n, start = [5, 0, 300, 1, 64], [0, 10, 100, 650, 255]
+    off = [3, 8, 8, 308, 309]
+    rows = 380
+    k, v = keys((5, 700, hkv, d), 90), keys((5, 700, hkv, d), 91)
+    q = synth.normal_bf16((rows, hq, d), 1.0, 92, "cuda")
+    out = torch.full_like(q, 7.0)
+    kinv.attn_prefill(q, k, v, i32(start), i32(n), i32(off), 300, 700, out=out, window=window, sinks=sinks)
+    assert (out[:3] == 7).all() and (out[373:] == 7).all()
+    for b in range(5):
+        if n[b]:
+            one = kinv.attn_prefill(q[off[b]: off[b] + n[b]], k[b: b + 1], v[b: b + 1], i32([start[b]]), i32([n[b]]), i32([0]), n[b],
+                                    start[b] + n[b], window=window, sinks=sinks)
+            assert_same_bits(out[off[b]: off[b] + n[b]], one, f"sequence {b}")
+    assert kinv.last_device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [NAN, float("inf"), torch.finfo(torch.bfloat16).min])
+def test_what_hidden_slots_hold_does_not_matter(kinv, bad):
+    hq, hkv, d, window, sinks = 8, 1, 128, 200, 5
+    lens = [1000, 600, 210, 700]
+    k, v = keys((4, 1024, hkv, d), 100), keys((4, 1024, hkv, d), 101)
+    q = synth.normal_bf16((4, hq, d), 1.0, 102, "cuda")
+    ref = kinv.attn_decode(q, k, v, i32(lens), window=window, sinks=sinks)
+    k2, v2 = k.clone(), v.clone()
+    for b, n in enumerate(lens):
+        for t in (k2, v2):
+            t[b, sinks: n - window] = bad
+            t[b, n:] = bad
+    assert_same_bits(kinv.attn_decode(q, k2, v2, i32(lens), window=window, sinks=sinks), ref, "decode")
+    # a chunk of rows: what is hidden from all of them
+    qs = synth.normal_bf16((50, hq, d), 1.0, 103, "cuda")
+    args = (i32([900]), i32([50]), i32([0]), 50, 950)
+    ref = kinv.attn_prefill(qs, k[:1], v[:1], *args, window=window, sinks=sinks)
+    k2, v2 = k[:1].clone(), v[:1].clone()
+    for t in (k2, v2):
+        t[0, sinks: 901 - window] = bad
+        t[0, 950:] = bad
+    assert_same_bits(kinv.attn_prefill(qs, k2, v2, *args, window=window, sinks=sinks), ref, "prefill")
+
+
+def test_window_with_every_cache_shape_of_a_batch(kinv):
+    """A row's bits in other batches, at other slots, and in a cache of other strides."""
+    hq, hkv, d, window, sinks = 4, 2, 64, 333, 7
+    lens = synth.uniform_int(40, 0, 2000, 110).tolist()
+    k, v = keys((40, 2000, hkv, d), 111), keys((40, 2000, hkv, d), 112)
+    q = synth.normal_bf16((40, hq, d), 1.0, 113, "cuda")
+    out = kinv.attn_decode(q, k, v, i32(lens), window=window, sinks=sinks)
+    perm = torch.randperm(40, generator=synth.gen(114), ).cuda()
+    wide_k, wide_v = (torch.full((40, 2100, hkv + 2, d), NAN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wide_k[:, :2000, :hkv], wide_v[:, :2000, :hkv] = k[perm], v[perm]
+    other = kinv.attn_decode(q[perm], wide_k[:, :, :hkv], wide_v[:, :, :hkv], i32(lens)[perm].contiguous(), window=window, sinks=sinks)
+    assert_same_bits(other, out[perm], "permuted, other strides")
+    assert kinv.last_device_status() == 0
+
+
+@pytest.mark.parametrize("length", [-1, 701])
+def test_window_lengths_outside_the_cache_give_zeros(kinv, length):
+    k, v = keys((2, 700, 2, 64), 120), keys((2, 700, 2, 64), 121)
+    q = synth.normal_bf16((2, 4, 64), 1.0, 122, "cuda")
+    out = kinv.attn_decode(q, k, v, i32([length, 300]), window=50, sinks=1)
+    assert kinv.last_device_status() == kinv.ERR_INVALID_ARG
+    assert (out[0] == 0).all() and not (out[1] == 0).all()
+    c, _ = cache8(kinv, k, v, "int8")
+    out8 = kinv.attn_decode8(q, c, i32([length, 300]))
+    assert kinv.last_device_status() == kinv.ERR_INVALID_ARG
+    assert (out8[0] == 0).all() and not (out8[1] == 0).all()
+
+
+# ------------------------------------------------------------ the 8-bit cache
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_decode8_has_the_bits_of_the_cache_read_back(kinv, hq, hkv, d, fmt):
+    k, v = keys((len(LENS), 1100, hkv, d), 130), keys((len(LENS), 1100, hkv, d), 131)
+    q = synth.normal_bf16((len(LENS), hq, d), 1.0, 132, "cuda")
+    c, (k16, v16) = cache8(kinv, k, v, fmt)
+    assert_same_bits(kinv.attn_decode8(q, c, i32(LENS)), kinv.attn_decode(q, k16, v16, i32(LENS)), "no window")
+    assert_same_bits(kinv.attn_decode8(q, c, i32(LENS), scale=0.31), kinv.attn_decode(q, k16, v16, i32(LENS), scale=0.31), "scale")
+    for window, sinks in WINDOWS:
+        assert_same_bits(kinv.attn_decode8(q, c, i32(LENS), window=window, sinks=sinks),
+                         kinv.attn_decode(q, k16, v16, i32(LENS), window=window, sinks=sinks), f"window {window}, sinks {sinks}")
+    assert kinv.last_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("k_loud,v_loud,q_loud", [(0, 0, 0), (20, 0, -20), (-30, 0, 30), (0, 40, 0), (0, -60, 0), (0, 90, 0), (10, 30, -5)])
+def test_decode8_at_every_loudness(kinv, fmt, k_loud, v_loud, q_loud):
+    """Scales far from 1, and values of very different loudness beside each other."""
+    hq, hkv, d, n = 8, 1, 128, 520
+    k, v = keys((1, n, hkv, d), 140), keys((1, n, hkv, d), 141)
+    k, v = k * 2.0 ** k_loud, v * 2.0 ** v_loud
+    v = v * torch.exp2(torch.randint(-25, 25, (1, n, 1, 1), generator=synth.gen(142, "cuda"), device="cuda").to(torch.bfloat16))
+    q = synth.normal_bf16((1, hq, d), 1.0, 143, "cuda") * 2.0 ** q_loud
+    c, (k16, v16) = cache8(kinv, k, v, fmt)
+    for n in (520, 256, 100):
+        assert_same_bits(kinv.attn_decode8(q, c, i32([n])), kinv.attn_decode(q, k16, v16, i32([n])), f"length {n}")
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("hq,hkv,d", HEADS[:4])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3)])
+def test_prefill8_has_the_bits_of_the_cache_read_back(kinv, hq, hkv, d, fmt, window, sinks):
+    n, start, off = [70, 0, 200, 1], [0, 5, 412, 699], [0, 70, 70, 270]
+    k, v = keys((4, 700, hkv, d), 150), keys((4, 700, hkv, d), 151)
+    q = synth.normal_bf16((271, hq, d), 1.0, 152, "cuda")
+    c, (k16, v16) = cache8(kinv, k, v, fmt)
+    args = (i32(start), i32(n), i32(off), 200, 700)
+    ws = torch.full((kinv.attn_prefill8_workspace(4, 271, hq, hkv, d, 700) // 2,), NAN, dtype=torch.bfloat16, device="cuda")
+    out = kinv.attn_prefill8(q, c, *args, workspace=ws, window=window, sinks=sinks)
+    # a window of all 700 keys hides nothing
+    assert_same_bits(out, kinv.attn_prefill(q, k16, v16, *args, window=window or 700, sinks=sinks), "prefill")
+    r, p = 70 + 199, 412 + 199
+    dec = kinv.attn_decode8(q[r: r + 1], c.sequences(2, 3), i32([p + 1]), window=window, sinks=sinks)
+    assert_same_bits(dec[0], out[r], "decode == prefill")
+    assert kinv.last_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_decode8_hidden_and_marked_slots(kinv, fmt):
+    hq, hkv, d, n = 32, 8, 128, 700
+    k, v = keys((1, 800, hkv, d), 160), keys((1, 800, hkv, d), 161)
+    q = synth.normal_bf16((1, hq, d), 1.0, 162, "cuda")
+    c, _ = cache8(kinv, k, v, fmt)
+    ref = kinv.attn_decode8(q, c, i32([n]), window=300, sinks=2)
+    for t in (c.k, c.v):     # any bytes where nothing is visible
+        t.view(torch.uint8)[:, 2:400] = 0xFF
+        t.view(torch.uint8)[:, n:] = 0x7F
+    for t in (c.k_exp, c.v_exp):
+        t[:, :, 2:400] = -128
+        t[:, :, n:] = -128
+    assert_same_bits(kinv.attn_decode8(q, c, i32([n]), window=300, sinks=2), ref, "hidden slots")
+    # a marked key or value makes its kv head's rows NaN, and no other's
+    c.k_exp[0, 3, 500] = -128
+    c.v_exp[0, 6, 699] = -128
+    out = kinv.attn_decode8(q, c, i32([n]), window=300, sinks=2)
+    bad = torch.isnan(out[0]).view(8, 4 * d).all(1).tolist()
+    assert bad == [g in (3, 6) for g in range(8)]
+    good = [h for h in range(hq) if h // 4 not in (3, 6)]
+    assert_same_bits(out[0, good], ref[0, good], "the other heads")
+
+
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_decode8_with_infinite_queries(kinv, what):
+    q = synth.normal_bf16((2, 4, 64), 1.0, 170, "cuda")
+    q[0, 1, 3] = NAN if what == "nan" else float("inf")
+    k, v = keys((2, 300, 2, 64), 171), keys((2, 300, 2, 64), 172)
+    c, (k16, v16) = cache8(kinv, k, v, "e4m3")
+    a, b = kinv.attn_decode8(q, c, i32([300, 300])), kinv.attn_decode(q, k16, v16, i32([300, 300]))
+    assert torch.equal(torch.isnan(a), torch.isnan(b))
+    assert_same_bits(torch.nan_to_num(a), torch.nan_to_num(b), "the rest")
+
+
+def test_decode8_in_other_batches_and_strides(kinv):
+    hq, hkv, d = 4, 2, 64
+    lens = synth.uniform_int(40, 0, 3000, 180).tolist()
+    k, v = keys((40, 3000, hkv, d), 181), keys((40, 3000, hkv, d), 182)
+    q = synth.normal_bf16((40, hq, d), 1.0, 183, "cuda")
+    c, (k16, v16) = cache8(kinv, k, v, "e4m3")
+    out = kinv.attn_decode8(q, c, i32(lens))
+    assert_same_bits(out, kinv.attn_decode(q, k16, v16, i32(lens)), "whole batch")
+    perm = torch.randperm(40, generator=synth.gen(184)).cuda()
+    wide = [torch.full((41, 3016, hkv + 3, d), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    exps = [torch.full((41, hkv + 1, 3016), 99, dtype=torch.int8, device="cuda") for _ in range(2)]
+    for w, t in zip(wide + exps, c.tensors):
+        if t.dim() == 4:
+            w[:40, :3000, :hkv] = t.view(torch.uint8)[perm]
+        else:
+            w[:40, :hkv, :3000] = t[perm]
+    c2 = kinv.Cache8(*(w[:40, :3000, :hkv].view(torch.float8_e4m3fn) for w in wide), *(e[:40, :hkv, :3000] for e in exps))
+    assert_same_bits(kinv.attn_decode8(q[perm], c2, i32(lens)[perm].contiguous()), out[perm], "permuted, other strides")
+    for b in (0, 17):
+        one = kinv.attn_decode8(q[b: b + 1], c.sequences(b, b + 1), i32([lens[b]]))
+        assert_same_bits(one[0], out[b], "alone")
+
+
+def test_long_contexts(kinv):
+    hq, hkv, d, n = 32, 8, 128, 40000
+    k, v = keys((2, n, hkv, d), 190), keys((2, n, hkv, d), 191)
+    q = synth.normal_bf16((2, hq, d), 1.0, 192, "cuda")
+    lens = i32([n, 33333])
+    for fmt in ("e4m3", "int8"):
+        c, (k16, v16) = cache8(kinv, k, v, fmt)
+        assert_same_bits(kinv.attn_decode8(q, c, lens), kinv.attn_decode(q, k16, v16, lens), fmt)
+        assert_same_bits(kinv.attn_decode8(q, c, lens, window=20000, sinks=1000),
+                         kinv.attn_decode(q, k16, v16, lens, window=20000, sinks=1000), fmt + " window")
+
+
+# --------------------------------------------------- a step, streams and graphs
+def _step(kinv, c, s, window, sinks, ws=None):
+    """Append the step's rows and attend, as a decode step does."""
+    kinv.rope_append8(s["qkv"], s["q"], c, s["seq"], s["pos"], 8, 2, 64, 1e4)
+    return kinv.attn_decode8(s["q"], c, s["len"], out=s["out"], workspace=ws, window=window, sinks=sinks)
+
+
+def _inputs(step, seed=200):
+    pos = torch.tensor([300, 5, 255, 511], **I32) + step
+    return dict(qkv=synth.normal_bf16((4, 12 * 64), 1.0, seed + step, "cuda"), seq=torch.arange(4, **I32), pos=pos, len=pos + 1,
+                q=torch.empty(4, 8, 64, dtype=torch.bfloat16, device="cuda"), out=torch.empty(4, 8, 64, dtype=torch.bfloat16, device="cuda"))
+
+
+def _filled(kinv):
+    k, v = keys((4, 600, 2, 64), 210), keys((4, 600, 2, 64), 211)
+    return cache8(kinv, k, v, "e4m3")[0]
+
+
+def test_captured_steps_equal_eager_ones(kinv):
+    """Steps of append and attention replayed from a graph on new rows, two captured
+    graphs with a workspace each, in turn."""
+    want = []
+    c = _filled(kinv)
+    for t in range(3):
+        want.append(_step(kinv, c, _inputs(t), 100, 2).clone())
+    c = _filled(kinv)
+    s = _inputs(0)
+    graphs = []
+    for _ in range(2):
+        ws = torch.empty(kinv.attn_decode8_workspace(4, 8, 64, 600, 100, 2), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _step(kinv, c, s, 100, 2, ws)
+        graphs.append((g, ws))
+    for t in range(3):
+        new = _inputs(t)
+        for name in ("qkv", "pos", "len"):
+            s[name].copy_(new[name])
+        graphs[t % 2][0].replay()
+        assert_same_bits(s["out"], want[t], f"step {t}")
+    assert kinv.last_device_status() == 0
+
+
+def test_steps_on_two_streams(kinv):
+    want = []
+    for w in (0, 64):
+        want.append(_step(kinv, _filled(kinv), _inputs(0), w, 1).clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    caches, ins = [_filled(kinv) for _ in range(2)], [_inputs(0) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, c, s, w in zip(streams, caches, ins, (0, 64)):
+            with torch.cuda.stream(st):
+                _step(kinv, c, s, w, 1)
+    torch.cuda.synchronize()
+    for s, w in zip(ins, want):
+        assert_same_bits(s["out"], w, "two streams")
+
+
+def test_calls_on_a_named_stream(kinv):
+    """stream= allocates from, runs on and holds memory for the named stream."""
+    c = _filled(kinv)
+    s = _inputs(0)
+    want = _step(kinv, c, s, 90, 1).clone()
+    x = keys((4, 50, 2, 64), 220)
+    start, n = i32([1, 2, 3, 4]), i32([50, 7, 0, 33])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out = kinv.attn_decode8(s["q"], c, s["len"], window=90, sinks=1, stream=side)
+    k16, v16 = kinv.cache8_read(c, i32([0] * 4), i32([600] * 4), 600, stream=side)
+    side.synchronize()
+    assert_same_bits(out, want, "decode8")
+    win = kinv.attn_decode(s["q"], k16, v16, s["len"], window=90, sinks=1, stream=side)
+    args = (i32([299]), i32([2]), i32([0]), 2, 301)
+    pre = kinv.attn_prefill(s["q"][:2].contiguous(), k16[:1], v16[:1], *args, window=90, sinks=1, stream=side)
+    pre8 = kinv.attn_prefill8(s["q"][:2].contiguous(), c.sequences(0, 1), *args, window=90, sinks=1, stream=side)
+    kinv.cache8_write(c, x, x, start, n, stream=side)
+    side.synchronize()
+    assert_same_bits(win, want, "decode")
+    assert_same_bits(pre, pre8, "prefill")
+    back = kinv.cache8_read(c, start, n, 50)[0]
+    ref = cache8(kinv, x, x, "e4m3")[1][0]
+    for b, m in enumerate([50, 7, 0, 33]):
+        assert_same_bits(back[b, :m], ref[b, :m], "written")
+    assert kinv.last_device_status() == 0
