@@ -16,6 +16,7 @@
 #include <cmath>
 
 #include "attn_mma.cuh"
+#include "attn_tc.cuh"
 #include "cache8.cuh"
 #include "cache8_read.cuh"
 #include "common.cuh"
@@ -34,240 +35,400 @@ struct Attn8Params {
   const int32_t* kv_len;
   float* ws_o;   // [B][Hq][S][D]
   float* ws_ml;  // [B][Hq][S][2]
-  int Hq, G, S;
+  int Hq, G, S, B;
   float c2;      // fp32(scale * log2 e), times 2^30 for e4m3
   Window win;
   int* status;
 };
 
-// One block per (kv head, listed split, sequence).  S^T = K . q^T and
-// O^T = V^T . P^T: the codes are the A operand (16 keys x 16 values, 16 values x
-// 16 keys), so each is expanded once whatever the number of query heads, and the
-// eight columns are the pairs.  Within a 16-value step of q . k the values are
-// taken in another order on both sides (0, 2, 4, 6, ... as the bytes of a word
-// come apart), which a step's sum does not depend on.
-template <int D, bool I8>
-__global__ void __launch_bounds__(kThreads) attn8_split_kernel(const Attn8Params p) {
+constexpr int kBox = 64;  // keys of one TMA copy
+
+// Blocks of a launch stay (three to an SM for D = 128, five for D = 64) and walk
+// the listed splits of all sequences: block (g, p) takes kv head g of places p,
+// p + gridDim.y, ... in the batch's one list of splits.  Each block has one K and
+// one V buffer; the next split's K is requested when this one's scores are done,
+// its V when this one's products are, so copies are in flight throughout.
+//
+// S^T = K . q^T and O^T = V^T . P^T: the codes are the A operand (16 keys x 16
+// values, 16 values x 16 keys), so each is expanded once whatever the number of
+// query heads, and the eight columns are the pairs.  Within a 16-value step of
+// q . k the values are taken in another order on both sides (0, 2, 4, 6, ... as
+// the bytes of a word come apart), which a step's sum does not depend on.
+// GP = 4: at most four query heads per kv head; the lanes of the other four
+// columns take half of the keys' softmax.
+template <int D, bool I8, int GP>
+__global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
+    attn8_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const Attn8Params p) {
   constexpr int C = D / 16;           // 16-byte chunks of a key's codes
   constexpr int TILE = kSplit * D;    // bytes of a split's K or V codes
   constexpr int kLift = I8 ? 100 : 127;  // weights go in times 2^kLift: 256 products of 127 or 448 * 2^-120 stay below 2^127
-  extern __shared__ __align__(128) unsigned char smem[];
-  unsigned char* pt = smem + 2 * TILE;             // P hi [8][256] bf16, then lo
-  float* fk = reinterpret_cast<float*>(pt + 2 * kPairs * kSplit * 2);    // [256] factors of the scores
+  constexpr int QROW = D * 2 + 16;    // bytes of a row of q (padded: eight rows in eight bank groups)
+  constexpr int PHALF = GP * kSplit * 2;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  // K, V; P hi and lo [GP][256] (before them, in the same place, q [8]); the factors; the warps' results
+  unsigned char* pt = smem + 2 * TILE;
+  constexpr int PQ = 2 * PHALF > 8 * QROW ? 2 * PHALF : 8 * QROW;
+  float* fk = reinterpret_cast<float*>(pt + PQ);                          // [256] factors of the scores
   __nv_bfloat16* fv = reinterpret_cast<__nv_bfloat16*>(fk + kSplit);      // [256] factors of the weights
-  __shared__ float wmax[kThreads / 32][kPairs], wsum[kThreads / 32][kPairs];
-  __shared__ int wexp[kThreads / 32];
-
-  pdl_launch_dependents();
-  pdl_wait();
-  const int g = blockIdx.x, b = blockIdx.z;
-  const int len = p.kv_len[b];
-  if (len <= 0 || len > p.cache.slots) return;  // the merge kernel reports a length out of bounds
-  const int lo_key = window_lo(p.win, len);
-  const SplitList list = visible_splits(p.win, lo_key, len);
-  if (static_cast<int>(blockIdx.y) >= list.count) return;
-  const int k0 = list.split(blockIdx.y) * kSplit;
-  const int cnt = min(kSplit, len - k0);       // keys of the split
-  const int lo = lo_key - k0, sink = p.win.sinks - k0;
-  auto visible = [&](int key) { return key < cnt && (key >= lo || key < sink); };
+  float* wmax = reinterpret_cast<float*>(fv + kSplit);                    // [8 warps][8 pairs]
+  float* wsum = wmax + 8 * kPairs;
+  int* wexp = reinterpret_cast<int*>(wsum + 8 * kPairs);                  // [8]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(wexp + 8);                 // K, V
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int gq = lane >> 2, tq = lane & 3;
-  const int G = p.G;
   const uint32_t k_base = smem_addr(smem), v_base = k_base + TILE, pt_base = smem_addr(pt);
+  const uint32_t k_bar = smem_addr(bars), v_bar = smem_addr(bars + 1);
+  if (k_base & 1023u) {  // the copies' swizzle goes by address bits
+    if (t == 0 && p.status) atomicExch(p.status, DEV_TIMEOUT_ATTN);
+    return;
+  }
+  if (t == 0) {
+    mbar_init(k_bar, 1);
+    mbar_init(v_bar, 1);
+    fence_mbar_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmK)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmV)) : "memory");
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  pdl_wait();
 
-  // chunk c of row r sits at chunk slot(r, c): the eight rows of an ldmatrix
-  // phase fall in eight different bank groups
-  auto at = [](int r, int c) {
-    return static_cast<uint32_t>(r * D + ((C == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
-  };
-  const uint64_t policy = l2_policy_evict_first();
-  const int64_t off = b * p.cache.seq_stride + static_cast<int64_t>(k0) * p.cache.tok_stride + g * D;
-  auto load = [&](const unsigned char* src, uint32_t dst) {
+  // The walk: lane j holds the length of sequence wb + j and the number of listed
+  // splits of sequences wb .. wb + j; `base` splits lie before wb.
+  const int g = blockIdx.x, G = p.G;
+  int wb = 0, base = 0, wlen = 0, winc = 0;
+  auto load_window = [&]() {
+    const int b = wb + lane;
+    wlen = b < p.B ? p.kv_len[b] : 0;
+    if (wlen < 0 || wlen > p.cache.slots) wlen = 0;  // the merge kernel reports it
+    winc = wlen > 0 ? visible_splits(p.win, window_lo(p.win, wlen), wlen).count : 0;
 #pragma unroll
-    for (int it = 0; it < kSplit * C / kThreads; ++it) {
-      const int idx = it * kThreads + t;
-      const int r = idx / C, c = idx % C;
-      if (visible(r)) cp_async16_hint(dst + at(r, c), src + off + static_cast<int64_t>(r) * p.cache.tok_stride + c * 16, policy);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, winc, o);
+      if (lane >= o) winc += x;
     }
-    cp_async_commit();
   };
-  load(p.cache.k, k_base);
-  load(p.cache.v, v_base);
-
-  // this thread's key: its exponents
-  int ek = kExpNaN, ev = kExpNaN;
-  {
-    const int64_t e = b * p.cache.eseq_stride + g * p.cache.ehead_stride + k0 + t;
-    if (visible(t)) {
+  struct Item {
+    int b, i, k0, cnt, lo, sink;  // b < 0: none
+  };
+  auto visible = [](const Item& x, int key) { return key < x.cnt && (key >= x.lo || key < x.sink); };
+  auto item_at = [&](int at) {
+    Item x;
+    x.b = -1;
+    int total;
+    while (at >= base + (total = __shfl_sync(0xffffffffu, winc, 31))) {
+      base += total;
+      wb += 32;
+      if (wb >= p.B) return x;
+      load_window();
+    }
+    const int rel = at - base;
+    const int j = __popc(__ballot_sync(0xffffffffu, winc <= rel));
+    const int before = j > 0 ? __shfl_sync(0xffffffffu, winc, j - 1) : 0;
+    const int len = __shfl_sync(0xffffffffu, wlen, j);
+    const int first = window_lo(p.win, len);
+    x.b = wb + j;
+    x.i = rel - before;
+    x.k0 = visible_splits(p.win, first, len).split(x.i) * kSplit;
+    x.cnt = min(kSplit, len - x.k0);
+    x.lo = first - x.k0;
+    x.sink = p.win.sinks - x.k0;
+    return x;
+  };
+  const uint64_t policy = l2_policy_evict_first();  // each code is read once per step
+  auto request = [&](const CUtensorMap* map, const Item& x, uint32_t dst, uint32_t bar) {
+    uint32_t live = 0;
+#pragma unroll
+    for (int j = 0; j < kSplit / kBox; ++j)
+      if (j * kBox < x.cnt && (j * kBox < x.sink || (j + 1) * kBox > x.lo)) live |= 1u << j;
+    mbar_arrive_expect_tx(bar, __popc(live) * kBox * D);
+#pragma unroll
+    for (int j = 0; j < kSplit / kBox; ++j)
+      if (live >> j & 1) tma_load_4d(dst + j * kBox * D, map, 0, g, x.k0 + j * kBox, x.b, bar, policy);
+  };
+  // what a thread holds of the next split: its key's exponents, and four values (D = 64: lanes 0-15) of query head `warp`
+  int ek, ev;
+  uint2 qv;
+  auto fetch = [&](const Item& x) {
+    ek = ev = kExpNaN;
+    if (visible(x, t)) {
+      const int64_t e = x.b * p.cache.eseq_stride + g * p.cache.ehead_stride + x.k0 + t;
       ek = p.cache.ke[e];
       ev = p.cache.ve[e];
     }
+    qv = make_uint2(0, 0);
+    if (warp < G && lane < D / 4)
+      qv = *reinterpret_cast<const uint2*>(p.q + (static_cast<int64_t>(x.b) * p.Hq + g * G + warp) * D + 4 * lane);
+  };
+  // chunk c of row r of a buffer (the copies' swizzle): the eight rows of an
+  // ldmatrix phase fall in eight different bank groups
+  auto at = [](int r, int c) {
+    return static_cast<uint32_t>(r * D + ((C == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
+  };
+
+  load_window();
+  int place = blockIdx.y;
+  Item cur = item_at(place);
+  if (cur.b < 0) return;
+  if (t == 0) {
+    request(&tmK, cur, k_base, k_bar);
+    request(&tmV, cur, v_base, v_bar);
   }
-  // q fragments (B operand: 16 values x 8 pairs): lane (gq, tq) holds values
-  // 4tq .. 4tq + 3 of each step, as (0, 2) and (1, 3)
-  uint32_t qb[C][2];
-  {
-    const __nv_bfloat16* q = p.q + (static_cast<int64_t>(b) * p.Hq + g * G + gq) * D + 4 * tq;
-#pragma unroll
-    for (int ks = 0; ks < C; ++ks) {
-      uint2 x = make_uint2(0, 0);
-      if (gq < G) x = *reinterpret_cast<const uint2*>(q + 16 * ks);
+  fetch(cur);
+  for (uint32_t phase = 0;; phase ^= 1) {
+    // this split's factors and q into shared memory; the next one's requested
+    const int my_ev = ev;
+    const bool my_vis = visible(cur, t);
+    fk[t] = exponent_factor(ek);
+    {
+      const int wm = __reduce_max_sync(0xffffffffu, my_ev);
+      if (lane == 0) wexp[warp] = wm;
       if (!I8) {
         const __nv_bfloat162 lift = __float2bfloat162_rn(0x1p90f);
-        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&x);
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&qv);
         h[0] = __hmul2(h[0], lift);
         h[1] = __hmul2(h[1], lift);
       }
-      qb[ks][0] = __byte_perm(x.x, x.y, 0x5410);
-      qb[ks][1] = __byte_perm(x.x, x.y, 0x7632);
-    }
-  }
-  fk[t] = exponent_factor(ek);
-  const int wm = __reduce_max_sync(0xffffffffu, ev);
-  if (lane == 0) wexp[warp] = wm;
-  cp_async_wait<1>();
-  __syncthreads();
-  int ev_max = wexp[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) ev_max = max(ev_max, wexp[w]);
-  // 0 for a hidden key, whose weight is 0
-  const int fe = !visible(t) ? 0 : ev == kExpNaN ? 0x7FFF : max(ev - ev_max + 127 + kLift, 0) << 7;
-  fv[t] = __ushort_as_bfloat16(static_cast<unsigned short>(fe));
-
-  // --- scores: warp w owns keys 32w .. 32w + 31, two 16-key tiles
-  float sc[2][4];
-#pragma unroll
-  for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sc[mt][i] = 0.f;
-    const int row = warp * 32 + mt * 16 + (lane & 15);
-#pragma unroll
-    for (int kp = 0; kp < C / 2; ++kp) {
-      // matrices: rows 0-7 and 8-15 of chunk 2kp, then of chunk 2kp + 1
-      uint32_t w0, w1, w2, w3, a[4];
-      ldsm_x4(k_base + at(row, 2 * kp + (lane >> 4)), w0, w1, w2, w3);
-      expand4<I8>(w0, a[0], a[2]);
-      expand4<I8>(w1, a[1], a[3]);
-      mma_bf16_16816(sc[mt], a, qb[2 * kp][0], qb[2 * kp][1]);
-      expand4<I8>(w2, a[0], a[2]);
-      expand4<I8>(w3, a[1], a[3]);
-      mma_bf16_16816(sc[mt], a, qb[2 * kp + 1][0], qb[2 * kp + 1][1]);
-    }
-    // rows gq and gq + 8 of the tile: columns (pairs) 2tq, 2tq + 1
-    const float f0 = fk[warp * 32 + mt * 16 + gq], f1 = fk[warp * 32 + mt * 16 + 8 + gq];
-    sc[mt][0] = __fmul_rn(sc[mt][0], f0);
-    sc[mt][1] = __fmul_rn(sc[mt][1], f0);
-    sc[mt][2] = __fmul_rn(sc[mt][2], f1);
-    sc[mt][3] = __fmul_rn(sc[mt][3], f1);
-  }
-  // Lanes gq and gq ^ 1 swap, so that a lane holds keys 8nb + 2 kq + e (kq =
-  // gq / 2) of one pair, 2tq + (gq & 1): the layout that the sums are ordered by.
-  const int kq = gq >> 1, pair = 2 * tq + (gq & 1);
-  float x[4][2];
-#pragma unroll
-  for (int nb = 0; nb < 4; ++nb) {
-    const float mine0 = sc[nb >> 1][2 * (nb & 1)], mine1 = sc[nb >> 1][2 * (nb & 1) + 1];
-    const float got = __shfl_xor_sync(0xffffffffu, (gq & 1) ? mine0 : mine1, 4);
-    x[nb][0] = (gq & 1) ? got : mine0;
-    x[nb][1] = (gq & 1) ? mine1 : got;
-  }
-  bool see[4][2];
-  float mx = -INFINITY;
-#pragma unroll
-  for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      see[nb][e] = visible(warp * 32 + nb * 8 + 2 * kq + e);
-      if (see[nb][e]) mx = fmaxf(mx, x[nb][e]);
-    }
-#pragma unroll
-  for (int o = 8; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (kq == 0) wmax[warp][pair] = mx;
-  __syncthreads();
-  float m = wmax[0][pair];
-#pragma unroll
-  for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, wmax[w][pair]);
-  m = __fmul_rn(m, p.c2);
-  float sum = 0.f;
-#pragma unroll
-  for (int nb = 0; nb < 4; ++nb) {
-    const int key = warp * 32 + nb * 8 + 2 * kq;
-    // the weight's halves, then their factor (exact: a power of two)
-    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(fv + key);
-    float w[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      w[e] = see[nb][e] ? ex2_approx(__fmaf_rn(x[nb][e], p.c2, -m)) : 0.f;
-      sum = __fadd_rn(sum, w[e]);
-    }
-    const __nv_bfloat162 h = __floats2bfloat162_rn(w[0], w[1]);
-    const float2 hf = __bfloat1622float2(h);
-    const __nv_bfloat162 l = __floats2bfloat162_rn(__fsub_rn(w[0], hf.x), __fsub_rn(w[1], hf.y));
-    const uint32_t to = static_cast<uint32_t>(pair * kSplit * 2 + (((warp * 4 + nb) ^ pair) << 4) + 4 * kq);
-    *reinterpret_cast<__nv_bfloat162*>(pt + to) = __hmul2(h, f);
-    *reinterpret_cast<__nv_bfloat162*>(pt + kPairs * kSplit * 2 + to) = __hmul2(l, f);
-  }
-#pragma unroll
-  for (int o = 8; o <= 16; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-  if (kq == 0) wsum[warp][pair] = sum;
-  cp_async_wait<0>();
-  __syncthreads();
-
-  // --- O^T = V^T . P^T: warp w owns values 16w .. 16w + 15 over all 256 keys,
-  // one chain of sixteen 16-key steps, each its high halves, then its low ones
-  if (warp < C) {
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int kk = 0; kk < kSplit / 32; ++kk) {
-      // transposed 8 x 8 matrices of byte pairs: keys 8i .. 8i + 7 of the 32
-      uint32_t w[4], bh[4], bl[4], a[4];
-      ldsm_x4_t(v_base + at(kk * 32 + lane, warp), w[0], w[1], w[2], w[3]);
-      const uint32_t from = static_cast<uint32_t>((lane & 7) * kSplit * 2 + (((4 * kk + (lane >> 3)) ^ (lane & 7)) << 4));
-      ldsm_x4(pt_base + from, bh[0], bh[1], bh[2], bh[3]);
-      ldsm_x4(pt_base + kPairs * kSplit * 2 + from, bl[0], bl[1], bl[2], bl[3]);
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        // rows gq: value 2gq, rows gq + 8: value 2gq + 1
-        expand4<I8>(w[2 * s], a[0], a[1]);
-        expand4<I8>(w[2 * s + 1], a[2], a[3]);
-        mma_bf16_16816(o, a, bh[2 * s], bh[2 * s + 1]);
-        mma_bf16_16816(o, a, bl[2 * s], bl[2 * s + 1]);
+      // of each sixteen values the even ones, then the odd ones
+      if (lane < D / 4) {
+        unsigned char* to = pt + warp * QROW + (lane >> 2) * 32 + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(to) = __byte_perm(qv.x, qv.y, 0x5410);
+        *reinterpret_cast<uint32_t*>(to + 16) = __byte_perm(qv.x, qv.y, 0x7632);
       }
     }
-    // 2^Emax and the constants back, the smaller factor first (no intermediate
-    // result is smaller than the product)
-    const float back0 = exponent_factor(min(ev_max, 0)), back1 = exponent_factor(max(ev_max, 0) + (I8 ? 0 : 120) - kLift);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = __fmul_rn(__fmul_rn(o[i], back0), back1);
-    const int64_t row = static_cast<int64_t>(b) * p.Hq + g * G;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (2 * tq + e < G)
-        *reinterpret_cast<float2*>(p.ws_o + ((row + 2 * tq + e) * p.S + blockIdx.y) * D + warp * 16 + 2 * gq) =
-            make_float2(o[e], o[2 + e]);
-    if (warp == 0 && kq == 0 && pair < G) {
-      float l = wsum[0][pair];
-#pragma unroll
-      for (int w = 1; w < kThreads / 32; ++w) l = __fadd_rn(l, wsum[w][pair]);
-      *reinterpret_cast<float2*>(p.ws_ml + ((row + pair) * p.S + blockIdx.y) * 2) = make_float2(m, l);
+    place += gridDim.y;
+    const Item next = item_at(place);
+    if (next.b >= 0) fetch(next);
+    bool ok = mbar_wait_bounded(k_bar, phase, p.status, DEV_TIMEOUT_ATTN);
+    if (__syncthreads_or(!ok)) {
+      mbar_wait_bounded(v_bar, phase, nullptr, 0);  // the copy in flight lands before the block leaves
+      return;
     }
+    int ev_max = wexp[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) ev_max = max(ev_max, wexp[w]);
+    // 0 for a hidden key, whose weight is 0
+    const int fe = !my_vis ? 0 : my_ev == kExpNaN ? 0x7FFF : max(my_ev - ev_max + 127 + kLift, 0) << 7;
+    fv[t] = __ushort_as_bfloat16(static_cast<unsigned short>(fe));
+
+    // --- scores: warp w owns keys 32w .. 32w + 31, two 16-key tiles
+    float sc[2][4];
+    {
+      uint32_t qb[C][2];  // q fragments (B operand: 16 values x 8 pairs)
+#pragma unroll
+      for (int kp = 0; kp < C / 2; ++kp)
+        ldsm_x4(pt_base + (lane & 7) * QROW + kp * 64 + (lane >> 3) * 16, qb[2 * kp][0], qb[2 * kp][1],
+                qb[2 * kp + 1][0], qb[2 * kp + 1][1]);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[mt][i] = 0.f;
+        const int row = warp * 32 + mt * 16 + (lane & 15);
+#pragma unroll
+        for (int kp = 0; kp < C / 2; ++kp) {
+          // matrices: rows 0-7 and 8-15 of chunk 2kp, then of chunk 2kp + 1
+          uint32_t w0, w1, w2, w3, a[4];
+          ldsm_x4(k_base + at(row, 2 * kp + (lane >> 4)), w0, w1, w2, w3);
+          expand4<I8>(w0, a[0], a[2]);
+          expand4<I8>(w1, a[1], a[3]);
+          mma_bf16_16816(sc[mt], a, qb[2 * kp][0], qb[2 * kp][1]);
+          expand4<I8>(w2, a[0], a[2]);
+          expand4<I8>(w3, a[1], a[3]);
+          mma_bf16_16816(sc[mt], a, qb[2 * kp + 1][0], qb[2 * kp + 1][1]);
+        }
+        // rows gq and gq + 8 of the tile: columns (pairs) 2tq, 2tq + 1
+        const float f0 = fk[warp * 32 + mt * 16 + gq], f1 = fk[warp * 32 + mt * 16 + 8 + gq];
+        sc[mt][0] = __fmul_rn(sc[mt][0], f0);
+        sc[mt][1] = __fmul_rn(sc[mt][1], f0);
+        sc[mt][2] = __fmul_rn(sc[mt][2], f1);
+        sc[mt][3] = __fmul_rn(sc[mt][3], f1);
+      }
+    }
+    // Lanes gq and gq ^ 1 swap, so that a lane holds keys 8nb + 2 kq + e (kq =
+    // gq / 2) of one pair, 2tq + (gq & 1): the layout that the sums are ordered by.
+    const int kq = gq >> 1;
+    float y[4][2];
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb) {
+      const float mine0 = sc[nb >> 1][2 * (nb & 1)], mine1 = sc[nb >> 1][2 * (nb & 1) + 1];
+      const float got = __shfl_xor_sync(0xffffffffu, (gq & 1) ? mine0 : mine1, 4);
+      y[nb][0] = (gq & 1) ? got : mine0;
+      y[nb][1] = (gq & 1) ? mine1 : got;
+    }
+    // GP = 4: lanes tq >= 2 (pairs 4 .. 7, which are none) take blocks nb = 2, 3 of lane tq - 2
+    constexpr int NB = GP == 4 ? 2 : 4;
+    const int nb0 = GP == 4 && tq >= 2 ? 2 : 0;
+    const int pair = GP == 4 ? 2 * (tq & 1) + (gq & 1) : 2 * tq + (gq & 1);
+    float x[NB][2];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[i][e] = y[i][e];
+        if (GP == 4) {
+          const float got = __shfl_xor_sync(0xffffffffu, y[2 + i][e], 2);
+          if (tq >= 2) x[i][e] = got;
+        }
+      }
+    const int key0 = warp * 32 + nb0 * 8 + 2 * kq;
+    // no key of the split hidden: no mask
+    const bool whole = cur.cnt == kSplit && (cur.lo <= 0 || cur.sink >= kSplit);
+    float mx = -INFINITY;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) mx = fmax3(mx, x[i][0], x[i][1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (visible(cur, key0 + 8 * i + e)) mx = fmaxf(mx, x[i][e]);
+    }
+#pragma unroll
+    for (int o = GP == 4 ? 2 : 8; o <= 16; o = o == 2 ? 8 : o << 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (kq == 0) wmax[warp * kPairs + pair] = mx;
+    __syncthreads();
+    if (t == 0 && next.b >= 0) request(&tmK, next, k_base, k_bar);  // every warp is done with K
+    float m = wmax[pair];
+#pragma unroll
+    for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, wmax[w * kPairs + pair]);
+    m = __fmul_rn(m, p.c2);
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) x[i][e] = ex2_approx(__fmaf_rn(x[i][e], p.c2, -m));
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!visible(cur, key0 + 8 * i + e)) x[i][e] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      // the weight's halves, then their factor (exact: a power of two)
+      const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(fv + key0 + 8 * i);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[i][0], x[i][1]);
+      const float2 hf = __bfloat1622float2(h);
+      const __nv_bfloat162 l = __floats2bfloat162_rn(__fsub_rn(x[i][0], hf.x), __fsub_rn(x[i][1], hf.y));
+      const uint32_t to = static_cast<uint32_t>(pair * kSplit * 2 + (((warp * 4 + nb0 + i) ^ pair) << 4) + 4 * kq);
+      *reinterpret_cast<__nv_bfloat162*>(pt + to) = __hmul2(h, f);
+      *reinterpret_cast<__nv_bfloat162*>(pt + PHALF + to) = __hmul2(l, f);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) sum = __fadd_rn(sum, x[i][e]);
+    if (GP == 4) {  // the sum goes on from blocks 0, 1 to blocks 2, 3
+      const float got = __shfl_xor_sync(0xffffffffu, sum, 2);
+      sum = got;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sum = __fadd_rn(sum, x[i][e]);
+    }
+#pragma unroll
+    for (int o = 8; o <= 16; o <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+    if (kq == 0 && (GP == 8 || tq >= 2)) wsum[warp * kPairs + pair] = sum;
+    ok = mbar_wait_bounded(v_bar, phase, p.status, DEV_TIMEOUT_ATTN);
+    if (__syncthreads_or(!ok)) {
+      if (next.b >= 0) mbar_wait_bounded(k_bar, phase ^ 1, nullptr, 0);
+      return;
+    }
+
+    // --- O^T = V^T . P^T: warp w owns values 16w .. 16w + 15 over all 256 keys,
+    // one chain of sixteen 16-key steps, each its high halves, then its low ones
+    if (warp < C) {
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+      const int prow = lane & (GP - 1);  // GP = 4: columns 4 .. 7 repeat, and are not used
+#pragma unroll 2
+      for (int kk = 0; kk < kSplit / 32; ++kk) {
+        // transposed 8 x 8 matrices of byte pairs: keys 8i .. 8i + 7 of the 32
+        uint32_t w[4], bh[4], bl[4], a[4];
+        ldsm_x4_t(v_base + at(kk * 32 + lane, warp), w[0], w[1], w[2], w[3]);
+        const uint32_t from = static_cast<uint32_t>(prow * kSplit * 2 + (((4 * kk + (lane >> 3)) ^ prow) << 4));
+        ldsm_x4(pt_base + from, bh[0], bh[1], bh[2], bh[3]);
+        ldsm_x4(pt_base + PHALF + from, bl[0], bl[1], bl[2], bl[3]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          // rows gq: value 2gq, rows gq + 8: value 2gq + 1
+          expand4<I8>(w[2 * s], a[0], a[1]);
+          expand4<I8>(w[2 * s + 1], a[2], a[3]);
+          mma_bf16_16816(o, a, bh[2 * s], bh[2 * s + 1]);
+          mma_bf16_16816(o, a, bl[2 * s], bl[2 * s + 1]);
+        }
+      }
+      // 2^Emax and the constants back, the smaller factor first (no intermediate
+      // result is smaller than the product)
+      const float back0 = exponent_factor(min(ev_max, 0)), back1 = exponent_factor(max(ev_max, 0) + (I8 ? 0 : 120) - kLift);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __fmul_rn(__fmul_rn(o[i], back0), back1);
+      const int64_t row = static_cast<int64_t>(cur.b) * p.Hq + g * G;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * tq + e < G)
+          *reinterpret_cast<float2*>(p.ws_o + ((row + 2 * tq + e) * p.S + cur.i) * D + warp * 16 + 2 * gq) =
+              make_float2(o[e], o[2 + e]);
+      if (warp == 0 && kq == 0 && pair < G && (GP == 8 || tq >= 2)) {
+        float l = wsum[pair];
+#pragma unroll
+        for (int w = 1; w < kThreads / 32; ++w) l = __fadd_rn(l, wsum[w * kPairs + pair]);
+        *reinterpret_cast<float2*>(p.ws_ml + ((row + pair) * p.S + cur.i) * 2) = make_float2(m, l);
+      }
+    }
+    if (next.b < 0) return;
+    __syncthreads();  // every warp is done with V, P and the sums
+    if (t == 0) request(&tmV, next, v_base, v_bar);
+    cur = next;
   }
 }
 
-template <int D>
+template <int D, int GP>
 constexpr size_t split8_smem_bytes() {
-  return 2 * static_cast<size_t>(kSplit) * D + 2 * static_cast<size_t>(kPairs) * kSplit * 2 + kSplit * 6;
+  constexpr size_t P = 2 * static_cast<size_t>(GP) * kSplit * 2, Q = 8 * (D * 2 + 16);
+  return 2 * static_cast<size_t>(kSplit) * D + (P > Q ? P : Q) + kSplit * 6 + 2 * 8 * kPairs * 4 + 8 * 4 + 2 * 8;
+}
+
+// The codes as bytes (D, Hkv, slots, B), boxes of 64 keys of one head, rows of
+// 128 bytes in the 128-byte swizzle or of 64 in the 64-byte one.
+inline bool encode_codes(CUtensorMap* map, const void* ptr, const Cache8View& c, int B, int Hkv, int D) {
+  auto fn = tma_encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(c.slots),
+                              static_cast<cuuint64_t>(B)};
+  // one sequence: any sequence stride describes it (the coordinate is 0)
+  const cuuint64_t seq = B > 1 ? c.seq_stride : static_cast<cuuint64_t>(c.slots) * c.tok_stride;
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(c.tok_stride), seq};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), 1, kBox, 1}, step[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool I8, int GP>
+kinv_status launch_decode8(const Attn8Params& p, const MergeParams& mp, int Hkv, cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  if (!encode_codes(&mk, p.cache.k, p.cache, p.B, Hkv, D) || !encode_codes(&mv, p.cache.v, p.cache, p.B, Hkv, D))
+    return KINV_ERR_UNSUPPORTED;
+  auto kernel = attn8_split_kernel<D, I8, GP>;
+  constexpr size_t smem = split8_smem_bytes<D, GP>();
+  kinv_status st = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (st != KINV_OK) return st;
+  // as many blocks as the GPU holds at a time, or as there can be splits
+  const int64_t resident = static_cast<int64_t>(sm_count()) * (D == 128 ? 3 : 5);
+  const int64_t most = static_cast<int64_t>(p.B) * p.S;
+  int64_t places = (resident + Hkv - 1) / Hkv;
+  if (places > most) places = most;
+  st = launch_kernel(kernel, dim3(Hkv, static_cast<unsigned>(places)), dim3(kThreads), smem, stream, 1, mk, mv, p);
+  if (st != KINV_OK) return st;
+  return launch_kernel(window_merge_kernel<D>, dim3(p.Hq, p.B), dim3(D), 0, stream, 1, mp);
 }
 
 template <int D, bool I8>
-kinv_status launch_decode8(const Attn8Params& p, const MergeParams& mp, int Hkv, int B, cudaStream_t stream) {
-  void (*kernel)(const Attn8Params) = attn8_split_kernel<D, I8>;
-  constexpr size_t smem = split8_smem_bytes<D>();
-  kinv_status st = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
-  if (st != KINV_OK) return st;
-  st = launch_kernel(kernel, dim3(Hkv, p.S, B), dim3(kThreads), smem, stream, 1, p);
-  if (st != KINV_OK) return st;
-  return launch_kernel(window_merge_kernel<D>, dim3(p.Hq, B), dim3(D), 0, stream, 1, mp);
+kinv_status launch_decode8(const Attn8Params& p, const MergeParams& mp, int Hkv, cudaStream_t stream) {
+  return p.G <= 4 ? launch_decode8<D, I8, 4>(p, mp, Hkv, stream) : launch_decode8<D, I8, 8>(p, mp, Hkv, stream);
 }
 
 size_t decode8_bytes(int64_t B, int Hq, int D, int64_t S) {
@@ -307,7 +468,8 @@ extern "C" kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache
   const int64_t S = cache->slots > 0 ? max_visible_splits(window, sinks, cache->slots) : 1;
   const bool i8 = cache->dtype == KINV_I8;
   p.c2 = base2_factor(scale, D) * (i8 ? 1.f : 0x1p30f);
-  if (B > 65535 || S > 65535 || !std::isfinite(p.c2)) return KINV_ERR_UNSUPPORTED;
+  if (B > 1 && cache->seq_stride == 0) return KINV_ERR_INVALID_ARG;
+  if (B > 65535 || B * S > 0x7F000000 || !std::isfinite(p.c2)) return KINV_ERR_UNSUPPORTED;
   if (ws_bytes < decode8_bytes(B, Hq, D, S)) return KINV_ERR_WORKSPACE;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.kv_len = kv_len;
@@ -317,12 +479,13 @@ extern "C" kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache
   p.Hq = Hq;
   p.G = Hq / Hkv;
   p.S = static_cast<int>(S);
+  p.B = B;
   p.win = Window{window, sinks};
   p.status = device_status_word();
   MergeParams mp{p.ws_o, p.ws_ml, kv_len, static_cast<__nv_bfloat16*>(out), Hq, p.S, cache->slots, p.win, p.status};
   if (D == 128)
-    return i8 ? launch_decode8<128, true>(p, mp, Hkv, B, stream) : launch_decode8<128, false>(p, mp, Hkv, B, stream);
-  return i8 ? launch_decode8<64, true>(p, mp, Hkv, B, stream) : launch_decode8<64, false>(p, mp, Hkv, B, stream);
+    return i8 ? launch_decode8<128, true>(p, mp, Hkv, stream) : launch_decode8<128, false>(p, mp, Hkv, stream);
+  return i8 ? launch_decode8<64, true>(p, mp, Hkv, stream) : launch_decode8<64, false>(p, mp, Hkv, stream);
 }
 
 // A prompt chunk: the keys and values that its rows see, read back into the
