@@ -398,10 +398,10 @@ kinv_status kinv_cache8_read(const kinv_cache8* cache, const int32_t* start, con
  * window and sinks as above (window = 0: every key).  A row gets the bits that
  * kinv_attn_decode_window and kinv_attn_prefill_window give on the cache read
  * back, wherever no score, product or sum on the way leaves the normal range of
- * fp32 (with e4m3 that asks for |q| below 2^37, and a weight below 2^-100 times
- * the largest scale among its 256 keys may lose bits), so all their invariances
- * hold; hidden slots and those behind a
- * sequence's last key may hold anything.
+ * fp32, in decode no value of q other than 0 lies below 2^-31 of the row and
+ * head's largest, and with e4m3 no weight that counts below 2^-100 times the
+ * largest scale among its 256 keys; so all their invariances hold.  Hidden slots
+ * and those behind a sequence's last key may hold anything.
  * kv_len[b] in [0, slots], else zeros and KINV_ERR_INVALID_ARG in the status
  * word; B at most the cache's, max_kv at most its slots; other arguments,
  * requirements and errors as there.  workspace: device, 16-byte aligned, as many

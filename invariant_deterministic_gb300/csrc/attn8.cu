@@ -36,12 +36,21 @@ struct Attn8Params {
   float* ws_o;   // [B][Hq][S][D]
   float* ws_ml;  // [B][Hq][S][2]
   int Hq, G, S, B;
-  float c2;      // fp32(scale * log2 e), times 2^30 for e4m3
+  float c2;      // fp32(scale * log2 e)
   Window win;
   int* status;
 };
 
 constexpr int kBox = 64;  // keys of one TMA copy
+
+// D = A . B + D, one 16 x 8 x 16 warp MMA, f16 inputs, fp32 accumulation.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
 // Blocks of a launch stay (three to an SM for D = 128, five for D = 64) and walk
 // the listed splits of all sequences: block (g, p) takes kv head g of places p,
@@ -52,8 +61,8 @@ constexpr int kBox = 64;  // keys of one TMA copy
 // S^T = K . q^T and O^T = V^T . P^T: the codes are the A operand (16 keys x 16
 // values, 16 values x 16 keys), so each is expanded once whatever the number of
 // query heads, and the eight columns are the pairs.  Within a 16-value step of
-// q . k the values are taken in another order on both sides (0, 2, 4, 6, ... as
-// the bytes of a word come apart), which a step's sum does not depend on.
+// q . k the values are taken in another order on both sides (a lane's word holds
+// four neighbours), which a step's sum does not depend on.
 // GP = 4: at most four query heads per kv head; the lanes of the other four
 // columns take half of the keys' softmax.
 template <int D, bool I8, int GP>
@@ -74,7 +83,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
   float* wmax = reinterpret_cast<float*>(fv + kSplit);                    // [8 warps][8 pairs]
   float* wsum = wmax + 8 * kPairs;
   int* wexp = reinterpret_cast<int*>(wsum + 8 * kPairs);                  // [8]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(wexp + 8);                 // K, V
+  float* qc2 = reinterpret_cast<float*>(wexp + 8);                        // [8] the pairs' softmax factors
+  uint64_t* bars = reinterpret_cast<uint64_t*>(qc2 + 8);                  // K, V
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   const uint32_t k_base = smem_addr(smem), v_base = k_base + TILE, pt_base = smem_addr(pt);
@@ -184,17 +194,19 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     {
       const int wm = __reduce_max_sync(0xffffffffu, my_ev);
       if (lane == 0) wexp[warp] = wm;
-      if (!I8) {
-        const __nv_bfloat162 lift = __float2bfloat162_rn(0x1p90f);
-        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&qv);
-        h[0] = __hmul2(h[0], lift);
-        h[1] = __hmul2(h[1], lift);
-      }
-      // of each sixteen values the even ones, then the odd ones
+      // q of head `warp` as f16 times 2^up
+      const uint32_t qm = __vmaxu2(qv.x & 0x7FFF7FFFu, qv.y & 0x7FFF7FFFu);
+      const int top = static_cast<int>(__reduce_max_sync(0xffffffffu, max(qm & 0xFFFFu, qm >> 16)) >> 7);
+      const int up = min(141 - min(top, 254), 120);
+      const float f = exponent_factor(up);
+      if (lane == 0) qc2[warp] = __fmul_rn(p.c2, exponent_factor(-up));
       if (lane < D / 4) {
+        // of each sixteen values 0, 1, 4, 5, 8, ..., then the others
+        const __half2 a = __floats2half2_rn(__fmul_rn(bf16_lo(qv.x), f), __fmul_rn(bf16_hi(qv.x), f));
+        const __half2 c = __floats2half2_rn(__fmul_rn(bf16_lo(qv.y), f), __fmul_rn(bf16_hi(qv.y), f));
         unsigned char* to = pt + warp * QROW + (lane >> 2) * 32 + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(to) = __byte_perm(qv.x, qv.y, 0x5410);
-        *reinterpret_cast<uint32_t*>(to + 16) = __byte_perm(qv.x, qv.y, 0x7632);
+        *reinterpret_cast<__half2*>(to) = a;
+        *reinterpret_cast<__half2*>(to + 16) = c;
       }
     }
     place += gridDim.y;
@@ -213,8 +225,13 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     fv[t] = __ushort_as_bfloat16(static_cast<unsigned short>(fe));
 
     // --- scores: warp w owns keys 32w .. 32w + 31, two 16-key tiles
-    float sc[2][4];
-    {
+    float sc[2][4] = {};
+    // the 32-key groups that hold a visible key: the others add nothing
+    uint32_t groups = 0;
+#pragma unroll
+    for (int j = 0; j < kSplit / 32; ++j)
+      if (j * 32 < cur.cnt && (j * 32 < cur.sink || (j + 1) * 32 > cur.lo)) groups |= 1u << j;
+    if (groups >> warp & 1) {
       uint32_t qb[C][2];  // q fragments (B operand: 16 values x 8 pairs)
 #pragma unroll
       for (int kp = 0; kp < C / 2; ++kp)
@@ -222,20 +239,18 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
                 qb[2 * kp + 1][0], qb[2 * kp + 1][1]);
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[mt][i] = 0.f;
         const int row = warp * 32 + mt * 16 + (lane & 15);
 #pragma unroll
         for (int kp = 0; kp < C / 2; ++kp) {
           // matrices: rows 0-7 and 8-15 of chunk 2kp, then of chunk 2kp + 1
           uint32_t w0, w1, w2, w3, a[4];
           ldsm_x4(k_base + at(row, 2 * kp + (lane >> 4)), w0, w1, w2, w3);
-          expand4<I8>(w0, a[0], a[2]);
-          expand4<I8>(w1, a[1], a[3]);
-          mma_bf16_16816(sc[mt], a, qb[2 * kp][0], qb[2 * kp][1]);
-          expand4<I8>(w2, a[0], a[2]);
-          expand4<I8>(w3, a[1], a[3]);
-          mma_bf16_16816(sc[mt], a, qb[2 * kp + 1][0], qb[2 * kp + 1][1]);
+          expand4_f16<I8>(w0, a[0], a[2]);
+          expand4_f16<I8>(w1, a[1], a[3]);
+          mma_f16_16816(sc[mt], a, qb[2 * kp][0], qb[2 * kp][1]);
+          expand4_f16<I8>(w2, a[0], a[2]);
+          expand4_f16<I8>(w3, a[1], a[3]);
+          mma_f16_16816(sc[mt], a, qb[2 * kp + 1][0], qb[2 * kp + 1][1]);
         }
         // rows gq and gq + 8 of the tile: columns (pairs) 2tq, 2tq + 1
         const float f0 = fk[warp * 32 + mt * 16 + gq], f1 = fk[warp * 32 + mt * 16 + 8 + gq];
@@ -293,11 +308,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     float m = wmax[pair];
 #pragma unroll
     for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, wmax[w * kPairs + pair]);
-    m = __fmul_rn(m, p.c2);
+    const float c2 = qc2[pair];
+    m = __fmul_rn(m, c2);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) x[i][e] = ex2_approx(__fmaf_rn(x[i][e], p.c2, -m));
+      for (int e = 0; e < 2; ++e) x[i][e] = ex2_approx(__fmaf_rn(x[i][e], c2, -m));
     if (!whole) {
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -345,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
       const int prow = lane & (GP - 1);  // GP = 4: columns 4 .. 7 repeat, and are not used
 #pragma unroll 2
       for (int kk = 0; kk < kSplit / 32; ++kk) {
+        if (!(groups >> kk & 1)) continue;
         // transposed 8 x 8 matrices of byte pairs: keys 8i .. 8i + 7 of the 32
         uint32_t w[4], bh[4], bl[4], a[4];
         ldsm_x4_t(v_base + at(kk * 32 + lane, warp), w[0], w[1], w[2], w[3]);
@@ -388,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
 template <int D, int GP>
 constexpr size_t split8_smem_bytes() {
   constexpr size_t P = 2 * static_cast<size_t>(GP) * kSplit * 2, Q = 8 * (D * 2 + 16);
-  return 2 * static_cast<size_t>(kSplit) * D + (P > Q ? P : Q) + kSplit * 6 + 2 * 8 * kPairs * 4 + 8 * 4 + 2 * 8;
+  return 2 * static_cast<size_t>(kSplit) * D + (P > Q ? P : Q) + kSplit * 6 + 2 * 8 * kPairs * 4 + 2 * 8 * 4 + 2 * 8;
 }
 
 // The codes as bytes (D, Hkv, slots, B), boxes of 64 keys of one head, rows of
@@ -467,9 +484,9 @@ extern "C" kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KINV_ERR_ALIGNMENT;
   const int64_t S = cache->slots > 0 ? max_visible_splits(window, sinks, cache->slots) : 1;
   const bool i8 = cache->dtype == KINV_I8;
-  p.c2 = base2_factor(scale, D) * (i8 ? 1.f : 0x1p30f);
+  p.c2 = base2_factor(scale, D);
   if (B > 1 && cache->seq_stride == 0) return KINV_ERR_INVALID_ARG;
-  if (B > 65535 || B * S > 0x7F000000 || !std::isfinite(p.c2)) return KINV_ERR_UNSUPPORTED;
+  if (B > 65535 || B * S > 0x7F000000) return KINV_ERR_UNSUPPORTED;
   if (ws_bytes < decode8_bytes(B, Hq, D, S)) return KINV_ERR_WORKSPACE;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.kv_len = kv_len;

@@ -127,10 +127,9 @@ __global__ void rope_append8_kernel(const __nv_bfloat16* __restrict__ qkv, int64
   }
 }
 
-// bf16 keys (z = 0) or values (z = 1) of kWriteTokens tokens of one sequence: a
-// group of D / 8 lanes per (token, head), 16 bytes a lane.  The exponents of the
-// block go out together, one run of bytes a head.
-constexpr int kWriteTokens = 32;
+// bf16 keys (z = 0) or values (z = 1) of `tokens` tokens of one sequence: a group
+// of D / 8 lanes per (token, head), 16 bytes a lane, four vectors a lane ahead.
+// The exponents of the block go out together, one run of bytes a head.
 constexpr int kWriteThreads = 256;
 
 struct WriteParams {
@@ -139,7 +138,7 @@ struct WriteParams {
   int64_t seq_stride, tok_stride;
   const int32_t* start;
   const int32_t* len;
-  int max_len, Hkv;
+  int max_len, Hkv, tokens;
   Cache8View cache;
   int* status;
 };
@@ -148,7 +147,8 @@ template <int D, bool I8>
 __global__ void __launch_bounds__(kWriteThreads) cache8_write_kernel(const WriteParams p) {
   constexpr int L = D / 8;                      // lanes of a vector
   constexpr int PER = kWriteThreads / L;        // vectors at a time
-  extern __shared__ int8_t exps[];              // [Hkv][kWriteTokens]
+  constexpr int AHEAD = 4;
+  extern __shared__ int8_t exps[];              // [Hkv][tokens]
   pdl_launch_dependents();
   pdl_wait();
   const int b = blockIdx.y;
@@ -157,38 +157,47 @@ __global__ void __launch_bounds__(kWriteThreads) cache8_write_kernel(const Write
     if (threadIdx.x == 0 && blockIdx.x == 0 && p.status) atomicExch(p.status, DEV_CACHE8_BAD_RANGE);
     return;
   }
-  const int i0 = blockIdx.x * kWriteTokens;
-  const int n = min(kWriteTokens, len - i0);
+  const int i0 = blockIdx.x * p.tokens;
+  const int n = min(p.tokens, len - i0);
   if (n <= 0) return;
   const bool values = blockIdx.z != 0;
-  const __nv_bfloat16* src = (values ? p.v : p.k) + b * p.seq_stride;
-  unsigned char* dst = (values ? p.cache.v : p.cache.k) + b * p.cache.seq_stride;
   const int sub = threadIdx.x % L;
+  const __nv_bfloat16* src = (values ? p.v : p.k) + b * p.seq_stride + i0 * p.tok_stride + sub * 8;
+  unsigned char* dst =
+      (values ? p.cache.v : p.cache.k) + b * p.cache.seq_stride + (start + i0) * p.cache.tok_stride + sub * 8;
   const int total = n * p.Hkv;
   // whole rounds, so that every lane takes part in the shuffles
-  for (int at = 0; at < total; at += PER) {
-    const int vec = at + threadIdx.x / L;
-    const bool live = vec < total;
-    const int i = live ? vec / p.Hkv : 0, g = live ? vec % p.Hkv : 0;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (live) x = *reinterpret_cast<const uint4*>(src + (i0 + i) * p.tok_stride + g * D + sub * 8);
-    uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  for (int at = 0; at < total; at += PER * AHEAD) {
+    uint4 x[AHEAD];
+    int tok[AHEAD], head[AHEAD];
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int E = scale_exponent<I8>(max(m & 0xFFFFu, m >> 16));
-    const float inv = encode_factor(E);
-    if (live) {
+    for (int j = 0; j < AHEAD; ++j) {
+      const int vec = at + j * PER + static_cast<int>(threadIdx.x) / L;
+      tok[j] = vec < total ? vec / p.Hkv : -1;
+      head[j] = vec - tok[j] * p.Hkv;
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (tok[j] >= 0) x[j] = __ldcs(reinterpret_cast<const uint4*>(src + tok[j] * p.tok_stride + head[j] * D));
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      uint32_t m = __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
+                            __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu));
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int E = scale_exponent<I8>(max(m & 0xFFFFu, m >> 16));
+      const float inv = encode_factor(E);
+      if (tok[j] < 0) continue;
       uint2 c;
-      c.x = encode2<I8>(bf16_lo(x.x), bf16_hi(x.x), inv) | (encode2<I8>(bf16_lo(x.y), bf16_hi(x.y), inv) << 16);
-      c.y = encode2<I8>(bf16_lo(x.z), bf16_hi(x.z), inv) | (encode2<I8>(bf16_lo(x.w), bf16_hi(x.w), inv) << 16);
-      *reinterpret_cast<uint2*>(dst + (start + i0 + i) * p.cache.tok_stride + g * D + sub * 8) = c;
-      if (sub == 0) exps[g * kWriteTokens + i] = static_cast<int8_t>(E);
+      c.x = encode2<I8>(bf16_lo(x[j].x), bf16_hi(x[j].x), inv) | (encode2<I8>(bf16_lo(x[j].y), bf16_hi(x[j].y), inv) << 16);
+      c.y = encode2<I8>(bf16_lo(x[j].z), bf16_hi(x[j].z), inv) | (encode2<I8>(bf16_lo(x[j].w), bf16_hi(x[j].w), inv) << 16);
+      *reinterpret_cast<uint2*>(dst + tok[j] * p.cache.tok_stride + head[j] * D) = c;
+      if (sub == 0) exps[head[j] * p.tokens + tok[j]] = static_cast<int8_t>(E);
     }
   }
   __syncthreads();
   int8_t* e = (values ? p.cache.ve : p.cache.ke) + b * p.cache.eseq_stride + start + i0;
-  for (int idx = threadIdx.x; idx < kWriteTokens * p.Hkv; idx += kWriteThreads) {
-    const int g = idx / kWriteTokens, i = idx % kWriteTokens;
+  for (int idx = threadIdx.x; idx < p.tokens * p.Hkv; idx += kWriteThreads) {
+    const int g = idx / p.tokens, i = idx % p.tokens;
     if (i < n) e[g * p.cache.ehead_stride + i] = exps[idx];
   }
 }
@@ -263,8 +272,9 @@ extern "C" kinv_status kinv_cache8_write(const void* k, const void* v, int64_t s
   p.max_len = max_len;
   p.Hkv = Hkv;
   p.status = device_status_word();
-  const dim3 grid((max_len + kWriteTokens - 1) / kWriteTokens, B, 2);
-  const size_t smem = static_cast<size_t>(Hkv) * kWriteTokens;
+  p.tokens = tokens_per_block(B, max_len, Hkv, D);
+  const dim3 grid((max_len + p.tokens - 1) / p.tokens, B, 2);
+  const size_t smem = static_cast<size_t>(Hkv) * p.tokens;
   auto run = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kWriteThreads), smem, stream, 1, p); };
   const bool i8 = cache->dtype == KINV_I8;
   if (D == 128) return i8 ? run(cache8_write_kernel<128, true>) : run(cache8_write_kernel<128, false>);

@@ -17,6 +17,7 @@
 // depend on which later tokens the cache already holds.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -92,6 +93,28 @@ __device__ __forceinline__ void expand4(uint32_t w, uint32_t& even, uint32_t& od
   } else {
     even = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
     odd = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+  }
+}
+
+// Four codes as two f16 pairs in their order, exactly (every e4m3 number and
+// every int8 is an f16 number; codes 7F and FF become NaN, which nothing reads).
+// int8: with the sign bit flipped the byte is v + 128, and 1024 + (v + 128) is an
+// f16 number whose low byte it is.
+template <bool I8>
+__device__ __forceinline__ void expand4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (I8) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
 }
 

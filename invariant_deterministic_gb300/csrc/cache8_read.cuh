@@ -7,8 +7,20 @@
 
 namespace kinv {
 
-constexpr int kReadTokens = 32;
 constexpr int kReadThreads = 256;
+
+// Tokens of one block of the kernels that write the cache or read it back: 32
+// (a sector of exponents a head) where that leaves four blocks to an SM, else
+// fewer, down to about one vector a lane: few tokens cost a load's latency for
+// each round of a block (500 tokens of 8 heads of 128: 17.4 us by 32, 3.7 by 2).
+inline int tokens_per_block(int B, int max_len, int Hkv, int D) {
+  int tokens = 32;
+  const int64_t want = 4 * static_cast<int64_t>(sm_count());
+  while (tokens > 1 && 2 * static_cast<int64_t>(B) * ((max_len + tokens - 1) / tokens) < want &&
+         tokens * Hkv * (D / 8) > kReadThreads)
+    tokens /= 2;
+  return tokens;
+}
 
 struct ReadParams {
   Cache8View cache;
@@ -19,12 +31,12 @@ struct ReadParams {
   const int32_t* len;
   const int32_t* q_start;  // ... or, with these, slot i < q_start[b] + q_len[b] where a row of the chunk sees it
   const int32_t* q_len;
-  int max_len, max_q_len, Hkv;
+  int max_len, max_q_len, Hkv, tokens;
   Window win;
   int* status;
 };
 
-// Keys (z = 0) or values (z = 1) of kReadTokens tokens of one sequence, D / 16
+// Keys (z = 0) or values (z = 1) of `tokens` tokens of one sequence, D / 16
 // lanes per (token, head): 16 codes in, 32 bytes out a lane.
 template <int D, bool I8>
 __global__ void __launch_bounds__(kReadThreads) cache8_read_kernel(const ReadParams p) {
@@ -48,8 +60,8 @@ __global__ void __launch_bounds__(kReadThreads) cache8_read_kernel(const ReadPar
       return;
     }
   }
-  const int i0 = blockIdx.x * kReadTokens;
-  const int n = min(kReadTokens, len - i0);
+  const int i0 = blockIdx.x * p.tokens;
+  const int n = min(p.tokens, len - i0);
   if (n <= 0 || (i0 >= p.win.sinks && i0 + n <= lo)) return;
   const bool values = blockIdx.z != 0;
   const unsigned char* src = (values ? p.cache.v : p.cache.k) + b * p.cache.seq_stride;
@@ -67,8 +79,9 @@ __global__ void __launch_bounds__(kReadThreads) cache8_read_kernel(const ReadPar
   }
 }
 
-inline kinv_status launch_cache8_read(const ReadParams& p, bool i8, int B, int D, cudaStream_t stream) {
-  const dim3 grid((p.max_len + kReadTokens - 1) / kReadTokens, B, 2);
+inline kinv_status launch_cache8_read(ReadParams p, bool i8, int B, int D, cudaStream_t stream) {
+  p.tokens = tokens_per_block(B, p.max_len, p.Hkv, D);
+  const dim3 grid((p.max_len + p.tokens - 1) / p.tokens, B, 2);
   auto run = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kReadThreads), 0, stream, 1, p); };
   if (D == 128) return i8 ? run(cache8_read_kernel<128, true>) : run(cache8_read_kernel<128, false>);
   return i8 ? run(cache8_read_kernel<64, true>) : run(cache8_read_kernel<64, false>);

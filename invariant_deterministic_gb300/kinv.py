@@ -349,8 +349,11 @@ def attn_decode_workspace(batch: int, n_q: int, head_dim: int, max_len: int,
 
 def _window_inputs(q, k_cache, v_cache, out, batch: int, what: str):
     """Checks of the windowed calls: (slots, Hkv, sequence and slot strides)."""
-    for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (out, "out")):
-        _need(t, torch.bfloat16, name)
+    bf = torch.bfloat16
+    if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is bf and q.is_cuda and out.is_cuda
+            and k_cache.is_cuda and v_cache.is_cuda):
+        for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (out, "out")):
+            _need(t, bf, name)
     shape, stride = k_cache.shape, k_cache.stride()
     if v_cache.shape != shape or v_cache.stride() != stride or len(shape) != 4:
         raise ValueError(f"{what}: the caches must be [B][slots][Hkv][D] and share shape and strides")
@@ -370,9 +373,11 @@ def _workspace(side, workspace, need: int, device):
 
 
 def _vectors(what: str, n: int, **tensors) -> None:
+    i32 = torch.int32
     for name, t in tensors.items():
-        _need(t, torch.int32, name)
-        if t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+        if t.dtype is not i32 or not t.is_cuda:
+            _need(t, i32, name)
+        if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be a contiguous vector of at least {n} entries")
 
 
@@ -556,18 +561,18 @@ def rope_append8(qkv, q_out, cache: Cache8, seq, pos, n_q, n_kv, head_dim, rope_
     [seq][pos]; q_out [rows][Hq][D] has rope_append's bits.  A row outside the cache
     is left out (its q_out too) and recorded in the device status."""
     bf = torch.bfloat16
-    for t, name in ((qkv, "qkv"), (q_out, "q_out")):
-        _need(t, bf, name)
+    if not (qkv.dtype is q_out.dtype is bf and qkv.is_cuda and q_out.is_cuda):
+        _need(qkv, bf, "qkv")
+        _need(q_out, bf, "q_out")
     (rows, width), (ld, step) = qkv.shape, qkv.stride()
     if (step != 1 and width > 1) or width != (n_q + 2 * n_kv) * head_dim or not q_out.is_contiguous() \
             or q_out.numel() < rows * n_q * head_dim or cache.n_kv != n_kv or cache.head_dim != head_dim:
         raise ValueError("rope_append8: shapes or layouts do not match")
     _vectors("rope_append8", rows, seq=seq, pos=pos)
     for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None:
+        if t is not None and not (t.dtype is bf and t.is_cuda and t.is_contiguous() and t.numel() >= head_dim):
             _need(t, bf, name)
-            if not t.is_contiguous() or t.numel() < head_dim:
-                raise ValueError(f"rope_append8: {name} must hold a contiguous gain for each of a head's values")
+            raise ValueError(f"rope_append8: {name} must hold a contiguous gain for each of a head's values")
     side = _side(stream)
     if side is not None:
         _hold(side, qkv, q_out, seq, pos, q_norm, k_norm, *cache.tensors)
@@ -579,8 +584,10 @@ def rope_append8(qkv, q_out, cache: Cache8, seq, pos, n_q, n_kv, head_dim, rope_
 
 def _tokens(k, v, cache: Cache8, what: str):
     """Shape and strides of bf16 k, v [B][n][Hkv][D] that go into or come out of ``cache``."""
-    for t, name in ((k, "k"), (v, "v")):
-        _need(t, torch.bfloat16, name)
+    bf = torch.bfloat16
+    if not (k.dtype is v.dtype is bf and k.is_cuda and v.is_cuda):
+        _need(k, bf, "k")
+        _need(v, bf, "v")
     shape, stride = k.shape, k.stride()
     if len(shape) != 4 or v.shape != shape or v.stride() != stride:
         raise ValueError(f"{what}: k and v must be [B][n][Hkv][D] and share shape and strides")
@@ -624,8 +631,10 @@ def cache8_read(cache: Cache8, start, length, n: int = 0, k=None, v=None, stream
 
 
 def _rows8(q, out, cache: Cache8, what: str):
-    for t, name in ((q, "q"), (out, "out")):
-        _need(t, torch.bfloat16, name)
+    bf = torch.bfloat16
+    if not (q.dtype is out.dtype is bf and q.is_cuda and out.is_cuda):
+        _need(q, bf, "q")
+        _need(out, bf, "out")
     if q.dim() != 3 or not q.is_contiguous() or not out.is_contiguous() or out.shape != q.shape \
             or q.shape[2] != cache.head_dim:
         raise ValueError(f"{what}: q and out must be contiguous [rows][Hq][D] of one shape, D the cache's")

@@ -130,7 +130,7 @@ def test_attention_refusals(lib):
     c = _cache(lib)
     assert _decode8(lib, c, n=None) == lib.ERR_INVALID_ARG and _decode8(lib, c, b=-1) == lib.ERR_INVALID_ARG
     assert _decode8(lib, c, b=0) == lib.OK
-    assert _decode8(lib, _cache(lib, dtype=lib.E4M3), scale=1e38) == lib.ERR_UNSUPPORTED
+    assert _decode8(lib, _cache(lib, seq_stride=0)) == lib.ERR_INVALID_ARG
     for name in ("s", "n", "o"):
         assert _prefill8(lib, c, **{name: None}) == lib.ERR_INVALID_ARG
     assert _prefill8(lib, c, kv=513) == lib.ERR_INVALID_ARG          # more than the cache's slots
