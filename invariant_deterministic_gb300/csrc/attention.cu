@@ -398,13 +398,9 @@ struct PrefillTcArgs {
   int max_len, max_q_len, total_rows;
   float c2;            // fp32(scale * log2 e) > 0
   int* status;
-  Window win;
 };
 
-// WIN: a tile walks the splits that hold a key one of its rows sees (`it` counts
-// them, split_of(it) names them); a pair's hidden keys get weight 0, and V rows
-// hidden from the whole tile are zeroed like those past its last key.
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                            const __grid_constant__ CUtensorMap tmV, const PrefillTcArgs a) {
@@ -452,10 +448,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int row0 = off + first;           // q / out row of the tile's first row
   const int len0 = st0 + first + 1;       // keys the first row sees (row r: len0 + r)
   const int len_last = len0 + nrows - 1;
-  const int tile_lo = WIN ? window_lo(a.win, len0) : 0;  // the first row's first window key
-  const SplitList list = visible_splits(a.win, tile_lo, len_last);
-  const int ns = WIN ? list.count : (len_last + kSplit - 1) / kSplit;
-  auto split_of = [&](int it) { return WIN ? list.split(it) : it; };
+  const int ns = (len_last + kSplit - 1) / kSplit;
 
   if (t == 0) {
     for (int i = 0; i < kTcBars; ++i) {
@@ -486,13 +479,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto load_k = [&](int s) {
       mbar_arrive_expect_tx(k_full, KV_BYTES);
       for (int ds = 0; ds < DS; ++ds)
-        tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, g, split_of(s) * kSplit, b, k_full, pol);
+        tma_load_4d(smem_addr(k_s + ds * KV_SLICE), &tmK, 64 * ds, g, s * kSplit, b, k_full, pol);
       k_issued = s + 1;
     };
     auto load_v = [&](int s) {
       mbar_arrive_expect_tx(v_full, KV_BYTES);
       for (int ds = 0; ds < DS; ++ds)
-        tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, g, split_of(s) * kSplit, b, v_full, pol);
+        tma_load_4d(smem_addr(v_s + ds * KV_SLICE), &tmV, 64 * ds, g, s * kSplit, b, v_full, pol);
       v_issued = s + 1;
     };
     if (lane == 0) {
@@ -518,17 +511,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       stop = __shfl_sync(0xffffffffu, *abort_flag, 0) != 0;
       if (stop) break;
-      const int nmax = min(kSplit, len_last - split_of(s) * kSplit);
+      const int nmax = min(kSplit, len_last - s * kSplit);
       for (int idx = lane; idx < (kSplit - nmax) * DS * 8; idx += 32) {
         const int key = nmax + idx / (DS * 8), rest = idx % (DS * 8);
         *reinterpret_cast<uint4*>(v_s + (rest / 8) * KV_SLICE + key * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
-      }
-      if (WIN) {
-        const int h0 = max(a.win.sinks - split_of(s) * kSplit, 0), h1 = min(tile_lo - split_of(s) * kSplit, nmax);
-        for (int idx = lane; idx < (h1 - h0) * DS * 8; idx += 32) {
-          const int key = h0 + idx / (DS * 8), rest = idx % (DS * 8);
-          *reinterpret_cast<uint4*>(v_s + (rest / 8) * KV_SLICE + key * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -667,14 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int jj = 0; jj < 32; jj += 2) {
             float2 o = make_float2(o_acc[32 * c + jj], o_acc[32 * c + jj + 1]);
             const float2 t = __fmul2_rn(make_float2(__uint_as_float(v[jj]), __uint_as_float(v[jj + 1])), fc2);
-            if (WIN) {
-              // single adds: a packed add behind packed products is compiled to a
-              // fused one, which rounds once where the merge kernel rounds twice
-              const float2 u = unit ? o : __fmul2_rn(o, fa2);
-              o = make_float2(__fadd_rn(u.x, t.x), __fadd_rn(u.y, t.y));
-            } else {
-              o = __fadd2_rn(unit ? o : __fmul2_rn(o, fa2), t);
-            }
+            o = __fadd2_rn(unit ? o : __fmul2_rn(o, fa2), t);
             o_acc[32 * c + jj] = o.x;
             o_acc[32 * c + jj + 1] = o.y;
           }
@@ -688,14 +667,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool in_prev = false;
     for (int s = 0; s < ns; ++s) {
       const uint32_t ph = s & 1;
-      const int k0 = split_of(s) * kSplit;
-      const int cnt = min(kSplit, len - k0);
-      // the pair's first window key and the sinks' end within the split
-      const int lo = WIN ? window_lo(a.win, len) - k0 : 0, sink = WIN ? a.win.sinks - k0 : 0;
+      const int cnt = min(kSplit, len - s * kSplit);
       // every pair of the tile sees the whole split: no key is masked
-      const bool whole = len0 - k0 >= kSplit &&
-                         (!WIN || window_lo(a.win, len_last) <= k0 || a.win.sinks >= k0 + kSplit);
-      auto sees = [&](int key) { return key < cnt && (!WIN || key >= lo || key < sink); };
+      const bool whole = len0 - s * kSplit >= kSplit;
       check(mbar_wait_bounded(s_full(half), ph, status, DEV_TIMEOUT_ATTN));
       tc_fence_after();
       // the raw maximum (exact in any order): this thread's 128 keys, four
@@ -717,7 +691,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int jj = 0; jj < 32; jj += 4) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (sees(32 * c + jj + e)) mx[e] = fmaxf(mx[e], __uint_as_float(v[jj + e]));
+              if (32 * c + jj + e < cnt) mx[e] = fmaxf(mx[e], __uint_as_float(v[jj + e]));
           }
         }
       }
@@ -752,7 +726,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               float x[2] = {ex2_approx(arg.x), ex2_approx(arg.y)};
               if (decltype(masked)::value) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) x[e] = sees(32 * c + jj + e) ? x[e] : 0.f;
+                for (int e = 0; e < 2; ++e) x[e] = 32 * c + jj + e < cnt ? x[e] : 0.f;
               }
               const __nv_bfloat162 h2 = __float22bfloat162_rn(make_float2(x[0], x[1]));
               const __nv_bfloat162 l2 = __float22bfloat162_rn(
@@ -795,7 +769,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (s > 0) fold(s - 1, m_prev, l_prev, in_prev);
       m_prev = m;
       l_prev = l;
-      in_prev = cnt > 0 && (!WIN || lo < kSplit || sink > 0);
+      in_prev = cnt > 0;
     }
     if (ok && ns > 0) fold(ns - 1, m_prev, l_prev, in_prev);
     if (ok && r < nrows) {
@@ -847,7 +821,7 @@ kinv_status launch(const AttnParams& p, dim3 split_grid, dim3 merge_grid, cudaSt
 
 // Prefill with the tcgen05 kernel: one block per (sequence, kv head, tile of
 // 128 (row, head) pairs).
-template <int D, bool WIN>
+template <int D>
 kinv_status launch_prefill_tc(const void* q, const void* k_cache, const void* v_cache, int64_t seq_stride,
                               int64_t tok_stride, PrefillTcArgs a, int B, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
@@ -866,9 +840,9 @@ kinv_status launch_prefill_tc(const void* q, const void* k_cache, const void* v_
     return KINV_ERR_UNSUPPORTED;
   const size_t smem = prefill_tc_smem_bytes<D>();
   if (smem > static_cast<size_t>(max_smem_optin())) return KINV_ERR_UNSUPPORTED;
-  const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(attn_prefill_tc_kernel<D, WIN>), smem);
+  const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(attn_prefill_tc_kernel<D>), smem);
   if (attr != KINV_OK) return attr;
-  return launch_kernel(attn_prefill_tc_kernel<D, WIN>, dim3(a.tiles_per_seq, a.Hkv, B), dim3(kTcThreads), smem, stream, 1,
+  return launch_kernel(attn_prefill_tc_kernel<D>, dim3(a.tiles_per_seq, a.Hkv, B), dim3(kTcThreads), smem, stream, 1,
                        mq, mk, mv, a);
 }
 
@@ -1002,12 +976,14 @@ extern "C" size_t kinv_attn_prefill_workspace(int total_rows, int Hq, int D, int
   return 0;
 }
 
-namespace kinv {
-namespace {
-kinv_status prefill(const void* q, const void* k_cache, const void* v_cache, int64_t seq_stride, int64_t tok_stride,
-                    const int32_t* q_start, const int32_t* q_len, const int32_t* q_offset, void* out, int B,
-                    int total_rows, int max_q_len, int max_kv, int Hq, int Hkv, int D, int split_len, float scale,
-                    void* workspace, kinv_stream stream, const Window& win, bool listed) {
+extern "C" kinv_status kinv_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
+                                         int64_t seq_stride, int64_t tok_stride,
+                                         const int32_t* q_start, const int32_t* q_len,
+                                         const int32_t* q_offset, void* out, int B,
+                                         int total_rows, int max_q_len, int max_kv, int Hq,
+                                         int Hkv, int D, int split_len, float scale,
+                                         void* workspace, size_t ws_bytes, kinv_stream stream) {
+  (void)ws_bytes;
   if (B < 0 || total_rows < 0 || max_q_len < 0 || max_kv < 0) return KINV_ERR_INVALID_ARG;
   if (B == 0 || total_rows == 0 || max_q_len == 0) return KINV_OK;
   if (!q_start || !q_len || !q_offset || max_kv <= 0) return KINV_ERR_INVALID_ARG;
@@ -1033,38 +1009,8 @@ kinv_status prefill(const void* q, const void* k_cache, const void* v_cache, int
   a.status = device_status_word();
   if (a.tiles_per_seq > 65535 || B > 65535) return KINV_ERR_UNSUPPORTED;
   if (B > 1 && seq_stride <= 0) return KINV_ERR_INVALID_ARG;
-  a.win = win;
-  if (listed)
-    return D == 128 ? launch_prefill_tc<128, true>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream)
-                    : launch_prefill_tc<64, true>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream);
-  return D == 128 ? launch_prefill_tc<128, false>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream)
-                  : launch_prefill_tc<64, false>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream);
-}
-}  // namespace
-}  // namespace kinv
-
-extern "C" kinv_status kinv_attn_prefill(const void* q, const void* k_cache, const void* v_cache,
-                                         int64_t seq_stride, int64_t tok_stride,
-                                         const int32_t* q_start, const int32_t* q_len,
-                                         const int32_t* q_offset, void* out, int B,
-                                         int total_rows, int max_q_len, int max_kv, int Hq,
-                                         int Hkv, int D, int split_len, float scale,
-                                         void* workspace, size_t ws_bytes, kinv_stream stream) {
-  (void)ws_bytes;
-  return prefill(q, k_cache, v_cache, seq_stride, tok_stride, q_start, q_len, q_offset, out, B, total_rows, max_q_len,
-                 max_kv, Hq, Hkv, D, split_len, scale, workspace, stream, Window{0, 0}, false);
-}
-
-extern "C" kinv_status kinv_attn_prefill_window(const void* q, const void* k_cache, const void* v_cache,
-                                                int64_t seq_stride, int64_t tok_stride, const int32_t* q_start,
-                                                const int32_t* q_len, const int32_t* q_offset, void* out, int B,
-                                                int total_rows, int max_q_len, int max_kv, int Hq, int Hkv, int D,
-                                                int split_len, int window, int sinks, float scale, void* workspace,
-                                                size_t ws_bytes, kinv_stream stream) {
-  (void)ws_bytes;
-  if (window < 0 || sinks < 0) return KINV_ERR_INVALID_ARG;
-  return prefill(q, k_cache, v_cache, seq_stride, tok_stride, q_start, q_len, q_offset, out, B, total_rows, max_q_len,
-                 max_kv, Hq, Hkv, D, split_len, scale, workspace, stream, Window{window, sinks}, true);
+  return D == 128 ? launch_prefill_tc<128>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream)
+                  : launch_prefill_tc<64>(q, k_cache, v_cache, seq_stride, tok_stride, a, B, stream);
 }
 
 // ---------------------------------------------------------------------------

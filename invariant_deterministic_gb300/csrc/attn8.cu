@@ -527,8 +527,9 @@ extern "C" kinv_status kinv_attn_prefill8(const void* q, const kinv_cache8* cach
   if (B == 0 || total_rows == 0 || max_q_len == 0) return KINV_OK;
   if (!q || !out || !q_start || !q_len || !q_offset || !workspace || max_kv <= 0) return KINV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KINV_ERR_ALIGNMENT;
-  const int tile_rows = 128 / (Hq / Hkv);  // of the prefill kernel
-  if (B > 65535 || (static_cast<int64_t>(max_q_len) + tile_rows - 1) / tile_rows > 65535) return KINV_ERR_UNSUPPORTED;
+  const int tile_rows = 128 / (Hq / Hkv);  // of the prefill kernel, which counts its tiles in an int
+  if (B > 65535 || (static_cast<int64_t>(max_q_len) + tile_rows - 1) / tile_rows * Hkv * B > 0x7F000000)
+    return KINV_ERR_UNSUPPORTED;
   const size_t need = kinv_attn_prefill8_workspace(B, total_rows, Hq, Hkv, D, max_kv, split_len);
   if (ws_bytes < need) return KINV_ERR_WORKSPACE;
   r.k = static_cast<__nv_bfloat16*>(workspace);

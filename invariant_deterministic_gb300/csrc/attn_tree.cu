@@ -627,18 +627,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
-// x - h, exactly: the mixed-precision fma takes the bf16 halves as they are (the
-// softmax's arithmetic alone, 256 keys by 128 pairs: 1,545 cycles an SM; 1,856 with
-// the halves widened first).
-__device__ __forceinline__ float2 less_bf16(float2 x, __nv_bfloat162 h) {
-  float2 r;
-  asm("{\n\t.reg .b16 a, b, m;\n\tmov.b32 {a, b}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
-      "fma.rn.f32.bf16 %0, a, m, %3;\n\tfma.rn.f32.bf16 %1, b, m, %4;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "r"(*reinterpret_cast<const uint32_t*>(&h)), "f"(x.x), "f"(x.y));
-  return r;
-}
-
 // An asynchronous copy of `bytes` (a multiple of 16) from shared to global
 // memory, in this thread's current bulk group.
 __device__ __forceinline__ void bulk_store(float* dst, uint32_t src, uint32_t bytes) {

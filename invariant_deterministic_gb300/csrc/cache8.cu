@@ -202,6 +202,19 @@ __global__ void __launch_bounds__(kWriteThreads) cache8_write_kernel(const Write
   }
 }
 
+// The last table a thread asked for: 64 powers are 4 us of a call.
+const RopeFreqs& rope_freqs(float base, int D) {
+  static thread_local RopeFreqs freqs;
+  static thread_local float of_base = 0.f;
+  static thread_local int of_dim = 0;
+  if (base != of_base || D != of_dim) {
+    for (int i = 0; i < D / 2; ++i) freqs.inv_freq[i] = std::pow(static_cast<double>(base), -2.0 * i / D);
+    of_base = base;
+    of_dim = D;
+  }
+  return freqs;
+}
+
 constexpr int kMaxKvHeads = 1024;  // the write kernel's exponents: 32 bytes a head in shared memory
 
 }  // namespace
@@ -221,8 +234,7 @@ extern "C" kinv_status kinv_rope_append8(const void* qkv, int64_t ld_qkv, void* 
   if (rows == 0) return KINV_OK;
   if (!qkv || !q_out || !seq || !pos || ld_qkv < static_cast<int64_t>(Hq + 2 * Hkv) * D) return KINV_ERR_INVALID_ARG;
   if (!aligned16(qkv) || !aligned16(q_out) || ld_qkv % 8) return KINV_ERR_ALIGNMENT;
-  RopeFreqs freqs;
-  for (int i = 0; i < D / 2; ++i) freqs.inv_freq[i] = std::pow(static_cast<double>(rope_base), -2.0 * i / D);
+  const RopeFreqs& freqs = rope_freqs(rope_base, D);
   const int heads = Hq + 2 * Hkv;
   const int hpb = rows >= 512 ? heads : 8;  // as kinv_rope_append
   const dim3 grid(rows, (heads + hpb - 1) / hpb);

@@ -37,7 +37,8 @@ struct ReadParams {
 };
 
 // Keys (z = 0) or values (z = 1) of `tokens` tokens of one sequence, D / 16
-// lanes per (token, head): 16 codes in, 32 bytes out a lane.
+// lanes per (token, head): 16 codes in, 32 bytes out a lane, four vectors
+// ahead.
 template <int D, bool I8>
 __global__ void __launch_bounds__(kReadThreads) cache8_read_kernel(const ReadParams p) {
   constexpr int L = D / 16;
@@ -68,14 +69,33 @@ __global__ void __launch_bounds__(kReadThreads) cache8_read_kernel(const ReadPar
   const int8_t* exps = (values ? p.cache.ve : p.cache.ke) + b * p.cache.eseq_stride + start + i0;
   __nv_bfloat16* dst = (values ? p.v : p.k) + b * p.seq_stride;
   const int sub = threadIdx.x % L;
-  for (int vec = threadIdx.x / L; vec < n * p.Hkv; vec += PER) {
-    const int i = vec / p.Hkv, g = vec % p.Hkv;
-    const uint4 c = *reinterpret_cast<const uint4*>(src + (start + i0 + i) * p.cache.tok_stride + g * D + sub * 16);
-    const float f = exponent_factor(exps[g * p.cache.ehead_stride + i]);
-    const uint2 x0 = decode4<I8>(c.x, f), x1 = decode4<I8>(c.y, f), x2 = decode4<I8>(c.z, f), x3 = decode4<I8>(c.w, f);
-    uint4* to = reinterpret_cast<uint4*>(dst + (i0 + i) * p.tok_stride + g * D + sub * 16);
-    to[0] = make_uint4(x0.x, x0.y, x1.x, x1.y);
-    to[1] = make_uint4(x2.x, x2.y, x3.x, x3.y);
+  src += (start + i0) * p.cache.tok_stride + sub * 16;
+  dst += i0 * p.tok_stride + sub * 16;
+  const int total = n * p.Hkv;
+  constexpr int AHEAD = 4;
+  for (int at = threadIdx.x / L; at < total; at += PER * AHEAD) {
+    uint4 c[AHEAD];
+    int e[AHEAD], tok[AHEAD], head[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int vec = at + j * PER;
+      tok[j] = vec < total ? vec / p.Hkv : -1;
+      head[j] = vec - tok[j] * p.Hkv;
+      if (tok[j] >= 0) {
+        c[j] = __ldcs(reinterpret_cast<const uint4*>(src + tok[j] * p.cache.tok_stride + head[j] * D));
+        e[j] = exps[head[j] * p.cache.ehead_stride + tok[j]];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (tok[j] < 0) continue;
+      const float f = exponent_factor(e[j]);
+      const uint2 x0 = decode4<I8>(c[j].x, f), x1 = decode4<I8>(c[j].y, f), x2 = decode4<I8>(c[j].z, f),
+                  x3 = decode4<I8>(c[j].w, f);
+      uint4* to = reinterpret_cast<uint4*>(dst + tok[j] * p.tok_stride + head[j] * D);
+      to[0] = make_uint4(x0.x, x0.y, x1.x, x1.y);
+      to[1] = make_uint4(x2.x, x2.y, x3.x, x3.y);
+    }
   }
 }
 

@@ -347,52 +347,61 @@ def attn_decode_workspace(batch: int, n_q: int, head_dim: int, max_len: int,
     return int(lib().kinv_attn_decode_workspace(batch, n_q, head_dim, max_len, split_len))
 
 
-def _window_inputs(q, k_cache, v_cache, out, batch: int, what: str):
-    """Checks of the windowed calls: (slots, Hkv, sequence and slot strides)."""
+def _rows_of(q, out, what: str) -> None:
+    """q and out [rows][Hq][D], bf16 and contiguous."""
     bf = torch.bfloat16
-    if not (q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is bf and q.is_cuda and out.is_cuda
-            and k_cache.is_cuda and v_cache.is_cuda):
-        for t, name in ((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (out, "out")):
-            _need(t, bf, name)
-    shape, stride = k_cache.shape, k_cache.stride()
-    if v_cache.shape != shape or v_cache.stride() != stride or len(shape) != 4:
-        raise ValueError(f"{what}: the caches must be [B][slots][Hkv][D] and share shape and strides")
-    if stride[3] != 1 or (stride[2] != shape[3] and shape[2] > 1) or shape[0] < batch:
-        raise ValueError(f"{what}: a slot's heads must be contiguous, and the caches hold every sequence")
-    if not q.is_contiguous() or not out.is_contiguous() or out.shape != q.shape or q.shape[2] != shape[3]:
+    if not (q.dtype is bf and q.is_cuda and q.is_contiguous() and q.dim() == 3
+            and (out is None or (out.dtype is bf and out.is_cuda and out.is_contiguous() and out.shape == q.shape))):
+        _need(q, bf, "q")
+        if out is not None:
+            _need(out, bf, "out")
         raise ValueError(f"{what}: q and out must be contiguous [rows][Hq][D] of one shape")
-    return shape[1], shape[2], stride[0], stride[1]
+
+
+def _window_caches(k_cache, v_cache, batch: int, head_dim: int, what: str):
+    """Checks of the windowed calls' caches: (shape, strides)."""
+    bf = torch.bfloat16
+    if not (k_cache.dtype is v_cache.dtype is bf and k_cache.is_cuda and v_cache.is_cuda):
+        _need(k_cache, bf, "k_cache")
+        _need(v_cache, bf, "v_cache")
+    shape, stride = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != stride:
+        raise ValueError(f"{what}: the caches must be [B][slots][Hkv][D] and share shape and strides")
+    if stride[3] != 1 or (stride[2] != head_dim and shape[2] > 1) or shape[3] != head_dim or shape[0] < batch:
+        raise ValueError(f"{what}: a slot's heads must be contiguous and of q's size, and the caches hold every sequence")
+    return shape, stride
+
+
+def _vector(t, n: int, name: str) -> None:
+    """An int32 vector on the device with an entry for each of n."""
+    if t.dtype is not torch.int32 or not t.is_cuda:
+        _need(t, torch.int32, name)
+    if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous vector of at least {n} entries")
 
 
 def _workspace(side, workspace, need: int, device):
-    if workspace is None:
-        return _scratch(side, torch.empty, max(need, 16), dtype=torch.uint8, device=device)
-    if not workspace.is_cuda or not workspace.is_contiguous():
+    """Scratch for a call that was given none, or none that it can use."""
+    if workspace is not None:
         raise ValueError("workspace: expected a contiguous CUDA tensor")
-    return workspace
-
-
-def _vectors(what: str, n: int, **tensors) -> None:
-    i32 = torch.int32
-    for name, t in tensors.items():
-        if t.dtype is not i32 or not t.is_cuda:
-            _need(t, i32, name)
-        if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be a contiguous vector of at least {n} entries")
+    return _scratch(side, torch.empty, max(need, 16), dtype=torch.uint8, device=device)
 
 
 def _attn_decode_window(q, k_cache, v_cache, kv_len, out, workspace, split_len, window, sinks, scale, stream):
-    side = _side(stream)
+    _rows_of(q, out, "attn_decode")
+    bsz, hq, d = q.shape
+    shape, stride = _window_caches(k_cache, v_cache, bsz, d, "attn_decode")
+    _vector(kv_len, bsz, "kv_len")
+    lmax = shape[1]
+    side = None if stream is None else _side(stream)
     if out is None:
         out = _empty_like(side)(q)
-    bsz, hq, d = q.shape
-    lmax, hkv, s0, s1 = _window_inputs(q, k_cache, v_cache, out, bsz, "attn_decode")
-    _vectors("attn_decode", bsz, kv_len=kv_len)
-    workspace = _workspace(side, workspace, attn_decode_workspace(bsz, hq, d, lmax, split_len, window, sinks), q.device)
+    if workspace is None or not (workspace.is_cuda and workspace.is_contiguous()):
+        workspace = _workspace(side, workspace, attn_decode_workspace(bsz, hq, d, lmax, split_len, window, sinks), q.device)
     if side is not None:
         _hold(side, q, k_cache, v_cache, kv_len, out, workspace)
-    _check(lib().kinv_attn_decode_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), s0, s1,
-                                         kv_len.data_ptr(), out.data_ptr(), bsz, hq, hkv, d, lmax, split_len, window,
+    _check(lib().kinv_attn_decode_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), stride[0], stride[1],
+                                         kv_len.data_ptr(), out.data_ptr(), bsz, hq, shape[2], d, lmax, split_len, window,
                                          sinks, scale, workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(), _stream(stream)),
            "kinv_attn_decode_window")
@@ -457,20 +466,23 @@ def attn_prefill_workspace(total_rows: int, n_q: int, head_dim: int, max_kv: int
 
 def _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len, max_kv, out, split_len, window,
                          sinks, scale, stream):
-    side = _side(stream)
-    if out is None:
-        out = _empty_like(side)(q)
+    _rows_of(q, out, "attn_prefill")
     rows, hq, d = q.shape
     bsz = q_start.shape[0]
-    slots, hkv, s0, s1 = _window_inputs(q, k_cache, v_cache, out, bsz, "attn_prefill")
-    if max_kv > slots:
+    shape, stride = _window_caches(k_cache, v_cache, bsz, d, "attn_prefill")
+    if max_kv > shape[1]:
         raise ValueError("attn_prefill: the caches are smaller than max_kv")
-    _vectors("attn_prefill", bsz, q_start=q_start, q_len=q_len, q_offset=q_offset)
+    _vector(q_start, bsz, "q_start")
+    _vector(q_len, bsz, "q_len")
+    _vector(q_offset, bsz, "q_offset")
+    side = None if stream is None else _side(stream)
+    if out is None:
+        out = _empty_like(side)(q)
     if side is not None:
         _hold(side, q, k_cache, v_cache, q_start, q_len, q_offset, out)
-    _check(lib().kinv_attn_prefill_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), s0, s1,
+    _check(lib().kinv_attn_prefill_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), stride[0], stride[1],
                                           q_start.data_ptr(), q_len.data_ptr(), q_offset.data_ptr(), out.data_ptr(),
-                                          bsz, rows, max_q_len, max_kv, hq, hkv, d, split_len, window, sinks, scale,
+                                          bsz, rows, max_q_len, max_kv, hq, shape[2], d, split_len, window, sinks, scale,
                                           None, 0, _stream(stream)), "kinv_attn_prefill_window")
     return out
 
@@ -558,25 +570,25 @@ class Cache8:
 def rope_append8(qkv, q_out, cache: Cache8, seq, pos, n_q, n_kv, head_dim, rope_base, q_norm=None, k_norm=None,
                  eps=1e-6, stream=None):
     """rope_append with the keys and values of the rows quantised into ``cache`` at
-    [seq][pos]; q_out [rows][Hq][D] has rope_append's bits.  A row outside the cache
-    is left out (its q_out too) and recorded in the device status."""
+    [seq][pos]; q_out [rows][Hq][D].  A row outside the cache is left out (its q_out
+    too) and recorded in the device status; no two rows may name one place."""
     bf = torch.bfloat16
     if not (qkv.dtype is q_out.dtype is bf and qkv.is_cuda and q_out.is_cuda):
         _need(qkv, bf, "qkv")
         _need(q_out, bf, "q_out")
     (rows, width), (ld, step) = qkv.shape, qkv.stride()
-    if (step != 1 and width > 1) or width != (n_q + 2 * n_kv) * head_dim or not q_out.is_contiguous() \
-            or q_out.numel() < rows * n_q * head_dim or cache.n_kv != n_kv or cache.head_dim != head_dim:
+    if (step != 1 or width != (n_q + 2 * n_kv) * head_dim or not q_out.is_contiguous()
+            or q_out.numel() < rows * n_q * head_dim or cache.n_kv != n_kv or cache.head_dim != head_dim):
         raise ValueError("rope_append8: shapes or layouts do not match")
-    _vectors("rope_append8", rows, seq=seq, pos=pos)
+    _vector(seq, rows, "seq")
+    _vector(pos, rows, "pos")
     for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if t is not None and not (t.dtype is bf and t.is_cuda and t.is_contiguous() and t.numel() >= head_dim):
             _need(t, bf, name)
             raise ValueError(f"rope_append8: {name} must hold a contiguous gain for each of a head's values")
-    side = _side(stream)
-    if side is not None:
+    if stream is not None and (side := _side(stream)) is not None:
         _hold(side, qkv, q_out, seq, pos, q_norm, k_norm, *cache.tensors)
-    _check(lib().kinv_rope_append8(qkv.data_ptr(), max(ld, width) if rows <= 1 else ld, q_out.data_ptr(), cache.ptr,
+    _check(lib().kinv_rope_append8(qkv.data_ptr(), ld if rows > 1 else max(ld, width), q_out.data_ptr(), cache.ptr,
                                    seq.data_ptr(), pos.data_ptr(), _ptr(q_norm), _ptr(k_norm), eps, rows, n_q, n_kv,
                                    head_dim, rope_base, _stream(stream)), "kinv_rope_append8")
     return q_out
@@ -591,10 +603,10 @@ def _tokens(k, v, cache: Cache8, what: str):
     shape, stride = k.shape, k.stride()
     if len(shape) != 4 or v.shape != shape or v.stride() != stride:
         raise ValueError(f"{what}: k and v must be [B][n][Hkv][D] and share shape and strides")
-    if tuple(shape[2:]) != (cache.n_kv, cache.head_dim) or shape[0] > cache.B or stride[3] != 1 \
-            or (stride[2] != shape[3] and shape[2] > 1):
+    bsz, n, hkv, d = shape
+    if hkv != cache.n_kv or d != cache.head_dim or bsz > cache.B or stride[3] != 1 or (stride[2] != d and hkv > 1):
         raise ValueError(f"{what}: k and v must match the cache's heads and sequences, a token's heads contiguous")
-    return shape[0], shape[1], stride[0], stride[1] if shape[1] > 1 else shape[2] * shape[3]
+    return bsz, n, stride[0], stride[1] if n > 1 else hkv * d
 
 
 def cache8_write(cache: Cache8, k, v, start, length, stream=None) -> None:
@@ -602,9 +614,9 @@ def cache8_write(cache: Cache8, k, v, start, length, stream=None) -> None:
     to slot start[b] + i (int32 [B], device).  A sequence that does not fit is left
     out and recorded in the device status."""
     bsz, n, s0, s1 = _tokens(k, v, cache, "cache8_write")
-    _vectors("cache8_write", bsz, start=start, length=length)
-    side = _side(stream)
-    if side is not None:
+    _vector(start, bsz, "start")
+    _vector(length, bsz, "length")
+    if stream is not None and (side := _side(stream)) is not None:
         _hold(side, k, v, start, length, *cache.tensors)
     _check(lib().kinv_cache8_write(k.data_ptr(), v.data_ptr(), s0, s1, cache.ptr, start.data_ptr(), length.data_ptr(),
                                    bsz, n, cache.n_kv, cache.head_dim, _stream(stream)), "kinv_cache8_write")
@@ -615,29 +627,26 @@ def cache8_read(cache: Cache8, start, length, n: int = 0, k=None, v=None, stream
     start[b] + i (n bounds length).  Tokens from length[b] on, and those of a
     sequence left out, keep what the given k and v held; where they are allocated
     here they hold anything."""
-    side = _side(stream)
-    if (k is None) != (v is None):
+    side = None if stream is None else _side(stream)
+    if k is None and v is None:
+        hkv, d = cache.n_kv, cache.head_dim
+        bsz, s1 = start.shape[0], hkv * d
+        s0 = n * s1
+        if bsz > cache.B:
+            raise ValueError("cache8_read: more sequences than the cache's")
+        k = _empty(side)((bsz, n, hkv, d), dtype=torch.bfloat16, device=cache.device)
+        v = _empty_like(side)(k)
+    elif k is None or v is None:
         raise ValueError("cache8_read: k and v are given together")
-    if k is None:
-        shape = (start.shape[0], n, cache.n_kv, cache.head_dim)
-        k, v = (_empty(side)(*shape, dtype=torch.bfloat16, device=cache.device) for _ in range(2))
-    bsz, n, s0, s1 = _tokens(k, v, cache, "cache8_read")
-    _vectors("cache8_read", bsz, start=start, length=length)
+    else:
+        bsz, n, s0, s1 = _tokens(k, v, cache, "cache8_read")
+    _vector(start, bsz, "start")
+    _vector(length, bsz, "length")
     if side is not None:
         _hold(side, k, v, start, length, *cache.tensors)
     _check(lib().kinv_cache8_read(cache.ptr, start.data_ptr(), length.data_ptr(), k.data_ptr(), v.data_ptr(), s0, s1,
                                   bsz, n, cache.n_kv, cache.head_dim, _stream(stream)), "kinv_cache8_read")
     return k, v
-
-
-def _rows8(q, out, cache: Cache8, what: str):
-    bf = torch.bfloat16
-    if not (q.dtype is out.dtype is bf and q.is_cuda and out.is_cuda):
-        _need(q, bf, "q")
-        _need(out, bf, "out")
-    if q.dim() != 3 or not q.is_contiguous() or not out.is_contiguous() or out.shape != q.shape \
-            or q.shape[2] != cache.head_dim:
-        raise ValueError(f"{what}: q and out must be contiguous [rows][Hq][D] of one shape, D the cache's")
 
 
 def attn_decode8_workspace(batch: int, n_q: int, head_dim: int, slots: int, window: int = 0, sinks: int = 0,
@@ -650,14 +659,17 @@ def attn_decode8(q, cache: Cache8, kv_len, out=None, workspace=None, window: int
     """attn_decode over an 8-bit cache: q [B][Hq][D], kv_len int32 [B].  With a window
     a row sees its last ``window`` keys and the first ``sinks`` of its sequence.  A row
     has the bits of attn_decode on the cache read back."""
-    side = _side(stream)
+    _rows_of(q, out, "attn_decode8")
+    bsz, hq, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError("attn_decode8: q's heads are not of the cache's size")
+    _vector(kv_len, bsz, "kv_len")
+    side = None if stream is None else _side(stream)
     if out is None:
         out = _empty_like(side)(q)
-    _rows8(q, out, cache, "attn_decode8")
-    bsz, hq, d = q.shape
-    _vectors("attn_decode8", bsz, kv_len=kv_len)
-    workspace = _workspace(side, workspace, attn_decode8_workspace(bsz, hq, d, cache.slots, window, sinks, split_len)
-                           if workspace is None else 0, q.device)
+    if workspace is None or not (workspace.is_cuda and workspace.is_contiguous()):
+        workspace = _workspace(side, workspace, attn_decode8_workspace(bsz, hq, d, cache.slots, window, sinks, split_len),
+                               q.device)
     if side is not None:
         _hold(side, q, out, kv_len, workspace, *cache.tensors)
     _check(lib().kinv_attn_decode8(q.data_ptr(), cache.ptr, kv_len.data_ptr(), out.data_ptr(), bsz, hq, cache.n_kv, d,
@@ -677,15 +689,20 @@ def attn_prefill8(q, cache: Cache8, q_start, q_len, q_offset, max_q_len: int, ma
     """attn_prefill over an 8-bit cache, which already holds the rows' keys and
     values: q [rows][Hq][D]; per-sequence int32 q_start, q_len, q_offset [B].  Rows of
     no sequence are not written."""
-    side = _side(stream)
-    if out is None:
-        out = _empty_like(side)(q)
-    _rows8(q, out, cache, "attn_prefill8")
+    _rows_of(q, out, "attn_prefill8")
     rows, hq, d = q.shape
     bsz = q_start.shape[0]
-    _vectors("attn_prefill8", bsz, q_start=q_start, q_len=q_len, q_offset=q_offset)
-    workspace = _workspace(side, workspace, attn_prefill8_workspace(bsz, rows, hq, cache.n_kv, d, max_kv, split_len)
-                           if workspace is None else 0, q.device)
+    if d != cache.head_dim:
+        raise ValueError("attn_prefill8: q's heads are not of the cache's size")
+    _vector(q_start, bsz, "q_start")
+    _vector(q_len, bsz, "q_len")
+    _vector(q_offset, bsz, "q_offset")
+    side = None if stream is None else _side(stream)
+    if out is None:
+        out = _empty_like(side)(q)
+    if workspace is None or not (workspace.is_cuda and workspace.is_contiguous()):
+        workspace = _workspace(side, workspace,
+                               attn_prefill8_workspace(bsz, rows, hq, cache.n_kv, d, max_kv, split_len), q.device)
     if side is not None:
         _hold(side, q, out, q_start, q_len, q_offset, workspace, *cache.tensors)
     _check(lib().kinv_attn_prefill8(q.data_ptr(), cache.ptr, q_start.data_ptr(), q_len.data_ptr(), q_offset.data_ptr(),

@@ -136,7 +136,8 @@ def test_attention_refusals(lib):
     assert _prefill8(lib, c, kv=513) == lib.ERR_INVALID_ARG          # more than the cache's slots
     assert _prefill8(lib, c, rows=0) == lib.OK and _prefill8(lib, c, most=0) == lib.OK and _prefill8(lib, c, b=0) == lib.OK
     assert _prefill8(lib, c, rows=-1) == lib.ERR_INVALID_ARG and _prefill8(lib, c, most=-1) == lib.ERR_INVALID_ARG
-    assert _prefill8(lib, c, most=65536 * 64) == lib.ERR_UNSUPPORTED
+    wide = _cache(lib, tok_stride=512, seq_stride=512 * 512)
+    assert _prefill8(lib, wide, most=2**31 - 1, rows=2**31 - 1, hq=64, hkv=8, wsb=2**40) == lib.ERR_UNSUPPORTED  # the number of tiles
 
 
 def test_window_refusals(lib):
