@@ -62,6 +62,8 @@ class DraftDecoder:
             raise ValueError(f"max_nodes must lie in 1..{kinv.TREE_MAX_NODES}")
         if dec.B * max_nodes > dec.max_rows:
             raise ValueError("the decoder's max_chunk must hold max_batch * max_nodes rows")
+        if getattr(dec, "cache", "bf16") != "bf16" or getattr(dec.s, "window", 0):
+            raise ValueError("drafted decoding needs a bf16 cache and attention without a window")
         self.dec, self.max_nodes = dec, max_nodes
         rows = dec.B * max_nodes
         i32 = dict(dtype=torch.int32, device=dec.dev)

@@ -18,7 +18,9 @@ Layouts (all bf16 unless noted):
   w_gu [2F][d] (gate rows then up rows; the decoder keeps a copy interleaved
   in blocks of 64 for the fused gate/up + SwiGLU GEMM), w_down [d][F], norm
   gains [d] / [D];
-  KV cache [layers][2][B][Lmax][Hkv][D] (k then v), token-major per sequence.
+  KV cache [layers][2][B][Lmax][Hkv][D] (k then v), token-major per sequence; or,
+  with cache="e4m3" or "int8", its 8-bit codes in that layout and their exponents
+  [layers][2][B][Hkv][Lmax] (kinv.Cache8).
 """
 from __future__ import annotations
 
@@ -43,6 +45,8 @@ class ModelShape:
     eps: float = 1e-6
     rope_base: float = 1e4
     qk_norm: bool = False
+    window: int = 0   # sliding window of every layer's attention (0: none) ...
+    sinks: int = 0    # ... beside which the first `sinks` tokens stay visible
 
     @property
     def qkv_dim(self) -> int:
@@ -94,10 +98,18 @@ SCORE_ROWS = 256
 class Decoder:
     """Owns weights, the KV cache and every activation buffer for up to
     ``max_batch`` sequences of up to ``max_len`` tokens (and prefill chunks of
-    up to ``max_chunk`` rows)."""
+    up to ``max_chunk`` rows).  ``cache``: "bf16", or "e4m3" or "int8" for keys and
+    values in 8 bits (half the memory, and half the bytes that a step reads; the
+    tokens are those of the rounded keys and values, the same for every batch and
+    chunking)."""
 
     def __init__(self, shape: ModelShape, weights: dict, max_batch: int, max_len: int,
-                 max_chunk: int = 0, device="cuda"):
+                 max_chunk: int = 0, device="cuda", cache: str = "bf16"):
+        if cache != "bf16" and cache not in kinv.CACHE8_DTYPES:
+            raise ValueError(f"cache: expected 'bf16' or one of {sorted(kinv.CACHE8_DTYPES)}, got {cache!r}")
+        if shape.window < 0 or shape.sinks < 0:
+            raise ValueError("window and sinks must not be negative")
+        self.cache = cache
         self.s = shape
         self.w = weights
         self.B = max_batch
@@ -107,7 +119,13 @@ class Decoder:
         rows = max(max_batch, max_chunk)
         self.max_rows = rows
         bf = dict(dtype=torch.bfloat16, device=self.dev)
-        self.kv = torch.zeros(s.n_layers, 2, max_batch, max_len, s.n_kv, s.head_dim, **bf)
+        kv_shape = (s.n_layers, 2, max_batch, max_len, s.n_kv, s.head_dim)
+        if cache == "bf16":
+            self.kv = torch.zeros(kv_shape, **bf)
+        else:
+            self.kv = torch.zeros(kv_shape, dtype=torch.uint8, device=self.dev).view(kinv.CACHE8_DTYPES[cache])
+            self.kv_exp = torch.zeros(s.n_layers, 2, max_batch, s.n_kv, max_len, dtype=torch.int8, device=self.dev)
+            self.kv8 = [kinv.Cache8(*self.kv[li], *self.kv_exp[li]) for li in range(s.n_layers)]
         self.x = torch.zeros(rows, s.d_model, **bf)
         self.qkv = torch.zeros(rows, s.qkv_dim, **bf)
         self.q = torch.zeros(rows, s.n_q, s.head_dim, **bf)
@@ -122,9 +140,13 @@ class Decoder:
         self.act = torch.zeros(rows, s.ffn, **bf)
         # per-row sums of squares of the residual stream over 128-column tiles
         self.ss = torch.zeros(rows, s.d_model // 128, dtype=torch.float32, device=self.dev)
-        ws = kinv.attn_decode_workspace(max_batch, s.n_q, s.head_dim, max_len)
-        if max_chunk:
-            ws = max(ws, kinv.attn_prefill_workspace(max_chunk, s.n_q, s.head_dim, max_len))
+        if cache == "bf16":
+            ws = kinv.attn_decode_workspace(max_batch, s.n_q, s.head_dim, max_len, window=s.window, sinks=s.sinks)
+            if max_chunk:
+                ws = max(ws, kinv.attn_prefill_workspace(max_chunk, s.n_q, s.head_dim, max_len))
+        else:
+            ws = kinv.attn_decode8_workspace(max_batch, s.n_q, s.head_dim, max_len, s.window, s.sinks)
+            ws = max(ws, kinv.attn_prefill8_workspace(1, rows, s.n_q, s.n_kv, s.head_dim, max_len))
         self.ws = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.dev)
         i32 = dict(dtype=torch.int32, device=self.dev)
         # decode state: row b is sequence b at position pos[b]; attention sees pos[b] + 1 keys
@@ -184,7 +206,13 @@ class Decoder:
         kc, vc = self.kv[li, 0], self.kv[li, 1]
         qn = lw.get("q_norm") if s.qk_norm else None
         kn = lw.get("k_norm") if s.qk_norm else None
-        if tree is not None:
+        if self.cache != "bf16":
+            with self._t("gemm_qkv"):
+                kinv.gemm_fused(x, self.w_qkv_f[li], norm_in, out=self.qkv[:rows])
+            with self._t("rope_append"):
+                kinv.rope_append8(self.qkv[:rows], self.q[:rows], self.kv8[li], seq, pos, s.n_q, s.n_kv,
+                                  s.head_dim, s.rope_base, qn, kn, s.eps)
+        elif tree is not None:
             with self._t("gemm_qkv"):
                 kinv.gemm_fused(x, self.w_qkv_f[li], norm_in, out=self.qkv[:rows])
             with self._t("rope_append"):
@@ -216,10 +244,16 @@ class Decoder:
         """All layers for one new token of sequences 0..bsz-1 (rows = bsz);
         the token's hidden state must be in x; leaves the final residual
         pieces in x and delta."""
+        s = self.s
+
         def attention(li, rows, kc, vc):
             with self._t("attn_decode"):
-                kinv.attn_decode(self.q[:rows], kc[:rows], vc[:rows], self.kv_len[:rows],
-                                 out=self.attn[:rows], workspace=self.ws)
+                if self.cache != "bf16":
+                    kinv.attn_decode8(self.q[:rows], self.kv8[li], self.kv_len[:rows], out=self.attn[:rows],
+                                      workspace=self.ws, window=s.window, sinks=s.sinks)
+                else:
+                    kinv.attn_decode(self.q[:rows], kc[:rows], vc[:rows], self.kv_len[:rows], out=self.attn[:rows],
+                                     workspace=self.ws, window=s.window, sinks=s.sinks)
         with self._t("row_sumsq"):
             kinv.row_sumsq(self.x[:bsz], self.ss[:bsz])
         for li in range(self.s.n_layers):
@@ -250,7 +284,11 @@ class Decoder:
         their tokens' embeddings); their keys and values go into the cache slots
         behind each sequence's context, and x ends as the final residual stream.
         Every row has the bits of the decode step that would follow its path.
-        workspace: kinv.attn_tree_workspace(tree, ...) bytes, the caller's."""
+        workspace: kinv.attn_tree_workspace(tree, ...) bytes, the caller's.
+        Whole attention over a bf16 cache only."""
+        if self.cache != "bf16" or self.s.window:
+            raise ValueError("drafted trees need a bf16 cache and attention without a window")
+
         def attention(li, n, kc, vc):
             with self._t("attn_tree"):
                 kinv.attn_tree(self.q[:n], kc, vc, tree, out=self.attn[:n], workspace=workspace)
@@ -306,11 +344,17 @@ class Decoder:
         q_len = torch.tensor([rows], **i32)
         q_off = torch.zeros(1, **i32)
 
+        s = self.s
+
         def attention(li, n, kc, vc):
             # a one-sequence view of the cache keeps the sequence index at 0
             with self._t("attn_prefill"):
-                kinv.attn_prefill(self.q[:n], kc[seq: seq + 1], vc[seq: seq + 1], q_start, q_len,
-                                  q_off, n, p0 + n, out=self.attn[:n], workspace=self.ws)
+                if self.cache != "bf16":
+                    kinv.attn_prefill8(self.q[:n], self.kv8[li].sequences(seq, seq + 1), q_start, q_len, q_off, n,
+                                       p0 + n, out=self.attn[:n], workspace=self.ws, window=s.window, sinks=s.sinks)
+                else:
+                    kinv.attn_prefill(self.q[:n], kc[seq: seq + 1], vc[seq: seq + 1], q_start, q_len, q_off, n,
+                                      p0 + n, out=self.attn[:n], workspace=self.ws, window=s.window, sinks=s.sinks)
         kinv.row_sumsq(self.x[:rows], self.ss[:rows])
         for li in range(self.s.n_layers):
             self.layer(li, rows, seq_t, pos_t, attention)
@@ -333,6 +377,36 @@ class Decoder:
         """Sequence dst takes sequence src's cached keys and values for
         positions 0..n-1 (every layer): a cached prompt prefix, reused."""
         self.kv[:, :, dst, :n].copy_(self.kv[:, :, src, :n])
+        if self.cache != "bf16":
+            self.kv_exp[:, :, dst, :, :n].copy_(self.kv_exp[:, :, src, :, :n])
+
+    def load_prefix(self, seq: int, k: torch.Tensor, v: torch.Tensor) -> None:
+        """Keys and values k, v [layers][n][Hkv][D] (bf16, rotated), kept elsewhere, as
+        positions 0..n-1 of sequence ``seq``; an 8-bit cache rounds them."""
+        s, n = self.s, k.shape[1] if k.dim() == 4 else -1
+        if tuple(k.shape) != (s.n_layers, n, s.n_kv, s.head_dim) or v.shape != k.shape or n > self.Lmax \
+                or not 0 <= seq < self.B:
+            raise ValueError("load_prefix: expected [layers][n][Hkv][D] for one of the cache's sequences")
+        if self.cache == "bf16":
+            self.kv[:, 0, seq, :n].copy_(k)
+            self.kv[:, 1, seq, :n].copy_(v)
+            return
+        i32 = dict(dtype=torch.int32, device=self.dev)
+        start, length = torch.zeros(1, **i32), torch.full((1,), n, **i32)
+        for li in range(s.n_layers):
+            kinv.cache8_write(self.kv8[li].sequences(seq, seq + 1), k[li: li + 1], v[li: li + 1], start, length)
+
+    def read_prefix(self, seq: int, n: int):
+        """Positions 0..n-1 of sequence ``seq`` as load_prefix takes them: (k, v) bf16
+        [layers][n][Hkv][D]; what an 8-bit cache holds comes back exactly."""
+        if not 0 <= seq < self.B or not 0 <= n <= self.Lmax:
+            raise ValueError("read_prefix: outside the cache")
+        if self.cache == "bf16":
+            return self.kv[:, 0, seq, :n].clone(), self.kv[:, 1, seq, :n].clone()
+        i32 = dict(dtype=torch.int32, device=self.dev)
+        start, length = torch.zeros(1, **i32), torch.full((1,), n, **i32)
+        got = [kinv.cache8_read(c.sequences(seq, seq + 1), start, length, n) for c in self.kv8]
+        return torch.cat([k for k, _ in got]), torch.cat([v for _, v in got])
 
     def close_residual(self, rows: int) -> torch.Tensor:
         """The last layer's output for rows [0, rows) (the residual stream;

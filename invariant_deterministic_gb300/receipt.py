@@ -180,13 +180,19 @@ def model_identity(shape, weight_seed: int) -> dict:
             "init": "projections ~N(0, 0.02) bf16, norm gains 1"}
 
 
-def settings_of(shape) -> dict:
+def settings_of(shape, cache: str = "bf16") -> dict:
     """The settings that change bits: the KV split length, the RoPE base,
     QK-norm, the RMSNorm eps and the prefill rule (all but the last prompt
-    token prefilled, the last one decoded)."""
+    token prefilled, the last one decoded); the cache's type where it is not bf16,
+    and the attention window where there is one."""
     from . import kinv
-    return {"split_len": kinv.SPLIT_LEN, "rope_base": shape.rope_base, "qk_norm": shape.qk_norm,
-            "eps": shape.eps, "prefill": "prompt[:-1], then decode from prompt[-1]"}
+    got = {"split_len": kinv.SPLIT_LEN, "rope_base": shape.rope_base, "qk_norm": shape.qk_norm,
+           "eps": shape.eps, "prefill": "prompt[:-1], then decode from prompt[-1]"}
+    if cache != "bf16":
+        got["cache"] = cache
+    if shape.window:
+        got["window"], got["sinks"] = shape.window, shape.sinks
+    return got
 
 
 def verify(record: dict, device="cuda", chunk: int = 0) -> str:
@@ -201,13 +207,15 @@ def verify(record: dict, device="cuda", chunk: int = 0) -> str:
         return "refused: the record does not identify the model"
     from . import kinv, model as M
     shape = M.ModelShape(**record["model"]["shape"])
-    if dict(record["device"]["settings"]) != settings_of(shape):
+    settings = dict(record["device"]["settings"])
+    cache = settings.get("cache", "bf16")
+    if cache not in ("bf16", *kinv.CACHE8_DTYPES) or settings != settings_of(shape, cache):
         return "refused: the recorded settings are not this library's"
     w = M.random_weights(shape, seed=record["model"]["weight_seed"], device=device)
     prompt = record["prompt"]["ids"]
     n_out = record["output"]["tokens"]["count"]
     dec = M.Decoder(shape, w, max_batch=1, max_len=len(prompt) + n_out + 8,
-                    max_chunk=chunk or max(len(prompt) - 1, 1), device=device)
+                    max_chunk=chunk or max(len(prompt) - 1, 1), device=device, cache=cache)
     s = dict(record["sampling"])
     if s.get("logit_bias"):
         s["logit_bias"] = {int(k): float(v) for k, v in s["logit_bias"].items()}
