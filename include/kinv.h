@@ -369,7 +369,7 @@ typedef struct {
  * rotated keys, rounded to bf16, and of the values.  The angles are carried a
  * little further than there, so a query or key may differ by a bf16 step where
  * it lies next to a rounding border.  Arguments, requirements and errors as
- * there; no two rows of a call may name the same place.  A row whose sequence or position lies
+ * there, and gains 16-byte aligned; no two rows of a call may name the same place.  A row whose sequence or position lies
  * outside the cache is left out -- its row of q_out too -- and the status word
  * records KINV_ERR_INVALID_ARG. */
 kinv_status kinv_rope_append8(const void* qkv, int64_t ld_qkv, void* q_out, const kinv_cache8* cache,

@@ -4,126 +4,173 @@
 
 #include "cache8.cuh"
 #include "cache8_read.cuh"
-#include "rope.cuh"
 
 namespace kinv {
 namespace {
 
-// cos and sin of p * inv_freq as rope_angle() forms them, corrected by what the
-// reduced angle loses in fp32 (its low part d: cos - d sin, sin + d cos): a
-// rounding that goes the other way moves a key's code by a whole step.
-__device__ __forceinline__ void rope_angle_corrected(int p, double inv_freq, float& c, float& s) {
-  const double theta = static_cast<double>(p) * inv_freq;
-  const double k = rint(theta * 0.15915494309189535);  // 1 / (2 pi)
-  double red = fma(-k, 6.283185307179586, theta);
-  red = fma(-k, 2.4492935982947064e-16, red);
-  const float hi = static_cast<float>(red);
-  const float d = static_cast<float>(red - static_cast<double>(hi));
+// Frequencies base^(-2i/D) in turns, as 64-bit fractions: p times one of them,
+// modulo 2^64, is the angle's fraction of a turn to p 2^-65 of it (and the
+// frequency's own 2^-53 relative, as in fp64).
+struct RopeTurns {
+  uint64_t turn[64];
+};
+
+// cos and sin of the angle of position p, correct to about their rounding in fp32:
+// integers instead of kinv_rope_append's fp64 (this GPU does two fp64 operations a
+// cycle and SM), and what the angle loses in fp32 put back (its low part d: cos - d
+// sin, sin + d cos), as a rounding that goes the other way moves a key's code by a
+// whole step.
+__device__ __forceinline__ void rope_angle_turns(int p, uint64_t turn, float& c, float& s) {
+  const int64_t x = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(p)) * turn);  // signed fraction * 2^64
+  const int32_t top = static_cast<int32_t>(x >> 32);
+  const float h = static_cast<float>(top);
+  // top - h is exact (a float of 2^31 and above is a multiple of 128)
+  const float l = static_cast<float>(static_cast<int64_t>(top) - static_cast<int64_t>(h)) +
+                  static_cast<float>(static_cast<uint32_t>(x)) * 0x1p-32f;
+  constexpr double kTurn = 6.283185307179586476925 * 0x1p-32;  // radians of a unit of `top`
+  constexpr float kHi = static_cast<float>(kTurn), kLo = static_cast<float>(kTurn - static_cast<double>(kHi));
+  const float hi = __fmul_rn(h, kHi);
+  const float d = __fmaf_rn(h, kHi, -hi) + __fmaf_rn(h, kLo, __fmul_rn(l, kHi));
   float c0, s0;
   sincosf(hi, &s0, &c0);
   c = __fmaf_rn(-d, s0, c0);
   s = __fmaf_rn(d, c0, s0);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(__nv_bfloat16 x) { return __bfloat16_as_ushort(x) & 0x7FFFu; }
+// D / 16 lanes hold a head, each lane eight rotation pairs (i, i + D/2) in two 16-byte
+// loads, so a warp takes four heads of 128 (eight of 64) at a time.  A block has one
+// row, or four where there are many, whose angles its threads form together beside the
+// first loads; each warp asks for its next heads before
+// it works on the last.  One warp per head with a pair of values a lane, as
+// kinv_rope_append has it, is bound by the instructions of its reductions: 4,096 rows
+// of the 8B shape 37 us against TBD.
+constexpr int kAppendRows = 4;
 
-// kinv_rope_append's layout of work: a block per row and `heads_per_block` of its
-// heads, a warp per head; the first D/2 threads form the row's rotation angles.
-// A key or value head's largest magnitude is a warp maximum over bit patterns.
-constexpr int kRopeWarps = 8;
+struct Append8Params {
+  const __nv_bfloat16* qkv;
+  int64_t ld_qkv;
+  __nv_bfloat16* q_out;
+  Cache8View cache;
+  const int32_t* seq;
+  const int32_t* pos;
+  const __nv_bfloat16* q_norm;
+  const __nv_bfloat16* k_norm;
+  float eps;
+  int rows, rows_per_block, Hq, Hkv;
+  RopeTurns turns;
+  int* status;
+};
 
 template <int D, bool I8>
-__global__ void rope_append8_kernel(const __nv_bfloat16* __restrict__ qkv, int64_t ld_qkv,
-                                    __nv_bfloat16* __restrict__ q_out, const Cache8View cache,
-                                    const int32_t* __restrict__ seq, const int32_t* __restrict__ pos,
-                                    const __nv_bfloat16* __restrict__ q_norm,
-                                    const __nv_bfloat16* __restrict__ k_norm, float eps, int Hq, int Hkv,
-                                    int heads_per_block, const RopeFreqs freqs, int* status) {
+__global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_constant__ Append8Params a) {
   constexpr int HALF = D / 2;
-  constexpr int P = D / 64;
-  __shared__ float cs[HALF], sn[HALF];
-  __shared__ __nv_bfloat16 key_rows[kRopeWarps][D];
+  constexpr int L = D / 16;   // lanes of a head
+  constexpr int HPW = 32 / L; // heads of a warp
+  __shared__ __align__(16) float cs[kAppendRows][HALF], sn[kAppendRows][HALF];
+  __shared__ int place[kAppendRows][2];  // of each row: sequence (-1: outside the cache), position
   pdl_launch_dependents();
   pdl_wait();
-  const int r = blockIdx.x;
-  const int p = pos[r], s = seq[r];
-  if (p < 0 || p >= cache.slots || s < 0 || s >= cache.B) {
-    if (threadIdx.x == 0 && blockIdx.y == 0 && status) atomicExch(status, DEV_CACHE8_BAD_RANGE);
-    return;
+  const int r0 = blockIdx.x * a.rows_per_block, n = min(a.rows_per_block, a.rows - r0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % L;
+  const int heads = a.Hq + 2 * a.Hkv;
+  const int groups = (heads + HPW - 1) / HPW;  // of a row, a warp's work at a time
+  const __nv_bfloat16* base = a.qkv + r0 * a.ld_qkv + sub * 8;
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+  int row = warp / groups, group = warp - row * groups;
+  auto load = [&]() {
+    const int h = group * HPW + lane / L;
+    if (row < n && h < heads) {
+      lo = *reinterpret_cast<const uint4*>(base + row * a.ld_qkv + h * D);
+      hi = *reinterpret_cast<const uint4*>(base + row * a.ld_qkv + h * D + HALF);
+    }
+  };
+  load();
+  if (threadIdx.x < n) {
+    const int p = a.pos[r0 + threadIdx.x], s = a.seq[r0 + threadIdx.x];
+    const bool fits = p >= 0 && p < a.cache.slots && s >= 0 && s < a.cache.B;
+    place[threadIdx.x][0] = fits ? s : -1;
+    place[threadIdx.x][1] = p;
+    if (!fits && a.status) atomicExch(a.status, DEV_CACHE8_BAD_RANGE);
   }
-  for (int i = threadIdx.x; i < HALF; i += blockDim.x) rope_angle_corrected(p, freqs.inv_freq[i], cs[i], sn[i]);
+  for (int i = threadIdx.x; i < n * HALF; i += blockDim.x)
+    rope_angle_turns(a.pos[r0 + i / HALF], a.turns.turn[i % HALF], cs[i / HALF][i % HALF], sn[i / HALF][i % HALF]);
   __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  const __nv_bfloat16* row = qkv + r * ld_qkv;
-  const int64_t tok = s * cache.seq_stride + p * cache.tok_stride;
-  const int heads = Hq + 2 * Hkv;
-  const int h_end = min(heads, (static_cast<int>(blockIdx.y) + 1) * heads_per_block);
-  for (int h = blockIdx.y * heads_per_block + warp; h < h_end; h += nwarps) {
-    const __nv_bfloat16* src = row + h * D;
-    if (h >= Hq + Hkv) {  // value head
-      const int g = h - Hq - Hkv;
-      uint32_t w[P];
-      if (P == 2) {
-        const uint2 v = reinterpret_cast<const uint2*>(src)[lane];
-        w[0] = v.x;
-        w[P - 1] = v.y;
-      } else {
-        w[0] = reinterpret_cast<const uint32_t*>(src)[lane];
-      }
-      uint32_t m = 0;
+  // whole warps, so that every lane takes part in the shuffles
+  while (row < n) {
+    const int h = group * HPW + lane / L, first = group * HPW, now = row;
+    const int s = place[now][0], p = place[now][1];
+    const int64_t r = r0 + now;
+    const bool live = h < heads && s >= 0, value = h >= a.Hq + a.Hkv;
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};  // the head's bf16 pairs: low half, high half
+    for (group += blockDim.x >> 5; group >= groups; group -= groups) ++row;
+    load();
+    const __nv_bfloat16* gain = !live || value ? nullptr : h < a.Hq ? a.q_norm : a.k_norm;
+    float x[16];
 #pragma unroll
-      for (int j = 0; j < P; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-      const int E = scale_exponent<I8>(__reduce_max_sync(0xffffffffu, m));
-      const float inv = encode_factor(E);
-      uint32_t code = encode2<I8>(bf16_lo(w[0]), bf16_hi(w[0]), inv);
-      unsigned char* dst = cache.v + tok + g * D;
-      if (P == 2) {
-        code |= encode2<I8>(bf16_lo(w[P - 1]), bf16_hi(w[P - 1]), inv) << 16;
-        reinterpret_cast<uint32_t*>(dst)[lane] = code;
-      } else {
-        reinterpret_cast<uint16_t*>(dst)[lane] = static_cast<uint16_t>(code);
-      }
-      if (lane == 0) cache.ve[s * cache.eseq_stride + g * cache.ehead_stride + p] = static_cast<int8_t>(E);
-      continue;
+    for (int j = 0; j < 8; ++j) {
+      x[2 * j] = bf16_lo(w[j]);
+      x[2 * j + 1] = bf16_hi(w[j]);
     }
-    float a[P], b[P], c[P], sv[P];
+    if (__any_sync(0xffffffffu, gain != nullptr)) {
+      float acc = 0.f;
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      a[j] = __bfloat162float(src[lane * P + j]);
-      b[j] = __bfloat162float(src[HALF + lane * P + j]);
-      c[j] = cs[lane * P + j];
-      sv[j] = sn[lane * P + j];
+      for (int j = 0; j < 16; ++j) acc = fmaf(x[j], x[j], acc);
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
+      if (gain) {
+        const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(acc, static_cast<float>(D)), a.eps)));
+        const uint4 g0 = *reinterpret_cast<const uint4*>(gain + sub * 8), g1 = *reinterpret_cast<const uint4*>(gain + HALF + sub * 8);
+        const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[2 * j] = __fmul_rn(__fmul_rn(x[2 * j], inv), bf16_lo(gw[j]));
+          x[2 * j + 1] = __fmul_rn(__fmul_rn(x[2 * j + 1], inv), bf16_hi(gw[j]));
+        }
+      }
     }
-    if (h < Hq) {
-      rope_norm_rotate<D>(a, b, c, sv, q_norm, eps, lane, q_out + (static_cast<int64_t>(r) * Hq + h) * D);
-      continue;
+    if (!value) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(&cs[now][sub * 8 + j]),
+                     sv = *reinterpret_cast<const float4*>(&sn[now][sub * 8 + j]);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = x[j + e], v = x[8 + j + e];
+          x[j + e] = __fmaf_rn(u, cc[e], -__fmul_rn(v, ss[e]));
+          x[8 + j + e] = __fmaf_rn(v, cc[e], __fmul_rn(u, ss[e]));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
     }
-    // the rotated key by way of shared memory, each lane its own values
-    __nv_bfloat16* turned = key_rows[warp];
-    rope_norm_rotate<D>(a, b, c, sv, k_norm, eps, lane, turned);
-    __nv_bfloat16 lo[P], hi[P];
+    if (live && h < a.Hq) {
+      __nv_bfloat16* dst = a.q_out + (r * a.Hq + h) * D + sub * 8;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + HALF) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    if (first + HPW <= a.Hq) continue;  // query heads only
+    // the largest magnitude by bit patterns
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      lo[j] = turned[lane * P + j];
-      hi[j] = turned[HALF + lane * P + j];
-      m = max(m, max(abs_bits(lo[j]), abs_bits(hi[j])));
-    }
-    const int E = scale_exponent<I8>(__reduce_max_sync(0xffffffffu, m));
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!live || h < a.Hq) continue;
+    const int E = scale_exponent<I8>(max(m & 0xFFFFu, m >> 16));
     const float inv = encode_factor(E);
-    const int g = h - Hq;
-    unsigned char* dst = cache.k + tok + g * D;
-    if (P == 2) {
-      const uint32_t x = encode2<I8>(__bfloat162float(lo[0]), __bfloat162float(lo[P - 1]), inv);
-      const uint32_t y = encode2<I8>(__bfloat162float(hi[0]), __bfloat162float(hi[P - 1]), inv);
-      reinterpret_cast<uint16_t*>(dst)[lane] = static_cast<uint16_t>(x);
-      reinterpret_cast<uint16_t*>(dst + HALF)[lane] = static_cast<uint16_t>(y);
-    } else {
-      const uint32_t x = encode2<I8>(__bfloat162float(lo[0]), __bfloat162float(hi[0]), inv);
-      dst[lane] = static_cast<unsigned char>(x);
-      dst[HALF + lane] = static_cast<unsigned char>(x >> 8);
-    }
-    if (lane == 0) cache.ke[s * cache.eseq_stride + g * cache.ehead_stride + p] = static_cast<int8_t>(E);
+    uint32_t code[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      code[j] = encode2<I8>(bf16_lo(w[2 * j]), bf16_hi(w[2 * j]), inv) |
+                (encode2<I8>(bf16_lo(w[2 * j + 1]), bf16_hi(w[2 * j + 1]), inv) << 16);
+    const int g = value ? h - a.Hq - a.Hkv : h - a.Hq;
+    unsigned char* dst =
+        (value ? a.cache.v : a.cache.k) + s * a.cache.seq_stride + p * a.cache.tok_stride + g * D + sub * 8;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+    *reinterpret_cast<uint2*>(dst + HALF) = make_uint2(code[2], code[3]);
+    if (sub == 0)
+      (value ? a.cache.ve : a.cache.ke)[s * a.cache.eseq_stride + g * a.cache.ehead_stride + p] = static_cast<int8_t>(E);
   }
 }
 
@@ -203,16 +250,20 @@ __global__ void __launch_bounds__(kWriteThreads) cache8_write_kernel(const Write
 }
 
 // The last table a thread asked for: 64 powers are 4 us of a call.
-const RopeFreqs& rope_freqs(float base, int D) {
-  static thread_local RopeFreqs freqs;
+const RopeTurns& rope_turns(float base, int D) {
+  static thread_local RopeTurns turns;
   static thread_local float of_base = 0.f;
   static thread_local int of_dim = 0;
   if (base != of_base || D != of_dim) {
-    for (int i = 0; i < D / 2; ++i) freqs.inv_freq[i] = std::pow(static_cast<double>(base), -2.0 * i / D);
+    for (int i = 0; i < D / 2; ++i) {
+      // turns a position, less whole ones (a base below 1 has frequencies above 1)
+      const double f = std::pow(static_cast<double>(base), -2.0 * i / D) * 0.15915494309189533577;  // 1 / (2 pi)
+      turns.turn[i] = static_cast<uint64_t>(std::ldexp(f - std::floor(f), 63)) << 1;
+    }
     of_base = base;
     of_dim = D;
   }
-  return freqs;
+  return turns;
 }
 
 constexpr int kMaxKvHeads = 1024;  // the write kernel's exponents: 32 bytes a head in shared memory
@@ -233,16 +284,21 @@ extern "C" kinv_status kinv_rope_append8(const void* qkv, int64_t ld_qkv, void* 
   if (cache->B > 1 && (cache->seq_stride == 0 || cache->exp_seq_stride == 0)) return KINV_ERR_INVALID_ARG;
   if (rows == 0) return KINV_OK;
   if (!qkv || !q_out || !seq || !pos || ld_qkv < static_cast<int64_t>(Hq + 2 * Hkv) * D) return KINV_ERR_INVALID_ARG;
-  if (!aligned16(qkv) || !aligned16(q_out) || ld_qkv % 8) return KINV_ERR_ALIGNMENT;
-  const RopeFreqs& freqs = rope_freqs(rope_base, D);
-  const int heads = Hq + 2 * Hkv;
-  const int hpb = rows >= 512 ? heads : 8;  // as kinv_rope_append
-  const dim3 grid(rows, (heads + hpb - 1) / hpb);
+  if (!aligned16(qkv) || !aligned16(q_out) || ld_qkv % 8 || (q_norm && !aligned16(q_norm)) ||
+      (k_norm && !aligned16(k_norm)))
+    return KINV_ERR_ALIGNMENT;
+  Append8Params p{static_cast<const __nv_bfloat16*>(qkv), ld_qkv, static_cast<__nv_bfloat16*>(q_out), view, seq, pos,
+                  static_cast<const __nv_bfloat16*>(q_norm), static_cast<const __nv_bfloat16*>(k_norm), eps, rows, 1, Hq, Hkv,
+                  rope_turns(rope_base, D), device_status_word()};
+  const int per_warp = 32 / (D / 16);
+  int warps = (Hq + 2 * Hkv + per_warp - 1) / per_warp;
+  if (rows >= 1024) {  // several rows on every SM
+    p.rows_per_block = kAppendRows;
+    warps = warps * kAppendRows < 8 ? warps * kAppendRows : 8;
+  }
   auto run = [&](auto kernel) {
-    return launch_kernel(kernel, grid, dim3(32 * kRopeWarps), 0, stream, 1, static_cast<const __nv_bfloat16*>(qkv), ld_qkv,
-                         static_cast<__nv_bfloat16*>(q_out), view, seq, pos,
-                         static_cast<const __nv_bfloat16*>(q_norm), static_cast<const __nv_bfloat16*>(k_norm), eps,
-                         Hq, Hkv, hpb, freqs, device_status_word());
+    return launch_kernel(kernel, dim3((rows + p.rows_per_block - 1) / p.rows_per_block), dim3(32 * (warps < 16 ? warps : 16)), 0,
+                         stream, 1, p);
   };
   const bool i8 = cache->dtype == KINV_I8;
   if (D == 128) return i8 ? run(rope_append8_kernel<128, true>) : run(rope_append8_kernel<128, false>);
