@@ -268,8 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int half = 0, q_uses = 0;  // halves of R so far
       auto wait = [&](uint32_t b, uint32_t parity) {
-        if (ok) ok = !*abort_flag && mbar_wait_bounded(b, parity, status, DEV_TIMEOUT_ATTN);
-        if (ok) tc_fence_after();
+        if (!mbar_try_wait(b, parity) && ok) ok = mbar_wait_bounded(b, parity, status, DEV_TIMEOUT_ATTN);
       };
       auto scores = [&](bool new_q) {
         if (new_q) wait(q_full, q_uses++ & 1);
@@ -288,8 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // O (+)= P . V over half h of step st, whose P is in buffer (2 st + h) % 3
       auto products = [&](int st, int h) {
         wait(v_ready(h), st & 1);
-        wait(p_full(h), st & 1);
+        // O of the step before is read by threads that have written this half of P
+        if (h == 0 && st > 0)
+          wait(o_free, (st - 1) & 1);
+        else
+          wait(p_full(h), st & 1);
         if (!ok) return;
+        tc_fence_after();
         const uint32_t p = tmem + static_cast<uint32_t>(128 * ((2 * st + h) % 3));
         const uint64_t v = vd + static_cast<uint64_t>((h * KV_BYTES) >> 4);
 #pragma unroll
@@ -310,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int st = 0; ok && (more || st > 0); ++st) {
         const bool last = !(more = more && walk.next());
         if (!last) scores(walk.s.it == 0);
-        if (st > 0) wait(o_free, (st - 1) & 1);
         products(st, 0);
         if (!last) {
           scores(false);
