@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
   constexpr int PQ = 2 * PHALF > 8 * QROW ? 2 * PHALF : 8 * QROW;
   float* fk = reinterpret_cast<float*>(pt + PQ);                          // [256] factors of the scores
   __nv_bfloat16* fv = reinterpret_cast<__nv_bfloat16*>(fk + kSplit);      // [256] factors of the weights
-  float* wmax = reinterpret_cast<float*>(fv + kSplit);                    // [8 warps][8 pairs]
+  float* wmax = reinterpret_cast<float*>(fv + kSplit);                    // [8 pairs][8 warps]
   float* wsum = wmax + 8 * kPairs;
   int* wexp = reinterpret_cast<int*>(wsum + 8 * kPairs);                  // [8]
   float* qc2 = reinterpret_cast<float*>(wexp + 8);                        // [8] the pairs' softmax factors
@@ -217,9 +217,8 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
       mbar_wait_bounded(v_bar, phase, nullptr, 0);  // the copy in flight lands before the block leaves
       return;
     }
-    int ev_max = wexp[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) ev_max = max(ev_max, wexp[w]);
+    const int4 e0 = *reinterpret_cast<const int4*>(wexp), e1 = *reinterpret_cast<const int4*>(wexp + 4);
+    const int ev_max = max(max(max(e0.x, e0.y), max(e0.z, e0.w)), max(max(e1.x, e1.y), max(e1.z, e1.w)));
     // 0 for a hidden key, whose weight is 0
     const int fe = !my_vis ? 0 : my_ev == kExpNaN ? 0x7FFF : max(my_ev - ev_max + 127 + kLift, 0) << 7;
     fv[t] = __ushort_as_bfloat16(static_cast<unsigned short>(fe));
@@ -227,10 +226,14 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     // --- scores: warp w owns keys 32w .. 32w + 31, two 16-key tiles
     float sc[2][4] = {};
     // the 32-key groups that hold a visible key: the others add nothing
-    uint32_t groups = 0;
+    const bool whole = cur.cnt == kSplit && (cur.lo <= 0 || cur.sink >= kSplit);  // no key hidden: no mask
+    uint32_t groups = 0xFF;
+    if (!whole) {
+      groups = 0;
 #pragma unroll
-    for (int j = 0; j < kSplit / 32; ++j)
-      if (j * 32 < cur.cnt && (j * 32 < cur.sink || (j + 1) * 32 > cur.lo)) groups |= 1u << j;
+      for (int j = 0; j < kSplit / 32; ++j)
+        if (j * 32 < cur.cnt && (j * 32 < cur.sink || (j + 1) * 32 > cur.lo)) groups |= 1u << j;
+    }
     if (groups >> warp & 1) {
       uint32_t qb[C][2];  // q fragments (B operand: 16 values x 8 pairs)
 #pragma unroll
@@ -287,8 +290,6 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
         }
       }
     const int key0 = warp * 32 + nb0 * 8 + 2 * kq;
-    // no key of the split hidden: no mask
-    const bool whole = cur.cnt == kSplit && (cur.lo <= 0 || cur.sink >= kSplit);
     float mx = -INFINITY;
     if (whole) {
 #pragma unroll
@@ -302,14 +303,12 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     }
 #pragma unroll
     for (int o = GP == 4 ? 2 : 8; o <= 16; o = o == 2 ? 8 : o << 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (kq == 0) wmax[warp * kPairs + pair] = mx;
+    if (kq == 0) wmax[pair * 8 + warp] = mx;
     __syncthreads();
     if (t == 0 && next.b >= 0) request(&tmK, next, k_base, k_bar);  // every warp is done with K
-    float m = wmax[pair];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) m = fmaxf(m, wmax[w * kPairs + pair]);
+    const float4 m0 = *reinterpret_cast<const float4*>(wmax + pair * 8), m1 = *reinterpret_cast<const float4*>(wmax + pair * 8 + 4);
     const float c2 = qc2[pair];
-    m = __fmul_rn(m, c2);
+    const float m = __fmul_rn(fmaxf(fmax3(fmax3(m0.x, m0.y, m0.z), m0.w, m1.x), fmax3(m1.y, m1.z, m1.w)), c2);
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
