@@ -80,10 +80,17 @@ __device__ __forceinline__ void report_bad_length(const AttnParams& p) {
   if (threadIdx.x == 0 && p.status) atomicExch(p.status, DEV_ATTN_BAD_LENGTH);
 }
 
+template <int D>
+__host__ __device__ constexpr size_t split_smem_bytes() {
+  return static_cast<size_t>(kSplit) * D * 2 + (2 * kRowsP + 1) * static_cast<size_t>(kSplit) * 2;
+}
+
 // WIN: a block takes a split that holds a key its row sees, loads the visible
-// keys alone and gives the others weight 0 and zero V.
-template <int D, bool WIN>
-__global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p) {
+// keys alone and gives the others weight 0 and zero V.  ONE: its partial goes to
+// shared memory, `one_o`: [8 pairs][D], then (m, l) [8].
+template <int D, bool WIN, bool ONE>
+__device__ __forceinline__ void attn_split_body(const AttnParams& p, const int g, const int s, const int b,
+                                                float* one_o) {
   constexpr int C8 = D / 8;               // 16-byte chunks per key row
   constexpr int SUB = 64;                 // keys per load stage
   constexpr int NSUB = kSplit / SUB;      // the K stages are reused for V
@@ -103,11 +110,7 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p
 
   pdl_launch_dependents();
   pdl_wait();
-  // kv heads are the fastest grid index: the blocks reading the 256-byte
-  // slices of the same token rows run side by side
-  const int g = blockIdx.x;
-  const int s = blockIdx.y;                            // place among the row's partials
-  const int b = blockIdx.z;
+  // s: place among the row's partials
   if (!seq_ok(p, b)) {
     report_bad_length(p);
     return;
@@ -289,19 +292,43 @@ __global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p
     // row gq = query head g G + gq of sequence b, columns 16w + 8nb + 2tq (+1)
     if (gq < G) {
       const int64_t base = (static_cast<int64_t>(b) * p.Hq + g * G + gq) * p.S + s;
+      float* o_at = ONE ? one_o + gq * D : p.ws_o + base * D;
+      float* ml_at = ONE ? one_o + kMaxG * D + 2 * gq : p.ws_ml + base * 2;
 #pragma unroll
       for (int nb = 0; nb < 2; ++nb)
-        *reinterpret_cast<float2*>(p.ws_o + base * D + warp * 16 + nb * 8 + 2 * tq) =
-            make_float2(oc[nb][0], oc[nb][1]);
+        *reinterpret_cast<float2*>(o_at + warp * 16 + nb * 8 + 2 * tq) = make_float2(oc[nb][0], oc[nb][1]);
       if (warp == 0 && tq == 0) {
         float l = wsum[0][gq];
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w) l = __fadd_rn(l, wsum[w][gq]);
-        p.ws_ml[base * 2 + 0] = m;
-        p.ws_ml[base * 2 + 1] = l;
+        ml_at[0] = m;
+        ml_at[1] = l;
       }
     }
   }
+}
+
+template <int D, bool WIN>
+__global__ void __launch_bounds__(kThreads) attn_split_kernel(const AttnParams p) {
+  // kv heads are the fastest grid index: the blocks reading the 256-byte
+  // slices of the same token rows run side by side
+  attn_split_body<D, WIN, false>(p, blockIdx.x, blockIdx.y, blockIdx.z, nullptr);
+}
+
+// The windowed form in one launch: a cluster per (sequence, kv head) with a block for
+// each split that there can be, at most eight, which folds the partials on chip.
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_window_one_kernel(const AttnParams p) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  float* one_o = reinterpret_cast<float*>(smem_raw + split_smem_bytes<D>());
+  const int g = blockIdx.x / p.S, rank = blockIdx.x - g * p.S, b = blockIdx.y;
+  attn_split_body<D, true, true>(p, g, rank, b, one_o);
+  cluster_sync();
+  const int len = seq_ok(p, b) ? p.kv_len[b] : 0;
+  const int count = len > 0 ? visible_splits(p.win, window_lo(p.win, len), len).count : 0;
+  fold_cluster<D, kThreads>(smem_addr(one_o), kMaxG, p.G, rank, p.S, count,
+                            p.out + (static_cast<int64_t>(b) * p.Hq + g * p.G) * D);
+  cluster_sync();  // no block leaves while its partial is read
 }
 
 // One block per (query head, row); thread d folds column d.
@@ -799,14 +826,23 @@ size_t prefill_tc_smem_bytes() {
          (kTcBars + 1) * 8 + 16 + 10 * kTcPairs * 4;
 }
 
-template <int D>
-size_t split_smem_bytes() {
-  return static_cast<size_t>(kSplit) * D * 2 + (2 * kRowsP + 1) * static_cast<size_t>(kSplit) * 2;
-}
-
 // Decode: attn_split_kernel, then the merge.
 template <int D, bool WIN>
 kinv_status launch(const AttnParams& p, dim3 split_grid, dim3 merge_grid, cudaStream_t stream) {
+  // One launch of clusters for rows of at most four splits while all blocks run at
+  // once, two to an SM: 7 sequences of 4/2 heads of 64, window 64, 8.3 us against 10.2;
+  // 32/8 heads of 128 take the same time either way up to there (12.4 us for 8
+  // sequences, window 200), a launch less to issue, and longer with clusters of eight
+  // (2 sequences, window 1,500: 12.3 against 10.3).
+  if (WIN && p.S <= 4) {
+    if (static_cast<int64_t>(split_grid.x) * split_grid.y * split_grid.z <= 2 * sm_count()) {
+      void (*one)(const AttnParams) = attn_window_one_kernel<D>;
+      const size_t smem = split_smem_bytes<D>() + kMaxG * (D + 2) * 4;
+      const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(one), smem);
+      if (attr != KINV_OK) return attr;
+      return launch_kernel(one, dim3(split_grid.x * p.S, split_grid.z), dim3(kThreads), smem, stream, p.S, p);
+    }
+  }
   void (*kernel)(const AttnParams) = attn_split_kernel<D, WIN>;
   const size_t smem = split_smem_bytes<D>();
   const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(kernel), smem);

@@ -39,6 +39,7 @@ struct Attn8Params {
   float c2;      // fp32(scale * log2 e)
   Window win;
   int* status;
+  __nv_bfloat16* out;  // of the one-launch form
 };
 
 constexpr int kBox = 64;  // keys of one TMA copy
@@ -65,7 +66,11 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
 // four neighbours), which a step's sum does not depend on.
 // GP = 4: at most four query heads per kv head; the lanes of the other four
 // columns take half of the keys' softmax.
-template <int D, bool I8, int GP>
+//
+// ONE: a cluster per (sequence, kv head) with a block for each split that there can
+// be, at most eight; the partials stay in shared memory and the cluster's blocks fold
+// them together, so the call is one launch.
+template <int D, bool I8, int GP, bool ONE>
 __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     attn8_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const Attn8Params p) {
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
 
   // The walk: lane j holds the length of sequence wb + j and the number of listed
   // splits of sequences wb .. wb + j; `base` splits lie before wb.
-  const int g = blockIdx.x, G = p.G;
+  const int g = ONE ? blockIdx.x / p.S : blockIdx.x, G = p.G;
   int wb = 0, base = 0, wlen = 0, winc = 0;
   auto load_window = [&]() {
     const int b = wb + lane;
@@ -177,16 +182,36 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     return static_cast<uint32_t>(r * D + ((C == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4));
   };
 
-  load_window();
-  int place = blockIdx.y;
-  Item cur = item_at(place);
-  if (cur.b < 0) return;
-  if (t == 0) {
+  int place = blockIdx.y, one_len = 0, one_count = 0;
+  Item cur;
+  if (ONE) {
+    one_len = p.kv_len[blockIdx.y];
+    const int rank = blockIdx.x - g * p.S;
+    if (one_len < 0 || one_len > p.cache.slots) {
+      if (t == 0 && p.status) atomicExch(p.status, DEV_ATTN_BAD_LENGTH);
+      one_len = 0;
+    }
+    const int first = window_lo(p.win, one_len);
+    const SplitList list = visible_splits(p.win, first, one_len);
+    one_count = list.count;
+    cur.b = rank < one_count ? static_cast<int>(blockIdx.y) : -1;
+    cur.i = rank;
+    cur.k0 = list.split(rank) * kSplit;
+    cur.cnt = min(kSplit, one_len - cur.k0);
+    cur.lo = first - cur.k0;
+    cur.sink = p.win.sinks - cur.k0;
+  } else {
+    load_window();
+    cur = item_at(place);
+    if (cur.b < 0) return;
+  }
+  float* one_o = reinterpret_cast<float*>(smem);  // over K, once the scores are done: [8 pairs][D], then (m, l) [8]
+  if (cur.b >= 0 && t == 0) {
     request(&tmK, cur, k_base, k_bar);
     request(&tmV, cur, v_base, v_bar);
   }
-  fetch(cur);
-  for (uint32_t phase = 0;; phase ^= 1) {
+  if (cur.b >= 0) fetch(cur);
+  for (uint32_t phase = 0; cur.b >= 0; phase ^= 1) {
     // this split's factors and q into shared memory; the next one's requested
     const int my_ev = ev;
     const bool my_vis = visible(cur, t);
@@ -209,13 +234,17 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
         *reinterpret_cast<__half2*>(to + 16) = c;
       }
     }
-    place += gridDim.y;
-    const Item next = item_at(place);
-    if (next.b >= 0) fetch(next);
+    Item next;
+    next.b = -1;
+    if (!ONE) {
+      place += gridDim.y;
+      next = item_at(place);
+      if (next.b >= 0) fetch(next);
+    }
     bool ok = mbar_wait_bounded(k_bar, phase, p.status, DEV_TIMEOUT_ATTN);
     if (__syncthreads_or(!ok)) {
       mbar_wait_bounded(v_bar, phase, nullptr, 0);  // the copy in flight lands before the block leaves
-      return;
+      break;
     }
     const int4 e0 = *reinterpret_cast<const int4*>(wexp), e1 = *reinterpret_cast<const int4*>(wexp + 4);
     const int ev_max = max(max(max(e0.x, e0.y), max(e0.z, e0.w)), max(max(e1.x, e1.y), max(e1.z, e1.w)));
@@ -350,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
     ok = mbar_wait_bounded(v_bar, phase, p.status, DEV_TIMEOUT_ATTN);
     if (__syncthreads_or(!ok)) {
       if (next.b >= 0) mbar_wait_bounded(k_bar, phase ^ 1, nullptr, 0);
-      return;
+      break;
     }
 
     // --- O^T = V^T . P^T: warp w owns values 16w .. 16w + 15 over all 256 keys,
@@ -384,20 +413,29 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
       const int64_t row = static_cast<int64_t>(cur.b) * p.Hq + g * G;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        if (2 * tq + e < G)
+        if (ONE)
+          *reinterpret_cast<float2*>(one_o + (2 * tq + e) * D + warp * 16 + 2 * gq) = make_float2(o[e], o[2 + e]);
+        else if (2 * tq + e < G)
           *reinterpret_cast<float2*>(p.ws_o + ((row + 2 * tq + e) * p.S + cur.i) * D + warp * 16 + 2 * gq) =
               make_float2(o[e], o[2 + e]);
       if (warp == 0 && kq == 0 && pair < G && (GP == 8 || tq >= 2)) {
         float l = wsum[pair];
 #pragma unroll
         for (int w = 1; w < kThreads / 32; ++w) l = __fadd_rn(l, wsum[w * kPairs + pair]);
-        *reinterpret_cast<float2*>(p.ws_ml + ((row + pair) * p.S + cur.i) * 2) = make_float2(m, l);
+        *reinterpret_cast<float2*>(ONE ? one_o + kPairs * D + 2 * pair : p.ws_ml + ((row + pair) * p.S + cur.i) * 2) =
+            make_float2(m, l);
       }
     }
-    if (next.b < 0) return;
+    if (next.b < 0) break;
     __syncthreads();  // every warp is done with V, P and the sums
     if (t == 0) request(&tmV, next, v_base, v_bar);
     cur = next;
+  }
+  if (ONE) {
+    cluster_sync();
+    fold_cluster<D, kThreads>(k_base, kPairs, G, blockIdx.x - g * p.S, p.S, one_count,
+                              p.out + (static_cast<int64_t>(blockIdx.y) * p.Hq + g * G) * D);
+    cluster_sync();  // no block leaves while its partial is read
   }
 }
 
@@ -428,13 +466,23 @@ kinv_status launch_decode8(const Attn8Params& p, const MergeParams& mp, int Hkv,
   CUtensorMap mk, mv;
   if (!encode_codes(&mk, p.cache.k, p.cache, p.B, Hkv, D) || !encode_codes(&mv, p.cache.v, p.cache, p.B, Hkv, D))
     return KINV_ERR_UNSUPPORTED;
-  auto kernel = attn8_split_kernel<D, I8, GP>;
   constexpr size_t smem = split8_smem_bytes<D, GP>();
+  const int64_t resident = static_cast<int64_t>(sm_count()) * (D == 128 ? 3 : 5);
+  const int64_t most = static_cast<int64_t>(p.B) * p.S;
+  // One launch of clusters where there are at most eight splits a row and all blocks
+  // run at once; clusters of more than four need more room to be placed (32/8 heads of
+  // 128: one request of 500 keys 8.2 us against 10.2, 24 of 500 10.4 against 12.4, 3 of
+  // 2,048 8.6 against 10.3, but 7 of 2,048, 448 blocks, 14.4 against 12.3).
+  if (p.S <= 8 && most * Hkv <= (p.S <= 4 ? resident : 2 * resident / 3)) {
+    auto one = attn8_split_kernel<D, I8, GP, true>;
+    const kinv_status st = ensure_smem(reinterpret_cast<const void*>(one), smem);
+    if (st != KINV_OK) return st;
+    return launch_kernel(one, dim3(Hkv * p.S, p.B), dim3(kThreads), smem, stream, p.S, mk, mv, p);
+  }
+  auto kernel = attn8_split_kernel<D, I8, GP, false>;
   kinv_status st = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
   if (st != KINV_OK) return st;
   // as many blocks as the GPU holds at a time, or as there can be splits
-  const int64_t resident = static_cast<int64_t>(sm_count()) * (D == 128 ? 3 : 5);
-  const int64_t most = static_cast<int64_t>(p.B) * p.S;
   int64_t places = (resident + Hkv - 1) / Hkv;
   if (places > most) places = most;
   st = launch_kernel(kernel, dim3(Hkv, static_cast<unsigned>(places)), dim3(kThreads), smem, stream, 1, mk, mv, p);
@@ -498,6 +546,7 @@ extern "C" kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache
   p.B = B;
   p.win = Window{window, sinks};
   p.status = device_status_word();
+  p.out = static_cast<__nv_bfloat16*>(out);
   MergeParams mp{p.ws_o, p.ws_ml, kv_len, static_cast<__nv_bfloat16*>(out), Hq, p.S, cache->slots, p.win, p.status};
   if (D == 128)
     return i8 ? launch_decode8<128, true>(p, mp, Hkv, stream) : launch_decode8<128, false>(p, mp, Hkv, stream);

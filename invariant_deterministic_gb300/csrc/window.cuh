@@ -62,6 +62,39 @@ struct MergeParams {
   int* status;
 };
 
+// The same fold by the threads of a cluster, whose block s holds partial s at the
+// shared address `at`: o [rows][D], then (m, l) [rows]; pairs < G, at most eight
+// partials, out [G][D].
+template <int D, int THREADS>
+__device__ __forceinline__ void fold_cluster(uint32_t at, int rows, int G, int rank, int blocks, int count,
+                                             __nv_bfloat16* out) {
+  for (int idx = rank * THREADS + static_cast<int>(threadIdx.x); idx < G * D; idx += blocks * THREADS) {
+    const int pair = idx / D;
+    float mv[8], lv[8], ov[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if (s < count) {
+        const uint32_t from = map_to_rank(at, s);
+        mv[s] = ld_dsmem_f32(from + (rows * D + 2 * pair) * 4);
+        lv[s] = ld_dsmem_f32(from + (rows * D + 2 * pair + 1) * 4);
+        ov[s] = ld_dsmem_f32(from + idx * 4);
+      }
+    }
+    float m_acc = -INFINITY, l_acc = 0.f, o_acc = 0.f;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if (s < count) {
+        const float m_new = fmaxf(m_acc, mv[s]);
+        const float fa = ex2_approx(__fsub_rn(m_acc, m_new)), fc = ex2_approx(__fsub_rn(mv[s], m_new));
+        l_acc = __fadd_rn(__fmul_rn(l_acc, fa), __fmul_rn(lv[s], fc));
+        o_acc = __fadd_rn(__fmul_rn(o_acc, fa), __fmul_rn(ov[s], fc));
+        m_acc = m_new;
+      }
+    }
+    out[idx] = __float2bfloat16_rn(count > 0 ? __fdiv_rn(o_acc, l_acc) : 0.f);
+  }
+}
+
 // One block per (query head, row); thread d folds column d.  A row whose length
 // is outside [0, max_len] gets zeros (the split kernel leaves it out).
 template <int D>
