@@ -144,6 +144,7 @@ def _check(status: int, where: str) -> None:
 # microseconds a call), where this PyTorch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _get_device = getattr(torch._C, "_cuda_getDevice", None)
+_INT_MAX = 2**31 - 1
 
 
 def _stream(stream=None) -> int:
@@ -347,11 +348,24 @@ def attn_decode_workspace(batch: int, n_q: int, head_dim: int, max_len: int,
     return int(lib().kinv_attn_decode_workspace(batch, n_q, head_dim, max_len, split_len))
 
 
+def _here(*named) -> None:
+    """The tensors lie on the current device, whose stream a call runs on."""
+    dev = 0 if _get_device is None else _get_device()
+    for name, t in named:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: expected a tensor on the current CUDA device, got one on {t.device}")
+
+
+def _window_ints(window: int, sinks: int) -> None:
+    if window > _INT_MAX or sinks > _INT_MAX:
+        raise ValueError("window and sinks are 32-bit numbers")
+
+
 def _rows_of(q, out, what: str) -> None:
     """q and out [rows][Hq][D], bf16 and contiguous."""
     bf = torch.bfloat16
-    if not (q.dtype is bf and q.is_cuda and q.is_contiguous() and q.dim() == 3
-            and (out is None or (out.dtype is bf and out.is_cuda and out.is_contiguous() and out.shape == q.shape))):
+    if not (q.dtype is bf and q.is_contiguous() and q.dim() == 3
+            and (out is None or (out.dtype is bf and out.is_contiguous() and out.shape == q.shape))):
         _need(q, bf, "q")
         if out is not None:
             _need(out, bf, "out")
@@ -361,7 +375,7 @@ def _rows_of(q, out, what: str) -> None:
 def _window_caches(k_cache, v_cache, batch: int, head_dim: int, what: str):
     """Checks of the windowed calls' caches: (shape, strides)."""
     bf = torch.bfloat16
-    if not (k_cache.dtype is v_cache.dtype is bf and k_cache.is_cuda and v_cache.is_cuda):
+    if not k_cache.dtype is v_cache.dtype is bf:
         _need(k_cache, bf, "k_cache")
         _need(v_cache, bf, "v_cache")
     shape, stride = k_cache.shape, k_cache.stride()
@@ -374,7 +388,7 @@ def _window_caches(k_cache, v_cache, batch: int, head_dim: int, what: str):
 
 def _vector(t, n: int, name: str) -> None:
     """An int32 vector on the device with an entry for each of n."""
-    if t.dtype is not torch.int32 or not t.is_cuda:
+    if t.dtype is not torch.int32:
         _need(t, torch.int32, name)
     if t.dim() != 1 or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous vector of at least {n} entries")
@@ -383,7 +397,7 @@ def _vector(t, n: int, name: str) -> None:
 def _workspace(side, workspace, need: int, device):
     """Scratch for a call that was given none, or none that it can use."""
     if workspace is not None:
-        raise ValueError("workspace: expected a contiguous CUDA tensor")
+        raise ValueError("workspace: expected a contiguous tensor")
     return _scratch(side, torch.empty, max(need, 16), dtype=torch.uint8, device=device)
 
 
@@ -392,11 +406,13 @@ def _attn_decode_window(q, k_cache, v_cache, kv_len, out, workspace, split_len, 
     bsz, hq, d = q.shape
     shape, stride = _window_caches(k_cache, v_cache, bsz, d, "attn_decode")
     _vector(kv_len, bsz, "kv_len")
+    _window_ints(window, sinks)
+    _here(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("kv_len", kv_len), ("out", out), ("workspace", workspace))
     lmax = shape[1]
     side = None if stream is None else _side(stream)
     if out is None:
         out = _empty_like(side)(q)
-    if workspace is None or not (workspace.is_cuda and workspace.is_contiguous()):
+    if workspace is None or not workspace.is_contiguous():
         workspace = _workspace(side, workspace, attn_decode_workspace(bsz, hq, d, lmax, split_len, window, sinks), q.device)
     if side is not None:
         _hold(side, q, k_cache, v_cache, kv_len, out, workspace)
@@ -475,6 +491,9 @@ def _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_le
     _vector(q_start, bsz, "q_start")
     _vector(q_len, bsz, "q_len")
     _vector(q_offset, bsz, "q_offset")
+    _window_ints(window, sinks)
+    _here(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("q_start", q_start), ("q_len", q_len),
+          ("q_offset", q_offset), ("out", out))
     side = None if stream is None else _side(stream)
     if out is None:
         out = _empty_like(side)(q)
@@ -536,6 +555,8 @@ class Cache8:
         for t, dt, name in ((k, k.dtype, "k"), (v, k.dtype, "v"), (k_exp, torch.int8, "k_exp"),
                             (v_exp, torch.int8, "v_exp")):
             _need(t, dt, name)
+            if t.device != k.device:
+                raise ValueError(f"Cache8: {name} is on {t.device}, k on {k.device}")
         if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride():
             raise ValueError("Cache8: the codes must be [B][slots][Hkv][D] and share shape and strides")
         bsz, slots, hkv, d = k.shape
@@ -573,7 +594,7 @@ def rope_append8(qkv, q_out, cache: Cache8, seq, pos, n_q, n_kv, head_dim, rope_
     [seq][pos]; q_out [rows][Hq][D].  A row outside the cache is left out (its q_out
     too) and recorded in the device status; no two rows may name one place."""
     bf = torch.bfloat16
-    if not (qkv.dtype is q_out.dtype is bf and qkv.is_cuda and q_out.is_cuda):
+    if not qkv.dtype is q_out.dtype is bf:
         _need(qkv, bf, "qkv")
         _need(q_out, bf, "q_out")
     (rows, width), (ld, step) = qkv.shape, qkv.stride()
@@ -583,9 +604,11 @@ def rope_append8(qkv, q_out, cache: Cache8, seq, pos, n_q, n_kv, head_dim, rope_
     _vector(seq, rows, "seq")
     _vector(pos, rows, "pos")
     for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None and not (t.dtype is bf and t.is_cuda and t.is_contiguous() and t.numel() >= head_dim):
+        if t is not None and not (t.dtype is bf and t.is_contiguous() and t.numel() >= head_dim):
             _need(t, bf, name)
             raise ValueError(f"rope_append8: {name} must hold a contiguous gain for each of a head's values")
+    _here(("qkv", qkv), ("q_out", q_out), ("cache", cache.k), ("seq", seq), ("pos", pos), ("q_norm", q_norm),
+          ("k_norm", k_norm))
     if stream is not None and (side := _side(stream)) is not None:
         _hold(side, qkv, q_out, seq, pos, q_norm, k_norm, *cache.tensors)
     _check(lib().kinv_rope_append8(qkv.data_ptr(), ld if rows > 1 else max(ld, width), q_out.data_ptr(), cache.ptr,
@@ -597,7 +620,7 @@ def rope_append8(qkv, q_out, cache: Cache8, seq, pos, n_q, n_kv, head_dim, rope_
 def _tokens(k, v, cache: Cache8, what: str):
     """Shape and strides of bf16 k, v [B][n][Hkv][D] that go into or come out of ``cache``."""
     bf = torch.bfloat16
-    if not (k.dtype is v.dtype is bf and k.is_cuda and v.is_cuda):
+    if not k.dtype is v.dtype is bf:
         _need(k, bf, "k")
         _need(v, bf, "v")
     shape, stride = k.shape, k.stride()
@@ -616,6 +639,7 @@ def cache8_write(cache: Cache8, k, v, start, length, stream=None) -> None:
     bsz, n, s0, s1 = _tokens(k, v, cache, "cache8_write")
     _vector(start, bsz, "start")
     _vector(length, bsz, "length")
+    _here(("k", k), ("v", v), ("cache", cache.k), ("start", start), ("length", length))
     if stream is not None and (side := _side(stream)) is not None:
         _hold(side, k, v, start, length, *cache.tensors)
     _check(lib().kinv_cache8_write(k.data_ptr(), v.data_ptr(), s0, s1, cache.ptr, start.data_ptr(), length.data_ptr(),
@@ -642,6 +666,7 @@ def cache8_read(cache: Cache8, start, length, n: int = 0, k=None, v=None, stream
         bsz, n, s0, s1 = _tokens(k, v, cache, "cache8_read")
     _vector(start, bsz, "start")
     _vector(length, bsz, "length")
+    _here(("k", k), ("v", v), ("cache", cache.k), ("start", start), ("length", length))
     if side is not None:
         _hold(side, k, v, start, length, *cache.tensors)
     _check(lib().kinv_cache8_read(cache.ptr, start.data_ptr(), length.data_ptr(), k.data_ptr(), v.data_ptr(), s0, s1,
@@ -664,10 +689,12 @@ def attn_decode8(q, cache: Cache8, kv_len, out=None, workspace=None, window: int
     if d != cache.head_dim:
         raise ValueError("attn_decode8: q's heads are not of the cache's size")
     _vector(kv_len, bsz, "kv_len")
+    _window_ints(window, sinks)
+    _here(("q", q), ("cache", cache.k), ("kv_len", kv_len), ("out", out), ("workspace", workspace))
     side = None if stream is None else _side(stream)
     if out is None:
         out = _empty_like(side)(q)
-    if workspace is None or not (workspace.is_cuda and workspace.is_contiguous()):
+    if workspace is None or not workspace.is_contiguous():
         workspace = _workspace(side, workspace, attn_decode8_workspace(bsz, hq, d, cache.slots, window, sinks, split_len),
                                q.device)
     if side is not None:
@@ -697,10 +724,13 @@ def attn_prefill8(q, cache: Cache8, q_start, q_len, q_offset, max_q_len: int, ma
     _vector(q_start, bsz, "q_start")
     _vector(q_len, bsz, "q_len")
     _vector(q_offset, bsz, "q_offset")
+    _window_ints(window, sinks)
+    _here(("q", q), ("cache", cache.k), ("q_start", q_start), ("q_len", q_len), ("q_offset", q_offset), ("out", out),
+          ("workspace", workspace))
     side = None if stream is None else _side(stream)
     if out is None:
         out = _empty_like(side)(q)
-    if workspace is None or not (workspace.is_cuda and workspace.is_contiguous()):
+    if workspace is None or not workspace.is_contiguous():
         workspace = _workspace(side, workspace,
                                attn_prefill8_workspace(bsz, rows, hq, cache.n_kv, d, max_kv, split_len), q.device)
     if side is not None:
