@@ -287,6 +287,84 @@ def test_long_contexts(kinv):
                          kinv.attn_decode(q, k16, v16, lens, window=20000, sinks=1000), fmt + " window")
 
 
+# ------------------------------------------- few and many splits, far addresses
+@pytest.mark.parametrize("splits", range(1, 10))
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (4, 2, 64), (8, 1, 64)])
+def test_few_and_many_sequences_of_few_splits(kinv, hq, hkv, d, splits):
+    """Up to eight splits a small batch is one launch and a large one is not: the same
+    bits, and those of attn_decode, for empty, short and out-of-range sequences too."""
+    n = splits * 256 - 9
+    lens = ([n, 1, 0, n - 1, max(n - 256, 0), 257 if n > 257 else 2] + synth.uniform_int(74, 0, n, 230 + splits).tolist())[:80]
+    k, v = keys((80, n, hkv, d), 231), keys((80, n, hkv, d), 232)
+    q = synth.normal_bf16((80, hq, d), 1.0, 233, "cuda")
+    full = kinv.attn_decode(q, k, v, i32(lens))
+    assert_same_bits(kinv.attn_decode(q, k, v, i32(lens), window=n), full, "a window of every key, large batch")
+    assert_same_bits(kinv.attn_decode(q[:6], k[:6], v[:6], i32(lens[:6]), window=n), full[:6], "a window of every key, small batch")
+    for window, sinks in ((max(n - 256, 1), 1), (40, 3)):
+        many = kinv.attn_decode(q, k, v, i32(lens), window=window, sinks=sinks)
+        for b in (0, 2, 77):
+            assert_same_bits(kinv.attn_decode(q[b: b + 3], k[b: b + 3], v[b: b + 3], i32(lens[b: b + 3]), window=window, sinks=sinks),
+                             many[b: b + 3], f"window {window}, small batch")
+    for fmt in ("e4m3", "int8"):
+        c, (k16, v16) = cache8(kinv, k, v, fmt)
+        for window, sinks in ((0, 0), (max(n - 256, 1), 1)):
+            ref = kinv.attn_decode(q, k16, v16, i32(lens), window=window, sinks=sinks)
+            assert_same_bits(kinv.attn_decode8(q, c, i32(lens), window=window, sinks=sinks), ref, fmt + " large batch")
+            for b in (0, 3):
+                assert_same_bits(kinv.attn_decode8(q[b: b + 3], c.sequences(b, b + 3), i32(lens[b: b + 3]), window=window, sinks=sinks),
+                                 ref[b: b + 3], fmt + " small batch")
+        assert kinv.last_device_status() == 0
+        c.v_exp[1, 0, 0] = -128
+        out = kinv.attn_decode8(q[:3], c.sequences(0, 3), i32([n, 1, n + 1]))
+        assert kinv.last_device_status() == kinv.ERR_INVALID_ARG
+        assert torch.isnan(out[1].view(hkv, -1)[0]).all() and (out[2] == 0).all() and not torch.isnan(out[0]).any()
+    out = kinv.attn_decode(q[:2], k[:2], v[:2], i32([-1, n + 1]), window=40, sinks=3)
+    assert kinv.last_device_status() == kinv.ERR_INVALID_ARG and (out == 0).all()
+
+
+def test_sequences_more_than_two_gigabytes_apart(kinv):
+    hq, hkv, d, n, far = 4, 2, 64, 600, 2**31 + 16 * 12345
+    k, v = keys((3, n, hkv, d), 240), keys((3, n, hkv, d), 241)
+    q = synth.normal_bf16((3, hq, d), 1.0, 242, "cuda")
+    near, (k16, v16) = cache8(kinv, k, v, "e4m3")
+    codes = [torch.empty(2 * far + n * hkv * d, dtype=torch.uint8, device="cuda").as_strided((3, n, hkv, d), (far, hkv * d, d, 1)) for _ in range(2)]
+    exps = [torch.empty(3, hkv, n, dtype=torch.int8, device="cuda") for _ in range(2)]
+    c = kinv.Cache8(*(t.view(torch.float8_e4m3fn) for t in codes), *exps)
+    zero, full = i32([0] * 3), i32([n] * 3)
+    kinv.cache8_write(c, k, v, zero, full)
+    for a, b in zip(kinv.cache8_read(c, zero, full, n), (k16, v16)):
+        assert_same_bits(a, b, "written and read")
+    lens = i32([n, 300, n - 1])
+    want = kinv.attn_decode(q, k16, v16, lens, window=400, sinks=3)
+    assert_same_bits(kinv.attn_decode8(q, c, lens, window=400, sinks=3), want, "decode8")
+    args = (i32([n - 1, 299, n - 2]), i32([1, 1, 1]), i32([0, 1, 2]), 1, n)
+    assert_same_bits(kinv.attn_prefill8(q, c, *args, window=400, sinks=3), want, "prefill8")
+    wide = [torch.empty(2 * far + n * hkv * d, dtype=torch.bfloat16, device="cuda").as_strided((3, n, hkv, d), (far, hkv * d, d, 1)) for _ in range(2)]
+    kinv.cache8_read(c, zero, full, k=wide[0], v=wide[1])
+    assert_same_bits(kinv.attn_decode(q, *wide, lens, window=400, sinks=3), want, "decode, bf16")
+    assert_same_bits(kinv.attn_prefill(q, *wide, *args, window=400, sinks=3), want, "prefill, bf16")
+    qkv = synth.normal_bf16((3, (hq + 2 * hkv) * d), 1.0, 243, "cuda")
+    qs = [torch.empty_like(q) for _ in range(2)]
+    for to, cc in zip(qs, (c, near)):
+        kinv.rope_append8(qkv, to, cc, i32([0, 1, 2]), i32([599, 0, 77]), hq, hkv, d, 1e4)
+    assert_same_bits(qs[0], qs[1], "q")
+    for a, b in zip(kinv.cache8_read(c, zero, full, n), kinv.cache8_read(near, zero, full, n)):
+        assert_same_bits(a, b, "appended")
+    assert kinv.last_device_status() == 0
+
+
+def test_prefill8_with_a_workspace_of_more_than_2_31_numbers(kinv):
+    hq, hkv, d, bsz, n = 8, 8, 128, 36, 60000
+    c = kinv.Cache8.empty(bsz, n, hkv, d, "int8")
+    for b in (0, 35):
+        x = keys((1, n, hkv, d), 250 + b)
+        kinv.cache8_write(c.sequences(b, b + 1), x, x, i32([0]), i32([n]))
+    q = synth.normal_bf16((bsz, hq, d), 1.0, 252, "cuda")
+    out = kinv.attn_prefill8(q, c, i32([n - 1] * bsz), i32([1] * bsz), i32(list(range(bsz))), 1, n)
+    assert_same_bits(out, kinv.attn_decode8(q, c, i32([n] * bsz)), "prefill8 == decode8")
+    assert kinv.last_device_status() == 0
+
+
 # --------------------------------------------------- a step, streams and graphs
 def _step(kinv, c, s, window, sinks, ws=None):
     """Append the step's rows and attend, as a decode step does."""
