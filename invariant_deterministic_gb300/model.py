@@ -391,6 +391,7 @@ class Decoder:
             self.kv[:, 0, seq, :n].copy_(k)
             self.kv[:, 1, seq, :n].copy_(v)
             return
+        k, v = (t.to(self.dev, torch.bfloat16).contiguous() for t in (k, v))
         i32 = dict(dtype=torch.int32, device=self.dev)
         start, length = torch.zeros(1, **i32), torch.full((1,), n, **i32)
         for li in range(s.n_layers):

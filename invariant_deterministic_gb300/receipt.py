@@ -174,9 +174,10 @@ def compare(receipt: dict, rerun_ids, build_id: str, device_class: str) -> str:
 
 
 def model_identity(shape, weight_seed: int) -> dict:
-    """The model fields of a record: every ModelShape field and the seed the
-    random-init weights are drawn with."""
-    return {"shape": dict(shape.__dict__), "weight_seed": int(weight_seed),
+    """The model fields of a record: every ModelShape field (the window's where
+    there is one) and the seed the random-init weights are drawn with."""
+    fields = {k: v for k, v in shape.__dict__.items() if shape.window or k not in ("window", "sinks")}
+    return {"shape": fields, "weight_seed": int(weight_seed),
             "init": "projections ~N(0, 0.02) bf16, norm gains 1"}
 
 

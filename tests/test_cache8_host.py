@@ -178,3 +178,14 @@ def test_more_sequences_than_the_cache_holds(here):
     with pytest.raises(ValueError):
         kinv.cache8_read(cache(a), a["start"], a["n"], k=a["k"])
     assert not here.calls
+
+
+def test_records_name_a_window_only_where_there_is_one():
+    from invariant_deterministic_gb300 import model, receipt
+    sizes = dict(n_layers=2, d_model=256, n_q=4, n_kv=2, head_dim=64, ffn=512, vocab=512)
+    plain, win = model.ModelShape(**sizes), model.ModelShape(**sizes, window=64, sinks=2)
+    assert not {"window", "sinks"} & (set(receipt.model_identity(plain, 0)["shape"]) | set(receipt.settings_of(plain)))
+    assert {"window": 64, "sinks": 2}.items() <= receipt.model_identity(win, 0)["shape"].items()
+    assert model.ModelShape(**receipt.model_identity(win, 0)["shape"]) == win
+    assert model.ModelShape(**receipt.model_identity(plain, 0)["shape"]) == plain
+    assert receipt.settings_of(win, "int8")["cache"] == "int8" and "cache" not in receipt.settings_of(win)

@@ -140,6 +140,11 @@ def test_prefixes_are_reused_read_and_loaded(M, weights, kind):
     other = decoder(M, weights, kind)
     other.load_prefix(1, k, v)
     assert_same_bits(other.prefill(1, prompt[260:], p0=260), whole, "loaded prefix")
+    # from the host, the values in another order of memory than the keys
+    third = decoder(M, weights, kind)
+    third.load_prefix(1, k.cpu(), v.transpose(1, 2).contiguous().transpose(1, 2))
+    for a, b in zip(third.read_prefix(1, 260), (k, v)):
+        assert_same_bits(a, b, "loaded from elsewhere")
     for bad in (dict(seq=4, n=3), dict(seq=0, n=641), dict(seq=0, n=-1)):
         with pytest.raises(ValueError):
             dec.read_prefix(**bad)
