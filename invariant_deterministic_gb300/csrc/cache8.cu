@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
 }
 
 // bf16 keys (z = 0) or values (z = 1) of `tokens` tokens of one sequence: a group
-// of D / 8 lanes per (token, head), 16 bytes a lane, four vectors a lane ahead.
+// of D / 8 lanes per (token, head), 16 bytes a lane, two vectors a lane ahead.
 // The exponents of the block go out together, one run of bytes a head.
 constexpr int kWriteThreads = 256;
 
@@ -194,7 +194,7 @@ template <int D, bool I8>
 __global__ void __launch_bounds__(kWriteThreads) cache8_write_kernel(const WriteParams p) {
   constexpr int L = D / 8;                      // lanes of a vector
   constexpr int PER = kWriteThreads / L;        // vectors at a time
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 2;
   extern __shared__ int8_t exps[];              // [Hkv][tokens]
   pdl_launch_dependents();
   pdl_wait();
