@@ -3,13 +3,13 @@
 // A row's arithmetic is that of kinv_attn_decode on the cache read back (see
 // attention.cu): 256-key splits at absolute offsets, the base-2 softmax, weights
 // carried as a bf16 pair, one fp32 chain over 16-key steps, the left fold over
-// the splits.  The codes enter the tensor cores as the bf16 numbers that
-// expand4() makes of them, and the powers of two that are missing are applied
-// where they cost least, which is exact: q is multiplied by 2^90 for e4m3 (whose
-// codes stand there times 2^-120), a score by its key's 2^E, and both halves of a
-// weight by its value's 2^(E - Emax) (Emax the split's largest) and a constant,
-// with the rest put back into the partial.  So the bits are those of attention over the
-// cache read back wherever no score, product or sum on the way leaves fp32's
+// the splits.  The codes enter the tensor cores exactly: a key's as f16 numbers, with q
+// as f16 times a power of two of the row and head; a value's as the bf16 numbers that
+// expand4() makes of them.  The powers of two that are missing are applied
+// where they cost least, which is exact: a score is multiplied by its key's 2^E, and
+// both halves of a weight by its value's 2^(E - Emax) (Emax the split's largest) and a
+// constant, with the rest put back into the partial.  So the bits are those of attention
+// over the cache read back wherever no score, product or sum on the way leaves fp32's
 // normal range.
 #include <math.h>
 
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
                        const Attn8Params p) {
   constexpr int C = D / 16;           // 16-byte chunks of a key's codes
   constexpr int TILE = kSplit * D;    // bytes of a split's K or V codes
-  constexpr int kLift = I8 ? 100 : 127;  // weights go in times 2^kLift: 256 products of 127 or 448 * 2^-120 stay below 2^127
+  constexpr int kLift = I8 ? 106 : 127;  // weights go in times 2^kLift: 256 products of 127 * 2^-6 or 448 * 2^-120 stay below 2^127
   constexpr int QROW = D * 2 + 16;    // bytes of a row of q (padded: eight rows in eight bank groups)
   constexpr int PHALF = GP * kSplit * 2;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, D == 128 ? 3 : 5)
       }
       // 2^Emax and the constants back, the smaller factor first (no intermediate
       // result is smaller than the product)
-      const float back0 = exponent_factor(min(ev_max, 0)), back1 = exponent_factor(max(ev_max, 0) + (I8 ? 0 : 120) - kLift);
+      const float back0 = exponent_factor(min(ev_max, 0)), back1 = exponent_factor(max(ev_max, 0) + expand_exp<I8>() - kLift);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = __fmul_rn(__fmul_rn(o[i], back0), back1);
       const int64_t row = static_cast<int64_t>(cur.b) * p.Hq + g * G;
