@@ -22,12 +22,10 @@ struct RopeTurns {
 // whole step.
 __device__ __forceinline__ void rope_angle_turns(int p, uint64_t turn, float& c, float& s) {
   const int64_t x = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(p)) * turn);  // signed fraction * 2^64
-  const int32_t top = static_cast<int32_t>(x >> 32);
-  const float h = static_cast<float>(top);
-  // top - h is exact (a float of 2^31 and above is a multiple of 128)
-  const float l = static_cast<float>(static_cast<int64_t>(top) - static_cast<int64_t>(h)) +
-                  static_cast<float>(static_cast<uint32_t>(x)) * 0x1p-32f;
-  constexpr double kTurn = 6.283185307179586476925 * 0x1p-32;  // radians of a unit of `top`
+  // x = (h + l) 2^40, to 2^-56 of a turn; h exact as a float, l to 2^-24 of it
+  const float h = static_cast<float>(static_cast<int32_t>(x >> 40));
+  const float l = static_cast<float>(static_cast<uint32_t>(x >> 8)) * 0x1p-32f;
+  constexpr double kTurn = 6.283185307179586476925 * 0x1p-24;  // radians of a unit of h
   constexpr float kHi = static_cast<float>(kTurn), kLo = static_cast<float>(kTurn - static_cast<double>(kHi));
   const float hi = __fmul_rn(h, kHi);
   const float d = __fmaf_rn(h, kHi, -hi) + __fmaf_rn(h, kLo, __fmul_rn(l, kHi));
@@ -39,12 +37,11 @@ __device__ __forceinline__ void rope_angle_turns(int p, uint64_t turn, float& c,
 
 // D / 16 lanes hold a head, each lane eight rotation pairs (i, i + D/2) in two 16-byte
 // loads, so a warp takes four heads of 128 (eight of 64) at a time.  A block has one
-// row, or four where there are many, whose angles its threads form together beside the
-// first loads; each warp asks for its next heads before
-// it works on the last.  One warp per head with a pair of values a lane, as
-// kinv_rope_append has it, and angles in fp64 took 37 us for 4,096 rows of the 8B shape
-// against 26 (a block per row at any number of rows: 41).
-constexpr int kAppendRows = 4;
+// row, or as many as make one wave of blocks, at most sixteen; its threads form the
+// angles together beside the first loads, and each warp asks for its next heads before
+// it works on the last.  Bound by the instructions: AT_WORK
+constexpr int kAppendRows = 16;
+constexpr int kAppendBlocks = 4;  // of 256 threads on an SM
 
 struct Append8Params {
   const __nv_bfloat16* qkv;
@@ -66,7 +63,8 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
   constexpr int HALF = D / 2;
   constexpr int L = D / 16;   // lanes of a head
   constexpr int HPW = 32 / L; // heads of a warp
-  __shared__ __align__(16) float cs[kAppendRows][HALF], sn[kAppendRows][HALF];
+  __shared__ __align__(16) float cs[kAppendRows][HALF], sn[kAppendRows][HALF], minus_sn[kAppendRows][HALF];
+  __shared__ __align__(16) float gains[2][D];  // of queries, of keys
   __shared__ int place[kAppendRows][2];  // of each row: sequence (-1: outside the cache), position
   pdl_launch_dependents();
   pdl_wait();
@@ -92,8 +90,21 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
     place[threadIdx.x][1] = p;
     if (!fits && a.status) atomicExch(a.status, DEV_CACHE8_BAD_RANGE);
   }
-  for (int i = threadIdx.x; i < n * HALF; i += blockDim.x)
-    rope_angle_turns(a.pos[r0 + i / HALF], a.turns.turn[i % HALF], cs[i / HALF][i % HALF], sn[i / HALF][i % HALF]);
+  const int at = threadIdx.x % HALF, step = blockDim.x / HALF;  // this thread's frequency, and rows at a time
+  if (threadIdx.x < step * HALF) {
+    const uint64_t turn = a.turns.turn[at];
+    for (int i = threadIdx.x / HALF; i < n; i += step) {
+      float c, sv;
+      rope_angle_turns(a.pos[r0 + i], turn, c, sv);
+      cs[i][at] = c;
+      sn[i][at] = sv;
+      minus_sn[i][at] = -sv;
+    }
+  }
+  for (int i = threadIdx.x; i < D; i += blockDim.x) {
+    if (a.q_norm) gains[0][i] = __bfloat162float(a.q_norm[i]);
+    if (a.k_norm) gains[1][i] = __bfloat162float(a.k_norm[i]);
+  }
   __syncthreads();
   // whole warps, so that every lane takes part in the shuffles
   while (row < n) {
@@ -104,45 +115,46 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
     uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};  // the head's bf16 pairs: low half, high half
     for (group += blockDim.x >> 5; group >= groups; group -= groups) ++row;
     load();
-    const __nv_bfloat16* gain = !live || value ? nullptr : h < a.Hq ? a.q_norm : a.k_norm;
-    float x[16];
+    const bool normed = live && !value && (h < a.Hq ? a.q_norm : a.k_norm) != nullptr;
+    float2 x[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[2 * j] = bf16_lo(w[j]);
-      x[2 * j + 1] = bf16_hi(w[j]);
-    }
-    if (__any_sync(0xffffffffu, gain != nullptr)) {
-      float acc = 0.f;
+    for (int j = 0; j < 8; ++j) x[j] = make_float2(bf16_lo(w[j]), bf16_hi(w[j]));
+    if (__any_sync(0xffffffffu, normed)) {
+      float2 acc2 = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) acc = fmaf(x[j], x[j], acc);
+      for (int j = 1; j < 8; ++j) acc2 = __ffma2_rn(x[j], x[j], acc2);
+      float acc = __fadd_rn(acc2.x, acc2.y);
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
-      if (gain) {
+      if (normed) {
         const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(acc, static_cast<float>(D)), a.eps)));
-        const uint4 g0 = *reinterpret_cast<const uint4*>(gain + sub * 8), g1 = *reinterpret_cast<const uint4*>(gain + HALF + sub * 8);
-        const uint32_t gw[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+        const float* g = gains[h < a.Hq ? 0 : 1] + sub * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[2 * j] = __fmul_rn(__fmul_rn(x[2 * j], inv), bf16_lo(gw[j]));
-          x[2 * j + 1] = __fmul_rn(__fmul_rn(x[2 * j + 1], inv), bf16_hi(gw[j]));
+        for (int j = 0; j < 8; j += 2) {
+          const float4 gv = *reinterpret_cast<const float4*>(g + (j < 4 ? 0 : HALF - 8) + 2 * j);
+          x[j] = __fmul2_rn(__fmul2_rn(x[j], make_float2(inv, inv)), make_float2(gv.x, gv.y));
+          x[j + 1] = __fmul2_rn(__fmul2_rn(x[j + 1], make_float2(inv, inv)), make_float2(gv.z, gv.w));
         }
       }
     }
     if (!value) {
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const float4 c = *reinterpret_cast<const float4*>(&cs[now][sub * 8 + j]),
-                     sv = *reinterpret_cast<const float4*>(&sn[now][sub * 8 + j]);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+      for (int j = 0; j < 4; j += 2) {
+        const float4 c = *reinterpret_cast<const float4*>(&cs[now][sub * 8 + 2 * j]),
+                     sv = *reinterpret_cast<const float4*>(&sn[now][sub * 8 + 2 * j]),
+                     ns = *reinterpret_cast<const float4*>(&minus_sn[now][sub * 8 + 2 * j]);
+        const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+        const float2 ss[2] = {make_float2(sv.x, sv.y), make_float2(sv.z, sv.w)};
+        const float2 nn[2] = {make_float2(ns.x, ns.y), make_float2(ns.z, ns.w)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float u = x[j + e], v = x[8 + j + e];
-          x[j + e] = __fmaf_rn(u, cc[e], -__fmul_rn(v, ss[e]));
-          x[8 + j + e] = __fmaf_rn(v, cc[e], __fmul_rn(u, ss[e]));
+        for (int e = 0; e < 2; ++e) {
+          const float2 u = x[j + e], v = x[4 + j + e];
+          x[j + e] = __ffma2_rn(u, cc[e], __fmul2_rn(v, nn[e]));
+          x[4 + j + e] = __ffma2_rn(v, cc[e], __fmul2_rn(u, ss[e]));
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+      for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[j].x, x[j].y);
     }
     if (live && h < a.Hq) {
       __nv_bfloat16* dst = a.q_out + (r * a.Hq + h) * D + sub * 8;
@@ -158,12 +170,9 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
     for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (!live || h < a.Hq) continue;
     const int E = scale_exponent<I8>(max(m & 0xFFFFu, m >> 16));
-    const float inv = encode_factor(E);
     uint32_t code[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      code[j] = encode2<I8>(bf16_lo(w[2 * j]), bf16_hi(w[2 * j]), inv) |
-                (encode2<I8>(bf16_lo(w[2 * j + 1]), bf16_hi(w[2 * j + 1]), inv) << 16);
+    for (int j = 0; j < 4; ++j) code[j] = encode4<I8>(w[2 * j], w[2 * j + 1], E);
     const int g = value ? h - a.Hq - a.Hkv : h - a.Hq;
     unsigned char* dst =
         (value ? a.cache.v : a.cache.k) + s * a.cache.seq_stride + p * a.cache.tok_stride + g * D + sub * 8;
@@ -232,11 +241,8 @@ __global__ void __launch_bounds__(kWriteThreads) cache8_write_kernel(const Write
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
       const int E = scale_exponent<I8>(max(m & 0xFFFFu, m >> 16));
-      const float inv = encode_factor(E);
       if (tok[j] < 0) continue;
-      uint2 c;
-      c.x = encode2<I8>(bf16_lo(x[j].x), bf16_hi(x[j].x), inv) | (encode2<I8>(bf16_lo(x[j].y), bf16_hi(x[j].y), inv) << 16);
-      c.y = encode2<I8>(bf16_lo(x[j].z), bf16_hi(x[j].z), inv) | (encode2<I8>(bf16_lo(x[j].w), bf16_hi(x[j].w), inv) << 16);
+      const uint2 c = make_uint2(encode4<I8>(x[j].x, x[j].y, E), encode4<I8>(x[j].z, x[j].w, E));
       *reinterpret_cast<uint2*>(dst + tok[j] * p.cache.tok_stride + head[j] * D) = c;
       if (sub == 0) exps[head[j] * p.tokens + tok[j]] = static_cast<int8_t>(E);
     }
@@ -292,10 +298,13 @@ extern "C" kinv_status kinv_rope_append8(const void* qkv, int64_t ld_qkv, void* 
                   rope_turns(rope_base, D), device_status_word()};
   const int per_warp = 32 / (D / 16);
   int warps = (Hq + 2 * Hkv + per_warp - 1) / per_warp;
-  if (rows >= 1024) {  // several rows on every SM
-    p.rows_per_block = kAppendRows;
-    warps = warps * kAppendRows < 8 ? warps * kAppendRows : 8;
+  const int resident = kAppendBlocks * sm_count();
+  if (rows > resident) {
+    const int64_t a_wave = static_cast<int64_t>(resident) * kAppendRows, waves = (rows + a_wave - 1) / a_wave;
+    p.rows_per_block = static_cast<int>((rows + resident * waves - 1) / (resident * waves));
+    warps = warps * p.rows_per_block < 8 ? warps * p.rows_per_block : 8;
   }
+  if (warps < D / 64) warps = D / 64;  // a thread for each of a row's angles
   auto run = [&](auto kernel) {
     return launch_kernel(kernel, dim3((rows + p.rows_per_block - 1) / p.rows_per_block), dim3(32 * (warps < 16 ? warps : 16)), 0,
                          stream, 1, p);

@@ -59,19 +59,28 @@ __device__ __forceinline__ float exponent_factor(int E) {
   return E == kExpNaN ? __int_as_float(0x7FFFFFFF) : __int_as_float(max(E + 127, 0) << 23);
 }
 
-// The codes of x0, x1 (bf16 values, `inv` = 2^-E or 0 for a marked vector), the first in the low byte.
+// The codes of four bf16 values (two words of pairs) with exponent E, the first in the
+// low byte.  int8: x * 2^-E + 1.5 * 2^23 is rounded to an integer whose low byte is the
+// code; only a vector with the largest E can reach 128.
 template <bool I8>
-__device__ __forceinline__ uint32_t encode2(float x0, float x1, float inv) {
-  if (inv == 0.f) return 0u;
-  const float y0 = __fmul_rn(x0, inv), y1 = __fmul_rn(x1, inv);
+__device__ __forceinline__ uint32_t encode4(uint32_t w0, uint32_t w1, int E) {
+  if (E == kExpNaN) return 0u;
+  const float inv = __int_as_float((127 - E) << 23);
+  const float2 inv2 = make_float2(inv, inv);
+  const float2 x = make_float2(bf16_lo(w0), bf16_hi(w0)), y = make_float2(bf16_lo(w1), bf16_hi(w1));
   if (I8) {
-    const int a = min(max(__float2int_rn(y0), -127), 127), b = min(max(__float2int_rn(y1), -127), 127);
-    return (static_cast<uint32_t>(a) & 0xFFu) | ((static_cast<uint32_t>(b) & 0xFFu) << 8);
+    const float2 half = make_float2(12582912.f, 12582912.f);
+    float2 a = __ffma2_rn(x, inv2, half), b = __ffma2_rn(y, inv2, half);
+    if (E == exp_max<true>()) {
+      a = make_float2(fminf(fmaxf(a.x, 12582912.f - 127.f), 12582912.f + 127.f), fminf(fmaxf(a.y, 12582912.f - 127.f), 12582912.f + 127.f));
+      b = make_float2(fminf(fmaxf(b.x, 12582912.f - 127.f), 12582912.f + 127.f), fminf(fmaxf(b.y, 12582912.f - 127.f), 12582912.f + 127.f));
+    }
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
   }
-  return __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+  return __nv_cvt_float2_to_fp8x2(__fmul2_rn(x, inv2), __NV_SATFINITE, __NV_E4M3) |
+         (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(__fmul2_rn(y, inv2), __NV_SATFINITE, __NV_E4M3)) << 16);
 }
-
-__device__ __forceinline__ float encode_factor(int E) { return E == kExpNaN ? 0.f : __int_as_float((127 - E) << 23); }
 
 // Four codes (a word) as two bf16 pairs: bytes 0 and 2, and bytes 1 and 3.
 // e4m3 s eeee mmm becomes the bf16 bits s 0000eeee mmm0000, which is the code's
