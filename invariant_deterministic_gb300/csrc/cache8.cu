@@ -66,6 +66,8 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
   __shared__ __align__(16) float cs[kAppendRows][HALF], sn[kAppendRows][HALF], minus_sn[kAppendRows][HALF];
   __shared__ __align__(16) float gains[2][D];  // of queries, of keys
   __shared__ int place[kAppendRows][2];  // of each row: sequence (-1: outside the cache), position
+  // where number i of a half stands: the lanes' first four beside each other, then their others
+  auto slot = [](int i) { return (i >> 2 & 1) * (HALF / 2) + (i >> 3) * 4 + (i & 3); };
   pdl_launch_dependents();
   pdl_wait();
   const int r0 = blockIdx.x * a.rows_per_block, n = min(a.rows_per_block, a.rows - r0);
@@ -96,14 +98,15 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
     for (int i = threadIdx.x / HALF; i < n; i += step) {
       float c, sv;
       rope_angle_turns(a.pos[r0 + i], turn, c, sv);
-      cs[i][at] = c;
-      sn[i][at] = sv;
-      minus_sn[i][at] = -sv;
+      cs[i][slot(at)] = c;
+      sn[i][slot(at)] = sv;
+      minus_sn[i][slot(at)] = -sv;
     }
   }
   for (int i = threadIdx.x; i < D; i += blockDim.x) {
-    if (a.q_norm) gains[0][i] = __bfloat162float(a.q_norm[i]);
-    if (a.k_norm) gains[1][i] = __bfloat162float(a.k_norm[i]);
+    const int to = i / HALF * HALF + slot(i % HALF);
+    if (a.q_norm) gains[0][to] = __bfloat162float(a.q_norm[i]);
+    if (a.k_norm) gains[1][to] = __bfloat162float(a.k_norm[i]);
   }
   __syncthreads();
   // whole warps, so that every lane takes part in the shuffles
@@ -128,10 +131,10 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
       for (int o = L / 2; o > 0; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
       if (normed) {
         const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(acc, static_cast<float>(D)), a.eps)));
-        const float* g = gains[h < a.Hq ? 0 : 1] + sub * 8;
+        const float* g = gains[h < a.Hq ? 0 : 1] + sub * 4;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const float4 gv = *reinterpret_cast<const float4*>(g + (j < 4 ? 0 : HALF - 8) + 2 * j);
+          const float4 gv = *reinterpret_cast<const float4*>(g + j / 2 * (HALF / 2));
           x[j] = __fmul2_rn(__fmul2_rn(x[j], make_float2(inv, inv)), make_float2(gv.x, gv.y));
           x[j + 1] = __fmul2_rn(__fmul2_rn(x[j + 1], make_float2(inv, inv)), make_float2(gv.z, gv.w));
         }
@@ -140,9 +143,9 @@ __global__ void __launch_bounds__(512, 2) rope_append8_kernel(const __grid_const
     if (!value) {
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
-        const float4 c = *reinterpret_cast<const float4*>(&cs[now][sub * 8 + 2 * j]),
-                     sv = *reinterpret_cast<const float4*>(&sn[now][sub * 8 + 2 * j]),
-                     ns = *reinterpret_cast<const float4*>(&minus_sn[now][sub * 8 + 2 * j]);
+        const float4 c = *reinterpret_cast<const float4*>(&cs[now][sub * 4 + j / 2 * (HALF / 2)]),
+                     sv = *reinterpret_cast<const float4*>(&sn[now][sub * 4 + j / 2 * (HALF / 2)]),
+                     ns = *reinterpret_cast<const float4*>(&minus_sn[now][sub * 4 + j / 2 * (HALF / 2)]);
         const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
         const float2 ss[2] = {make_float2(sv.x, sv.y), make_float2(sv.z, sv.w)};
         const float2 nn[2] = {make_float2(ns.x, ns.y), make_float2(ns.z, ns.w)};
