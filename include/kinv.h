@@ -313,7 +313,9 @@ kinv_status kinv_attn_prefill(const void* q, const void* k_cache, const void* v_
  * get NaN as well, as in kinv_attn_prefill.
  * Arguments, requirements and errors as above; window < 0 or sinks < 0:
  * KINV_ERR_INVALID_ARG.  The decode call's workspace grows with the window and
- * the sinks instead of Lmax. */
+ * the sinks instead of Lmax.  The prefill call needs none (NULL); with as many bytes as
+ * its query says (0 where it would not help) it spreads short chunks over long contexts
+ * over the whole GPU, with the same bits. */
 size_t kinv_attn_decode_window_workspace(int B, int Hq, int D, int Lmax, int split_len, int window, int sinks);
 kinv_status kinv_attn_decode_window(const void* q, const void* k_cache, const void* v_cache,
                                     int64_t seq_stride, int64_t tok_stride,
@@ -321,6 +323,8 @@ kinv_status kinv_attn_decode_window(const void* q, const void* k_cache, const vo
                                     int B, int Hq, int Hkv, int D, int Lmax, int split_len,
                                     int window, int sinks, float scale, void* workspace,
                                     size_t workspace_bytes, kinv_stream stream);
+size_t kinv_attn_prefill_window_workspace(int B, int max_q_len, int Hq, int Hkv, int D, int max_kv,
+                                          int split_len, int window, int sinks);
 kinv_status kinv_attn_prefill_window(const void* q, const void* k_cache, const void* v_cache,
                                      int64_t seq_stride, int64_t tok_stride,
                                      const int32_t* q_start, const int32_t* q_len,
@@ -407,7 +411,9 @@ kinv_status kinv_cache8_read(const kinv_cache8* cache, const int32_t* start, con
  * requirements and errors as there.  workspace: device, 16-byte aligned, as many
  * bytes as the query says; calls that may run at the same time need one each.
  * The decode call's holds the split partials; the prefill call's holds the keys
- * and values that its rows see, read back: B max_kv Hkv D 4 bytes. */
+ * and values that its rows see, read back, B max_kv Hkv D 4 bytes, without which it
+ * refuses, and behind them, where the chunk is short, what kinv_attn_prefill_window may
+ * use. */
 size_t kinv_attn_decode8_workspace(int B, int Hq, int D, int slots, int window, int sinks, int split_len);
 kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache, const int32_t* kv_len, void* out,
                               int B, int Hq, int Hkv, int D, int split_len, int window, int sinks,

@@ -553,12 +553,19 @@ extern "C" kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache
   return i8 ? launch_decode8<64, true>(p, mp, Hkv, stream) : launch_decode8<64, false>(p, mp, Hkv, stream);
 }
 
+namespace kinv {
+namespace {
+size_t read_back_bytes(int B, int max_kv, int Hkv, int D) { return static_cast<size_t>(B) * max_kv * Hkv * D * 4; }
+}  // namespace
+}  // namespace kinv
+
 // A prompt chunk: the keys and values that its rows see, read back into the
 // workspace, then kinv_attn_prefill's kernel.
 extern "C" size_t kinv_attn_prefill8_workspace(int B, int total_rows, int Hq, int Hkv, int D, int max_kv,
                                                int split_len) {
   if (B <= 0 || total_rows <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_kv <= 0 || split_len != kSplit) return 0;
-  return static_cast<size_t>(B) * max_kv * Hkv * D * 4;
+  return read_back_bytes(B, max_kv, Hkv, D) +
+         kinv_attn_prefill_window_workspace(B, total_rows, Hq, Hkv, D, max_kv, split_len, 0, 0);
 }
 
 extern "C" kinv_status kinv_attn_prefill8(const void* q, const kinv_cache8* cache, const int32_t* q_start,
@@ -578,7 +585,7 @@ extern "C" kinv_status kinv_attn_prefill8(const void* q, const kinv_cache8* cach
   const int tile_rows = 128 / (Hq / Hkv);  // of the prefill kernel, which counts its tiles in an int
   if (B > 65535 || (static_cast<int64_t>(max_q_len) + tile_rows - 1) / tile_rows * Hkv * B > 0x7F000000)
     return KINV_ERR_UNSUPPORTED;
-  const size_t need = kinv_attn_prefill8_workspace(B, total_rows, Hq, Hkv, D, max_kv, split_len);
+  const size_t need = read_back_bytes(B, max_kv, Hkv, D);
   if (ws_bytes < need) return KINV_ERR_WORKSPACE;
   r.k = static_cast<__nv_bfloat16*>(workspace);
   r.v = r.k + need / 4;
@@ -594,6 +601,6 @@ extern "C" kinv_status kinv_attn_prefill8(const void* q, const kinv_cache8* cach
   st = launch_cache8_read(r, cache->dtype == KINV_I8, B, D, stream);
   if (st != KINV_OK) return st;
   return kinv_attn_prefill_window(q, r.k, r.v, r.seq_stride, r.tok_stride, q_start, q_len, q_offset, out, B,
-                                  total_rows, max_q_len, max_kv, Hq, Hkv, D, split_len, window, sinks, scale, nullptr,
-                                  0, stream);
+                                  total_rows, max_q_len, max_kv, Hq, Hkv, D, split_len, window, sinks, scale,
+                                  static_cast<char*>(workspace) + need, ws_bytes - need, stream);
 }

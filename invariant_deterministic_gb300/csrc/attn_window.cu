@@ -14,6 +14,12 @@
 // the tile before (a block per tile left about 5 of 31 us between tiles of six
 // splits).
 //
+// Few tiles over many splits (a short chunk behind a long context) would leave most
+// SMs without work, and a row's fold is one chain.  There (PARTS) the steps of all tiles
+// are dealt to the blocks in equal runs, counted on the device; a step leaves its
+// partial in the workspace, columns by pairs so that a warp's stores are whole lines,
+// and prefill_fold_kernel folds the partials in the same order: the same bits.
+//
 // Roles (608 threads).  Warps 0-15: four threads per pair (TMEM lane = pair),
 // quarter w / 4 taking the 32-key groups w / 4 and w / 4 + 4 of each split and D / 4
 // columns of the fold; they exchange raw maxima and 32-key sums through shared
@@ -61,58 +67,123 @@ struct Args {
   float c2;               // fp32(scale * log2 e) > 0
   int* status;
   Window win;
+  float* parts;           // PARTS: [step][D / 4][128 pairs][4] ...
+  float2* parts_ml;       // ... and (m, l), [step][128 pairs]
 };
+
+// At most this many tiles are spread over the GPU by their splits (a quarter of its
+// SMs), from this many splits on: 
+constexpr int kFewTiles = 38, kFewSplits = 4;
 
 // One step of a block: a split of a tile.
 struct Step {
   int b, g, row0, nrows, len0;  // rows of q / out; row r sees keys below len0 + r
   int lo, it, ns;               // the first row's first window key; step it of ns of the tile
+  bool fresh;                   // the block's first step of the tile
   SplitList list;
   __device__ int k0() const { return list.split(it) * kSplit; }
   __device__ int len_last() const { return len0 + nrows - 1; }
 };
 
+// Tile `at` in the order of the walk (whose tiles get shorter), or false: a tile behind
+// its sequence's rows, or a sequence whose device-side numbers break the stated bounds.
+__device__ __forceinline__ bool tile_at(const Args& a, int at, Step& s) {
+  const int per = a.Hkv * a.B, rank = at / per, rest = at - rank * per;
+  const int tile = a.tiles_per_seq - 1 - rank;
+  s.g = rest % a.Hkv;
+  s.b = rest / a.Hkv;
+  const int n = a.q_len[s.b], st0 = a.q_start[s.b], off = a.q_offset[s.b];
+  if (!(n >= 0 && n <= a.max_q_len && st0 >= 0 && st0 <= a.max_len - n && off >= 0 && off <= a.total_rows - n)) {
+    if (threadIdx.x == 0 && tile == 0 && a.status) atomicExch(a.status, DEV_ATTN_BAD_LENGTH);
+    return false;
+  }
+  const int first = tile * a.RT;
+  if (first >= n) return false;
+  s.nrows = min(a.RT, n - first);
+  s.row0 = off + first;
+  s.len0 = st0 + first + 1;
+  s.lo = window_lo(a.win, s.len0);
+  s.list = visible_splits(a.win, s.lo, s.len_last());
+  s.ns = s.list.count;
+  return true;
+}
+
+__device__ __forceinline__ int lane_tile_splits(const Args& a, int at, int tiles) {
+  Step s;
+  return at < tiles && tile_at(a, at, s) ? s.ns : 0;
+}
+
 // The block's steps in order.  Round r of the blocks over the tiles runs forwards
 // for even r, backwards for odd r: the tiles get shorter, and who had the longest
-// of one round gets the shortest of the next.
+// of one round gets the shortest of the next.  PARTS: steps begin .. end - 1 of all
+// tiles' steps one behind the other.
+template <bool PARTS>
 struct Walk {
   const Args& a;
-  int round;
+  int round;           // PARTS: the tile
+  int at_step, left;   // PARTS: the step among all tiles' steps; how many follow it
   Step s;
-  __device__ explicit Walk(const Args& args) : a(args), round(0) { s.it = s.ns = 0; }
+  __device__ explicit Walk(const Args& args) : a(args), round(0), at_step(0), left(0) {
+    s.it = s.ns = 0;
+    if (PARTS) {
+      const int lane = threadIdx.x & 31, tiles = a.tiles_per_seq * a.Hkv * a.B;
+      const int n0 = lane_tile_splits(a, lane, tiles), n1 = lane_tile_splits(a, lane + 32, tiles);
+      int i0 = n0, i1 = n1;  // inclusive sums
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u0 = __shfl_up_sync(0xffffffffu, i0, o), u1 = __shfl_up_sync(0xffffffffu, i1, o);
+        if (lane >= o) {
+          i0 += u0;
+          i1 += u1;
+        }
+      }
+      i1 += __shfl_sync(0xffffffffu, i0, 31);
+      const int64_t all = __shfl_sync(0xffffffffu, i1, 31);
+      const int begin = static_cast<int>(all * blockIdx.x / gridDim.x);
+      left = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x) - begin;
+      // the tile that holds step `begin`: the first whose inclusive sum is above it
+      const int tile = __popc(__ballot_sync(0xffffffffu, i0 <= begin)) + __popc(__ballot_sync(0xffffffffu, i1 <= begin));
+      const int excl0 = __shfl_sync(0xffffffffu, i0 - n0, tile & 31), excl1 = __shfl_sync(0xffffffffu, i1 - n1, tile & 31);
+      at_step = begin - 1;
+      round = tile;
+      if (left > 0) {
+        tile_at(a, tile, s);
+        s.it = begin - (tile < 32 ? excl0 : excl1) - 1;
+        s.fresh = false;
+        first = true;
+      }
+    }
+  }
+  bool first = false;  // PARTS: no step yet
   __device__ bool next() {
+    if (PARTS) {
+      if (left <= 0) return false;
+      --left;
+      ++at_step;
+      s.fresh = first;
+      first = false;
+      if (++s.it < s.ns) return true;
+      while (!tile_at(a, ++round, s)) {}  // one follows: steps are left
+      s.it = 0;
+      s.fresh = true;
+      return true;
+    }
+    s.fresh = false;
     if (++s.it < s.ns) return true;
     const int grid = gridDim.x, total = a.tiles_per_seq * a.Hkv * a.B;
     for (;; ++round) {
       if (static_cast<int64_t>(round) * grid >= total) return false;
       const int at = round * grid + (round & 1 ? grid - 1 - static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x));
-      if (at >= total) continue;
-      const int per = a.Hkv * a.B, rank = at / per, rest = at - rank * per;
-      const int tile = a.tiles_per_seq - 1 - rank;
-      s.g = rest % a.Hkv;
-      s.b = rest / a.Hkv;
-      const int n = a.q_len[s.b], st0 = a.q_start[s.b], off = a.q_offset[s.b];
-      // the sequence's device-side numbers within the stated bounds, else left out
-      if (!(n >= 0 && n <= a.max_q_len && st0 >= 0 && st0 <= a.max_len - n && off >= 0 && off <= a.total_rows - n)) {
-        if (threadIdx.x == 0 && tile == 0 && a.status) atomicExch(a.status, DEV_ATTN_BAD_LENGTH);
-        continue;
-      }
-      const int first = tile * a.RT;
-      if (first >= n) continue;
-      s.nrows = min(a.RT, n - first);
-      s.row0 = off + first;
-      s.len0 = st0 + first + 1;
-      s.lo = window_lo(a.win, s.len0);
-      s.list = visible_splits(a.win, s.lo, s.len_last());
-      s.ns = s.list.count;
+      if (at >= total || !tile_at(a, at, s)) continue;
       s.it = 0;
+      s.fresh = true;
       ++round;
       return true;
     }
   }
 };
 
-template <int D>
+template <int D, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prefill_window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                                const __grid_constant__ CUtensorMap tmV, const Args a) {
@@ -159,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();  // after the TMEM allocation (see the GEMM kernels)
   pdl_wait();
   int* status = a.status;
-  Walk walk(a);
+  Walk<PARTS> walk(a);
 
   if (warp == 17) {
     // ---- Q and K, as early as their place is free: K half i when half i - 3's R is
@@ -171,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int half = 0, q_loads = 0;
       bool ok = true;
       while (ok && walk.next()) {
-        if (walk.s.it == 0) {
+        if (walk.s.fresh) {
           if (half > 0) ok = !*abort_flag && mbar_wait_bounded(k_empty(half - 1), ((half - 1) / 3) & 1, status, DEV_TIMEOUT_ATTN);
           if (!ok) break;
           mbar_arrive_expect_tx(q_full, Q_BYTES);
@@ -313,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int st = 0; ok && (more || st > 0); ++st) {
         const bool last = !(more = more && walk.next());
-        if (!last) scores(walk.s.it == 0);
+        if (!last) scores(walk.s.fresh);
         products(st, 0);
         if (!last) {
           scores(false);
@@ -365,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       l_acc = 0.f;
     };
     // folds step sf (maximum mf; whether the pair saw a key) into the running state,
-    // this thread's columns of O, once its products are done
-    auto fold = [&](int sf, float mf, bool in) {
+    // this thread's columns of O, once its products are done; PARTS: stores it as partial `part`
+    auto fold = [&](int sf, float mf, bool in, int64_t part, int nrows) {
       wait(o_full, sf & 1);
       uint32_t v[DQ];
       const uint32_t col = lane_base + 384 + static_cast<uint32_t>(quarter * DQ);
@@ -376,12 +447,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(col, v);
       tc_fence_before();
       mbar_arrive(o_free);
-      if (!in) return;
+      if (!in || (PARTS && (!ok || r >= nrows))) return;
+      if (PARTS) {
+        float4* to = reinterpret_cast<float4*>(a.parts) + (part * (D / 4) + quarter * (DQ / 4)) * kPairs + pr;
+#pragma unroll
+        for (int d = 0; d < DQ; d += 4)
+          to[d / 4 * kPairs] = make_float4(__uint_as_float(v[d]), __uint_as_float(v[d + 1]), __uint_as_float(v[d + 2]),
+                                           __uint_as_float(v[d + 3]));
+        if (quarter != 0) return;
+      }
       // l: the eight groups' sums in order
       const float* w = x_w + (sf & 1) * 8 * kPairs + pr;
       float lf = w[0];
 #pragma unroll
       for (int q = 1; q < 8; ++q) lf = __fadd_rn(lf, w[q * kPairs]);
+      if (PARTS) {
+        a.parts_ml[part * kPairs + pr] = make_float2(mf, lf);
+        return;
+      }
       const float m_new = fmaxf(m_acc, mf);
       const float fa = ex2_approx(__fsub_rn(m_acc, m_new));
       const float fc = ex2_approx(__fsub_rn(mf, m_new));
@@ -494,8 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(p_full(h));
         // step s - 1's sums and maximum were published by this step's barrier
         if (h == 0 && s > 0) {
-          fold(s - 1, m_prev, in_prev);
-          if (walk.s.it == 0) {
+          fold(s - 1, m_prev, in_prev, walk.at_step - 1, prev_nrows);
+          if (!PARTS && walk.s.fresh) {
             finish(prev_row0, prev_nrows, prev_g);
             begin();
           }
@@ -508,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       prev_g = walk.s.g;
     }
     if (!left && s > 0 && !quad_sync_or(!ok || *abort_flag)) {
-      fold(s - 1, m_prev, in_prev);
-      finish(prev_row0, prev_nrows, prev_g);
+      fold(s - 1, m_prev, in_prev, walk.at_step, prev_nrows);
+      if (!PARTS) finish(prev_row0, prev_nrows, prev_g);
     }
   }
   tc_fence_before();
@@ -520,6 +603,71 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Folds a tile's partials, left to right, and writes its rows: a thread per pair and
+// four columns, whose next four partials are on the way while it folds.
+constexpr int kFoldThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kFoldThreads) prefill_fold_kernel(const Args a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, pr = threadIdx.x % kPairs;
+  const int col4 = blockIdx.y * (kFoldThreads / kPairs) + threadIdx.x / kPairs;
+  int before = 0;  // steps of the tiles before this one
+#pragma unroll
+  for (int j = 0; j < 2; ++j) before += lane_tile_splits(a, lane + 32 * j, blockIdx.x);
+  before = __reduce_add_sync(0xffffffffu, before);
+  Step s;
+  if (!tile_at(a, blockIdx.x, s)) return;
+  const int r = pr / a.G, head = pr % a.G;
+  if (r >= s.nrows) return;
+  const float4* o = reinterpret_cast<const float4*>(a.parts) + (static_cast<int64_t>(before) * (D / 4) + col4) * kPairs + pr;
+  const float2* ml = a.parts_ml + static_cast<int64_t>(before) * kPairs + pr;
+  const int len = s.len0 + r, first = window_lo(a.win, len);
+  float m_acc = -INFINITY, l_acc = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int CH = 4;
+  for (int i0 = 0; i0 < s.ns; i0 += CH) {
+    float4 ov[CH];
+    float2 mlv[CH];
+    bool in[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int k0 = s.list.split(i0 + i) * kSplit;
+      // the row sees a key of the split
+      in[i] = i0 + i < s.ns && k0 < len && (first < k0 + kSplit || a.win.sinks > k0);
+      if (in[i]) {
+        ov[i] = o[static_cast<int64_t>(i0 + i) * (D / 4) * kPairs];
+        mlv[i] = ml[static_cast<int64_t>(i0 + i) * kPairs];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (!in[i]) continue;
+      const float m_new = fmaxf(m_acc, mlv[i].x);
+      const float fa = ex2_approx(__fsub_rn(m_acc, m_new)), fc = ex2_approx(__fsub_rn(mlv[i].x, m_new));
+      l_acc = __fadd_rn(__fmul_rn(l_acc, fa), __fmul_rn(mlv[i].y, fc));
+      acc.x = __fadd_rn(__fmul_rn(acc.x, fa), __fmul_rn(ov[i].x, fc));
+      acc.y = __fadd_rn(__fmul_rn(acc.y, fa), __fmul_rn(ov[i].y, fc));
+      acc.z = __fadd_rn(__fmul_rn(acc.z, fa), __fmul_rn(ov[i].z, fc));
+      acc.w = __fadd_rn(__fmul_rn(acc.w, fa), __fmul_rn(ov[i].w, fc));
+      m_acc = m_new;
+    }
+  }
+  __nv_bfloat16* dst = a.out + (static_cast<int64_t>(s.row0 + r) * a.Hq + s.g * a.G + head) * D + col4 * 4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(__fdiv_rn(acc.x, l_acc), __fdiv_rn(acc.y, l_acc)),
+                                              pack_bf16(__fdiv_rn(acc.z, l_acc), __fdiv_rn(acc.w, l_acc)));
+}
+
+// Steps that the tiles of a call can have in all, or 0 where they stay whole.
+int64_t parts_steps(int64_t tiles, int RT, int window, int sinks, int max_kv) {
+  const int64_t rows = window > 0 ? static_cast<int64_t>(window) + RT - 1 : 0;  // keys that some row of a tile has in its window
+  const int64_t splits = max_visible_splits(static_cast<int>(rows < 0x7FFFFFFF ? rows : 0x7FFFFFFF), sinks, max_kv);
+  return tiles > kFewTiles || splits < kFewSplits ? 0 : tiles * splits;
+}
+
+constexpr size_t part_bytes(int D) { return static_cast<size_t>(kPairs) * (D * 4 + 8); }
+
 template <int D>
 constexpr size_t window_smem_bytes() {
   return 1024 + 6 * static_cast<size_t>(D / 64) * kPairs * 128 +
@@ -528,7 +676,7 @@ constexpr size_t window_smem_bytes() {
 
 template <int D>
 kinv_status launch_window(const void* q, const void* k_cache, const void* v_cache, int64_t seq_stride,
-                          int64_t tok_stride, const Args& a, cudaStream_t stream) {
+                          int64_t tok_stride, const Args& a, int64_t steps, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
   const uint64_t qd[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.total_rows)};
   const uint64_t qs[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.Hq) * D * 2};
@@ -544,11 +692,19 @@ kinv_status launch_window(const void* q, const void* k_cache, const void* v_cach
       !encode_map(&mv, v_cache, 4, kd, ks, kb))
     return KINV_ERR_UNSUPPORTED;
   constexpr size_t smem = window_smem_bytes<D>();
-  const kinv_status attr = ensure_smem(reinterpret_cast<const void*>(attn_prefill_window_kernel<D>), smem);
-  if (attr != KINV_OK) return attr;
   const int tiles = a.tiles_per_seq * a.Hkv * a.B, sms = sm_count();
-  return launch_kernel(attn_prefill_window_kernel<D>, dim3(tiles < sms ? tiles : sms), dim3(kThreads), smem, stream, 1,
-                       mq, mk, mv, a);
+  if (a.parts) {
+    auto kernel = attn_prefill_window_kernel<D, true>;
+    kinv_status st = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (st != KINV_OK) return st;
+    st = launch_kernel(kernel, dim3(steps < sms ? static_cast<int>(steps) : sms), dim3(kThreads), smem, stream, 1, mq, mk, mv, a);
+    if (st != KINV_OK) return st;
+    return launch_kernel(prefill_fold_kernel<D>, dim3(tiles, D / 4 / (kFoldThreads / kPairs)), dim3(kFoldThreads), 0, stream, 1, a);
+  }
+  auto kernel = attn_prefill_window_kernel<D, false>;
+  const kinv_status st = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
+  if (st != KINV_OK) return st;
+  return launch_kernel(kernel, dim3(tiles < sms ? tiles : sms), dim3(kThreads), smem, stream, 1, mq, mk, mv, a);
 }
 
 }  // namespace
@@ -562,8 +718,6 @@ extern "C" kinv_status kinv_attn_prefill_window(const void* q, const void* k_cac
                                                 int total_rows, int max_q_len, int max_kv, int Hq, int Hkv, int D,
                                                 int split_len, int window, int sinks, float scale, void* workspace,
                                                 size_t ws_bytes, kinv_stream stream) {
-  (void)ws_bytes;
-  (void)workspace;  // the splits are folded on chip
   if (B < 0 || total_rows < 0 || max_q_len < 0 || max_kv < 0 || window < 0 || sinks < 0) return KINV_ERR_INVALID_ARG;
   if (B == 0 || total_rows == 0 || max_q_len == 0) return KINV_OK;
   if (!q || !k_cache || !v_cache || !out || !q_start || !q_len || !q_offset || max_kv <= 0) return KINV_ERR_INVALID_ARG;
@@ -573,7 +727,8 @@ extern "C" kinv_status kinv_attn_prefill_window(const void* q, const void* k_cac
   if ((D != 64 && D != 128) || split_len != kSplit) return KINV_ERR_UNSUPPORTED;
   if (tok_stride < static_cast<int64_t>(Hkv) * D || seq_stride < 0 || (B > 1 && seq_stride == 0))
     return KINV_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || seq_stride % 8 || tok_stride % 8)
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || seq_stride % 8 || tok_stride % 8 ||
+      !aligned16(workspace))
     return KINV_ERR_ALIGNMENT;
   Args a{};
   a.q_start = q_start;
@@ -594,6 +749,26 @@ extern "C" kinv_status kinv_attn_prefill_window(const void* q, const void* k_cac
   // the tiles are counted in an int
   if (B > 65535 || static_cast<int64_t>(a.tiles_per_seq) * Hkv * B > 0x7F000000) return KINV_ERR_UNSUPPORTED;
   a.status = device_status_word();
-  return D == 128 ? launch_window<128>(q, k_cache, v_cache, seq_stride, tok_stride, a, stream)
-                  : launch_window<64>(q, k_cache, v_cache, seq_stride, tok_stride, a, stream);
+  const int64_t steps = parts_steps(static_cast<int64_t>(a.tiles_per_seq) * Hkv * B, a.RT, window, sinks, max_kv);
+  if (steps > 0 && workspace && ws_bytes >= steps * part_bytes(D)) {
+    a.parts = static_cast<float*>(workspace);
+    a.parts_ml = reinterpret_cast<float2*>(a.parts + steps * kPairs * D);
+  }
+  return D == 128 ? launch_window<128>(q, k_cache, v_cache, seq_stride, tok_stride, a, steps, stream)
+                  : launch_window<64>(q, k_cache, v_cache, seq_stride, tok_stride, a, steps, stream);
+}
+
+extern "C" size_t kinv_attn_prefill_window_workspace(int B, int max_q_len, int Hq, int Hkv, int D, int max_kv,
+                                                     int split_len, int window, int sinks) {
+  if (B <= 0 || max_q_len <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_kv <= 0 || window < 0 || sinks < 0 ||
+      split_len != kSplit)
+    return 0;
+  const int G = Hq / Hkv;
+  if (G > 8) return 0;
+  // the largest of a call with up to max_q_len rows of a sequence: as many tiles of each as are spread
+  const int RT = kPairs / G;
+  int64_t per_seq = (static_cast<int64_t>(max_q_len) + RT - 1) / RT;
+  const int64_t most = kFewTiles / (static_cast<int64_t>(Hkv) * B);
+  if (per_seq > most) per_seq = most;
+  return static_cast<size_t>(parts_steps(per_seq * Hkv * B, RT, window, sinks, max_kv)) * part_bytes(D);
 }

@@ -68,6 +68,7 @@ SIGNATURES = {
                                        _i32, _i32, _i32, _f32, _c_p, _sz, _c_p]),
     "kinv_attn_prefill_window": (_i32, [_c_p, _c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _c_p, _i32, _i32, _i32,
                                         _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _c_p, _sz, _c_p]),
+    "kinv_attn_prefill_window_workspace": (_sz, [_i32] * 9),
     "kinv_rope_append8": (_i32, [_c_p, _i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _f32, _i32, _i32, _i32, _i32,
                                  _f32, _c_p]),
     "kinv_cache8_write": (_i32, [_c_p, _c_p, _i64, _i64, _c_p, _c_p, _c_p, _i32, _i32, _i32, _i32, _c_p]),
@@ -480,8 +481,16 @@ def attn_prefill_workspace(total_rows: int, n_q: int, head_dim: int, max_kv: int
     return int(lib().kinv_attn_prefill_workspace(total_rows, n_q, head_dim, max_kv, split_len))
 
 
-def _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len, max_kv, out, split_len, window,
-                         sinks, scale, stream):
+def attn_prefill_window_workspace(batch: int, max_q_len: int, n_q: int, n_kv: int, head_dim: int, max_kv: int,
+                                  window: int = 0, sinks: int = 0, split_len: int = SPLIT_LEN) -> int:
+    """Bytes with which attn_prefill with a window spreads short chunks over the whole
+    GPU (the bits are the same without); 0 where it would not help."""
+    return int(lib().kinv_attn_prefill_window_workspace(batch, max_q_len, n_q, n_kv, head_dim, max_kv, split_len, window,
+                                                        sinks))
+
+
+def _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len, max_kv, out, workspace,
+                         split_len, window, sinks, scale, stream):
     _rows_of(q, out, "attn_prefill")
     rows, hq, d = q.shape
     bsz = q_start.shape[0]
@@ -493,16 +502,20 @@ def _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_le
     _vector(q_offset, bsz, "q_offset")
     _window_ints(window, sinks)
     _here(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("q_start", q_start), ("q_len", q_len),
-          ("q_offset", q_offset), ("out", out))
+          ("q_offset", q_offset), ("out", out), ("workspace", workspace))
     side = None if stream is None else _side(stream)
     if out is None:
         out = _empty_like(side)(q)
+    if workspace is None or not workspace.is_contiguous():
+        need = attn_prefill_window_workspace(bsz, max_q_len, hq, shape[2], d, max_kv, window, sinks, split_len)
+        workspace = _workspace(side, workspace, need, q.device) if need or workspace is not None else None
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     if side is not None:
-        _hold(side, q, k_cache, v_cache, q_start, q_len, q_offset, out)
+        _hold(side, q, k_cache, v_cache, q_start, q_len, q_offset, out, workspace)
     _check(lib().kinv_attn_prefill_window(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), stride[0], stride[1],
                                           q_start.data_ptr(), q_len.data_ptr(), q_offset.data_ptr(), out.data_ptr(),
                                           bsz, rows, max_q_len, max_kv, hq, shape[2], d, split_len, window, sinks, scale,
-                                          None, 0, _stream(stream)), "kinv_attn_prefill_window")
+                                          ws, ws_bytes, _stream(stream)), "kinv_attn_prefill_window")
     return out
 
 
@@ -513,8 +526,8 @@ def attn_prefill(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len: int, 
     window a row sees its last ``window`` keys and the first ``sinks`` of its
     sequence; rows of no sequence are not written."""
     if window or sinks < 0:
-        return _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len, max_kv, out, split_len,
-                                    window, sinks, scale, stream)
+        return _attn_prefill_window(q, k_cache, v_cache, q_start, q_len, q_offset, max_q_len, max_kv, out, workspace,
+                                    split_len, window, sinks, scale, stream)
     _need(q, torch.bfloat16, "q")
     rows, hq, d = q.shape
     hkv = k_cache.shape[2]

@@ -146,15 +146,15 @@ def test_window_refusals(lib):
     def decode(window=5, sinks=1, d=64, hq=2, split=256, ws=FAKE, wsb=1 << 30, q=FAKE, n=FAKE):
         return L.kinv_attn_decode_window(q, FAKE, FAKE, 64 * 512, 64, n, FAKE, 2, hq, 1, d, 512, split, window, sinks, 0.0, ws, wsb, None)
 
-    def prefill(window=5, sinks=1, d=64, hq=2, split=256, q=FAKE, rows=20):
+    def prefill(window=5, sinks=1, d=64, hq=2, split=256, q=FAKE, rows=20, ws=None):
         return L.kinv_attn_prefill_window(q, FAKE, FAKE, 64 * 512, 64, FAKE, FAKE, FAKE, FAKE, 2, rows, 10, 512, hq, 1, d, split, window, sinks, 0.0,
-                                          None, 0, None)
+                                          ws, 0, None)
     for call in (decode, prefill):
         assert call(window=-1) == lib.ERR_INVALID_ARG and call(sinks=-1) == lib.ERR_INVALID_ARG
         assert call(d=96) == lib.ERR_UNSUPPORTED and call(hq=3) == lib.ERR_UNSUPPORTED and call(split=128) == lib.ERR_UNSUPPORTED
         assert call(q=None) == lib.ERR_INVALID_ARG and call(q=FAKE + 2) == lib.ERR_ALIGNMENT
     assert decode(n=None) == lib.ERR_INVALID_ARG and decode(ws=None) == lib.ERR_INVALID_ARG and decode(wsb=100) == lib.ERR_WORKSPACE
-    assert prefill(rows=0) == lib.OK and prefill(rows=-1) == lib.ERR_INVALID_ARG
+    assert prefill(rows=0) == lib.OK and prefill(rows=-1) == lib.ERR_INVALID_ARG and prefill(ws=FAKE + 8) == lib.ERR_ALIGNMENT
 
 
 def test_workspaces_grow_with_the_window(lib):
@@ -169,7 +169,14 @@ def test_workspaces_grow_with_the_window(lib):
         assert lib.attn_decode8_workspace(4, 32, 128, 32768, window, sinks) == want
     assert lib.attn_decode8_workspace(4, 32, 128, 100, 4096, 4) == one
     assert lib.attn_decode8_workspace(0, 32, 128, 100) == 0 and lib.attn_decode8_workspace(4, 32, 128, 100, -1) == 0
-    assert lib.attn_prefill8_workspace(3, 10, 32, 8, 128, 1000) == 3 * 1000 * 8 * 128 * 4
+    # the keys and values read back, and the partials of 24 tiles over four splits
+    assert lib.attn_prefill8_workspace(3, 10, 32, 8, 128, 1000) == 3 * 1000 * 8 * 128 * 4 + 24 * 4 * 128 * (128 + 2) * 4
+    assert lib.attn_prefill8_workspace(3, 10, 32, 8, 128, 700) == 3 * 700 * 8 * 128 * 4
+    for rows in (32, 33, 128, 4096):   # never less for a longer chunk
+        assert lib.attn_prefill_window_workspace(1, rows, 32, 8, 128, 32768) == min((rows + 31) // 32, 4) * 8 * 128 * 128 * (128 + 2) * 4
+    # rows of a tile see 4,096 + 31 keys: 18 splits, and one of sinks
+    assert lib.attn_prefill_window_workspace(1, 32, 32, 8, 128, 32768, 4096, 4) == 8 * 19 * 128 * (128 + 2) * 4
+    assert lib.attn_prefill_window_workspace(5, 32, 32, 8, 128, 32768) == 0 and lib.attn_prefill_window_workspace(1, 32, 32, 8, 128, 768) == 0
     assert lib.attn_prefill8_workspace(3, 0, 32, 8, 128, 1000) == 0
 
 

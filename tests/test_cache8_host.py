@@ -153,10 +153,9 @@ def test_outputs_workspaces_and_windows_are_checked(here, name):
             call(args(), None, out=Here(shape, dtype, strides))
     with pytest.raises(ValueError):
         call(args(), None, out=Here((3, 4, 64), BF, device=1))
-    if name != "attn_prefill":
-        for ws in (Here((1 << 20,), U8, (2,)), Here((1 << 20,), U8, device=1)):
-            with pytest.raises(ValueError):
-                call(args(), None, workspace=ws)
+    for ws in (Here((1 << 20,), U8, (2,)), Here((1 << 20,), U8, device=1)):
+        with pytest.raises(ValueError):
+            call(args(), None, workspace=ws)
     with pytest.raises(ValueError):
         call(args(), None, sinks=2**31)
     if name.endswith("8"):

@@ -451,3 +451,94 @@ def test_calls_on_a_named_stream(kinv):
     for b, m in enumerate([50, 7, 0, 33]):
         assert_same_bits(back[b, :m], ref[b, :m], "written")
     assert kinv.last_device_status() == 0
+
+
+# ------------------------------------------- short chunks over many splits
+FEW = [  # query heads, kv heads, D; rows of each sequence; their first positions; window, sinks
+    ((32, 8, 128), [1], [8000], 0, 0), ((32, 8, 128), [33], [3000], 0, 0), ((32, 8, 128), [64], [5000], 700, 300),
+    ((32, 8, 128), [128], [2100], 4000, 1), ((32, 8, 128), [0, 5, 32, 1], [10, 2500, 1000, 0], 0, 0),
+    ((4, 2, 64), [100, 0, 64, 1, 65, 100], [0, 5, 1900, 1999, 1000, 255], 0, 0), ((4, 2, 64), [130, 7], [1500, 2000], 900, 4),
+    ((8, 1, 128), [16, 17, 300], [1, 2000, 1500], 0, 0), ((8, 1, 64), [64] * 9, list(range(100, 1900, 200)), 1000, 0), ((2, 2, 64), [300], [1700], 0, 0),
+    ((4, 4, 128), [1, 128], [1279, 4000], 1200, 600),
+]
+
+
+@pytest.mark.parametrize("heads,n,start,window,sinks", FEW, ids=str)
+def test_short_chunks_spread_over_the_gpu_keep_their_bits(kinv, heads, n, start, window, sinks):
+    hq, hkv, d = heads
+    slots = max(a + b for a, b in zip(n, start)) + 9
+    rows, bsz = sum(n) + 3, len(n)
+    off = [2 + sum(n[:i]) for i in range(bsz)]
+    k, v = keys((bsz, slots, hkv, d), 260), keys((bsz, slots, hkv, d), 261)
+    q = synth.normal_bf16((rows, hq, d), 1.0, 262, "cuda")
+    args = (i32(start), i32(n), i32(off), max(n), slots)
+    big = window or slots + 1
+    need = kinv.attn_prefill_window_workspace(bsz, max(n), hq, hkv, d, slots, big, sinks)
+    assert need > 0
+    out = torch.full_like(q, 7.0)
+    ws = torch.full((need // 4,), NAN, dtype=torch.float32, device="cuda")
+    kinv.attn_prefill(q, k, v, *args, out=out, workspace=ws, window=big, sinks=sinks)
+    small = torch.empty(need - 16, dtype=torch.uint8, device="cuda")     # too small: a block per tile
+    whole = torch.full_like(q, 7.0)
+    kinv.attn_prefill(q, k, v, *args, out=whole, workspace=small, window=big, sinks=sinks)
+    assert_same_bits(out, whole, "spread == whole tiles")
+    assert (out[:2] == 7).all() and (out[rows - 1:] == 7).all()
+    for b in range(bsz):
+        for i in sorted({0, n[b] // 2, n[b] - 1}) if n[b] else []:
+            dec = kinv.attn_decode(q[off[b] + i: off[b] + i + 1], k[b: b + 1], v[b: b + 1], i32([start[b] + i + 1]), window=window, sinks=sinks)
+            assert_same_bits(out[off[b] + i], dec[0], f"row {i} of sequence {b}")
+    for fmt in ("e4m3", "int8"):
+        c, (k16, v16) = cache8(kinv, k, v, fmt)
+        got = torch.full_like(q, 7.0)
+        kinv.attn_prefill8(q, c, *args, out=got, window=window, sinks=sinks)
+        want = torch.full_like(q, 7.0)
+        kinv.attn_prefill(q, k16, v16, *args, out=want, workspace=small, window=big, sinks=sinks)
+        assert_same_bits(got, want, fmt)
+    assert kinv.last_device_status() == 0
+
+
+def test_short_chunks_with_numbers_outside_their_bounds_and_hidden_slots(kinv):
+    """A sequence that breaks a bound is left out and reported; NaN where no row sees it;
+    an infinite score stays with its rows."""
+    hq, hkv, d, slots = 8, 1, 128, 3000
+    k, v = keys((4, slots, hkv, d), 270), keys((4, slots, hkv, d), 271)
+    q = synth.normal_bf16((20, hq, d), 1.0, 272, "cuda")
+    good = (i32([2000, 2990, 1500, 100]), i32([5, 5, 5, 5]), i32([0, 5, 10, 15]), 5, slots)
+    ref = kinv.attn_prefill(q, k, v, *good, window=1300, sinks=2)
+    for t in (k, v):
+        t[0, 2: 2001 - 1300] = NAN
+        t[0, 2005:] = NAN
+    out = torch.full_like(q, 7.0)
+    kinv.attn_prefill(q, k, v, i32([2000, 2996, 1500, -1]), i32([5, 5, 6, 5]), i32([0, 5, 10, 15]), 5, slots, out=out, window=1300, sinks=2)
+    assert kinv.last_device_status() == kinv.ERR_INVALID_ARG
+    assert (out[5:] == 7).all()
+    assert_same_bits(out[:5], ref[:5], "the sequence that is left")
+    kinv.attn_prefill(q, k, v, i32([2000, 2990, 1500, 100]), i32([5] * 4), i32([0, 16, 10, 15]), 5, slots, out=out, window=1300, sinks=2)
+    assert kinv.last_device_status() == kinv.ERR_INVALID_ARG     # rows 16 .. 20 of 20
+    assert_same_bits(out[10:15], ref[10:15], "another")
+
+
+def test_short_chunks_on_two_streams_and_in_a_graph(kinv):
+    hq, hkv, d, slots = 32, 8, 128, 4000
+    k, v = keys((1, slots, hkv, d), 280), keys((1, slots, hkv, d), 281)
+    c, _ = cache8(kinv, k, v, "int8")
+    qs = [synth.normal_bf16((16, hq, d), 1.0, 282 + i, "cuda") for i in range(3)]
+    args = (i32([3900]), i32([16]), i32([0]), 16, slots)
+    want = [kinv.attn_prefill8(q, c, *args, window=3000, sinks=4) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            got.append((i, kinv.attn_prefill8(qs[i], c, *args, window=3000, sinks=4, stream=st)))
+    torch.cuda.synchronize()
+    for i, o in got:
+        assert_same_bits(o, want[i], "two streams")
+    q = qs[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = kinv.attn_prefill8(q, c, *args, window=3000, sinks=4)
+    for i in (2, 1, 0):
+        q.copy_(qs[i])
+        g.replay()
+        assert_same_bits(o, want[i], "replayed")
