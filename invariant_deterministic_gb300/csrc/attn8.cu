@@ -564,8 +564,7 @@ size_t read_back_bytes(int B, int max_kv, int Hkv, int D) { return static_cast<s
 extern "C" size_t kinv_attn_prefill8_workspace(int B, int total_rows, int Hq, int Hkv, int D, int max_kv,
                                                int split_len) {
   if (B <= 0 || total_rows <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_kv <= 0 || split_len != kSplit) return 0;
-  return read_back_bytes(B, max_kv, Hkv, D) +
-         kinv_attn_prefill_window_workspace(B, total_rows, Hq, Hkv, D, max_kv, split_len, 0, 0);
+  return read_back_bytes(B, max_kv, Hkv, D) + most_parts_bytes(B, total_rows, Hq, Hkv, D, max_kv);
 }
 
 extern "C" kinv_status kinv_attn_prefill8(const void* q, const kinv_cache8* cache, const int32_t* q_start,

@@ -71,9 +71,12 @@ struct Args {
   float2* parts_ml;       // ... and (m, l), [step][128 pairs]
 };
 
-// At most this many tiles are spread over the GPU by their splits (a quarter of its
-// SMs), from this many splits on: 
-constexpr int kFewTiles = 38, kFewSplits = 4;
+// At most this many tiles (a quarter of the SMs) are spread over the GPU, from this many
+// splits on.  32/8 heads of 128, whole tiles against spread: 16 rows behind 300 keys
+// (two splits) 16.6 and 16.5 us, behind 600 20.6 and 16.5, 8,000 108 and 27, 32,000 392
+// and 66; 128 rows (32 tiles) 20.6 and 19.5 behind 600, 109 and 53 behind 8,000; 256 rows
+// (64 tiles) 112 and 110 there, with 134 MB of partials.
+constexpr int kFewTiles = 38, kFewSplits = 3;
 
 // One step of a block: a split of a tile.
 struct Step {
@@ -666,6 +669,8 @@ int64_t parts_steps(int64_t tiles, int RT, int window, int sinks, int max_kv) {
   return tiles > kFewTiles || splits < kFewSplits ? 0 : tiles * splits;
 }
 
+int64_t tiles_of(int rows, int RT) { return (static_cast<int64_t>(rows) + RT - 1) / RT; }
+
 constexpr size_t part_bytes(int D) { return static_cast<size_t>(kPairs) * (D * 4 + 8); }
 
 template <int D>
@@ -761,14 +766,15 @@ extern "C" kinv_status kinv_attn_prefill_window(const void* q, const void* k_cac
 extern "C" size_t kinv_attn_prefill_window_workspace(int B, int max_q_len, int Hq, int Hkv, int D, int max_kv,
                                                      int split_len, int window, int sinks) {
   if (B <= 0 || max_q_len <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || max_kv <= 0 || window < 0 || sinks < 0 ||
-      split_len != kSplit)
+      split_len != kSplit || Hq / Hkv > kPairs)
     return 0;
-  const int G = Hq / Hkv;
-  if (G > 8) return 0;
-  // the largest of a call with up to max_q_len rows of a sequence: as many tiles of each as are spread
-  const int RT = kPairs / G;
-  int64_t per_seq = (static_cast<int64_t>(max_q_len) + RT - 1) / RT;
-  const int64_t most = kFewTiles / (static_cast<int64_t>(Hkv) * B);
-  if (per_seq > most) per_seq = most;
-  return static_cast<size_t>(parts_steps(per_seq * Hkv * B, RT, window, sinks, max_kv)) * part_bytes(D);
+  const int RT = kPairs / (Hq / Hkv);
+  return parts_steps(tiles_of(max_q_len, RT) * Hkv * B, RT, window, sinks, max_kv) * part_bytes(D);
+}
+
+size_t kinv::most_parts_bytes(int B, int most_rows, int Hq, int Hkv, int D, int max_kv) {
+  if (Hq % Hkv || Hq / Hkv > kPairs) return 0;
+  const int RT = kPairs / (Hq / Hkv);
+  const int64_t per_seq = tiles_of(most_rows, RT), most = kFewTiles / (static_cast<int64_t>(Hkv) * B);
+  return parts_steps((per_seq < most ? per_seq : most) * Hkv * B, RT, 0, 0, max_kv) * part_bytes(D);
 }

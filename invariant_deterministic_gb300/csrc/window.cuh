@@ -50,6 +50,10 @@ inline int64_t max_visible_splits(int window, int sinks, int max_len) {
   return some < all ? some : all;
 }
 
+// Bytes of the partials that kinv_attn_prefill_window may use for a call of at most
+// most_rows rows of a sequence, whatever the window.
+size_t most_parts_bytes(int B, int most_rows, int Hq, int Hkv, int D, int max_kv);
+
 // The fold of a row's split partials, in ascending split order with the
 // log-sum-exp update: the arithmetic of decode attention without a window.
 struct MergeParams {

@@ -144,8 +144,9 @@ class Decoder:
             ws = kinv.attn_decode_workspace(max_batch, s.n_q, s.head_dim, max_len, window=s.window, sinks=s.sinks)
             if max_chunk:
                 ws = max(ws, kinv.attn_prefill_workspace(max_chunk, s.n_q, s.head_dim, max_len))
-                if s.window:
-                    ws = max(ws, kinv.attn_prefill_window_workspace(1, max_chunk, s.n_q, s.n_kv, s.head_dim, max_len, s.window, s.sinks))
+                if s.window:  # every number of tiles of a chunk (a tile has 16 rows or more)
+                    ws = max(ws, *(kinv.attn_prefill_window_workspace(1, r, s.n_q, s.n_kv, s.head_dim, max_len, s.window, s.sinks)
+                                   for r in range(1, max_chunk + 1, 16)))
         else:
             ws = kinv.attn_decode8_workspace(max_batch, s.n_q, s.head_dim, max_len, s.window, s.sinks)
             ws = max(ws, kinv.attn_prefill8_workspace(1, rows, s.n_q, s.n_kv, s.head_dim, max_len))

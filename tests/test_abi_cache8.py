@@ -171,12 +171,15 @@ def test_workspaces_grow_with_the_window(lib):
     assert lib.attn_decode8_workspace(0, 32, 128, 100) == 0 and lib.attn_decode8_workspace(4, 32, 128, 100, -1) == 0
     # the keys and values read back, and the partials of 24 tiles over four splits
     assert lib.attn_prefill8_workspace(3, 10, 32, 8, 128, 1000) == 3 * 1000 * 8 * 128 * 4 + 24 * 4 * 128 * (128 + 2) * 4
-    assert lib.attn_prefill8_workspace(3, 10, 32, 8, 128, 700) == 3 * 700 * 8 * 128 * 4
-    for rows in (32, 33, 128, 4096):   # never less for a longer chunk
-        assert lib.attn_prefill_window_workspace(1, rows, 32, 8, 128, 32768) == min((rows + 31) // 32, 4) * 8 * 128 * 128 * (128 + 2) * 4
+    assert lib.attn_prefill8_workspace(3, 10, 32, 8, 128, 500) == 3 * 500 * 8 * 128 * 4
+    for rows in (1, 32, 33, 128, 129, 4096):   # at most 38 tiles are spread
+        bytes_of = lambda r: (r + 31) // 32 * 8 * 128 * 128 * (128 + 2) * 4
+        assert lib.attn_prefill_window_workspace(1, rows, 32, 8, 128, 32768) == (bytes_of(rows) if rows <= 128 else 0)
+        # over an 8-bit cache as much as any chunk of up to so many rows can use
+        assert lib.attn_prefill8_workspace(1, rows, 32, 8, 128, 32768) == 32768 * 8 * 128 * 4 + bytes_of(min(rows, 128))
     # rows of a tile see 4,096 + 31 keys: 18 splits, and one of sinks
     assert lib.attn_prefill_window_workspace(1, 32, 32, 8, 128, 32768, 4096, 4) == 8 * 19 * 128 * (128 + 2) * 4
-    assert lib.attn_prefill_window_workspace(5, 32, 32, 8, 128, 32768) == 0 and lib.attn_prefill_window_workspace(1, 32, 32, 8, 128, 768) == 0
+    assert lib.attn_prefill_window_workspace(5, 32, 32, 8, 128, 32768) == 0 and lib.attn_prefill_window_workspace(1, 32, 32, 8, 128, 512) == 0
     assert lib.attn_prefill8_workspace(3, 0, 32, 8, 128, 1000) == 0
 
 

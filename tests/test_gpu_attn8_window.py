@@ -459,7 +459,7 @@ FEW = [  # query heads, kv heads, D; rows of each sequence; their first position
     ((32, 8, 128), [128], [2100], 4000, 1), ((32, 8, 128), [0, 5, 32, 1], [10, 2500, 1000, 0], 0, 0),
     ((4, 2, 64), [100, 0, 64, 1, 65, 100], [0, 5, 1900, 1999, 1000, 255], 0, 0), ((4, 2, 64), [130, 7], [1500, 2000], 900, 4),
     ((8, 1, 128), [16, 17, 300], [1, 2000, 1500], 0, 0), ((8, 1, 64), [64] * 9, list(range(100, 1900, 200)), 1000, 0), ((2, 2, 64), [300], [1700], 0, 0),
-    ((4, 4, 128), [1, 128], [1279, 4000], 1200, 600),
+    ((4, 4, 128), [1, 128], [1279, 4000], 1200, 600), ((32, 8, 128), [17, 3], [600, 0], 0, 0), ((4, 2, 64), [70], [500], 600, 1),
 ]
 
 
