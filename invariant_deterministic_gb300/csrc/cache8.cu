@@ -15,24 +15,61 @@ struct RopeTurns {
   uint64_t turn[64];
 };
 
-// cos and sin of the angle of position p, correct to about their rounding in fp32:
-// integers instead of kinv_rope_append's fp64 (this GPU does two fp64 operations a
-// cycle and SM), and what the angle loses in fp32 put back (its low part d: cos - d
-// sin, sin + d cos), as a rounding that goes the other way moves a key's code by a
-// whole step.
+// A number as the sum of two floats, the second below half a step of the first.
+struct Two {
+  float h, l;
+};
+
+// a + b exactly, |a| >= |b| or a = 0.
+__device__ __forceinline__ Two fast_sum(float a, float b) {
+  const float h = __fadd_rn(a, b);
+  return {h, __fadd_rn(__fsub_rn(a, h), b)};
+}
+
+__device__ __forceinline__ Two product_of(float a, float b) {
+  const float h = __fmul_rn(a, b);
+  return {h, __fmaf_rn(a, b, -h)};
+}
+
+// cos and sin of the angle of position p, rounded to fp32 from 2^-27: integers instead of
+// kinv_rope_append's fp64 (this GPU does two fp64 operations a cycle and SM) down to an
+// eighth of a turn, then the Taylor series with their first terms in two floats (a
+// rounding that goes the other way moves a key's code by a whole step).
 __device__ __forceinline__ void rope_angle_turns(int p, uint64_t turn, float& c, float& s) {
-  const int64_t x = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(p)) * turn);  // signed fraction * 2^64
-  // x = (h + l) 2^40, to 2^-56 of a turn; h exact as a float, l to 2^-24 of it
-  const float h = static_cast<float>(static_cast<int32_t>(x >> 40));
-  const float l = static_cast<float>(static_cast<uint32_t>(x >> 8)) * 0x1p-32f;
-  constexpr double kTurn = 6.283185307179586476925 * 0x1p-24;  // radians of a unit of h
+  const uint64_t x = static_cast<uint64_t>(static_cast<uint32_t>(p)) * turn;  // fraction of a turn * 2^64
+  const uint32_t quarter = static_cast<uint32_t>((x + (1ull << 61)) >> 62);
+  const int64_t y = static_cast<int64_t>(x - (static_cast<uint64_t>(quarter) << 62));
+  // y = (h + l) 2^38, h exact as a float
+  const float h = static_cast<float>(static_cast<int32_t>(y >> 38));
+  const float l = __fmul_rn(static_cast<float>(static_cast<uint32_t>(y >> 6)), 0x1p-32f);
+  constexpr double kTurn = 6.283185307179586476925 * 0x1p-26;  // radians of a unit of h
   constexpr float kHi = static_cast<float>(kTurn), kLo = static_cast<float>(kTurn - static_cast<double>(kHi));
-  const float hi = __fmul_rn(h, kHi);
-  const float d = __fmaf_rn(h, kHi, -hi) + __fmaf_rn(h, kLo, __fmul_rn(l, kHi));
-  float c0, s0;
-  sincosf(hi, &s0, &c0);
-  c = __fmaf_rn(-d, s0, c0);
-  s = __fmaf_rn(d, c0, s0);
+  const Two a0 = product_of(h, kHi);
+  const Two a = fast_sum(a0.h, __fadd_rn(a0.l, __fmaf_rn(h, kLo, __fmul_rn(l, kHi))));
+  Two z = product_of(a.h, a.h);
+  z.l = __fmaf_rn(__fmul_rn(2.f, a.h), a.l, z.l);
+  // cos = 1 - z / 2 + z^2 (1/4! - z/6! + z^2/8! - z^3/10!)
+  float t = __fmaf_rn(z.h, -2.7557319e-7f, 2.4801587e-5f);
+  t = __fmaf_rn(z.h, t, -1.3888889e-3f);
+  t = __fmaf_rn(z.h, t, 4.1666667e-2f);
+  const Two c0 = fast_sum(1.f, __fmul_rn(-0.5f, z.h));
+  const Two cc = fast_sum(c0.h, __fadd_rn(c0.l, __fmaf_rn(__fmul_rn(z.h, z.h), t, __fmul_rn(-0.5f, z.l))));
+  // sin = a - a z / 3! + a z^2 (1/5! - z/7! + z^2/9! - z^3/11!)
+  t = __fmaf_rn(z.h, -2.5052108e-8f, 2.7557319e-6f);
+  t = __fmaf_rn(z.h, t, -1.9841270e-4f);
+  t = __fmaf_rn(z.h, t, 8.3333333e-3f);
+  Two q = product_of(a.h, z.h);
+  q.l = __fadd_rn(q.l, __fmaf_rn(a.h, z.l, __fmul_rn(a.l, z.h)));
+  constexpr float kSixth = 1.f / 6.f, kSixthLo = static_cast<float>(1.0 / 6.0 - static_cast<double>(kSixth));
+  const Two w = product_of(q.h, kSixth);
+  const float wl = __fadd_rn(w.l, __fmaf_rn(q.h, kSixthLo, __fmul_rn(q.l, kSixth)));
+  const Two s0 = fast_sum(a.h, -w.h);
+  const Two ss = fast_sum(s0.h, __fadd_rn(s0.l, __fadd_rn(__fsub_rn(a.l, wl), __fmul_rn(__fmul_rn(q.h, z.h), t))));
+  const bool swap = quarter & 1, minus_c = (quarter + 1) & 2, minus_s = quarter & 2;
+  c = swap ? ss.h : cc.h;
+  s = swap ? cc.h : ss.h;
+  if (minus_c) c = -c;
+  if (minus_s) s = -s;
 }
 
 // D / 16 lanes hold a head, each lane eight rotation pairs (i, i + D/2) in two 16-byte
