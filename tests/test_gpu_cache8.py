@@ -53,10 +53,10 @@ def rotated_range(x, pos, base, gain, eps):
     """fp64 rotated heads x [T][H][D] -> (least, most) that fp32 arithmetic may give
     before the rounding to bf16.  An fp32 rotation of a pair (a, b), each with a
     relative error r1 from the norm, and sin and cos with errors r2, is off by at
-    most (r1 + r2 + 2 u) (|a| + |b|) with u = 2^-24; r1 <= 9 u (a sum of 64 to 128
-    squares by chains of at most 4 and five pair sums, the division, sum, root,
-    reciprocal and two products; half of what is before the root), r2 <= 4 u (two
-    ulps of sincosf, the correction's rounding)."""
+    most (r1 + r2 + 2 u) (|a| + |b|) with u = 2^-24; r1 <= 11 u (a sum of 64 to 128
+    squares by chains of eight and four pair sums, the sum with eps, root, reciprocal
+    and two products; half of what is before the root), r2 <= 2 u (one rounding of
+    a value that is right to 2^-27)."""
     y = obf.to_f64(synth.bits(x))
     if gain is not None:
         y = rmsnorm_f64(y, obf.to_f64(synth.bits(gain)), eps)
