@@ -76,7 +76,7 @@ __device__ __forceinline__ void rope_angle_turns(int p, uint64_t turn, float& c,
 // loads, so a warp takes four heads of 128 (eight of 64) at a time.  A block has one
 // row, or as many as make one wave of blocks, at most sixteen; its threads form the
 // angles together beside the first loads, and each warp asks for its next heads before
-// it works on the last.  Bound by the instructions (issue slots 65 % busy, 2.1 TB/s at
+// it works on the last.  Bound by the instructions (issue slots 68 % busy, 2.4 TB/s at
 // 4,096 rows): so fp32 products go in pairs, gains and angles stand in shared memory in
 // the order of the lanes, and nothing is converted by the slow unit that a sum can
 // round.  4,096 rows of the 8B shape 22.8 us, 16,384 rows 71 (5.2 TB/s); a warp per head

@@ -38,7 +38,7 @@ struct ReadParams {
 
 // Keys (z = 0) or values (z = 1) of `tokens` tokens of one sequence, D / 16
 // lanes per (token, head): 16 codes in, 32 bytes out a lane, two vectors ahead.
-// Writing and reading back 8 x 32,768 tokens of 8 heads of 128 take 552 us, 5.85 TB/s
+// Writing and reading back 8 x 32,768 tokens of 8 heads of 128 take 547 us, 5.9 TB/s
 // (four ahead 561, half as many codes a lane 569).
 template <int D, bool I8>
 __global__ void __launch_bounds__(kReadThreads) cache8_read_kernel(const ReadParams p) {
