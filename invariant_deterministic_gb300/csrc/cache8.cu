@@ -49,15 +49,15 @@ __device__ __forceinline__ void rope_angle_turns(int p, uint64_t turn, float& c,
   Two z = product_of(a.h, a.h);
   z.l = __fmaf_rn(__fmul_rn(2.f, a.h), a.l, z.l);
   // cos = 1 - z / 2 + z^2 (1/4! - z/6! + z^2/8! - z^3/10!)
-  float t = __fmaf_rn(z.h, -2.7557319e-7f, 2.4801587e-5f);
-  t = __fmaf_rn(z.h, t, -1.3888889e-3f);
-  t = __fmaf_rn(z.h, t, 4.1666667e-2f);
+  float t = __fmaf_rn(z.h, -1.f / 3628800.f, 1.f / 40320.f);
+  t = __fmaf_rn(z.h, t, -1.f / 720.f);
+  t = __fmaf_rn(z.h, t, 1.f / 24.f);
   const Two c0 = fast_sum(1.f, __fmul_rn(-0.5f, z.h));
   const Two cc = fast_sum(c0.h, __fadd_rn(c0.l, __fmaf_rn(__fmul_rn(z.h, z.h), t, __fmul_rn(-0.5f, z.l))));
   // sin = a - a z / 3! + a z^2 (1/5! - z/7! + z^2/9! - z^3/11!)
-  t = __fmaf_rn(z.h, -2.5052108e-8f, 2.7557319e-6f);
-  t = __fmaf_rn(z.h, t, -1.9841270e-4f);
-  t = __fmaf_rn(z.h, t, 8.3333333e-3f);
+  t = __fmaf_rn(z.h, -1.f / 39916800.f, 1.f / 362880.f);
+  t = __fmaf_rn(z.h, t, -1.f / 5040.f);
+  t = __fmaf_rn(z.h, t, 1.f / 120.f);
   Two q = product_of(a.h, z.h);
   q.l = __fadd_rn(q.l, __fmaf_rn(a.h, z.l, __fmul_rn(a.l, z.h)));
   constexpr float kSixth = 1.f / 6.f, kSixthLo = static_cast<float>(1.0 / 6.0 - static_cast<double>(kSixth));
