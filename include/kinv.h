@@ -313,7 +313,7 @@ kinv_status kinv_attn_prefill(const void* q, const void* k_cache, const void* v_
  * get NaN as well, as in kinv_attn_prefill.
  * Arguments, requirements and errors as above; window < 0 or sinks < 0:
  * KINV_ERR_INVALID_ARG.  The decode call's workspace grows with the window and
- * the sinks instead of Lmax.  The prefill call needs none (NULL); with as many bytes as
+ * the sinks instead of Lmax (Lmax = 0: none, and zeros).  The prefill call needs none (NULL); with as many bytes as
  * its query says (0 where it would not help) it spreads short chunks over long contexts
  * over the whole GPU, with the same bits. */
 size_t kinv_attn_decode_window_workspace(int B, int Hq, int D, int Lmax, int split_len, int window, int sinks);
@@ -407,7 +407,7 @@ kinv_status kinv_cache8_read(const kinv_cache8* cache, const int32_t* start, con
  * largest scale among its 256 keys; so all their invariances hold.  Hidden slots
  * and those behind a sequence's last key may hold anything.
  * kv_len[b] in [0, slots], else zeros and KINV_ERR_INVALID_ARG in the status
- * word; B at most the cache's, max_kv at most its slots; other arguments,
+ * word (a cache of no slots gives zeros, without a workspace); B at most the cache's, max_kv at most its slots; other arguments,
  * requirements and errors as there.  workspace: device, 16-byte aligned, as many
  * bytes as the query says; calls that may run at the same time need one each.
  * The decode call's holds the split partials; the prefill call's holds the keys

@@ -853,8 +853,8 @@ kinv_status launch(const AttnParams& p, dim3 split_grid, dim3 merge_grid, cudaSt
   const kinv_status st = launch_kernel(kernel, split_grid, dim3(kThreads), smem, stream, 1, p);
   if (st != KINV_OK) return st;
   if (WIN)
-    return launch_kernel(window_merge_kernel<D>, merge_grid, dim3(D), 0, stream, 1,
-                         MergeParams{p.ws_o, p.ws_ml, p.kv_len, p.out, p.Hq, p.S, p.max_len, p.win, p.status});
+    return launch_window_merge<D>(MergeParams{p.ws_o, p.ws_ml, p.kv_len, p.out, p.Hq, p.S, p.max_len, p.win, p.status},
+                                  static_cast<int>(merge_grid.y), stream);
   return launch_kernel(attn_merge_kernel<D>, merge_grid, dim3(D), 0, stream, 1, p);
 }
 
@@ -997,9 +997,17 @@ extern "C" kinv_status kinv_attn_decode_window(const void* q, const void* k_cach
                                                kinv_stream stream) {
   if (window < 0 || sinks < 0) return KINV_ERR_INVALID_ARG;
   const Window win{window, sinks};
+  if (Lmax == 0) {  // no keys and no partials: an aligned stand-in keeps the shared checks
+    if (!workspace) workspace = reinterpret_cast<void*>(static_cast<uintptr_t>(256));
+    ws_bytes = SIZE_MAX;
+  }
   const kinv_status st = decode_check(q, k_cache, v_cache, seq_stride, tok_stride, kv_len, out, B, Hq, Hkv,
                                       D, Lmax, split_len, workspace, ws_bytes, win);
   if (st != KINV_OK || B == 0) return st;
+  if (Lmax == 0) {
+    const MergeParams p{nullptr, nullptr, kv_len, static_cast<__nv_bfloat16*>(out), Hq, 0, 0, win, device_status_word()};
+    return D == 128 ? launch_window_merge<128>(p, B, stream) : launch_window_merge<64>(p, B, stream);
+  }
   return decode_launch(q, k_cache, v_cache, seq_stride, tok_stride, kv_len, out, B, Hq, Hkv, D, Lmax, scale,
                        workspace, stream, win);
 }

@@ -487,11 +487,12 @@ kinv_status launch_decode8(const Attn8Params& p, const MergeParams& mp, int Hkv,
   if (places > most) places = most;
   st = launch_kernel(kernel, dim3(Hkv, static_cast<unsigned>(places)), dim3(kThreads), smem, stream, 1, mk, mv, p);
   if (st != KINV_OK) return st;
-  return launch_kernel(window_merge_kernel<D>, dim3(p.Hq, p.B), dim3(D), 0, stream, 1, mp);
+  return launch_window_merge<D>(mp, p.B, stream);
 }
 
 template <int D, bool I8>
 kinv_status launch_decode8(const Attn8Params& p, const MergeParams& mp, int Hkv, cudaStream_t stream) {
+  if (p.S == 0) return launch_window_merge<D>(mp, p.B, stream);
   return p.G <= 4 ? launch_decode8<D, I8, 4>(p, mp, Hkv, stream) : launch_decode8<D, I8, 8>(p, mp, Hkv, stream);
 }
 
@@ -527,9 +528,9 @@ extern "C" kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache
   if (st != KINV_OK) return st;
   if (B > cache->B) return KINV_ERR_INVALID_ARG;
   if (B == 0) return KINV_OK;
-  if (!q || !out || !kv_len || !workspace) return KINV_ERR_INVALID_ARG;
+  if (!q || !out || !kv_len || (!workspace && cache->slots > 0)) return KINV_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return KINV_ERR_ALIGNMENT;
-  const int64_t S = cache->slots > 0 ? max_visible_splits(window, sinks, cache->slots) : 1;
+  const int64_t S = max_visible_splits(window, sinks, cache->slots);  // 0 for a cache of no slots
   const bool i8 = cache->dtype == KINV_I8;
   p.c2 = base2_factor(scale, D);
   if (B > 1 && cache->seq_stride == 0) return KINV_ERR_INVALID_ARG;

@@ -147,4 +147,11 @@ __global__ void window_merge_kernel(const MergeParams p) {
   *dst = __float2bfloat16_rn(__fdiv_rn(o_acc, l_acc));
 }
 
+// Of B rows; with a cache of no slots it is the whole call: zeros, and lengths that are
+// not 0 reported.
+template <int D>
+inline kinv_status launch_window_merge(const MergeParams& p, int B, cudaStream_t stream) {
+  return launch_kernel(window_merge_kernel<D>, dim3(p.Hq, B), dim3(D), 0, stream, 1, p);
+}
+
 }  // namespace kinv
