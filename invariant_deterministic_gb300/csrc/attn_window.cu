@@ -39,6 +39,7 @@
 // their weights, when its products are done.
 #include <math.h>
 
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -745,7 +746,10 @@ extern "C" kinv_status kinv_attn_prefill_window(const void* q, const void* k_cac
   a.Hkv = Hkv;
   a.G = G;
   a.RT = kPairs / G;
-  a.tiles_per_seq = (max_q_len + a.RT - 1) / a.RT;
+  // a sequence's rows are rows of the call and keys of the cache: a bound above both
+  // leaves no room for more tiles (and max_q_len + RT within 32 bits)
+  const int most_rows = std::min({max_q_len, total_rows, max_kv});
+  a.tiles_per_seq = static_cast<int>(tiles_of(most_rows, a.RT));
   a.max_len = max_kv;
   a.max_q_len = max_q_len;
   a.total_rows = total_rows;

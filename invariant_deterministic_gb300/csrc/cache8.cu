@@ -375,6 +375,13 @@ kinv_status check_ranges(const void* k, const void* v, int64_t seq_stride, int64
   if (B > 65535 || Hkv > kMaxKvHeads) return KINV_ERR_UNSUPPORTED;
   return KINV_OK;
 }
+
+// No sequence of more tokens than the cache has slots fits, so a bound above them asks
+// for no more blocks (one at least, which reports what does not fit).
+int most_tokens(int max_len, const kinv_cache8& cache) {
+  const int slots = cache.slots > 0 ? cache.slots : 1;
+  return max_len < slots ? max_len : slots;
+}
 }  // namespace
 }  // namespace kinv
 
@@ -391,11 +398,11 @@ extern "C" kinv_status kinv_cache8_write(const void* k, const void* v, int64_t s
   p.tok_stride = tok_stride;
   p.start = start;
   p.len = len;
-  p.max_len = max_len;
+  p.max_len = most_tokens(max_len, *cache);
   p.Hkv = Hkv;
   p.status = device_status_word();
-  p.tokens = tokens_per_block(B, max_len, Hkv, D);
-  const dim3 grid((max_len + p.tokens - 1) / p.tokens, B, 2);
+  p.tokens = tokens_per_block(B, p.max_len, Hkv, D);
+  const dim3 grid((p.max_len + p.tokens - 1) / p.tokens, B, 2);
   const size_t smem = static_cast<size_t>(Hkv) * p.tokens;
   auto run = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kWriteThreads), smem, stream, 1, p); };
   const bool i8 = cache->dtype == KINV_I8;
@@ -416,7 +423,7 @@ extern "C" kinv_status kinv_cache8_read(const kinv_cache8* cache, const int32_t*
   p.tok_stride = tok_stride;
   p.start = start;
   p.len = len;
-  p.max_len = max_len;
+  p.max_len = most_tokens(max_len, *cache);
   p.Hkv = Hkv;
   p.status = device_status_word();
   return launch_cache8_read(p, cache->dtype == KINV_I8, B, D, stream);
