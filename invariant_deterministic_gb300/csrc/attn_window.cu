@@ -167,7 +167,15 @@ struct Walk {
       s.fresh = first;
       first = false;
       if (++s.it < s.ns) return true;
-      while (!tile_at(a, ++round, s)) {}  // one follows: steps are left
+      // a tile follows, for steps are left; without one (lengths written over while the
+      // call runs) the walk ends
+      const int tiles = a.tiles_per_seq * a.Hkv * a.B;
+      do {
+        if (++round >= tiles) {
+          left = 0;
+          return false;
+        }
+      } while (!tile_at(a, round, s));
       s.it = 0;
       s.fresh = true;
       return true;
