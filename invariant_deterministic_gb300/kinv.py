@@ -720,8 +720,16 @@ def attn_decode8(q, cache: Cache8, kv_len, out=None, workspace=None, window: int
 
 
 def attn_prefill8_workspace(batch: int, total_rows: int, n_q: int, n_kv: int, head_dim: int, max_kv: int,
-                            split_len: int = SPLIT_LEN) -> int:
-    return int(lib().kinv_attn_prefill8_workspace(batch, total_rows, n_q, n_kv, head_dim, max_kv, split_len))
+                            split_len: int = SPLIT_LEN, max_q_len=None, window: int = 0, sinks: int = 0) -> int:
+    """Bytes for attn_prefill8: with max_q_len, for a call of that bound, window and
+    sinks; without, enough for every window and every chunk of up to total_rows (1.6 GB
+    behind 131,072 keys of 32/8 heads of 128, of which a 4,096-key window needs 0.6)."""
+    most = int(lib().kinv_attn_prefill8_workspace(batch, total_rows, n_q, n_kv, head_dim, max_kv, split_len))
+    if max_q_len is None or not most:
+        return most
+    rows = min(max_q_len, total_rows, max_kv)
+    return batch * max_kv * n_kv * head_dim * 4 + attn_prefill_window_workspace(batch, rows, n_q, n_kv, head_dim, max_kv,
+                                                                                window, sinks, split_len)
 
 
 def attn_prefill8(q, cache: Cache8, q_start, q_len, q_offset, max_q_len: int, max_kv: int, out=None, workspace=None,
@@ -744,8 +752,8 @@ def attn_prefill8(q, cache: Cache8, q_start, q_len, q_offset, max_q_len: int, ma
     if out is None:
         out = _empty_like(side)(q)
     if workspace is None or not workspace.is_contiguous():
-        workspace = _workspace(side, workspace,
-                               attn_prefill8_workspace(bsz, rows, hq, cache.n_kv, d, max_kv, split_len), q.device)
+        need = attn_prefill8_workspace(bsz, rows, hq, cache.n_kv, d, max_kv, split_len, max_q_len, window, sinks)
+        workspace = _workspace(side, workspace, need, q.device)
     if side is not None:
         _hold(side, q, out, q_start, q_len, q_offset, workspace, *cache.tensors)
     _check(lib().kinv_attn_prefill8(q.data_ptr(), cache.ptr, q_start.data_ptr(), q_len.data_ptr(), q_offset.data_ptr(),

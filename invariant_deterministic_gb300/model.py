@@ -149,8 +149,13 @@ class Decoder:
                                    for r in range(1, max_chunk + 1, 16)))
         else:
             ws = kinv.attn_decode8_workspace(max_batch, s.n_q, s.head_dim, max_len, s.window, s.sinks)
-            ws = max(ws, kinv.attn_prefill8_workspace(1, rows, s.n_q, s.n_kv, s.head_dim, max_len))
+            for r in range(1, max_chunk + 1, 16):
+                ws = max(ws, kinv.attn_prefill8_workspace(1, r, s.n_q, s.n_kv, s.head_dim, max_len, max_q_len=r, window=s.window,
+                                                          sinks=s.sinks))
         self.ws = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.dev)
+        # prefill over an 8-bit cache reads the keys back into scratch: kept where the
+        # decoder is made for chunks, else each call's own
+        self.prefill_ws = self.ws if cache == "bf16" or max_chunk else None
         i32 = dict(dtype=torch.int32, device=self.dev)
         # decode state: row b is sequence b at position pos[b]; attention sees pos[b] + 1 keys
         self.seq = torch.arange(max_batch, **i32)
@@ -354,10 +359,10 @@ class Decoder:
             with self._t("attn_prefill"):
                 if self.cache != "bf16":
                     kinv.attn_prefill8(self.q[:n], self.kv8[li].sequences(seq, seq + 1), q_start, q_len, q_off, n,
-                                       p0 + n, out=self.attn[:n], workspace=self.ws, window=s.window, sinks=s.sinks)
+                                       p0 + n, out=self.attn[:n], workspace=self.prefill_ws, window=s.window, sinks=s.sinks)
                 else:
                     kinv.attn_prefill(self.q[:n], kc[seq: seq + 1], vc[seq: seq + 1], q_start, q_len, q_off, n,
-                                      p0 + n, out=self.attn[:n], workspace=self.ws, window=s.window, sinks=s.sinks)
+                                      p0 + n, out=self.attn[:n], workspace=self.prefill_ws, window=s.window, sinks=s.sinks)
         kinv.row_sumsq(self.x[:rows], self.ss[:rows])
         for li in range(self.s.n_layers):
             self.layer(li, rows, seq_t, pos_t, attention)
