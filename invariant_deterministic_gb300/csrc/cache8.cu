@@ -8,9 +8,9 @@
 namespace kinv {
 namespace {
 
-// Frequencies base^(-2i/D) in turns, as 64-bit fractions: p times one of them,
-// modulo 2^64, is the angle's fraction of a turn to p 2^-65 of it (and the
-// frequency's own 2^-53 relative, as in fp64).
+// Frequencies base^(-2i/D) in turns, formed in fp64 and held as 64-bit fractions (the
+// last bit 0): p times one of them, modulo 2^64, is the angle's fraction of a turn to
+// p 2^-63 of a turn beside p times the fp64 frequency's own error.
 struct RopeTurns {
   uint64_t turn[64];
 };
