@@ -407,7 +407,8 @@ kinv_status kinv_cache8_read(const kinv_cache8* cache, const int32_t* start, con
  * largest scale among its 256 keys; so all their invariances hold.  Hidden slots
  * and those behind a sequence's last key may hold anything.
  * kv_len[b] in [0, slots], else zeros and KINV_ERR_INVALID_ARG in the status
- * word (a cache of no slots gives zeros, without a workspace); B at most the cache's, max_kv at most its slots; other arguments,
+ * word (a cache of no slots gives zeros, without a workspace); B at most the cache's,
+ * max_kv at most its slots; seq_stride > 0 in decode when B > 1; other arguments,
  * requirements and errors as there.  workspace: device, 16-byte aligned, as many
  * bytes as the query says; calls that may run at the same time need one each.
  * The decode call's holds the split partials; the prefill call's holds the keys

@@ -76,12 +76,15 @@ __device__ __forceinline__ void rope_angle_turns(int p, uint64_t turn, float& c,
 // loads, so a warp takes four heads of 128 (eight of 64) at a time.  A block has one
 // row, or as many as make one wave of blocks, at most sixteen; its threads form the
 // angles together beside the first loads, and each warp asks for its next heads before
-// it works on the last.  Bound by the instructions (issue slots 68 % busy, 2.4 TB/s at
-// 4,096 rows): so fp32 products go in pairs, gains and angles stand in shared memory in
-// the order of the lanes, and nothing is converted by the slow unit that a sum can
-// round.  4,096 rows of the 8B shape 22.8 us, 16,384 rows 71 (5.2 TB/s); a warp per head
-// with a pair of values a lane and angles in fp64, as kinv_rope_append has it, 37 us;
-// four rows a block whatever the number of blocks 26.7; a row a block 41.
+// it works on the last.  What bounds many rows: about 16 us for each 4,096 (5.7 TB/s),
+// and about 4 us that do not depend on them, a block's positions, angles and barrier in
+// the only wave there is (4,096 rows of the 8B shape 20.6 us, 4,864 22.6, 9,728 41.3,
+// 16,384 68.7).  To keep the instructions below that (68 % of the issue slots at 4,096
+// rows) fp32 products go in pairs, gains and angles stand in shared memory in the order
+// of the lanes, and nothing is converted by the slow unit that a sum can round.  Before
+// those steps 4,096 rows took 26.7 us with four rows a block whatever the number of
+// blocks, 41 with a row a block, 37 with a warp per head, a pair of values a lane and
+// angles in fp64, as kinv_rope_append has it.
 constexpr int kAppendRows = 16;
 constexpr int kAppendBlocks = 4;  // of 256 threads on an SM
 
