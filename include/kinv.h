@@ -415,8 +415,8 @@ kinv_status kinv_cache8_read(const kinv_cache8* cache, const int32_t* start, con
  * and values that its rows see, read back, B max_kv Hkv D 4 bytes, without which it
  * refuses, and behind them, where the chunk is short, what kinv_attn_prefill_window may
  * use.  kinv_attn_prefill8_workspace() is enough for every window and every chunk of up
- * to total_rows; a call of given max_q_len, window and sinks uses no more than those
- * B max_kv Hkv D 4 bytes and kinv_attn_prefill_window_workspace() of them. */
+ * to total_rows; for a call of one max_q_len (no larger than its rows), window and sinks
+ * those B max_kv Hkv D 4 bytes and kinv_attn_prefill_window_workspace() of them are. */
 size_t kinv_attn_decode8_workspace(int B, int Hq, int D, int slots, int window, int sinks, int split_len);
 kinv_status kinv_attn_decode8(const void* q, const kinv_cache8* cache, const int32_t* kv_len, void* out,
                               int B, int Hq, int Hkv, int D, int split_len, int window, int sinks,
